@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, c_char_p, c_int, c_int32, c_int64, c_void_p
+from ctypes import POINTER, Structure, c_char_p, c_float, c_int, c_int32, c_int64, c_void_p
 from typing import Dict, Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -83,6 +83,9 @@ _SIGS = {
     "moe_quantize_cols_fp8": [c_int64, c_int64, c_int32] + [c_void_p] * 4,
     "moe_expert_dgrad_fp8": [POINTER(MoeDesc), c_int] + [c_void_p] * 14,
     "moe_expert_wgrad_fp8": [POINTER(MoeDesc)] + [c_void_p] * 16,
+    "moe_router_loss_bytes": [POINTER(MoeDesc), c_int32, POINTER(c_int64)],
+    "moe_router_loss": [POINTER(MoeDesc), c_int32, c_float, c_float] + [c_void_p] * 11,
+    "moe_router_loss_bwd": [POINTER(MoeDesc), c_int32, c_float, c_float] + [c_void_p] * 9,
     "moe_stash_store": [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_int64, c_void_p,
                         c_void_p, c_int32, c_int32, c_void_p],
     "moe_stash_load": [c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
@@ -253,6 +256,20 @@ def moe_quantize_rows_fp8(rows, cols, src_bf16, codes, scale, stream=None):
            "moe_quantize_rows_fp8")
 
 
+def moe_router_loss(d, n_segments, balance_coef, z_coef, logits, topk_idx, seg_offsets, token_mask, lse, seg_counts,
+                    seg_tokens, seg_probs, loss, workspace, stream=None):
+    _check(lib().moe_router_loss(ctypes.byref(d), n_segments, balance_coef, z_coef, _ptr(logits), _ptr(topk_idx),
+                                 _ptr(seg_offsets), _ptr(token_mask), _ptr(lse), _ptr(seg_counts), _ptr(seg_tokens),
+                                 _ptr(seg_probs), _ptr(loss), _ptr(workspace), _stream(stream)), "moe_router_loss")
+
+
+def moe_router_loss_bwd(d, n_segments, balance_coef, z_coef, logits, lse, seg_offsets, token_mask, seg_counts,
+                        seg_tokens, dloss, dlogits, stream=None):
+    _check(lib().moe_router_loss_bwd(ctypes.byref(d), n_segments, balance_coef, z_coef, _ptr(logits), _ptr(lse),
+                                     _ptr(seg_offsets), _ptr(token_mask), _ptr(seg_counts), _ptr(seg_tokens),
+                                     _ptr(dloss), _ptr(dlogits), _stream(stream)), "moe_router_loss_bwd")
+
+
 def moe_stash_store(src, src_scale, live_rows, row_bytes, pool, pool_scale, num_pages, page_rows, pages,
                     page_meta=None, owner=0, max_ctas=0, stream=None):
     _check(lib().moe_stash_store(_ptr(src), _ptr(src_scale), live_rows, row_bytes, _ptr(pool), _ptr(pool_scale),
@@ -305,6 +322,13 @@ def workspace_bytes(d) -> Dict[str, int]:
     s = MoeWorkspaceSizes()
     _check(lib().moe_workspace_bytes(ctypes.byref(d), ctypes.byref(s)), "moe_workspace_bytes")
     return {f: getattr(s, f) for f in SIZE_FIELDS}
+
+
+def moe_router_loss_bytes(d, n_segments=1) -> int:
+    """Bytes of moe_router_loss's workspace (allocate it zero-filled)."""
+    n = c_int64()
+    _check(lib().moe_router_loss_bytes(ctypes.byref(d), n_segments, ctypes.byref(n)), "moe_router_loss_bytes")
+    return n.value
 
 
 class ExtentTracker:

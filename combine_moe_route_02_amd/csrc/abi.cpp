@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstdarg>
 #include <cstdio>
@@ -569,6 +570,56 @@ moe_status moe_quantize_cols_fp8(int64_t batch, int64_t rows, int32_t cols, cons
   MOE_NEED(src_bf16); MOE_NEED(codes_t); MOE_NEED(scale);
   MOE_HIP(moe::launch_quantize_cols_fp8(src_bf16, codes_t, scale, batch, rows, cols, (hipStream_t)stream),
           "quantize_cols_fp8");
+  return MOE_OK;
+}
+
+// ----------------------------------------------------------------------------- router loss
+
+static moe_status check_router_loss(const char* fn, const moe_desc* d, int32_t n_segments, float balance_coef,
+                                    float z_coef, const void* seg_offsets) {
+  MOE_TRY(validate(d));
+  if (n_segments < 1) return fail(MOE_ERR_ARG, "%s: n_segments = %d below 1", fn, n_segments);
+  if (n_segments > 65536) return fail(MOE_ERR_UNSUPPORTED, "%s: n_segments = %d above 65536", fn, n_segments);
+  if (!seg_offsets && n_segments != 1)
+    return fail(MOE_ERR_ARG, "%s: argument 'seg_offsets' is NULL with n_segments = %d", fn, n_segments);
+  if (!std::isfinite(balance_coef) || !std::isfinite(z_coef))
+    return fail(MOE_ERR_ARG, "%s: the loss coefficients must be finite", fn);
+  return MOE_OK;
+}
+
+moe_status moe_router_loss_bytes(const moe_desc* d, int32_t n_segments, int64_t* workspace) {
+  if (!workspace) return fail(MOE_ERR_ARG, "output pointer is NULL");
+  MOE_TRY(check_router_loss(__func__, d, n_segments, 0.f, 0.f, workspace));
+  *workspace = moe::router_loss_ws_bytes(d->T, n_segments, d->E);
+  return MOE_OK;
+}
+
+moe_status moe_router_loss(const moe_desc* d, int32_t n_segments, float balance_coef, float z_coef,
+                           const float* logits, const int32_t* topk_idx, const int32_t* seg_offsets,
+                           const uint8_t* token_mask, float* lse, int32_t* seg_counts, int32_t* seg_tokens,
+                           float* seg_probs, float* loss, void* workspace, void* stream) {
+  MOE_TRY(check_router_loss(__func__, d, n_segments, balance_coef, z_coef, seg_offsets));
+  if (d->T > 0) { MOE_NEED(logits); MOE_NEED(topk_idx); MOE_NEED(lse); }
+  MOE_NEED(seg_counts); MOE_NEED(seg_tokens); MOE_NEED(seg_probs); MOE_NEED(loss); MOE_NEED(workspace);
+  if ((uintptr_t)workspace & 15) return fail(MOE_ERR_ARG, "%s: workspace must be 16-byte aligned", __func__);
+  MOE_HIP(moe::launch_router_loss(logits, topk_idx, seg_offsets, token_mask, lse, seg_counts, seg_tokens, seg_probs,
+                                  loss, workspace, d->T, d->E, d->k, n_segments, balance_coef, z_coef,
+                                  (hipStream_t)stream),
+          "router_loss");
+  return MOE_OK;
+}
+
+moe_status moe_router_loss_bwd(const moe_desc* d, int32_t n_segments, float balance_coef, float z_coef,
+                               const float* logits, const float* lse, const int32_t* seg_offsets,
+                               const uint8_t* token_mask, const int32_t* seg_counts, const int32_t* seg_tokens,
+                               const float* dloss, float* dlogits, void* stream) {
+  MOE_TRY(check_router_loss(__func__, d, n_segments, balance_coef, z_coef, seg_offsets));
+  if (d->T == 0) return MOE_OK;
+  MOE_NEED(logits); MOE_NEED(lse); MOE_NEED(seg_counts); MOE_NEED(seg_tokens); MOE_NEED(dlogits);
+  if (dlogits == logits) return fail(MOE_ERR_ARG, "%s: dlogits may not be the logits buffer", __func__);
+  MOE_HIP(moe::launch_router_loss_bwd(logits, lse, seg_offsets, token_mask, seg_counts, seg_tokens, dloss, dlogits,
+                                      d->T, d->E, d->k, n_segments, balance_coef, z_coef, (hipStream_t)stream),
+          "router_loss_bwd");
   return MOE_OK;
 }
 

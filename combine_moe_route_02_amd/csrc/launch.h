@@ -25,6 +25,17 @@ hipError_t launch_route(const float* logits, int32_t* topk_idx, float* gates, in
                         int64_t T, int E, int e0, int El, int K, int n, int chunk0, int nchunks,
                         int64_t P_c, hipStream_t s);
 
+// router loss (router_loss.hip): workspace bytes, forward (two launches) and backward
+int64_t router_loss_ws_bytes(int64_t T, int S, int E);
+hipError_t launch_router_loss(const float* logits, const int32_t* topk_idx, const int32_t* seg_offsets,
+                              const uint8_t* mask, float* lse, int32_t* seg_counts, int32_t* seg_tokens,
+                              float* seg_probs, float* loss, void* workspace, int64_t T, int E, int K, int S,
+                              float balance_coef, float z_coef, hipStream_t s);
+hipError_t launch_router_loss_bwd(const float* logits, const float* lse, const int32_t* seg_offsets,
+                                  const uint8_t* mask, const int32_t* seg_counts, const int32_t* seg_tokens,
+                                  const float* dloss, float* dlogits, int64_t T, int E, int K, int S,
+                                  float balance_coef, float z_coef, hipStream_t s);
+
 // row copies
 hipError_t launch_dispatch(const void* x, const int32_t* row_of, void* xd, int64_t t0, int64_t t1,
                            int K, int64_t row_bytes, hipStream_t s);

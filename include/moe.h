@@ -275,6 +275,47 @@ moe_status moe_quantize_cols_fp8(int64_t batch, int64_t rows, int32_t cols, cons
                                  void* codes_t, float* scale, void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Router loss: balance loss over segments (packed sequences), z-loss and per-expert counts, with
+ * their gradient to the router logits. The pages run without an auxiliary loss (ChunkedEP "Tests and
+ * limitations"); a training step that wants one adds these calls.
+ *
+ * Segment s holds tokens [seg_offsets[s], seg_offsets[s+1]) (device int32 [n_segments + 1],
+ * ascending; entries are clamped to [0, T]); NULL with n_segments = 1 is one segment of all T
+ * tokens. Tokens before the first and behind the last segment, tokens whose token_mask entry
+ * (device uint8 [T], nullable) is 0, and tokens whose logits are all -inf are left out: their
+ * logits may hold anything (a masked row is not read) and reach no sum. For the counted tokens,
+ * with p_t = softmax(logits_t) over all E experts:
+ *   seg_tokens[s] = n_s, seg_tokens[n_segments] = N = sum n_s, seg_tokens[n_segments + 1] = S',
+ *     the segments with n_s > 0;                              int32 [n_segments + 2]
+ *   seg_counts[s][e] = slots of segment s whose topk_idx is e;  int32 [n_segments, E]
+ *   seg_probs[s][e] = sum_t p_te;                             FP32 [n_segments, E]
+ *   lse[t] = log sum_e exp(logits[t][e]), 0 for a token left out;  FP32 [T]
+ *   loss[1] = L_bal = 1/S' sum_s E sum_e (seg_counts[s][e] / (n_s k)) (seg_probs[s][e] / n_s)
+ *   loss[2] = L_z = 1/N sum_t lse_t^2
+ *   loss[0] = balance_coef * L_bal + z_coef * L_z;             FP32 [3]
+ * (all 0 without a counted token). A NaN or +inf logit of a counted token gives NaN in the sums it
+ * reaches and in that row's gradient. Sums over tokens are FP32 inside a tile of at most 256 and FP64
+ * across tiles (L_z: FP64 throughout), in a fixed order: results repeat bit for bit. An empty segment has zeros.
+ *
+ * workspace: moe_router_loss_bytes() bytes; its first 4 bytes (an arrival counter) must be zero
+ * when it is first used, and every call leaves them zero. Calls that share a workspace must be
+ * ordered. n_segments 1..65536 (MOE_ERR_ARG below, MOE_ERR_UNSUPPORTED above); the coefficients
+ * must be finite (MOE_ERR_ARG). Any payload dtype: only d->T, E and k are used.
+ *
+ * Backward: dlogits[t][e] = *dloss * d loss[0] / d logits[t][e] (counts are constants), zero rows
+ * for tokens left out; every row is written. dloss is a device FP32 scalar, NULL for 1. It takes
+ * the forward's logits, lse, seg_counts and seg_tokens unchanged. dlogits may not alias logits. */
+moe_status moe_router_loss_bytes(const moe_desc* d, int32_t n_segments, int64_t* workspace);
+moe_status moe_router_loss(const moe_desc* d, int32_t n_segments, float balance_coef, float z_coef,
+                           const float* logits, const int32_t* topk_idx, const int32_t* seg_offsets,
+                           const uint8_t* token_mask, float* lse, int32_t* seg_counts, int32_t* seg_tokens,
+                           float* seg_probs, float* loss, void* workspace, void* stream);
+moe_status moe_router_loss_bwd(const moe_desc* d, int32_t n_segments, float balance_coef, float z_coef,
+                               const float* logits, const float* lse, const int32_t* seg_offsets,
+                               const uint8_t* token_mask, const int32_t* seg_counts, const int32_t* seg_tokens,
+                               const float* dloss, float* dlogits, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * Paged activation stash (torchtitan PR 5541, "AI-Generated Details": page-aligned multi-token
  * copy tiles, one page resolved per tile, the first tile of a page records or recycles it,
  * live-prefix and page-tail masks, 64-bit addressing, a bounded copy grid).

@@ -1,0 +1,68 @@
+"""Refusals and sizes of the router loss (no GPU: every check runs before a launch)."""
+import os
+
+import pytest
+
+mh = pytest.importorskip("combine_moe_route_02_amd")
+
+
+def _desc(**kw):
+    if not os.path.exists(mh.LIB_PATH):
+        pytest.skip("libmoe.so not built (run __graft_entry__.build())")
+    base = dict(T=1000, H=64, I=64, E=32, E_local=8, k=4, n_chunks=2, dtype="bf16")
+    base.update(kw)
+    return mh.make_desc(**base)
+
+
+def _status(fn, *a):
+    try:
+        fn(*a)
+    except mh.MoeError as e:
+        return e.status
+    return 0
+
+
+def _fwd(d, S=1, a=0.1, z=0.1, **null):
+    names = ("logits", "topk_idx", "seg_offsets", "token_mask", "lse", "seg_counts", "seg_tokens", "seg_probs", "loss",
+             "workspace")
+    return _status(mh.moe_router_loss, d, S, a, z, *[null.get(n, 16) for n in names], 0)
+
+
+def _bwd(d, S=1, a=0.1, z=0.1, **null):
+    names = ("logits", "lse", "seg_offsets", "token_mask", "seg_counts", "seg_tokens", "dloss", "dlogits")
+    return _status(mh.moe_router_loss_bwd, d, S, a, z, *[null.get(n, 16 + i) for i, n in enumerate(names)], 0)
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+def test_segments_and_coefficients_are_checked(call):
+    d = _desc()
+    assert call(d, S=0) == -1 and call(d, S=-3) == -1
+    assert call(d, S=65537) == -3
+    assert call(d, S=2, seg_offsets=None) == -1
+    assert call(d, a=float("nan")) == -1 and call(d, z=float("inf")) == -1
+    assert call(_desc(k=40)) == -1
+
+
+@pytest.mark.parametrize("name", ["logits", "topk_idx", "lse", "seg_counts", "seg_tokens", "seg_probs", "loss", "workspace"])
+def test_forward_needs_its_buffers(name):
+    assert _fwd(_desc(), **{name: None}) == -1
+
+
+@pytest.mark.parametrize("name", ["logits", "lse", "seg_counts", "seg_tokens", "dlogits"])
+def test_backward_needs_its_buffers(name):
+    assert _bwd(_desc(), **{name: None}) == -1
+
+
+def test_alias_alignment_and_empty():
+    d = _desc()
+    assert _bwd(d, logits=64, dlogits=64) == -1
+    assert _fwd(d, workspace=20) == -1
+    assert _bwd(_desc(T=0), logits=None, lse=None, seg_counts=None, seg_tokens=None, dlogits=None) == 0
+
+
+def test_workspace_bytes():
+    a, b = mh.moe_router_loss_bytes(_desc()), mh.moe_router_loss_bytes(_desc(), 64)
+    assert 0 < a < b
+    # a tile of 32 rows holds E sums and E counts
+    assert a >= (1000 // 32) * 32 * 8
+    assert _status(mh.moe_router_loss_bytes, _desc(), 0) == -1
