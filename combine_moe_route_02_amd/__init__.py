@@ -17,8 +17,8 @@ from typing import Dict, Optional
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
-MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
-DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3}
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_INT8 = 0, 1, 2, 3
+DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3, "int8": MOE_INT8}
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_ARG", -2: "MOE_ERR_CAPACITY", -3: "MOE_ERR_UNSUPPORTED",
           -4: "MOE_ERR_HIP"}
 
@@ -80,6 +80,8 @@ _SIGS = {
     "moe_expert_wgrad": [POINTER(MoeDesc)] + [c_void_p] * 9,
     "moe_dispatch_bwd": [POINTER(MoeDesc), c_int] + [c_void_p] * 7,
     "moe_quantize_rows_fp8": [c_int64, c_int32] + [c_void_p] * 4,
+    "moe_quantize_rows_i8": [c_int64, c_int32] + [c_void_p] * 4,
+    "moe_expert_matmul_i8": [c_int32, c_int64, c_int32, c_int32] + [c_void_p] * 7,
     "moe_quantize_cols_fp8": [c_int64, c_int64, c_int32] + [c_void_p] * 4,
     "moe_expert_dgrad_fp8": [POINTER(MoeDesc), c_int] + [c_void_p] * 14,
     "moe_expert_wgrad_fp8": [POINTER(MoeDesc)] + [c_void_p] * 16,
@@ -256,6 +258,16 @@ def moe_quantize_rows_fp8(rows, cols, src_bf16, codes, scale, stream=None):
            "moe_quantize_rows_fp8")
 
 
+def moe_quantize_rows_i8(rows, cols, src_bf16, codes, scale, stream=None):
+    _check(lib().moe_quantize_rows_i8(rows, cols, _ptr(src_bf16), _ptr(codes), _ptr(scale), _stream(stream)),
+           "moe_quantize_rows_i8")
+
+
+def moe_expert_matmul_i8(groups, rows, N, K, x, x_scale, w, w_scale, offsets, y, stream=None):
+    _check(lib().moe_expert_matmul_i8(groups, rows, N, K, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale),
+                                      _ptr(offsets), _ptr(y), _stream(stream)), "moe_expert_matmul_i8")
+
+
 def moe_router_loss(d, n_segments, balance_coef, z_coef, logits, topk_idx, seg_offsets, token_mask, lse, seg_counts,
                     seg_tokens, seg_probs, loss, workspace, stream=None):
     _check(lib().moe_router_loss(ctypes.byref(d), n_segments, balance_coef, z_coef, _ptr(logits), _ptr(topk_idx),
@@ -398,25 +410,26 @@ def allocate(d: MoeDesc, device="cuda", backward: bool = True, fill=None):
     """Allocate every caller buffer of a descriptor with torch (fresh ``torch.empty``).
 
     Returns a dict name -> tensor. Payload tensors use torch.float32 / torch.bfloat16 / torch.uint8
-    (FP8 codes) as the descriptor's dtype says; index arrays are int32; scales, gates and
+    (FP8 codes) / torch.int8 (integer codes) as the descriptor's dtype says; index arrays are int32; scales, gates and
     accumulators float32. ``out`` is a fresh [P_out, H] tensor; use ``out[:T]`` for the logical rows.
     """
     import torch
     T, H, I, E, El, k, n = d.T, d.H, d.I, d.E, d.E_local, d.k, d.n_chunks
     P = n * d.P_c
-    fp8 = d.dtype == MOE_FP8_E4M3
+    i8 = d.dtype == MOE_INT8
+    fp8 = d.dtype == MOE_FP8_E4M3 or i8  # one-byte payloads: forward only
     pay = torch.float32 if d.dtype == MOE_F32 else torch.bfloat16
     ws = workspace_bytes(d)
     i32, f32, u8 = torch.int32, torch.float32, torch.uint8
     spec = {
         "topk_idx": ((T, k), i32), "gates": ((T, k), f32), "counts": ((n, E), i32),
         "offsets": ((n, El + 1), i32), "row_of": ((T, k), i32), "src_token": ((P,), i32),
-        "xd": ((P, H), u8 if fp8 else pay), "h": ((P, I), pay), "yd": ((P, H), pay),
+        "xd": ((P, H), torch.int8 if i8 else u8 if fp8 else pay), "h": ((P, I), pay), "yd": ((P, H), pay),
         "out": ((d.P_out, H), pay), "workspace": ((max(1, ws["workspace"]),), u8),
     }
     if fp8:
-        # h: [P, I] BF16 values followed by their [P, I] e4m3 codes
-        spec.update({"xd_scale": ((P,), f32), "h_scale": ((P,), f32), "h": ((3 * P * I,), u8)})
+        # h: [P, I] BF16 values (INT8: FP32) followed by their [P, I] codes
+        spec.update({"xd_scale": ((P,), f32), "h_scale": ((P,), f32), "h": (((5 if i8 else 3) * P * I,), u8)})
     else:
         spec["gu"] = ((P, 2 * I), pay)
     if backward and not fp8:

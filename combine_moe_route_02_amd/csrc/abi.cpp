@@ -50,14 +50,16 @@ int64_t min_pc(const moe_desc* d) {
   int64_t kk = d->k < d->E_local ? d->k : d->E_local;
   return tokens_per_chunk(d) * kk;
 }
-int elem_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }  // payload rows (FP8: BF16 x/yd)
+int elem_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }  // payload rows (FP8, INT8: BF16 x/yd)
+bool one_byte(const moe_desc* d) { return d->dtype == MOE_FP8_E4M3 || d->dtype == MOE_INT8; }  // forward only
+constexpr int kI8MaxK = 131008;  // 128 * 128 * K <= 2^31 - 1, K a multiple of 64
 constexpr int64_t kRsrcMax = 0x7fffffff;  // bytes one raw buffer descriptor addresses
 
 moe_status validate(const moe_desc* d) {
   if (!d) return fail(MOE_ERR_ARG, "descriptor is NULL");
   if (d->flags & ~(MOE_FLAG_FP8_DGRAD | MOE_FLAG_FP8_WGRAD | MOE_FLAG_FP8_DXD))
     return fail(MOE_ERR_ARG, "descriptor flags 0x%x hold an unknown bit", d->flags);
-  if (d->dtype != MOE_F32 && d->dtype != MOE_BF16 && d->dtype != MOE_FP8_E4M3)
+  if (d->dtype != MOE_F32 && d->dtype != MOE_BF16 && d->dtype != MOE_FP8_E4M3 && d->dtype != MOE_INT8)
     return fail(MOE_ERR_ARG, "unknown dtype %d", d->dtype);
   if (d->T < 0) return fail(MOE_ERR_ARG, "T = %lld is negative", (long long)d->T);
   if (d->n_chunks < 1) return fail(MOE_ERR_ARG, "n_chunks = %d must be >= 1", d->n_chunks);
@@ -84,8 +86,10 @@ moe_status validate(const moe_desc* d) {
   if (d->P_out < d->T) return fail(MOE_ERR_CAPACITY, "P_out = %lld below T = %lld", (long long)d->P_out, (long long)d->T);
   if ((int64_t)d->n_chunks * d->P_c > INT32_MAX || d->T * d->k > INT32_MAX)
     return fail(MOE_ERR_UNSUPPORTED, "row indices exceed int32");
+  if (d->dtype == MOE_INT8 && (d->H > kI8MaxK || d->I > kI8MaxK))
+    return fail(MOE_ERR_UNSUPPORTED, "8-bit integer products sum at most %d terms in int32", kI8MaxK);
   // the expert GEMMs address one expert's weights through a buffer descriptor
-  const int64_t wes = d->dtype == MOE_F32 ? 4 : 2;
+  const int64_t wes = d->dtype == MOE_F32 ? 4 : d->dtype == MOE_INT8 ? 1 : 2;
   if (2 * (int64_t)d->I * d->H * wes > kRsrcMax)
     return fail(MOE_ERR_UNSUPPORTED, "one expert's W1 (2I x H = %lld elements) exceeds a 2 GiB buffer descriptor",
                 (long long)(2 * (int64_t)d->I * d->H));
@@ -174,7 +178,7 @@ int64_t wgrad_scratch(const moe_desc* d) {
 }
 int64_t wgrad_offset(const moe_desc* d) {
   const int64_t a = moe::route_scratch_bytes(d->T, d->n_chunks, d->E);
-  const int64_t b = d->dtype == MOE_FP8_E4M3 ? 0 : router_scratch(d);
+  const int64_t b = one_byte(d) ? 0 : router_scratch(d);
   return ((a > b ? a : b) + 255) / 256 * 256;
 }
 void* wgrad_ws(const moe_desc* d, void* workspace) {
@@ -205,7 +209,7 @@ moe_status moe_workspace_bytes(const moe_desc* d, moe_workspace_sizes* o) {
   const int64_t T = d->T, H = d->H, I = d->I, E = d->E, El = d->E_local, K = d->k, n = d->n_chunks;
   const int64_t P = n * d->P_c;
   const int64_t es = elem_size(d->dtype);
-  const bool fp8 = d->dtype == MOE_FP8_E4M3;
+  const bool fp8 = one_byte(d);
   *o = moe_workspace_sizes{};
   o->topk_idx = T * K * 4;
   o->gates = T * K * 4;
@@ -216,7 +220,7 @@ moe_status moe_workspace_bytes(const moe_desc* d, moe_workspace_sizes* o) {
   o->xd = P * H * (fp8 ? 1 : es);
   o->xd_scale = fp8 ? P * 4 : 0;
   o->gu = fp8 ? 0 : P * 2 * I * es;
-  o->h = P * I * (fp8 ? 3 : es);  // FP8: BF16 values, then e4m3 codes
+  o->h = P * I * (d->dtype == MOE_INT8 ? 5 : fp8 ? 3 : es);  // FP8: BF16 values, then codes; INT8: FP32 values, then codes
   o->h_scale = fp8 ? P * 4 : 0;
   o->yd = P * H * es;
   o->out = d->P_out * H * es;
@@ -333,6 +337,10 @@ moe_status moe_dispatch(const moe_desc* d, int chunk, const void* x, const int32
     MOE_NEED(xd_scale); MOE_NEED(h_scale);
     MOE_HIP(moe::launch_dispatch_fp8(x, row_of, xd, xd_scale, h_scale, r.t0, r.t1, d->k, d->H,
                                      (hipStream_t)stream), "dispatch_fp8");
+  } else if (d->dtype == MOE_INT8) {
+    MOE_NEED(xd_scale);
+    MOE_HIP(moe::launch_dispatch_i8(x, row_of, xd, xd_scale, r.t0, r.t1, d->k, d->H, (hipStream_t)stream),
+            "dispatch_i8");
   } else {
     MOE_HIP(moe::launch_dispatch(x, row_of, xd, r.t0, r.t1, d->k, (int64_t)d->H * elem_size(d->dtype),
                                  (hipStream_t)stream), "dispatch");
@@ -354,6 +362,13 @@ moe_status moe_expert_ffn(const moe_desc* d, int chunk, const void* xd, const fl
     MOE_HIP(moe::launch_expert_fwd_fp8(xd, xd_scale, w1, w1_scale, w2, w2_scale, offsets, h, h_scale,
                                        yd, d->H, d->I, d->E_local, r.c0, r.nc, d->P_c,
                                        rows_of(d), (hipStream_t)stream), "expert_ffn_fp8");
+    return MOE_OK;
+  }
+  if (d->dtype == MOE_INT8) {
+    MOE_NEED(xd_scale); MOE_NEED(w1_scale); MOE_NEED(w2_scale); MOE_NEED(h_scale);
+    MOE_HIP(moe::launch_expert_fwd_i8(xd, xd_scale, w1, w1_scale, w2, w2_scale, offsets, h, h_scale, yd, d->H, d->I,
+                                      d->E_local, r.c0, r.nc, d->P_c, rows_of(d), (hipStream_t)stream),
+            "expert_ffn_i8");
     return MOE_OK;
   }
   MOE_HIP(moe::launch_expert_fwd(is_bf16_rows(d), xd, w1, w2, offsets, gu, h, yd, d->H, d->I,
@@ -383,6 +398,7 @@ static float* dxd_scales(const moe_desc* d, const void* dxd) {
 
 static moe_status no_fp8_bwd(const moe_desc* d) {
   if (d->dtype == MOE_FP8_E4M3) return fail(MOE_ERR_UNSUPPORTED, "the FP8 payload path is forward only");
+  if (d->dtype == MOE_INT8) return fail(MOE_ERR_UNSUPPORTED, "the 8-bit integer path is forward only");
   return MOE_OK;
 }
 
@@ -561,6 +577,40 @@ moe_status moe_quantize_rows_fp8(int64_t rows, int32_t cols, const void* src_bf1
   return MOE_OK;
 }
 
+moe_status moe_quantize_rows_i8(int64_t rows, int32_t cols, const void* src_bf16, void* codes, float* scale,
+                                void* stream) {
+  if (rows < 0 || cols <= 0 || cols % 8) return fail(MOE_ERR_ARG, "rows/cols invalid (cols %% 8 == 0 required)");
+  if (rows == 0) return MOE_OK;
+  MOE_NEED(src_bf16); MOE_NEED(codes); MOE_NEED(scale);
+  if (((uintptr_t)src_bf16 & 15) || ((uintptr_t)codes & 7))
+    return fail(MOE_ERR_ARG, "%s: the rows must be 16-byte aligned and the codes 8-byte aligned", __func__);
+  if (rows > 4 * (int64_t)INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: rows = %lld above 4 (2^31 - 1)", __func__, (long long)rows);
+  MOE_HIP(moe::launch_quantize_rows_i8(src_bf16, codes, scale, rows, cols, (hipStream_t)stream), "quantize_rows_i8");
+  return MOE_OK;
+}
+
+moe_status moe_expert_matmul_i8(int32_t groups, int64_t rows, int32_t N, int32_t K, const void* x,
+                                const float* x_scale, const void* w, const float* w_scale, const int32_t* offsets,
+                                void* y, void* stream) {
+  if (groups < 0 || rows < 0) return fail(MOE_ERR_ARG, "%s: negative groups or rows", __func__);
+  if (groups > 1024) return fail(MOE_ERR_UNSUPPORTED, "%s: groups = %d above 1024", __func__, groups);
+  if (rows > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: row indices exceed int32", __func__);
+  if (N <= 0 || N % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: N = %d must be a positive multiple of 8", __func__, N);
+  if (K <= 0 || K % 64 || K > kI8MaxK)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: K = %d must be a positive multiple of 64, at most %d", __func__, K, kI8MaxK);
+  if ((int64_t)N * K > kRsrcMax)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: one group's weights (%lld bytes) exceed a 2 GiB buffer descriptor", __func__,
+                (long long)N * K);
+  if (!offsets && groups > 1) return fail(MOE_ERR_ARG, "%s: argument 'offsets' is NULL with groups = %d", __func__, groups);
+  if (groups == 0 || rows == 0) return MOE_OK;
+  MOE_NEED(x); MOE_NEED(x_scale); MOE_NEED(w); MOE_NEED(w_scale); MOE_NEED(y);
+  if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)y) & 15)
+    return fail(MOE_ERR_ARG, "%s: x, w and y must be 16-byte aligned", __func__);
+  MOE_HIP(moe::launch_expert_matmul_i8(groups, rows, N, K, x, x_scale, w, w_scale, offsets, y, (hipStream_t)stream),
+          "expert_matmul_i8");
+  return MOE_OK;
+}
+
 moe_status moe_quantize_cols_fp8(int64_t batch, int64_t rows, int32_t cols, const void* src_bf16, void* codes_t,
                                  float* scale, void* stream) {
   if (batch < 0 || rows < 0 || rows % 16 || cols <= 0 || cols % 8)
@@ -684,7 +734,7 @@ static moe_status check_fwd_tensors(const moe_desc* d, const moe_tensors* t) {
   if ((int64_t)d->n_chunks * d->P_c > 0) MOE_NEED(t->src_token);  // rows past N_c are marked -1
   if (rows_of(d) > 0) {
     MOE_NEED(t->w1); MOE_NEED(t->w2); MOE_NEED(t->xd); MOE_NEED(t->h); MOE_NEED(t->yd);
-    if (d->dtype == MOE_FP8_E4M3) { MOE_NEED(t->xd_scale); MOE_NEED(t->h_scale); MOE_NEED(t->w1_scale); MOE_NEED(t->w2_scale); }
+    if (one_byte(d)) { MOE_NEED(t->xd_scale); MOE_NEED(t->h_scale); MOE_NEED(t->w1_scale); MOE_NEED(t->w2_scale); }
   }
   return MOE_OK;
 }

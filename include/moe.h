@@ -43,6 +43,8 @@
  *                                                            (3*P*I bytes), h_scale f32 [P]; yd bf16
  *        out                            f32       bf16       bf16
  *        dw1, dw2                       f32       bf16       -
+ *     MOE_INT8 (forward only) is laid out like MOE_FP8_E4M3 with 8-bit integer codes (xd, W1, W2),
+ *     except h: [P,I] f32 then [P,I] codes (5*P*I bytes).
  *     logits, gates, dgates, dlogits, dwr_acc are always f32; every index array is int32.
  *   - Shapes: logits [T,E]; topk_idx, gates, row_of, dgates [T,k]; counts [n,E];
  *     offsets [n,E_l+1]; src_token [P]; xd, yd, dyd, dxd [P,H]; gu, dgu [P,2I]; h [P,I];
@@ -58,7 +60,7 @@
 extern "C" {
 #endif
 
-typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
+typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_INT8 = 3 } moe_dtype;
 
 typedef enum moe_status {
   MOE_OK = 0,
@@ -149,8 +151,9 @@ moe_status moe_route_x(const moe_desc* d, int chunk, const void* x, const void* 
  * xd[row_of[t][j]] = x[t] for every local slot (a bitwise row copy for F32/BF16;
  * each touched token row is read once). FP8: per token amax over the BF16 row,
  * xd = e4m3(x * (448/amax)) with FP32 steps, RNE, saturating; xd_scale[row] = amax/448 (1 for
- * an all-zero row); h_scale[row] is cleared (moe_expert_ffn writes it). Rows N_c..P_c-1 are not
- * written. xd_scale/h_scale may be NULL unless dtype is FP8. */
+ * an all-zero row); h_scale[row] is cleared (moe_expert_ffn writes it). INT8: the same with
+ * moe_quantize_rows_i8's codes and scale; h_scale is not touched. Rows N_c..P_c-1 are not
+ * written. xd_scale may be NULL unless dtype is FP8 or INT8, h_scale unless it is FP8. */
 moe_status moe_dispatch(const moe_desc* d, int chunk, const void* x, const int32_t* row_of,
                         void* xd, float* xd_scale, float* h_scale, void* stream);
 
@@ -162,7 +165,9 @@ moe_status moe_dispatch(const moe_desc* d, int chunk, const void* x, const int32
  * FP8 MFMA with FP32 accumulation dequantised by s_row*s_col; h is written in BF16, then each
  * dispatch row of h is quantised to e4m3 (per-row absmax, the FP32 steps of moe_dispatch) into
  * the codes half of the h buffer with its scale in h_scale, and the down projection reads the
- * codes. gu is unused for FP8. */
+ * codes. gu is unused for FP8. INT8: both products are exact int32 sums of 8-bit codes, dequantised by
+ * s_row*s_col in FP32; h is written in FP32 at the start of the h buffer and quantised per row as
+ * moe_quantize_rows_i8 does (codes after the FP32 values, scale in h_scale); gu is unused. */
 moe_status moe_expert_ffn(const moe_desc* d, int chunk, const void* xd, const float* xd_scale,
                           const void* w1, const float* w1_scale, const void* w2,
                           const float* w2_scale, const int32_t* offsets, void* gu, void* h,
@@ -265,6 +270,26 @@ moe_status moe_dispatch_bwd(const moe_desc* d, int chunk, const void* dxd, const
  * codes = e4m3(w * (448/amax)) and scale = amax/448 with the FP32 steps of moe_dispatch. */
 moe_status moe_quantize_rows_fp8(int64_t rows, int32_t cols, const void* src_bf16, void* codes,
                                  float* scale, void* stream);
+
+/* 8-bit integer quantisation of the rows of a [rows, cols] BF16 matrix (weights per output channel,
+ * activations per token): codes = RNE(v * (127/amax)) in [-127, 127] and scale = amax/127, each step
+ * rounded once in FP32; a row of zeros (or of values so small that 127/amax overflows) has codes 0
+ * and scale 1; a row with a NaN or an infinity has codes 0 and scale NaN. cols a multiple of 8, src
+ * 16-byte and codes 8-byte aligned (MOE_ERR_ARG). */
+moe_status moe_quantize_rows_i8(int64_t rows, int32_t cols, const void* src_bf16, void* codes,
+                                float* scale, void* stream);
+
+/* 8-bit integer matrix product with a scale per token and channel, grouped over experts:
+ * y[r][o] = RNE_bf16(sum_k x[r][k] w[g][o][k] * (x_scale[r] * w_scale[g][o])) for the rows r of group
+ * g, [offsets[g], offsets[g+1]) (device int32 [groups + 1], ascending; entries are clamped to
+ * [0, rows]); NULL with groups = 1 is one group of every row (a dense product). x [rows, K] and w
+ * [groups, N, K] are codes in [-128, 127], x_scale [rows], w_scale [groups, N] FP32, y [rows, N] BF16.
+ * The sum is exact in int32 and rounded once to FP32. Rows in no group are not written. groups up to
+ * 1024, N a multiple of 8, K a multiple of 64 up to 131008, N * K below 2^31 (MOE_ERR_UNSUPPORTED);
+ * x, w and y 16-byte aligned (MOE_ERR_ARG). */
+moe_status moe_expert_matmul_i8(int32_t groups, int64_t rows, int32_t N, int32_t K, const void* x,
+                                const float* x_scale, const void* w, const float* w_scale,
+                                const int32_t* offsets, void* y, void* stream);
 
 /* Per-column FP8 quantisation, stored transposed (the weights of moe_expert_dgrad_fp8): for each of
  * `batch` BF16 matrices src [rows, cols] (row-major, contiguous), column j's absmax gives

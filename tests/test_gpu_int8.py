@@ -1,0 +1,219 @@
+"""GPU parity of the 8-bit integer path against the NumPy oracle.
+
+Codes and scales are compared bit for bit (both sides take the same FP32 steps); so are products of the same codes
+computed by different calls, since the sums are exact. A product's value is an exact integer, rounded once to FP32
+(2^-24), times the rounded product of two scales (two more), rounded once to BF16: 2^-8 of the value plus 3 * 2^-24.
+The layer's output differs from the oracle's by the BF16 rounding of yd and of out (2^-8 / sqrt(3) rms each at most)
+and by codes of h that fall on the other side of a half because h carries FP32 rounding (a relative 1e-6 moves a share
+2e-6 / step of the codes, under 1e-3 of the norm): 2^-8 * sqrt(2 / 3) + 1e-3 = 4.2e-3 of the norm."""
+import numpy as np
+import pytest
+
+import moe_inputs
+import oracle
+from moe_inputs import MoeConfig
+from oracle import int8 as oi8
+
+pytestmark = pytest.mark.gpu
+harness = pytest.importorskip("harness")
+OUT_TOL = 4.2e-3
+MM_TOL = 2.0 ** -8 + 3 * 2.0 ** -24
+
+
+def _gpu():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import combine_moe_route_02_amd as mh
+    mh.lib()
+    return torch, mh
+
+
+def _bf16(torch, a):
+    """FP32 values -> device BF16 tensor and the rounded values."""
+    bits = moe_inputs.f32_to_bf16_bits(a)
+    return torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16), moe_inputs.bf16_bits_to_f32(bits)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 8), (3, 64), (5, 520), (17, 1024), (64, 2048), (7, 4104), (9, 8192), (3, 8200), (2, 20000)])
+def test_quantize_rows_bitwise(rows, cols):
+    torch, mh = _gpu()
+    rng = np.random.default_rng(rows * cols)
+    a = rng.standard_normal((rows, cols)).astype(np.float32)
+    if rows > 2:
+        a[1] = 0.0
+        a[2] *= 1e-39           # the multiplier overflows
+    if rows > 6:
+        a[3, 5], a[4, 6], a[5, 7] = np.nan, np.inf, -np.inf
+        a[6] = 1.5              # all equal
+    dev, val = _bf16(torch, a)
+    codes = torch.full((rows, cols), 77, dtype=torch.int8, device="cuda")
+    scale = torch.full((rows,), 7.0, device="cuda")
+    mh.moe_quantize_rows_i8(rows, cols, dev, codes, scale)
+    torch.cuda.synchronize()
+    q, s = oi8.quantize_rows(val)
+    np.testing.assert_array_equal(codes.cpu().numpy(), q)
+    np.testing.assert_array_equal(scale.cpu().numpy(), s)
+
+
+def _product(torch, mh, rows, N, K, G, off, seed, lo=-127):
+    rng = np.random.default_rng(seed)
+    x, w = rng.integers(lo, 128, (rows, K)).astype(np.int8), rng.integers(lo, 128, (G, N, K)).astype(np.int8)
+    xs, ws = (rng.random(rows) + 0.1).astype(np.float32), (rng.random((G, N)) + 0.1).astype(np.float32)
+    y = torch.full((rows, N), -3.0, dtype=torch.bfloat16, device="cuda")
+    off_d = None if off is None else torch.tensor(off, dtype=torch.int32, device="cuda")
+    mh.moe_expert_matmul_i8(G, rows, N, K, torch.from_numpy(x).cuda(), torch.from_numpy(xs).cuda(), torch.from_numpy(w).cuda(),
+                            torch.from_numpy(ws).cuda(), off_d, y)
+    torch.cuda.synchronize()
+    return y.float().cpu().numpy().astype(np.float64), oi8.matmul(x, xs, w, ws, off)
+
+
+def _assert_product(got, want):
+    out = np.isnan(want)
+    assert np.all(got[out] == -3.0), "a row outside every group was written"
+    assert np.all(np.abs(got - want)[~out] <= MM_TOL * np.abs(want[~out]))
+
+
+# rows around every row tile, columns and K that end inside a tile
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 31, 33, 64, 65, 100, 129, 300])
+@pytest.mark.parametrize("N,K", [(8, 64), (72, 192), (256, 128), (520, 1088), (128, 2048)])
+def test_dense_product(rows, N, K):
+    torch, mh = _gpu()
+    _assert_product(*_product(torch, mh, rows, N, K, 1, None, rows + N + K))
+
+
+@pytest.mark.parametrize("off", [
+    [0, 0, 5, 5, 40], [3, 3, 3, 3, 3], [2, 19, 20, 36, 37],   # empty groups, rows in no group
+    [0, 1, 2, 3, 4], [0, 300, 300, 301, 700], [-5, 10, 2000, 2000, 9999],
+])
+@pytest.mark.parametrize("N,K", [(64, 64), (200, 320)])
+def test_grouped_product(off, N, K):
+    torch, mh = _gpu()
+    rows = 40 if max(off) <= 40 else 700
+    _assert_product(*_product(torch, mh, rows, N, K, 4, off, len(off) + N))
+
+
+def test_product_of_the_extreme_codes():
+    """-128 everywhere at a long K: the int32 sum is 2^14 K."""
+    torch, mh = _gpu()
+    for rows in (1, 40, 300):
+        K, N = 65536, 16
+        x = torch.full((rows, K), -128, dtype=torch.int8, device="cuda")
+        w = torch.full((1, N, K), -128, dtype=torch.int8, device="cuda")
+        y = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+        one = torch.ones(max(rows, N), device="cuda")
+        mh.moe_expert_matmul_i8(1, rows, N, K, x, one, w, one, None, y)
+        torch.cuda.synchronize()
+        assert (y == 2.0 ** 30).all()
+
+
+def test_product_does_not_depend_on_the_other_rows():
+    """A row's product is the same bits alone, among a few rows and among many: the sums are exact, so the kernels that
+    serve few and many rows agree."""
+    torch, mh = _gpu()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rows, N, K = 700, 320, 1024
+    x = torch.randint(-127, 128, (rows, K), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-127, 128, (1, N, K), generator=g, device="cuda", dtype=torch.int8)
+    xs, ws = torch.rand(rows, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+    full = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+    mh.moe_expert_matmul_i8(1, rows, N, K, x, xs, w, ws, None, full)
+    for n in (1, 3, 16, 20, 64, 130):
+        y = torch.empty(n, N, dtype=torch.bfloat16, device="cuda")
+        mh.moe_expert_matmul_i8(1, n, N, K, x, xs, w, ws, None, y)
+        torch.cuda.synchronize()
+        assert torch.equal(y, full[:n]), n
+
+
+CASES = [
+    MoeConfig("i8_t1", T=1, H=128, I=64, E=8, E_local=8, k=2, n_chunks=1, dtype="int8", seed_base=900),
+    MoeConfig("i8_t1_remote", T=1, H=128, I=64, E=64, E_local=2, e0=60, k=1, n_chunks=1, dtype="int8", seed_base=905),
+    MoeConfig("i8_t3", T=3, H=320, I=192, E=16, E_local=16, k=8, n_chunks=1, dtype="int8", seed_base=910),
+    MoeConfig("i8_t33", T=33, H=256, I=128, E=8, E_local=8, k=4, n_chunks=1, dtype="int8", seed_base=920),
+    MoeConfig("i8_t70_n3", T=70, H=512, I=320, E=32, E_local=12, e0=5, k=5, n_chunks=3, dtype="int8", seed_base=930),
+    MoeConfig("i8_t200_few_experts", T=200, H=192, I=64, E=4, E_local=3, k=2, n_chunks=1, dtype="int8", seed_base=935),
+    MoeConfig("i8_t1000", T=1000, H=256, I=192, E=32, E_local=8, e0=4, k=4, n_chunks=2, dtype="int8", seed_base=940),
+    MoeConfig("i8_zipf", T=3000, H=512, I=256, E=32, E_local=8, k=8, n_chunks=2, dtype="int8", seed_base=950,
+              zipf_s=1.2, n_empty=2),
+    MoeConfig("i8_wide", T=20, H=9216, I=64, E=8, E_local=4, k=2, n_chunks=1, dtype="int8", seed_base=960),
+]
+
+
+def _layer(torch, mh, cfg, stages, two_streams=True):
+    inp = moe_inputs.make_inputs(cfg, parts=("x", "logits", "w1", "w2"))
+    d = mh.make_desc(T=cfg.T, H=cfg.H, I=cfg.I, E=cfg.E, E_local=cfg.E_local, k=cfg.k, n_chunks=cfg.n_chunks, dtype="int8",
+                     e0=cfg.e0)
+    b = mh.allocate(d)
+    b["out"].fill_(-7.0)
+    b["yd"].fill_(-9.0)
+    for name in ("x", "logits"):
+        b[name] = harness.to_dev(inp, name, "bf16")
+    for name, rows, cols in (("w1", 2 * cfg.I, cfg.H), ("w2", cfg.H, cfg.I)):
+        w = harness.to_dev(inp, name, "bf16")
+        b[name] = torch.empty(w.shape, dtype=torch.int8, device="cuda")
+        b[name + "_scale"] = torch.empty(w.shape[:-1], device="cuda")
+        mh.moe_quantize_rows_i8(cfg.E_local * rows, cols, w, b[name], b[name + "_scale"])
+    cs = torch.cuda.current_stream()
+    if stages:
+        harness.run_stages(mh, d, b, False, cs)
+    else:
+        mh.moe_layer_forward(d, b, cs, torch.cuda.Stream() if two_streams else cs)
+    torch.cuda.synchronize()
+    return inp, d, b
+
+
+@pytest.mark.parametrize("cfg", CASES, ids=[c.name for c in CASES])
+def test_layer_forward(cfg):
+    torch, mh = _gpu()
+    print(f"[int8] {cfg}", flush=True)
+    inp, d, b = _layer(torch, mh, cfg, stages=False)
+    w1q, w1s = oi8.quantize_rows(inp["w1"])
+    w2q, w2s = oi8.quantize_rows(inp["w2"])
+    np.testing.assert_array_equal(b["w1"].cpu().numpy(), w1q)
+    ref = oi8.forward(inp["x"], inp["logits"], w1q, w1s, w2q, w2s, k=cfg.k, e0=cfg.e0, E_local=cfg.E_local,
+                      n_chunks=cfg.n_chunks, P_c=d.P_c)
+    for n in ("offsets", "row_of", "src_token"):
+        np.testing.assert_array_equal(b[n].cpu().numpy(), ref[n])
+    used = ref["src_token"] >= 0
+    np.testing.assert_array_equal(b["xd"].cpu().numpy()[used], ref["xdq"][used])
+    np.testing.assert_array_equal(b["xd_scale"].cpu().numpy()[used], ref["xds"][used])
+    out = harness.to_np(b["out"])
+    assert np.all(out[cfg.T:] == -7.0) and np.all(harness.to_np(b["yd"])[~used] == -9.0)
+    err = np.linalg.norm(out[:cfg.T] - ref["out"])
+    assert err <= OUT_TOL * np.linalg.norm(ref["out"]), err / np.linalg.norm(ref["out"])
+    _, _, c = _layer(torch, mh, cfg, stages=True)
+    _, _, e = _layer(torch, mh, cfg, stages=False, two_streams=False)
+    for o in (c, e):
+        assert torch.equal(b["out"], o["out"]) and torch.equal(b["yd"], o["yd"])
+
+
+def test_a_row_that_is_not_finite_stays_visible_and_alone():
+    torch, mh = _gpu()
+    cfg = CASES[3]
+    inp, d, b = _layer(torch, mh, cfg, stages=True)
+    want = b["out"].clone()
+    b["x"][7, 3] = float("nan")
+    harness.run_stages(mh, d, b, False, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert torch.isnan(b["out"][7]).all()
+    keep = [t for t in range(cfg.T) if t != 7]
+    assert torch.equal(b["out"][keep], want[keep])
+
+
+@pytest.mark.parametrize("cfg", [CASES[0], CASES[3], CASES[6]], ids=["t1", "t33", "t1000"])
+def test_replays_of_a_graph(cfg):
+    torch, mh = _gpu()
+    inp, d, b = _layer(torch, mh, cfg, stages=True)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        harness.run_stages(mh, d, b, False, torch.cuda.current_stream())
+    x0 = b["x"].clone()
+    for i in range(3):
+        b["x"].copy_(x0 * (i + 1.25))
+        g.replay()
+        torch.cuda.synchronize()
+        got = b["out"].clone()
+        b["out"].fill_(0.0)
+        harness.run_stages(mh, d, b, False, torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        assert torch.equal(got[:cfg.T], b["out"][:cfg.T]), i
