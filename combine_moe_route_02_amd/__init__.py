@@ -40,17 +40,24 @@ FLAG_FP8_WGRAD = 2
 FLAG_FP8_DXD = 4  # dxd as block-scaled e4m3 rows (codes, then per-256-column scales) in the dxd buffer
 
 
+FLAG_ROUTER_LOSS = 16  # the router logits carry an auxiliary loss: dense dlogits (8 is not a flag)
+
+
 TENSOR_FIELDS = ["x", "logits", "w1", "w1_scale", "w2", "w2_scale", "w_r", "dy",
                  "topk_idx", "gates", "counts", "offsets", "row_of", "src_token", "xd", "xd_scale",
                  "gu", "h", "h_scale", "yd", "out",
                  "dyd", "dgates", "dlogits", "dwr_acc", "dgu", "dxd", "dx", "dw1", "dw2", "dwr",
                  "workspace",
                  "w1t", "w1t_scale", "w2t", "w2t_scale", "dyd_q", "dyd_scale", "dgu_q", "dgu_scale",
-                 "dyd_t", "dyd_cs", "dgu_t", "dgu_cs", "xd_t", "xd_cs", "h_t", "h_cs"]
+                 "dyd_t", "dyd_cs", "dgu_t", "dgu_cs", "xd_t", "xd_cs", "h_t", "h_cs",
+                 "seg_offsets", "token_mask", "router_logits", "router_lse", "seg_counts", "seg_tokens", "seg_probs",
+                 "router_loss", "dloss", "loss_workspace"]
+# plain values behind the pointers (FLAG_ROUTER_LOSS), with what a dict of buffers without them means
+LOSS_OPTIONS = {"n_segments": (c_int32, 1), "balance_coef": (c_float, 0.0), "z_coef": (c_float, 0.0)}
 
 
 class MoeTensors(Structure):
-    _fields_ = [(f, c_void_p) for f in TENSOR_FIELDS]
+    _fields_ = [(f, c_void_p) for f in TENSOR_FIELDS] + [(f, t) for f, (t, _) in LOSS_OPTIONS.items()]
 
 
 SIZE_FIELDS = ["topk_idx", "gates", "counts", "offsets", "row_of", "src_token", "xd", "xd_scale", "gu",
@@ -300,6 +307,8 @@ def _tensors(bufs: Dict[str, object]) -> MoeTensors:
     t = MoeTensors()
     for f in TENSOR_FIELDS:
         setattr(t, f, _ptr(bufs.get(f)))
+    for f, (_, default) in LOSS_OPTIONS.items():
+        setattr(t, f, bufs.get(f, default))
     return t
 
 
@@ -406,12 +415,14 @@ def moe_trace_timeline():
 
 # ------------------------------------------------------------------ device buffers (torch plumbing)
 
-def allocate(d: MoeDesc, device="cuda", backward: bool = True, fill=None):
+def allocate(d: MoeDesc, device="cuda", backward: bool = True, fill=None, n_segments: int = 1):
     """Allocate every caller buffer of a descriptor with torch (fresh ``torch.empty``).
 
     Returns a dict name -> tensor. Payload tensors use torch.float32 / torch.bfloat16 / torch.uint8
     (FP8 codes) / torch.int8 (integer codes) as the descriptor's dtype says; index arrays are int32; scales, gates and
-    accumulators float32. ``out`` is a fresh [P_out, H] tensor; use ``out[:T]`` for the logical rows.
+    accumulators float32. With FLAG_ROUTER_LOSS the loss's outputs and workspace for ``n_segments``
+    segments are among them; ``seg_offsets``, ``token_mask``, ``dloss`` and the coefficients are the
+    caller's. ``out`` is a fresh [P_out, H] tensor; use ``out[:T]`` for the logical rows.
     """
     import torch
     T, H, I, E, El, k, n = d.T, d.H, d.I, d.E, d.E_local, d.k, d.n_chunks
@@ -449,9 +460,14 @@ def allocate(d: MoeDesc, device="cuda", backward: bool = True, fill=None):
         for name in ("dyd_cs", "dgu_cs", "xd_cs", "h_cs"):
             spec[name] = ((max(1, ws[name] // 4),), f32)
     out = {}
+    if d.flags & FLAG_ROUTER_LOSS:
+        spec.update({"router_logits": ((T, E), f32), "router_lse": ((T,), f32), "seg_counts": ((n_segments, E), i32),
+                     "seg_tokens": ((n_segments + 2,), i32), "seg_probs": ((n_segments, E), f32),
+                     "router_loss": ((3,), f32), "loss_workspace": ((moe_router_loss_bytes(d, n_segments),), u8)})
+        out["n_segments"] = n_segments
     for name, (shape, dt) in spec.items():
-        if name == "workspace":
-            # zeroed: the weight-gradient counters inside it must be zero when first used
+        if name in ("workspace", "loss_workspace"):
+            # zeroed: the counters inside them must be zero when first used
             out[name] = torch.zeros(shape, dtype=dt, device=device)
             continue
         out[name] = torch.empty(shape, dtype=dt, device=device)

@@ -57,7 +57,7 @@ constexpr int64_t kRsrcMax = 0x7fffffff;  // bytes one raw buffer descriptor add
 
 moe_status validate(const moe_desc* d) {
   if (!d) return fail(MOE_ERR_ARG, "descriptor is NULL");
-  if (d->flags & ~(MOE_FLAG_FP8_DGRAD | MOE_FLAG_FP8_WGRAD | MOE_FLAG_FP8_DXD))
+  if (d->flags & ~(MOE_FLAG_FP8_DGRAD | MOE_FLAG_FP8_WGRAD | MOE_FLAG_FP8_DXD | MOE_FLAG_ROUTER_LOSS))
     return fail(MOE_ERR_ARG, "descriptor flags 0x%x hold an unknown bit", d->flags);
   if (d->dtype != MOE_F32 && d->dtype != MOE_BF16 && d->dtype != MOE_FP8_E4M3 && d->dtype != MOE_INT8)
     return fail(MOE_ERR_ARG, "unknown dtype %d", d->dtype);
@@ -74,8 +74,10 @@ moe_status validate(const moe_desc* d) {
   if (d->H <= 0 || d->H % 64) return fail(MOE_ERR_UNSUPPORTED, "H = %d must be a positive multiple of 64", d->H);
   if (d->I <= 0 || d->I % 64) return fail(MOE_ERR_UNSUPPORTED, "I = %d must be a positive multiple of 64", d->I);
   if (d->dtype == MOE_BF16 && d->E % 4) return fail(MOE_ERR_UNSUPPORTED, "BF16 path needs E %% 4 == 0 (E = %d)", d->E);
-  if (d->flags && d->dtype != MOE_BF16)
+  if ((d->flags & ~MOE_FLAG_ROUTER_LOSS) && d->dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "the FP8 backward flags need the BF16 dtype");
+  if ((d->flags & MOE_FLAG_ROUTER_LOSS) && one_byte(d))
+    return fail(MOE_ERR_UNSUPPORTED, "the router loss flag needs a dtype with a backward (F32 or BF16)");
   if (d->dtype == MOE_FP8_E4M3 && d->H > 8192)
     return fail(MOE_ERR_UNSUPPORTED, "FP8 dispatch keeps a row in registers: H = %d above 8192", d->H);
   if (d->P_c % 4) return fail(MOE_ERR_CAPACITY, "P_c = %lld is not a multiple of 4", (long long)d->P_c);
@@ -449,7 +451,8 @@ moe_status moe_route_bwd(const moe_desc* d, int chunk, const float* dgates, cons
   for (int c = cfirst; c <= clast; ++c) {
     Range r = range_of(d, c);
     MOE_HIP(moe::launch_route_bwd_dlogits(dgates, gates, topk_idx, dlogits, r.t0, r.t1, d->k, d->E,
-                                          (hipStream_t)stream, hi, lo, ldl, pitch), "route_bwd_dlogits");
+                                          (hipStream_t)stream, hi, lo, ldl, pitch, d->flags & MOE_FLAG_ROUTER_LOSS),
+            "route_bwd_dlogits");
     MOE_HIP(moe::launch_router_wgrad(is_bf16_rows(d), dlogits, hi, lo, ldl, x, (float*)workspace, dwr_acc, c == 0,
                                      c == d->n_chunks - 1 ? dwr : nullptr, r.t0, r.t1, d->E, d->H,
                                      (hipStream_t)stream), "router_wgrad");
@@ -560,6 +563,12 @@ moe_status moe_dispatch_bwd(const moe_desc* d, int chunk, const void* dxd, const
   if (r.t1 <= r.t0) return MOE_OK;
   MOE_NEED(row_of); MOE_NEED(topk_idx); MOE_NEED(dlogits); MOE_NEED(w_r); MOE_NEED(dx);
   if (rows_of(d) > 0) MOE_NEED(dxd);
+  if (d->flags & MOE_FLAG_ROUTER_LOSS) {
+    MOE_HIP(moe::launch_dispatch_bwd_dense(is_bf16_rows(d), dxd, dxd_scales(d, dxd), row_of, dlogits, w_r, dx, r.t0,
+                                           r.t1, d->k, d->E, d->H, (hipStream_t)stream),
+            "dispatch_bwd_dense");
+    return MOE_OK;
+  }
   MOE_HIP(moe::launch_dispatch_bwd(is_bf16_rows(d), dxd, dxd_scales(d, dxd), row_of, topk_idx, dlogits, w_r, dx,
                                    r.t0, r.t1, d->k, d->E, d->H, (int64_t)d->H * elem_size(d->dtype),
                                    (hipStream_t)stream),
@@ -764,8 +773,34 @@ static moe_status route_any(const moe_desc* d, int c, const moe_tensors* t, hipS
   if (t->logits || d->T == 0)
     return moe_route(d, c, t->logits, t->topk_idx, t->gates, t->counts, t->offsets, t->row_of, t->src_token,
                      t->workspace, s);
-  return moe_route_x(d, c, t->x, t->w_r, nullptr, t->topk_idx, t->gates, t->counts, t->offsets, t->row_of,
+  return moe_route_x(d, c, t->x, t->w_r, (d->flags & MOE_FLAG_ROUTER_LOSS) ? t->router_logits : nullptr, t->topk_idx, t->gates, t->counts, t->offsets, t->row_of,
                      t->src_token, t->workspace, s);
+}
+
+// MOE_FLAG_ROUTER_LOSS: the loss over every chunk's tokens once all of them are routed, and its
+// gradient into dlogits before the first chunk's route backward.
+static const float* loss_logits(const moe_tensors* t) { return t->logits ? t->logits : t->router_logits; }
+static moe_status check_loss_tensors(const moe_desc* d, const moe_tensors* t, bool backward) {
+  if (!(d->flags & MOE_FLAG_ROUTER_LOSS)) return MOE_OK;
+  MOE_TRY(check_router_loss(__func__, d, t->n_segments, t->balance_coef, t->z_coef, t->seg_offsets));
+  if (d->T > 0) { MOE_NEED(loss_logits(t)); MOE_NEED(t->router_lse); }
+  MOE_NEED(t->seg_counts); MOE_NEED(t->seg_tokens); MOE_NEED(t->seg_probs); MOE_NEED(t->router_loss);
+  MOE_NEED(t->loss_workspace);
+  if ((uintptr_t)t->loss_workspace & 15) return fail(MOE_ERR_ARG, "layer: loss_workspace must be 16-byte aligned");
+  if (backward && d->T > 0 && t->dlogits == loss_logits(t))
+    return fail(MOE_ERR_ARG, "layer: dlogits may not be the logits buffer");
+  return MOE_OK;
+}
+static moe_status layer_loss(const moe_desc* d, const moe_tensors* t, hipStream_t s) {
+  if (!(d->flags & MOE_FLAG_ROUTER_LOSS)) return MOE_OK;
+  return moe_router_loss(d, t->n_segments, t->balance_coef, t->z_coef, loss_logits(t), t->topk_idx, t->seg_offsets,
+                         t->token_mask, t->router_lse, t->seg_counts, t->seg_tokens, t->seg_probs, t->router_loss,
+                         t->loss_workspace, s);
+}
+static moe_status layer_loss_bwd(const moe_desc* d, const moe_tensors* t, hipStream_t s) {
+  if (!(d->flags & MOE_FLAG_ROUTER_LOSS)) return MOE_OK;
+  return moe_router_loss_bwd(d, t->n_segments, t->balance_coef, t->z_coef, loss_logits(t), t->router_lse,
+                             t->seg_offsets, t->token_mask, t->seg_counts, t->seg_tokens, t->dloss, t->dlogits, s);
 }
 
 // Two-stream schedules. A wait of one stream on the other's event costs the waiting stream
@@ -818,6 +853,9 @@ static moe_status forward_sched(const moe_desc* d, const moe_tensors* t, hipStre
       MOE_TRY(moe_combine(d, c, t->yd, t->gates, t->row_of, t->out, cs));
     }
   }
+  // every chunk is routed in front of this point of the side stream (chunk 0 on the compute stream, which
+  // the side stream waited for)
+  MOE_TRY(layer_loss(d, t, two ? as : cs));
   if (two && join) {
     MOE_HIP(hipEventRecord(done, as), "hipEventRecord");
     MOE_HIP(hipStreamWaitEvent(cs, done, 0), "hipStreamWaitEvent");
@@ -872,6 +910,7 @@ static moe_status backward_sched(const moe_desc* d, const moe_tensors* t, hipStr
       if (two) MOE_HIP(hipEventRecord(cb[c + 1], as), "hipEventRecord");
       if (wq8 && c + 2 == n) MOE_TRY(wgrad_operands());
     }
+    if (c == 0) MOE_TRY(layer_loss_bwd(d, t, side));
     MOE_TRY(moe_route_bwd(d, c, t->dgates, t->gates, t->topk_idx, t->x, t->dlogits, t->dwr_acc, t->dwr,
                           t->workspace, side));
     if (two && c >= 1) MOE_HIP(hipStreamWaitEvent(cs, cb[c], 0), "hipStreamWaitEvent");
@@ -923,7 +962,9 @@ static moe::ExpertGemm expert_gemm(const moe_desc* d, const moe_tensors* t) {
 static bool merged_gemms(const moe_desc* d) { return d->dtype == MOE_BF16 && d->T > 0 && rows_of(d) > 0; }
 // the merged backward launches pair BF16 GEMMs; with an FP8 GEMM flag the backward runs per chunk (FP8
 // dxd rows only change the gate/up dgrad's epilogue and dispatch backward, both in the merged launches)
-static bool merged_bwd(const moe_desc* d) { return merged_gemms(d) && (d->flags & ~MOE_FLAG_FP8_DXD) == 0; }
+static bool merged_bwd(const moe_desc* d) {
+  return merged_gemms(d) && (d->flags & ~(MOE_FLAG_FP8_DXD | MOE_FLAG_ROUTER_LOSS)) == 0;
+}
 
 //   compute: R0 D0 GU0 | wait(disp1) [DN0 GU1] | wait(disp2) [DN1 GU2] | ... | DN n-1, C n-1
 //   aux:     wait(disp0) R1 D1 | R2 D2, wait(ffn0) C0 | R3 D3, wait(ffn1) C1 | ...
@@ -998,6 +1039,9 @@ static moe_status forward_sched_merged(const moe_desc* d, const moe_tensors* t, 
       MOE_TRY(moe_combine(d, c, t->yd, t->gates, t->row_of, t->out, cs));
     }
   }
+  // every chunk is routed in front of this point of the side stream (chunk 0 on the compute stream, which
+  // the side stream waited for)
+  MOE_TRY(layer_loss(d, t, two ? as : cs));
   if (two && join) {
     MOE_HIP(hipEventRecord(done, as), "hipEventRecord");
     MOE_HIP(hipStreamWaitEvent(cs, done, 0), "hipStreamWaitEvent");
@@ -1039,6 +1083,7 @@ static moe_status backward_sched_merged(const moe_desc* d, const moe_tensors* t,
   }
   if (deferred_combine) MOE_TRY(moe_combine(d, n - 1, t->yd, t->gates, t->row_of, t->out, side));
   if (two) MOE_HIP(hipStreamWaitEvent(as, cb[0], 0), "hipStreamWaitEvent");
+  MOE_TRY(layer_loss_bwd(d, t, side));
   MOE_TRY(route_bwd(0));
   MOE_HIP(moe::gg_down_dgrad(g, 0, cs), "expert_dgrad");
   for (int c = 0; c < n; ++c) {
@@ -1070,6 +1115,7 @@ static moe_status backward_sched_merged(const moe_desc* d, const moe_tensors* t,
 moe_status moe_layer_forward(const moe_desc* d, const moe_tensors* t, void* compute_stream, void* aux_stream) {
   MOE_TRY(validate(d));
   MOE_TRY(check_fwd_tensors(d, t));
+  MOE_TRY(check_loss_tensors(d, t, false));
   if (merged_gemms(d)) return forward_sched_merged(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream, true);
   return forward_sched(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream, true);
 }
@@ -1077,6 +1123,7 @@ moe_status moe_layer_forward(const moe_desc* d, const moe_tensors* t, void* comp
 moe_status moe_layer_backward(const moe_desc* d, const moe_tensors* t, void* compute_stream, void* aux_stream) {
   MOE_TRY(validate(d));
   MOE_TRY(check_fwd_tensors(d, t));
+  MOE_TRY(check_loss_tensors(d, t, true));
   MOE_TRY(check_bwd_tensors(d, t));
   if (merged_bwd(d)) return backward_sched_merged(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream);
   return backward_sched(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream);
@@ -1086,6 +1133,7 @@ moe_status moe_layer_forward_backward(const moe_desc* d, const moe_tensors* t, v
                                       void* aux_stream) {
   MOE_TRY(validate(d));
   MOE_TRY(check_fwd_tensors(d, t));
+  MOE_TRY(check_loss_tensors(d, t, true));
   MOE_TRY(check_bwd_tensors(d, t));
   // no join between the two: the backward's first wait of the auxiliary stream follows the
   // whole forward on the compute stream, and its final join covers the forward's aux work

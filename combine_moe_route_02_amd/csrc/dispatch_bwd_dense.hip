@@ -1,0 +1,244 @@
+// Dispatch backward with a dense router gradient (MOE_FLAG_ROUTER_LOSS): an auxiliary loss reaches the
+// logits of every expert, so
+//   dx[t] = RNE( sum over local slots j of dxd[row_of[t][j]] + sum over all e of dlogits[t][e] W_r[e] ).
+// The second sum is a [T, E] x [E, H] product whose epilogue gathers the expert rows, so dx is written
+// once and no [T, H] term goes through memory. dlogits is FP32: it is split into a BF16 high and low
+// part (the remainder is under 2^-17 of the value, far under the BF16 rounding of dx; W_r is BF16
+// itself) and both run on BF16 MFMA into the same FP32 sums.
+//
+// A workgroup (4 waves) keeps its column slice of W_r in registers as MFMA fragments for every expert
+// and walks 32-token tiles: the tile's dlogits are split into LDS once for the four waves, each wave
+// multiplies its columns, the FP32 sums go through LDS into rows of 16-byte vectors, and there the
+// slots' dxd rows are added as they are loaded. Each XCD owns a range of tokens, so that the tile's
+// dlogits, which every slice reads, come from its L2.
+#include "gg_engine.h"
+
+namespace moe {
+namespace {
+
+using gg::frag_ks;
+using gg::ks_off;
+
+constexpr int kDT = 32;        // tokens per tile
+constexpr int kDThreads = 256;
+constexpr int kStageK = 64;    // W_r rows staged at once
+
+// KS: K steps of 16 experts (E <= 16 KS); CW: columns per wave
+template <int KS, int CW>
+struct DenseLds {
+  static constexpr int kSlice = 4 * CW;
+  static constexpr int kPitchA = KS * 32 + 16;        // bytes per token of one part
+  static constexpr int kPartA = kDT * kPitchA;
+  static constexpr int kPitchC = (kSlice + 4) * 4;    // bytes per token of the FP32 sums
+  static constexpr int kC = 2 * kPartA;
+  static constexpr int kSums = kDT * kPitchC;
+  static constexpr int kW = kStageK * kSlice * 2;     // W_r staging, before the first tile
+  static constexpr int kRows = kC + (kSums > kW ? kSums : kW);
+  static constexpr int kBytes = kRows + 2 * kDT * 8 * 4;  // slot rows of two tiles
+};
+
+// Adds one vector of 8 columns of dispatch row r.
+template <bool Q>
+MOE_DEV void add_row(float (&f)[8], const void* dxd, const float* dxs, int64_t r, int64_t nvec, int64_t vec, int nblk) {
+  float g[8];
+  if constexpr (Q) {
+    deq8(((const uint2*)dxd)[r * nvec + vec], dxs[r * nblk + (vec >> 5)], g);
+  } else {
+    const u32x4 v = ((const u32x4*)dxd)[r * nvec + vec];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { g[2 * i] = bf2f(w[i] & 0xffff); g[2 * i + 1] = bf2f(w[i] >> 16); }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] += g[i];
+}
+
+struct DenseArgs {
+  const void* dxd;        // [P, H] BF16 rows, or e4m3 codes (Q)
+  const float* dxs;       // Q: [P, ceil(H / 256)]
+  const int32_t* row_of;  // [T, K]
+  const float* dlogits;   // [T, E]
+  const uint16_t* w_r;    // [E, H]
+  uint16_t* dx;           // [T, H]
+  int64_t t0, t1;
+  int K, E, H, nsl, lanes;  // column slices; workgroups per XCD and slice
+};
+
+template <int KS, int CW, bool Q>
+__global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_kernel(DenseArgs a) {
+  using L = DenseLds<KS, CW>;
+  constexpr int TN = CW / 32, SL = L::kSlice;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  char* const sc = lds + L::kC;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t tiles = (a.t1 - a.t0 + kDT - 1) / kDT, px = (tiles + 7) / 8;
+  const int xcd = blockIdx.x % 8, j = blockIdx.x / 8;
+  const int n0 = (j % a.nsl) * SL, first = j / a.nsl;
+  if (xcd * px + first >= tiles || first >= px) return;
+
+  // the slice of W_r as fragments: rows of W_r through LDS, transposed by the fragment reads
+  bf16x8_t w[KS][TN];
+#pragma unroll
+  for (int s = 0; s < KS * 16 / kStageK; ++s) {
+    __syncthreads();
+    constexpr int CPR = SL / 8;  // 16-byte vectors per W_r row
+    for (int i = tid; i < kStageK * CPR; i += kDThreads) {
+      const int k = i / CPR, c = i % CPR, e = s * kStageK + k, n = n0 + 8 * c;
+      u32x4 v{0u, 0u, 0u, 0u};
+      if (e < a.E && n < a.H) v = *(const u32x4*)(a.w_r + (int64_t)e * a.H + n);
+      *(u32x4*)(sc + ks_off<SL>(k, c)) = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int kk = 0; kk < kStageK / 16; ++kk)
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn) w[s * (kStageK / 16) + kk][tn] = frag_ks<SL>(sc, wave * CW + 32 * tn, kk, lane);
+  }
+
+  const int64_t nvec = a.H / 8;
+  const int nblk = (a.H + 255) / 256;
+  const int evec = a.E / 4;
+  // Two barriers per tile. A wave may start the next tile while others still add rows of this one, so
+  // the slot rows alternate between two buffers; the parts and the sums are separate areas.
+  int par = 0;
+  for (int64_t l = first; l < px; l += a.lanes, par ^= 1) {
+    const int64_t tile = xcd * px + l;
+    if (tile >= tiles) break;
+    int* const srow = (int*)(lds + L::kRows) + par * (kDT * 8);
+    const int64_t r0 = a.t0 + tile * kDT;
+    const int nt = (int)(a.t1 - r0 < kDT ? a.t1 - r0 : kDT);
+    // dlogits of the tile (one contiguous block) as high and low parts; columns past E and tokens past
+    // the chunk are zeros
+    for (int i = tid; i < kDT * KS * 4; i += kDThreads) {
+      const int r = i / (KS * 4), c = i % (KS * 4);
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nt && c < evec) f = *(const float4*)(a.dlogits + (r0 + r) * a.E + 4 * c);
+      const uint2 h = gg::pack4(f.x, f.y, f.z, f.w);
+      float hf[4];
+      gg::unpack4(h, hf);
+      *(uint2*)(lds + r * L::kPitchA + 8 * c) = h;
+      *(uint2*)(lds + L::kPartA + r * L::kPitchA + 8 * c) = gg::pack4(f.x - hf[0], f.y - hf[1], f.z - hf[2], f.w - hf[3]);
+    }
+    for (int i = tid; i < kDT * a.K; i += kDThreads) srow[i] = i < nt * a.K ? a.row_of[r0 * a.K + i] : -1;
+    __syncthreads();
+
+    f32x16_t acc[TN];
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[tn][q] = 0.f;
+    const char* fa = lds + (lane & 31) * L::kPitchA + 16 * (lane >> 5);
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      const bf16x8_t hi = *(const bf16x8_t*)(fa + 32 * kk), lo = *(const bf16x8_t*)(fa + L::kPartA + 32 * kk);
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn) {
+        acc[tn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[kk][tn], hi, acc[tn], 0, 0, 0);
+        acc[tn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[kk][tn], lo, acc[tn], 0, 0, 0);
+      }
+    }
+    // lane: token lane & 31, four consecutive columns per accumulator group
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *(float4*)(sc + (lane & 31) * L::kPitchC + 4 * (wave * CW + 32 * tn + gg::out_col(g, lane))) =
+            make_float4(acc[tn][4 * g], acc[tn][4 * g + 1], acc[tn][4 * g + 2], acc[tn][4 * g + 3]);
+    __syncthreads();
+
+    constexpr int VPR = SL / 8;  // vectors of 8 columns per token
+    for (int i = tid; i < nt * VPR; i += kDThreads) {
+      const int r = i / VPR, c = i % VPR, n = n0 + 8 * c;
+      if (n >= a.H) continue;
+      const float4 x = *(const float4*)(sc + r * L::kPitchC + 32 * c), y = *(const float4*)(sc + r * L::kPitchC + 32 * c + 16);
+      float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      for (int k = 0; k < a.K; ++k) {
+        const int row = srow[r * a.K + k];
+        if (row >= 0) add_row<Q>(f, a.dxd, a.dxs, row, nvec, n / 8, nblk);
+      }
+      *(u32x4*)(a.dx + (r0 + r) * a.H + n) = u32x4{pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7])};
+    }
+  }
+}
+
+// FP32 payloads (small configurations): 64 columns and 16 tokens per block, four tokens per thread.
+constexpr int kFT = 16;
+__global__ __launch_bounds__(256) void dispatch_bwd_dense_f32_kernel(
+    const float* __restrict__ dxd, const int32_t* __restrict__ row_of, const float* __restrict__ dlogits,
+    const float* __restrict__ w_r, float* __restrict__ dx, int64_t t0, int64_t t1, int K, int E, int H) {
+  constexpr int EB = 128;  // experts staged at once
+  __shared__ float dl[kFT][EB];
+  const int tid = threadIdx.x, n = blockIdx.y * 64 + (tid & 63), g = tid >> 6;
+  const int64_t r0 = t0 + (int64_t)blockIdx.x * kFT;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int e0 = 0; e0 < E; e0 += EB) {
+    __syncthreads();
+    for (int i = tid; i < kFT * EB; i += 256) {
+      const int r = i / EB, e = e0 + i % EB;
+      dl[r][i % EB] = r0 + r < t1 && e < E ? dlogits[(r0 + r) * E + e] : 0.f;
+    }
+    __syncthreads();
+    const int ne = min(EB, E - e0);
+    for (int e = 0; e < ne; ++e) {
+      const float w = w_r[(int64_t)(e0 + e) * H + n];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(dl[4 * g + i][e], w, acc[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t t = r0 + 4 * g + i;
+    if (t >= t1) continue;
+    float f = acc[i];
+    for (int k = 0; k < K; ++k) {
+      const int row = row_of[t * K + k];
+      if (row >= 0) f += dxd[(int64_t)row * H + n];
+    }
+    dx[t * H + n] = f;
+  }
+}
+
+template <int KS, int CW, bool Q>
+hipError_t run_dense(DenseArgs a, hipStream_t s) {
+  using L = DenseLds<KS, CW>;
+  auto k = dispatch_bwd_dense_kernel<KS, CW, Q>;
+  hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != hipSuccess) return e;
+  a.nsl = (a.H + L::kSlice - 1) / L::kSlice;
+  // two workgroups per CU, and the tiles of an XCD spread evenly over its workgroups of a slice
+  const int64_t px = ((a.t1 - a.t0 + kDT - 1) / kDT + 7) / 8;
+  int64_t lanes = (int64_t)gg::cu_count() / 8 * 2 / a.nsl;
+  if (lanes < 1) lanes = 1;
+  if (lanes > px) lanes = px;
+  const int64_t per = (px + lanes - 1) / lanes;
+  a.lanes = (int)((px + per - 1) / per);
+  {
+    MOE_TRACE("dispatch_bwd_dense", s);
+    MOE_LAUNCH(k, dim3((unsigned)(8 * a.nsl * a.lanes)), dim3(kDThreads), L::kBytes, s, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dispatch_bwd_dense(bool bf16, const void* dxd, const float* dxd_scales, const int32_t* row_of,
+                                     const float* dlogits, const void* w_r, void* dx, int64_t t0, int64_t t1, int K,
+                                     int E, int H, hipStream_t s) {
+  if (t1 <= t0) return hipSuccess;
+  if (!bf16) {
+    MOE_TRACE("dispatch_bwd_dense_f32", s);
+    MOE_LAUNCH(dispatch_bwd_dense_f32_kernel, dim3((unsigned)((t1 - t0 + kFT - 1) / kFT), (unsigned)(H / 64)), dim3(256), 0,
+               s, (const float*)dxd, row_of, dlogits, (const float*)w_r, (float*)dx, t0, t1, K, E, H);
+    return hipGetLastError();
+  }
+  DenseArgs a{dxd, dxd_scales, row_of, dlogits, (const uint16_t*)w_r, (uint16_t*)dx, t0, t1, K, E, H, 0, 0};
+  // fragments of a wave: 64 columns of up to 256 experts, 32 of up to 1024 (at most 256 registers)
+#define MOE_DENSE(KS_, CW_) return dxd_scales ? run_dense<KS_, CW_, true>(a, s) : run_dense<KS_, CW_, false>(a, s)
+  if (E <= 128) MOE_DENSE(8, 64);
+  if (E <= 256) MOE_DENSE(16, 64);
+  if (E <= 512) MOE_DENSE(32, 32);
+  MOE_DENSE(64, 32);
+#undef MOE_DENSE
+}
+
+}  // namespace moe

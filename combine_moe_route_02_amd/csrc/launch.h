@@ -55,12 +55,18 @@ hipError_t launch_combine_bwd(bool bf16, const void* dy, const void* yd, const f
 hipError_t launch_route_bwd_dlogits(const float* dgates, const float* gates, const int32_t* idx,
                                     float* dlogits, int64_t t0, int64_t t1, int K, int E,
                                     hipStream_t s, uint16_t* dl_hi = nullptr, uint16_t* dl_lo = nullptr,
-                                    int ldl = 0, int64_t pitch = 0);
+                                    int ldl = 0, int64_t pitch = 0,
+                                    bool add = false);  // add: dlogits holds another term already
 // dxd_scales non-null: dxd holds block-scaled e4m3 rows (codes [., H], one FP32 scale per row
 // and 256-column block, dxd_scales [., ceil(H/256)]); BF16 payloads only
 hipError_t launch_dispatch_bwd(bool bf16, const void* dxd, const float* dxd_scales, const int32_t* row_of,
                                const int32_t* idx, const float* dlogits, const void* w_r, void* dx, int64_t t0,
                                int64_t t1, int K, int E, int H, int64_t row_bytes, hipStream_t s);
+
+// the same with the router term over every expert (dense dlogits; dispatch_bwd_dense.hip)
+hipError_t launch_dispatch_bwd_dense(bool bf16, const void* dxd, const float* dxd_scales, const int32_t* row_of,
+                                     const float* dlogits, const void* w_r, void* dx, int64_t t0, int64_t t1, int K,
+                                     int E, int H, hipStream_t s);
 
 // grouped GEMMs
 hipError_t launch_expert_fwd(bool bf16, const void* xd, const void* w1, const void* w2,

@@ -442,7 +442,10 @@ __global__ __launch_bounds__(kBlockThreads) void combine_bwd_q_kernel(
 
 // Route backward, per token: dlogits[t][e] = g_j (dg_j - sum_i g_i dg_i) where e = idx[t][j],
 // zero for every other expert (the full row of E columns is written): the row is cleared with
-// coalesced stores, then lanes 0..K-1 store their slot's value (same wave, program order).
+// coalesced stores, then lanes 0..K-1 store their slot's value (same wave, program order). ADD: the
+// row already holds the gradient of an auxiliary loss; the slots' values are added to it, and the
+// planes hold the dense sum.
+template <bool ADD>
 __global__ __launch_bounds__(256) void route_bwd_dlogits_kernel(
     const float* __restrict__ dgates, const float* __restrict__ gates, const int32_t* __restrict__ idx,
     float* __restrict__ dlogits, uint16_t* __restrict__ dl_hi, uint16_t* __restrict__ dl_lo, int ldl, int64_t pitch,
@@ -457,9 +460,13 @@ __global__ __launch_bounds__(256) void route_bwd_dlogits_kernel(
   for (int j = 0; j < K; ++j)
     s = fmaf(bcast_f(g, j), bcast_f(d, j), s);
   float* row = dlogits + t * (int64_t)E;
-  for (int e = lane; e < E; e += 64) row[e] = 0.f;
   const float v = g * (d - s);
-  if (lane < K) row[id] = v;
+  if constexpr (ADD) {
+    if (!dl_hi && lane < K) row[id] += v;
+  } else {
+    for (int e = lane; e < E; e += 64) row[e] = 0.f;
+    if (lane < K) row[id] = v;
+  }
   if (dl_hi) {
     // BF16 high and low parts of the row for the router weight gradient (row t - t0 of the
     // planes; zeros past E up to ldl columns)
@@ -479,6 +486,14 @@ __global__ __launch_bounds__(256) void route_bwd_dlogits_kernel(
       for (int j = 0; j < 8; ++j) {
         if (ids[j] == e) x0 = vs[j];
         if (ids[j] == e + 1) x1 = vs[j];
+      }
+      if constexpr (ADD) {  // E is a multiple of 4 where planes are written: pairs end inside the row
+        if (e < E) {
+          const float2 old = *(const float2*)(row + e);
+          x0 += old.x;
+          x1 += old.y;
+          *(float2*)(row + e) = make_float2(x0, x1);
+        }
       }
       const uint16_t h0 = f2bf(x0), h1 = f2bf(x1);
       hr[e / 2] = (uint32_t)h0 | ((uint32_t)h1 << 16);
@@ -862,12 +877,14 @@ hipError_t launch_combine_bwd(bool bf16, const void* dy, const void* yd, const f
 
 hipError_t launch_route_bwd_dlogits(const float* dgates, const float* gates, const int32_t* idx,
                                     float* dlogits, int64_t t0, int64_t t1, int K, int E,
-                                    hipStream_t s, uint16_t* dl_hi, uint16_t* dl_lo, int ldl, int64_t pitch) {
+                                    hipStream_t s, uint16_t* dl_hi, uint16_t* dl_lo, int ldl, int64_t pitch,
+                                    bool add) {
   if (dl_hi && (!dl_lo || ldl < E || ldl % 8 || pitch % 2 || pitch < ldl)) return hipErrorInvalidValue;
   if (t1 <= t0) return hipSuccess;
   {
     MOE_TRACE("route_bwd_dlogits", s);
-    MOE_LAUNCH(route_bwd_dlogits_kernel, tok_grid(t1 - t0), dim3(256), 0, s, dgates, gates,
+    auto k = add ? route_bwd_dlogits_kernel<true> : route_bwd_dlogits_kernel<false>;
+    MOE_LAUNCH(k, tok_grid(t1 - t0), dim3(256), 0, s, dgates, gates,
                        idx, dlogits, dl_hi, dl_lo, ldl, pitch, t0, t1, K, E);
   }
   return hipGetLastError();

@@ -107,6 +107,16 @@ typedef struct moe_desc {
  * saturated; scale amax / 448; an all-zero block stores codes 0 and scale 1). dx is the FP32 sum of
  * code * scale over the token's local slots plus the router term, rounded once to BF16. */
 #define MOE_FLAG_FP8_DXD 4
+/* (8 is not a flag.) */
+/* The router logits carry the gradient of an auxiliary loss (moe_router_loss, or any other term of the
+ * caller's); F32 and BF16 dtypes (MOE_ERR_UNSUPPORTED otherwise), with or without the FP8 flags.
+ * dlogits [T, E] holds that gradient when moe_route_bwd is called, which adds the selected experts'
+ * terms to it (a second call on the same dlogits would add them again); dwr is the product of the dense
+ * sum, and moe_dispatch_bwd adds dlogits[t] W_r over all E experts (BF16: FP32 sums of dlogits split
+ * into a BF16 high and low part). The layer primitives then run the loss themselves: the forward
+ * writes it over every token once all chunks are routed, and the backward writes its gradient to
+ * dlogits first (the loss fields of moe_tensors). */
+#define MOE_FLAG_ROUTER_LOSS 16
 
 /* ---------------------------------------------------------------------------------------
  * Stage calls
@@ -190,7 +200,8 @@ moe_status moe_combine_bwd(const moe_desc* d, int chunk, const void* dy, const v
 
 /* Route backward (ChunkedEP "Numerical status": FP32 accumulation across chunks, then one
  * conversion). dlogits[t][idx[t][j]] = g_j * (dg_j - sum_i g_i dg_i), zero for unselected
- * experts (all E columns written for the chunk's rows). Router weight gradient of the
+ * experts (all E columns written for the chunk's rows; with MOE_FLAG_ROUTER_LOSS added to what
+ * dlogits holds). Router weight gradient of the
  * caller's projection logits = x W_r^T: the chunk's dlogits^T x is computed in FP32 (dlogits
  * split into a BF16 high and low part, x exact) and stored into dwr_acc for the first chunk,
  * added to it for later chunks; after the last chunk (or chunk = -1) dwr = dwr_acc converted
@@ -261,7 +272,8 @@ moe_status moe_expert_wgrad_fp8(const moe_desc* d, const void* dyd, const void* 
  * token order; the router term is the input gradient of the projection whose weight gradient
  * "Numerical status -- unresolved" accumulates): dx[t] = RNE( sum over local slots of dxd[row_of[t][j]]
  * + sum_j dlogits[t][idx[t][j]] * W_r[idx[t][j]] ) with FP32 accumulation (the second sum is
- * the router projection's input gradient; dlogits is zero off the selected experts). */
+ * the router projection's input gradient; dlogits is zero off the selected experts; with
+ * MOE_FLAG_ROUTER_LOSS it is dense and the sum runs over all E experts). */
 moe_status moe_dispatch_bwd(const moe_desc* d, int chunk, const void* dxd, const int32_t* row_of,
                             const int32_t* topk_idx, const float* dlogits, const void* w_r,
                             void* dx, void* stream);
@@ -412,6 +424,14 @@ typedef struct moe_tensors {
   void* dyd_q; float* dyd_scale; void* dgu_q; float* dgu_scale;
   /* MOE_FLAG_FP8_WGRAD only (see moe_expert_wgrad_fp8): the per-expert transposed FP8 operands */
   void* dyd_t; float* dyd_cs; void* dgu_t; float* dgu_cs; void* xd_t; float* xd_cs; void* h_t; float* h_cs;
+  /* MOE_FLAG_ROUTER_LOSS only, read under that flag alone (see moe_router_loss): segments and mask
+   * (nullable with n_segments = 1), the loss's outputs, its upstream gradient (nullable: 1), its
+   * workspace of moe_router_loss_bytes() bytes, and, where `logits` is NULL, the buffer [T,E] that
+   * receives the logits routed on. */
+  const int32_t* seg_offsets; const uint8_t* token_mask; float* router_logits; float* router_lse;
+  int32_t* seg_counts; int32_t* seg_tokens; float* seg_probs; float* router_loss; const float* dloss;
+  void* loss_workspace;
+  int32_t n_segments; float balance_coef; float z_coef;
 } moe_tensors;
 
 moe_status moe_layer_forward(const moe_desc* d, const moe_tensors* t, void* compute_stream,

@@ -66,3 +66,32 @@ def test_workspace_bytes():
     # a tile of 32 rows holds E sums and E counts
     assert a >= (1000 // 32) * 32 * 8
     assert _status(mh.moe_router_loss_bytes, _desc(), 0) == -1
+
+
+# ------------------------------------------------------------------ MOE_FLAG_ROUTER_LOSS
+
+def test_flag_needs_a_backward_dtype():
+    for dt, st in (("f32", 0), ("bf16", 0), ("fp8", -3), ("int8", -3)):
+        assert _status(mh.workspace_bytes, _desc(dtype=dt, flags=mh.FLAG_ROUTER_LOSS)) == st
+    assert _status(mh.workspace_bytes, _desc(dtype="f32", flags=mh.FLAG_ROUTER_LOSS | mh.FLAG_FP8_DXD)) == -3
+    assert _status(mh.workspace_bytes, _desc(flags=8)) == -1 and _status(mh.workspace_bytes, _desc(flags=32)) == -1
+    # the buffers of the flag are outside the workspace of the other calls
+    assert mh.workspace_bytes(_desc(flags=mh.FLAG_ROUTER_LOSS)) == mh.workspace_bytes(_desc())
+
+
+@pytest.mark.parametrize("name", ["router_lse", "seg_counts", "seg_tokens", "seg_probs", "router_loss", "loss_workspace"])
+def test_layer_needs_the_loss_buffers(name):
+    bufs = {f: 16 * (i + 1) for i, f in enumerate(mh.TENSOR_FIELDS)}
+    bufs[name] = None
+    for fn in (mh.moe_layer_forward, mh.moe_layer_backward, mh.moe_layer_forward_backward):
+        assert _status(fn, _desc(flags=mh.FLAG_ROUTER_LOSS), bufs, 0, 0) == -1
+
+
+def test_layer_checks_the_loss_options():
+    d = _desc(flags=mh.FLAG_ROUTER_LOSS)
+    bufs = {f: 16 * (i + 1) for i, f in enumerate(mh.TENSOR_FIELDS)}
+    for bad, st in (({"n_segments": 0}, -1), ({"n_segments": 70000}, -3), ({"n_segments": 2, "seg_offsets": None}, -1),
+                    ({"balance_coef": float("nan")}, -1), ({"logits": None, "router_logits": None}, -1),
+                    ({"loss_workspace": 8}, -1)):
+        assert _status(mh.moe_layer_forward, d, {**bufs, **bad}, 0, 0) == st, bad
+    assert _status(mh.moe_layer_backward, d, {**bufs, "dlogits": bufs["logits"]}, 0, 0) == -1
