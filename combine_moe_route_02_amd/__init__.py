@@ -149,10 +149,23 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None  # torch's current stream of the current device as an integer
+
+
 def _stream(s) -> Optional[int]:
+    global _raw_stream
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            import torch
+            handle = torch.cuda.current_stream().cuda_stream  # initialises the device's context
+            try:  # without the Stream object that current_stream() builds on every call
+                get, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+                get(dev())
+                _raw_stream = lambda: get(dev())  # noqa: E731
+            except AttributeError:
+                _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+            return handle
+        return _raw_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

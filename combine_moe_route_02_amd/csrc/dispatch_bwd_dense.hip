@@ -32,26 +32,38 @@ struct DenseLds {
   static constexpr int kPitchC = (kSlice + 4) * 4;    // bytes per token of the FP32 sums
   static constexpr int kC = 2 * kPartA;
   static constexpr int kSums = kDT * kPitchC;
-  static constexpr int kW = kStageK * kSlice * 2;     // W_r staging, before the first tile
+  static constexpr int kW = (KS * 16 < kStageK ? KS * 16 : kStageK) * kSlice * 2;  // W_r staging, before the first tile
   static constexpr int kRows = kC + (kSums > kW ? kSums : kW);
   static constexpr int kBytes = kRows + 2 * kDT * 8 * 4;  // slot rows of two tiles
 };
 
-// Adds one vector of 8 columns of dispatch row r.
-template <bool Q>
-MOE_DEV void add_row(float (&f)[8], const void* dxd, const float* dxs, int64_t r, int64_t nvec, int64_t vec, int nblk) {
-  float g[8];
-  if constexpr (Q) {
-    deq8(((const uint2*)dxd)[r * nvec + vec], dxs[r * nblk + (vec >> 5)], g);
-  } else {
-    const u32x4 v = ((const u32x4*)dxd)[r * nvec + vec];
+// One vector of 8 columns of a dispatch row: BF16 values, or (Q) e4m3 codes with their block's scale.
+template <bool Q> struct RowVec;
+template <> struct RowVec<false> {
+  u32x4 v;
+  MOE_DEV void load(const void* dxd, const float*, int64_t r, int64_t nvec, int vec, int) {
+    v = ((const u32x4*)dxd)[r * nvec + vec];
+  }
+  MOE_DEV void add(float (&f)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { g[2 * i] = bf2f(w[i] & 0xffff); g[2 * i + 1] = bf2f(w[i] >> 16); }
+    for (int i = 0; i < 4; ++i) { f[2 * i] += bf2f(w[i] & 0xffff); f[2 * i + 1] += bf2f(w[i] >> 16); }
   }
+};
+template <> struct RowVec<true> {
+  uint2 v;
+  float s;
+  MOE_DEV void load(const void* dxd, const float* dxs, int64_t r, int64_t nvec, int vec, int nblk) {
+    v = ((const uint2*)dxd)[r * nvec + vec];
+    s = dxs[r * nblk + (vec >> 5)];
+  }
+  MOE_DEV void add(float (&f)[8]) const {
+    float g[8];
+    deq8(v, s, g);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] += g[i];
-}
+    for (int i = 0; i < 8; ++i) f[i] += g[i];
+  }
+};
 
 struct DenseArgs {
   const void* dxd;        // [P, H] BF16 rows, or e4m3 codes (Q)
@@ -76,28 +88,67 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_kernel(DenseArgs
   const int n0 = (j % a.nsl) * SL, first = j / a.nsl;
   if (xcd * px + first >= tiles || first >= px) return;
 
-  // the slice of W_r as fragments: rows of W_r through LDS, transposed by the fragment reads
-  bf16x8_t w[KS][TN];
-#pragma unroll
-  for (int s = 0; s < KS * 16 / kStageK; ++s) {
-    __syncthreads();
-    constexpr int CPR = SL / 8;  // 16-byte vectors per W_r row
-    for (int i = tid; i < kStageK * CPR; i += kDThreads) {
-      const int k = i / CPR, c = i % CPR, e = s * kStageK + k, n = n0 + 8 * c;
-      u32x4 v{0u, 0u, 0u, 0u};
-      if (e < a.E && n < a.H) v = *(const u32x4*)(a.w_r + (int64_t)e * a.H + n);
-      *(u32x4*)(sc + ks_off<SL>(k, c)) = v;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < kStageK / 16; ++kk)
-#pragma unroll
-      for (int tn = 0; tn < TN; ++tn) w[s * (kStageK / 16) + kk][tn] = frag_ks<SL>(sc, wave * CW + 32 * tn, kk, lane);
-  }
-
   const int64_t nvec = a.H / 8;
   const int nblk = (a.H + 255) / 256;
   const int evec = a.E / 4;
+  constexpr int ND = kDT * KS * 4 / kDThreads;  // 16-byte vectors of the tile's dlogits per thread
+  constexpr int VPR = SL / 8;                   // vectors of 8 columns per token
+  constexpr int NI = kDT * VPR / kDThreads;     // of them per thread: tokens tid / VPR + it * (256 / VPR)
+  const int c = tid % VPR, rt = tid / VPR, n = n0 + 8 * c;
+  const bool in_cols = n < a.H;
+  float4 dl[ND];
+  int slots[8];
+  // dlogits of the tile (one contiguous block; columns past E and tokens past the chunk are zeros) and the
+  // slot rows of token tid: issued one tile ahead
+  auto fetch = [&](int64_t tile) {
+    const int64_t r0 = a.t0 + tile * kDT;
+    const int nt = (int)(a.t1 - r0 < kDT ? a.t1 - r0 : kDT);
+#pragma unroll
+    for (int u = 0; u < ND; ++u) {
+      const int i = tid + u * kDThreads, r = i / (KS * 4), e4 = i % (KS * 4);
+      dl[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nt && e4 < evec) dl[u] = *(const float4*)(a.dlogits + (r0 + r) * a.E + 4 * e4);
+    }
+    if (tid < kDT)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) slots[k] = k < a.K && tid < nt ? a.row_of[(r0 + tid) * a.K + k] : -1;
+  };
+  fetch(xcd * px + first);
+
+  // the slice of W_r as fragments: rows of W_r through LDS, transposed by the fragment reads; two
+  // stages' rows are loaded together
+  bf16x8_t w[KS][TN];
+  {
+    constexpr int SK = KS * 16 < kStageK ? KS * 16 : kStageK;  // rows per stage
+    constexpr int NS = KS * 16 / SK, SB = NS < 2 ? NS : 2;     // stages, of them loaded at once
+    constexpr int CPR = SL / 8, NV = SK * CPR / kDThreads;     // 16-byte vectors per row, per thread and stage
+#pragma unroll
+    for (int s0 = 0; s0 < NS; s0 += SB) {
+      u32x4 x[SB][NV];
+#pragma unroll
+      for (int s = 0; s < SB; ++s)
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+          const int i = tid + u * kDThreads, e = (s0 + s) * SK + i / CPR, col = n0 + 8 * (i % CPR);
+          x[s][u] = u32x4{0u, 0u, 0u, 0u};
+          if (e < a.E && col < a.H) x[s][u] = *(const u32x4*)(a.w_r + (int64_t)e * a.H + col);
+        }
+#pragma unroll
+      for (int s = 0; s < SB; ++s) {
+        gg::lds_barrier();  // the stage before this one has been read
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+          const int i = tid + u * kDThreads;
+          *(u32x4*)(sc + ks_off<SL>(i / CPR, i % CPR)) = x[s][u];
+        }
+        gg::lds_barrier();
+#pragma unroll
+        for (int kk = 0; kk < SK / 16; ++kk)
+#pragma unroll
+          for (int tn = 0; tn < TN; ++tn) w[(s0 + s) * (SK / 16) + kk][tn] = frag_ks<SL>(sc, wave * CW + 32 * tn, kk, lane);
+      }
+    }
+  }
   // Two barriers per tile. A wave may start the next tile while others still add rows of this one, so
   // the slot rows alternate between two buffers; the parts and the sums are separate areas.
   int par = 0;
@@ -107,20 +158,36 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_kernel(DenseArgs
     int* const srow = (int*)(lds + L::kRows) + par * (kDT * 8);
     const int64_t r0 = a.t0 + tile * kDT;
     const int nt = (int)(a.t1 - r0 < kDT ? a.t1 - r0 : kDT);
-    // dlogits of the tile (one contiguous block) as high and low parts; columns past E and tokens past
-    // the chunk are zeros
-    for (int i = tid; i < kDT * KS * 4; i += kDThreads) {
-      const int r = i / (KS * 4), c = i % (KS * 4);
-      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < nt && c < evec) f = *(const float4*)(a.dlogits + (r0 + r) * a.E + 4 * c);
-      const uint2 h = gg::pack4(f.x, f.y, f.z, f.w);
+#pragma unroll
+    for (int u = 0; u < ND; ++u) {
+      const int i = tid + u * kDThreads, r = i / (KS * 4), e4 = i % (KS * 4);
+      const uint2 h = gg::pack4(dl[u].x, dl[u].y, dl[u].z, dl[u].w);
       float hf[4];
       gg::unpack4(h, hf);
-      *(uint2*)(lds + r * L::kPitchA + 8 * c) = h;
-      *(uint2*)(lds + L::kPartA + r * L::kPitchA + 8 * c) = gg::pack4(f.x - hf[0], f.y - hf[1], f.z - hf[2], f.w - hf[3]);
+      *(uint2*)(lds + r * L::kPitchA + 8 * e4) = h;
+      *(uint2*)(lds + L::kPartA + r * L::kPitchA + 8 * e4) =
+          gg::pack4(dl[u].x - hf[0], dl[u].y - hf[1], dl[u].z - hf[2], dl[u].w - hf[3]);
     }
-    for (int i = tid; i < kDT * a.K; i += kDThreads) srow[i] = i < nt * a.K ? a.row_of[r0 * a.K + i] : -1;
+    if (tid < kDT) {  // the token's local rows first, in slot order
+      int m = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (slots[k] >= 0) srow[tid * 8 + m++] = slots[k];
+      for (; m < 8; ++m) srow[tid * 8 + m] = -1;
+    }
     __syncthreads();
+
+    // the tokens' first two rows and the next tile's inputs travel behind the products
+    RowVec<Q> v[2][NI];
+    int row[2][NI];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int u = 0; u < NI; ++u) {
+        row[s][u] = srow[(rt + u * (kDThreads / VPR)) * 8 + s];
+        if (row[s][u] >= 0 && in_cols) v[s][u].load(a.dxd, a.dxs, row[s][u], nvec, n / 8, nblk);
+      }
+    if (l + a.lanes < px && tile + a.lanes < tiles) fetch(tile + a.lanes);
 
     f32x16_t acc[TN];
 #pragma unroll
@@ -144,19 +211,43 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_kernel(DenseArgs
       for (int g = 0; g < 4; ++g)
         *(float4*)(sc + (lane & 31) * L::kPitchC + 4 * (wave * CW + 32 * tn + gg::out_col(g, lane))) =
             make_float4(acc[tn][4 * g], acc[tn][4 * g + 1], acc[tn][4 * g + 2], acc[tn][4 * g + 3]);
-    __syncthreads();
+    gg::lds_barrier();  // the loads above stay in flight
 
-    constexpr int VPR = SL / 8;  // vectors of 8 columns per token
-    for (int i = tid; i < nt * VPR; i += kDThreads) {
-      const int r = i / VPR, c = i % VPR, n = n0 + 8 * c;
-      if (n >= a.H) continue;
+    if (!in_cols) continue;
+    float f[NI][8];
+#pragma unroll
+    for (int u = 0; u < NI; ++u) {
+      const int r = rt + u * (kDThreads / VPR);
       const float4 x = *(const float4*)(sc + r * L::kPitchC + 32 * c), y = *(const float4*)(sc + r * L::kPitchC + 32 * c + 16);
-      float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      for (int k = 0; k < a.K; ++k) {
-        const int row = srow[r * a.K + k];
-        if (row >= 0) add_row<Q>(f, a.dxd, a.dxs, row, nvec, n / 8, nblk);
+      f[u][0] = x.x; f[u][1] = x.y; f[u][2] = x.z; f[u][3] = x.w;
+      f[u][4] = y.x; f[u][5] = y.y; f[u][6] = y.z; f[u][7] = y.w;
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int u = 0; u < NI; ++u)
+        if (row[s][u] >= 0) v[s][u].add(f[u]);
+    // tokens with more local slots: the next slot of every token in flight together
+    for (int s = 2; s < a.K; ++s) {
+      bool any = false;
+#pragma unroll
+      for (int u = 0; u < NI; ++u) {
+        row[0][u] = row[1][u] < 0 ? -1 : srow[(rt + u * (kDThreads / VPR)) * 8 + s];
+        row[1][u] = row[0][u];
+        any |= row[0][u] >= 0;
+        if (row[0][u] >= 0) v[0][u].load(a.dxd, a.dxs, row[0][u], nvec, n / 8, nblk);
       }
-      *(u32x4*)(a.dx + (r0 + r) * a.H + n) = u32x4{pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7])};
+      if (!any) break;
+#pragma unroll
+      for (int u = 0; u < NI; ++u)
+        if (row[0][u] >= 0) v[0][u].add(f[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < NI; ++u) {
+      const int r = rt + u * (kDThreads / VPR);
+      if (r < nt)
+        *(u32x4*)(a.dx + (r0 + r) * a.H + n) = u32x4{pack_bf2(f[u][0], f[u][1]), pack_bf2(f[u][2], f[u][3]),
+                                                     pack_bf2(f[u][4], f[u][5]), pack_bf2(f[u][6], f[u][7])};
     }
   }
 }
@@ -234,6 +325,8 @@ hipError_t launch_dispatch_bwd_dense(bool bf16, const void* dxd, const float* dx
   DenseArgs a{dxd, dxd_scales, row_of, dlogits, (const uint16_t*)w_r, (uint16_t*)dx, t0, t1, K, E, H, 0, 0};
   // fragments of a wave: 64 columns of up to 256 experts, 32 of up to 1024 (at most 256 registers)
 #define MOE_DENSE(KS_, CW_) return dxd_scales ? run_dense<KS_, CW_, true>(a, s) : run_dense<KS_, CW_, false>(a, s)
+  if (E <= 32) MOE_DENSE(2, 64);
+  if (E <= 64) MOE_DENSE(4, 64);
   if (E <= 128) MOE_DENSE(8, 64);
   if (E <= 256) MOE_DENSE(16, 64);
   if (E <= 512) MOE_DENSE(32, 32);

@@ -24,6 +24,7 @@
 namespace moe {
 
 constexpr int kLossThreads = 256;
+constexpr int kLossBatch = 4;                         // rows of a lane group in flight
 constexpr int kRedThreads = 1024;
 constexpr int kRedCols = 16;                          // columns per reduce block
 constexpr int kRedGroups = kRedThreads / kRedCols;    // tiles read side by side
@@ -94,6 +95,10 @@ struct Pieces {
 struct Tile { int piece; int64_t r0, r1; };
 MOE_DEV Tile find_tile(const Pieces& q) {
   const int64_t blk = blockIdx.x;
+  if (!q.off) {  // one segment: pieces 0 and 2 are empty, block 0 has no tile
+    const int64_t r0 = (blk - 1) * q.R;
+    return {1, blk > 0 ? r0 : q.T, q.T < r0 + q.R ? q.T : r0 + q.R};
+  }
   int i = -1;
   for (int s0 = 0; s0 < q.S + 2; s0 += kLossThreads) {
     const int s = s0 + (int)threadIdx.x;
@@ -104,18 +109,33 @@ MOE_DEV Tile find_tile(const Pieces& q) {
   return {i, r0, b1 < r0 + q.R ? b1 : r0 + q.R};
 }
 
-template <int G>
-MOE_DEV float group_sum(float v) {
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+// Reductions over aligned groups of G lanes, every lane getting the result: DPP steps inside 16 lanes
+// (quad permutes, then mirrors of 8 and of 16), gfx950's row and half swaps above. A shuffle through
+// LDS takes several times a DPP step, and a row has two such chains.
+template <int CTRL>
+MOE_DEV float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int G, class Op>
+MOE_DEV float group_reduce(float v, Op&& op) {
+  v = op(v, dpp<0xB1>(v));   // lane ^ 1
+  v = op(v, dpp<0x4E>(v));   // lane ^ 2
+  v = op(v, dpp<0x141>(v));  // mirror of 8 lanes
+  v = op(v, dpp<0x140>(v));  // mirror of 16 lanes
+  if constexpr (G >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if constexpr (G >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
   return v;
 }
 template <int G>
-MOE_DEV float group_max(float v) {
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-  return v;
-}
+MOE_DEV float group_sum(float v) { return group_reduce<G>(v, [](float a, float b) { return a + b; }); }
+template <int G>
+MOE_DEV float group_max(float v) { return group_reduce<G>(v, [](float a, float b) { return fmaxf(a, b); }); }
 
 // One row in a group of G lanes: lane q holds columns W * (i * G + q) .. + W of i < NV; columns past
 // E hold -inf.
@@ -158,41 +178,50 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_stats_kernel(
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
   double z = 0.0;  // lse reaches 1e38 where a row holds the lowest value: its square passes FP32
   int n = 0;
-  // every lane runs the same trip count, so the shuffles are never divergent
-  for (int64_t rb = t.r0; rb < t.r1; rb += RP) {
-    const int64_t r = rb + g;
-    const bool in = r < t.r1;
-    const bool counted = in && (!mask || mask[r] != 0);
-    float v[C];
-    int my = -1;
-    if (counted) {
-      load_row<G, NV, W>(logits + r * E, E, q, v);
-      if (q < K) my = idx[r * K + q];
-    } else {
+  // U rows of a group are loaded together: a short input is bound by the latency of its loads. Every lane
+  // runs the same trip count, so the reductions are never divergent.
+  constexpr int U = kLossBatch;
+  for (int64_t rb = t.r0; rb < t.r1; rb += RP * U) {
+    float v[U][C];
+    int my[U];
 #pragma unroll
-      for (int c = 0; c < C; ++c) v[c] = -__builtin_huge_valf();
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = rb + u * RP + g;
+      const bool counted = r < t.r1 && (!mask || mask[r] != 0);
+      my[u] = -1;
+      if (counted) {
+        load_row<G, NV, W>(logits + r * E, E, q, v[u]);
+        if (q < K) my[u] = idx[r * K + q];
+      } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[u][c] = -__builtin_huge_valf();
+      }
     }
-    float m = v[0];
 #pragma unroll
-    for (int c = 1; c < C; ++c) m = fmaxf(m, v[c]);
-    m = group_max<G>(m);
-    if (m == -__builtin_huge_valf()) m = 0.f;  // no finite logit: the sum below is 0, or NaN
-    float s = 0.f;
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = rb + u * RP + g;
+      float m = v[u][0];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      v[c] = __expf(v[c] - m);
-      s += v[c];
+      for (int c = 1; c < C; ++c) m = fmaxf(m, v[u][c]);
+      m = group_max<G>(m);
+      if (m == -__builtin_huge_valf()) m = 0.f;  // no finite logit: the sum below is 0, or NaN
+      float s = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        v[u][c] = __expf(v[u][c] - m);
+        s += v[u][c];
+      }
+      s = group_sum<G>(s);
+      const bool live = s != 0.f;  // a row of -inf only is left out like a masked one
+      const float lse = live ? m + __logf(s) : 0.f;
+      const float inv = live ? 1.0f / s : 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] = fmaf(v[u][c], inv, acc[c]);
+      z = fma((double)lse, (double)lse, z);
+      n += live ? 1 : 0;
+      if (r < t.r1 && q == 0) lse_out[r] = lse;
+      if (live && my[u] >= 0 && my[u] < E) atomicAdd(&hist[my[u]], 1);
     }
-    s = group_sum<G>(s);
-    const bool live = s != 0.f;  // a row of -inf only is left out like a masked one
-    const float lse = live ? m + __logf(s) : 0.f;
-    const float inv = live ? 1.0f / s : 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = fmaf(v[c], inv, acc[c]);
-    z = fma((double)lse, (double)lse, z);
-    n += live ? 1 : 0;
-    if (in && q == 0) lse_out[r] = lse;
-    if (live && my >= 0 && my < E) atomicAdd(&hist[my], 1);
   }
   // sums[g][column as held]: column W * (i * G + q) + w of the lane sits at its own index
 #pragma unroll
@@ -219,101 +248,116 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_stats_kernel(
   }
 }
 
-// Adds the tiles of each segment in order: one block per segment and 16 columns, 64 tiles side by
-// side. The last block to arrive forms the losses from the segments' sums.
+template <class T>
+MOE_DEV void st_device(T* p, T v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+template <class T>
+MOE_DEV T ld_device(T* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// Sums over the wave's lanes of equal lane % W.
+template <int W>
+MOE_DEV double lanes_sum(double v) {
+#pragma unroll
+  for (int o = 32; o >= W; o >>= 1) v += __shfl_xor(v, o, kWave);
+  return v;
+}
+template <int W>
+MOE_DEV int lanes_sum(int v) {
+#pragma unroll
+  for (int o = 32; o >= W; o >>= 1) v += __shfl_xor(v, o, kWave);
+  return v;
+}
+
+// Adds the tiles of each segment in a fixed order: one block per segment and 16 columns, 64 tiles side
+// by side (a wave holds 4 tiles x 16 columns), one barrier. With more than one block the last to
+// arrive forms the losses from the segments' sums.
 __global__ __launch_bounds__(kRedThreads) void router_loss_reduce_kernel(
     Pieces pc, LossWs ws, int64_t slots, int E, int K, float balance_coef, float z_coef, int32_t* __restrict__ seg_counts,
     int32_t* __restrict__ seg_tokens, float* __restrict__ seg_probs, float* __restrict__ loss) {
-  __shared__ double red[kRedThreads];
-  __shared__ int redc[kRedThreads];
+  constexpr int NW = kRedThreads / kWave;
+  __shared__ double red[NW][kRedCols + 1];
+  __shared__ int redc[NW][kRedCols + 1];
   __shared__ bool last;
   const int nb = (E + kRedCols - 1) / kRedCols;
   const int s = blockIdx.x / nb, cb = blockIdx.x % nb;
-  const int tid = threadIdx.x, col = tid % kRedCols, grp = tid / kRedCols;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = tid % kRedCols, grp = tid / kRedCols;
   const int e = cb * kRedCols + col;
   const int64_t b0 = pc.bound(s + 1), b1 = pc.bound(s + 2);
-  const int64_t first = pc.base(s + 1);
+  const int64_t first = b0 / pc.R + s + 1;
   int64_t end = b1 > b0 ? first + (b1 - b0 + pc.R - 1) / pc.R : first;
   if (end > slots) end = slots;
 
-  double p = 0.0;
-  int c = 0;
+  double p = 0.0, z = 0.0;
+  int c = 0, n = 0;
   if (e < E)
 #pragma unroll 4
     for (int64_t i = first + grp; i < end; i += kRedGroups) {
       p += (double)ws.p[i * E + e];
       c += ws.c[i * E + e];
     }
-  red[tid] = p;
-  redc[tid] = c;
-  for (int o = kRedThreads / 2; o >= kRedCols; o >>= 1) {
-    __syncthreads();
-    if (tid < o) { red[tid] += red[tid + o]; redc[tid] += redc[tid + o]; }
+  if (cb == 0)
+    for (int64_t i = first + tid; i < end; i += kRedThreads) { z += ws.z[i]; n += ws.n[i]; }
+  p = lanes_sum<kRedCols>(p);
+  c = lanes_sum<kRedCols>(c);
+  if (lane < kRedCols) { red[wave][lane] = p; redc[wave][lane] = c; }
+  if (cb == 0) {
+    z = lanes_sum<1>(z);
+    n = lanes_sum<1>(n);
+    if (lane == 0) { red[wave][kRedCols] = z; redc[wave][kRedCols] = n; }
   }
   __syncthreads();
-  if (tid < kRedCols && e < E) {
-    seg_probs[(int64_t)s * E + e] = (float)red[tid];
-    seg_counts[(int64_t)s * E + e] = redc[tid];
-  }
-  if (tid == 0) {
-    double cp = 0.0;
-    for (int j = 0; j < kRedCols && cb * kRedCols + j < E; ++j) cp += red[j] * (double)redc[j];
-    ws.cp[(int64_t)s * nb + cb] = cp;
-  }
-  if (cb == 0) {
-    __syncthreads();
-    double z = 0.0;
-    int n = 0;
-    for (int64_t i = first + tid; i < end; i += kRedThreads) { z += ws.z[i]; n += ws.n[i]; }
-    red[tid] = z;
-    redc[tid] = n;
-    for (int o = kRedThreads / 2; o > 0; o >>= 1) {
-      __syncthreads();
-      if (tid < o) { red[tid] += red[tid + o]; redc[tid] += redc[tid + o]; }
+  if (wave == 0) {
+    p = 0.0;
+    c = 0;
+    if (lane < kRedCols || (cb == 0 && lane == kRedCols))
+#pragma unroll
+      for (int w = 0; w < NW; ++w) { p += red[w][lane]; c += redc[w][lane]; }
+    if (lane < kRedCols && e < E) {
+      seg_probs[(int64_t)s * E + e] = (float)p;
+      seg_counts[(int64_t)s * E + e] = c;
     }
-    if (tid == 0) { ws.zs[s] = red[0]; seg_tokens[s] = redc[0]; }
-  }
-  if (tid == 0) {
-    __threadfence();
-    last = atomicAdd(ws.arrived, 1) == (int)gridDim.x - 1;
+    const double cp = lanes_sum<1>(lane < kRedCols && e < E ? p * (double)c : 0.0);
+    // What the last block reads is stored and loaded past the XCD's L2 (device-scope atomics), so the
+    // stores need only be complete before the arrival: a fence would write the whole L2 back.
+    if (lane == 0) st_device(&ws.cp[(int64_t)s * nb + cb], cp);
+    if (cb == 0 && lane == kRedCols) { st_device(&ws.zs[s], p); st_device(&seg_tokens[s], c); }
+    asm volatile("" ::: "memory");
+    wait_vm<0>();
+    asm volatile("" ::: "memory");
+    if (lane == 0) last = atomicAdd(ws.arrived, 1) == (int)gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  double bal = 0.0, z = 0.0;
-  int n = 0, full = 0;
+  double bal = 0.0;
+  z = 0.0;
+  n = 0;
+  int full = 0;
   for (int i = tid; i < pc.S; i += kRedThreads) {
-    const int ns = seg_tokens[i];
+    const int ns = ld_device(&seg_tokens[i]);
     if (ns <= 0) continue;
     double cp = 0.0;
-    for (int j = 0; j < nb; ++j) cp += ws.cp[(int64_t)i * nb + j];
+    for (int j = 0; j < nb; ++j) cp += ld_device(&ws.cp[(int64_t)i * nb + j]);
     bal += cp * (double)E / ((double)ns * (double)ns * (double)K);
-    z += ws.zs[i];
+    z += ld_device(&ws.zs[i]);
     n += ns;
     full += 1;
   }
-  __shared__ double redz[kRedThreads];
-  __shared__ int redf[kRedThreads];
-  red[tid] = bal;
-  redz[tid] = z;
-  redc[tid] = n;
-  redf[tid] = full;
-  for (int o = kRedThreads / 2; o > 0; o >>= 1) {
-    __syncthreads();
-    if (tid < o) {
-      red[tid] += red[tid + o];
-      redz[tid] += redz[tid + o];
-      redc[tid] += redc[tid + o];
-      redf[tid] += redf[tid + o];
-    }
-  }
+  bal = lanes_sum<1>(bal);
+  z = lanes_sum<1>(z);
+  n = lanes_sum<1>(n);
+  full = lanes_sum<1>(full);
+  if (lane == 0) { red[wave][0] = bal; red[wave][1] = z; redc[wave][0] = n; redc[wave][1] = full; }
+  __syncthreads();
   if (tid == 0) {
-    const double lb = redf[0] ? red[0] / redf[0] : 0.0, lz = redc[0] ? redz[0] / redc[0] : 0.0;
-    loss[0] = (float)((double)balance_coef * lb + (z_coef != 0.f ? (double)z_coef * lz : 0.0));  // unused: it may be infinite
+    bal = z = 0.0;
+    n = full = 0;
+    for (int w = 0; w < NW; ++w) { bal += red[w][0]; z += red[w][1]; n += redc[w][0]; full += redc[w][1]; }
+    const double lb = full ? bal / full : 0.0, lz = n ? z / n : 0.0;
+    // a z part that is not used stays out: it may be infinite
+    loss[0] = (float)((double)balance_coef * lb + (z_coef != 0.f ? (double)z_coef * lz : 0.0));
     loss[1] = (float)lb;
     loss[2] = (float)lz;
-    seg_tokens[pc.S] = redc[0];
-    seg_tokens[pc.S + 1] = redf[0];
+    seg_tokens[pc.S] = n;
+    seg_tokens[pc.S + 1] = full;
     *ws.arrived = 0;
   }
 }
@@ -336,49 +380,62 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_bwd_kernel(
   const double share = ns > 0 ? (double)E / ((double)ns * (double)K) : 0.0;
   const float zc = N > 0 ? (float)(2.0 * (double)z_coef / (double)N) : 0.f;
   const float gl = dloss ? *dloss : 1.f;
+  constexpr int U = kLossBatch;
   float w[C];
+  bool have_w = false;
+  for (int64_t rb = t.r0; rb < t.r1; rb += RP * U) {
+    float v[U][C], lse[U];
+    bool counted[U];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = rb + u * RP + g;
+      counted[u] = r < t.r1 && !outside && (!mask || mask[r] != 0);
+      lse[u] = 0.f;
+      if (counted[u]) {
+        load_row<G, NV, W>(logits + r * E, E, q, v[u]);
+        lse[u] = lse_in[r];
+      } else {
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      const int e = W * (i * G + q) + j;
-      w[i * W + j] = ns > 0 && e < E ? (float)(per * ((double)seg_counts[(int64_t)s * E + e] * share - 1.0)) : 0.f;
+        for (int c = 0; c < C; ++c) v[u][c] = -__builtin_huge_valf();
+      }
     }
-  for (int64_t rb = t.r0; rb < t.r1; rb += RP) {
-    const int64_t r = rb + g;
-    const bool in = r < t.r1;
-    const bool counted = in && !outside && (!mask || mask[r] != 0);
-    float v[C], lse = 0.f;
-    if (counted) {
-      load_row<G, NV, W>(logits + r * E, E, q, v);
-      lse = lse_in[r];
-    } else {
+    if (!have_w) {  // the segment's coefficients, behind the first rows' loads
+      have_w = true;
 #pragma unroll
-      for (int c = 0; c < C; ++c) v[c] = -__builtin_huge_valf();
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const int e = W * (i * G + q) + j;
+          w[i * W + j] = ns > 0 && e < E ? (float)(per * ((double)seg_counts[(int64_t)s * E + e] * share - 1.0)) : 0.f;
+        }
     }
     // lse keeps only the digits that its size leaves, up to log E is lost where the logits are huge,
     // so the probabilities are normalised again (the exponent stays within log E of the true one)
-    float d = 0.f, sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      v[c] = __expf(v[c] - lse);
-      sum += v[c];
-      d = fmaf(v[c], w[c], d);
-    }
-    sum = group_sum<G>(sum);
-    d = group_sum<G>(d);
-    if (!in) continue;
-    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
-    const float add = zc * lse - d * inv, scale = gl * inv;
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = rb + u * RP + g;
+      float d = 0.f, sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = W * (i * G + q);
-      if (e >= E) continue;
-      float o[W];
+      for (int c = 0; c < C; ++c) {
+        v[u][c] = __expf(v[u][c] - lse[u]);
+        sum += v[u][c];
+        d = fmaf(v[u][c], w[c], d);
+      }
+      sum = group_sum<G>(sum);
+      d = group_sum<G>(d);
+      if (r >= t.r1) continue;
+      const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+      const float add = zc * lse[u] - d * inv, scale = gl * inv;
 #pragma unroll
-      for (int j = 0; j < W; ++j) o[j] = counted ? scale * v[i * W + j] * (w[i * W + j] + add) : 0.f;
-      if constexpr (W == 4) *(float4*)(dlogits + r * E + e) = make_float4(o[0], o[1], o[2], o[3]);
-      else dlogits[r * E + e] = o[0];
+      for (int i = 0; i < NV; ++i) {
+        const int e = W * (i * G + q);
+        if (e >= E) continue;
+        float o[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[j] = counted[u] ? scale * v[u][i * W + j] * (w[i * W + j] + add) : 0.f;
+        if constexpr (W == 4) *(float4*)(dlogits + r * E + e) = make_float4(o[0], o[1], o[2], o[3]);
+        else dlogits[r * E + e] = o[0];
+      }
     }
   }
 }
