@@ -55,6 +55,19 @@ bool one_byte(const moe_desc* d) { return d->dtype == MOE_FP8_E4M3 || d->dtype =
 constexpr int kI8MaxK = 131008;  // 128 * 128 * K <= 2^31 - 1, K a multiple of 64
 constexpr int64_t kRsrcMax = 0x7fffffff;  // bytes one raw buffer descriptor addresses
 
+// Whether an 8-bit integer product of `groups` groups with `rows` rows each on average and N columns goes
+// to the few-rows kernels. They stream the weights whatever the rows are, but load the rows again for every
+// column slice; the GEMM's time is that of a 256 x 256 tile's K loop times its rounds over the CUs.
+// Measured (few-rows / GEMM, us): 128 groups of K = 2048 and 768, 2 rows 126 / 168, 16 rows 182 / 183, 32
+// rows 236 / 194; 16 groups, 4 rows 29 / 44, 32 rows 43 / 46, 64 rows 65 / 47; one group of K = 2048, N =
+// 2048, 16 rows 9 / 21, 256 rows 25 / 33, 512 rows 44 / 33; N = 7168, 77 rows 14 / 23, 256 rows 29 / 33, 512
+// rows 52 / 34; K = 7168, N = 4096, 128 rows 39 / 66, 512 rows 127 / 92.
+bool few_rows(int64_t groups, int64_t rows, int64_t N) {
+  if (rows <= 16) return true;
+  const int64_t tiles = groups * cdiv(N, 256) * cdiv(rows, 256);
+  return rows <= 320 && rows * groups * N <= 1000000 * cdiv(tiles, 256);
+}
+
 moe_status validate(const moe_desc* d) {
   if (!d) return fail(MOE_ERR_ARG, "descriptor is NULL");
   if (d->flags & ~(MOE_FLAG_FP8_DGRAD | MOE_FLAG_FP8_WGRAD | MOE_FLAG_FP8_DXD | MOE_FLAG_ROUTER_LOSS))
@@ -368,6 +381,15 @@ moe_status moe_expert_ffn(const moe_desc* d, int chunk, const void* xd, const fl
   }
   if (d->dtype == MOE_INT8) {
     MOE_NEED(xd_scale); MOE_NEED(w1_scale); MOE_NEED(w2_scale); MOE_NEED(h_scale);
+    const int64_t slots = min_pc(d) * r.nc;  // the rows that routing can make, whatever P_c is
+    const int64_t usual = cdiv(tokens_per_chunk(d) * d->k, d->E);
+    if (few_rows(d->E_local, usual, 2 * (int64_t)d->I)) {
+      MOE_HIP(moe::launch_expert_fwd_i8_few(xd, xd_scale, w1, w1_scale, w2, w2_scale, offsets, h, yd, d->H, d->I,
+                                            d->E_local, r.c0, r.nc, d->P_c, rows_of(d), slots, usual,
+                                            (hipStream_t)stream),
+              "expert_ffn_i8");
+      return MOE_OK;
+    }
     MOE_HIP(moe::launch_expert_fwd_i8(xd, xd_scale, w1, w1_scale, w2, w2_scale, offsets, h, h_scale, yd, d->H, d->I,
                                       d->E_local, r.c0, r.nc, d->P_c, rows_of(d), (hipStream_t)stream),
             "expert_ffn_i8");
@@ -615,7 +637,9 @@ moe_status moe_expert_matmul_i8(int32_t groups, int64_t rows, int32_t N, int32_t
   MOE_NEED(x); MOE_NEED(x_scale); MOE_NEED(w); MOE_NEED(w_scale); MOE_NEED(y);
   if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)y) & 15)
     return fail(MOE_ERR_ARG, "%s: x, w and y must be 16-byte aligned", __func__);
-  MOE_HIP(moe::launch_expert_matmul_i8(groups, rows, N, K, x, x_scale, w, w_scale, offsets, y, (hipStream_t)stream),
+  const bool few = few_rows(groups, cdiv(rows, groups), N);
+  MOE_HIP((few ? moe::launch_expert_matmul_i8_few : moe::launch_expert_matmul_i8)(groups, rows, N, K, x, x_scale, w,
+                                                                                  w_scale, offsets, y, (hipStream_t)stream),
           "expert_matmul_i8");
   return MOE_OK;
 }

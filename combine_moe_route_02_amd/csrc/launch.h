@@ -92,6 +92,15 @@ hipError_t launch_expert_fwd_i8(const void* xd, const float* xd_scale, const voi
 hipError_t launch_expert_matmul_i8(int groups, int64_t rows, int N, int K, const void* x, const float* x_scale,
                                    const void* w, const float* w_scale, const int32_t* offsets, void* y,
                                    hipStream_t s);
+// the same products for a few rows per group (few_rows_i8.hip); rows: a bound of the rows of all groups,
+// usual: one group's on average
+hipError_t launch_expert_fwd_i8_few(const void* xd, const float* xd_scale, const void* w1, const float* w1_scale,
+                                    const void* w2, const float* w2_scale, const int32_t* offsets, void* h,
+                                    void* yd, int H, int I, int El, int c0, int nc, int64_t P_c, int64_t P,
+                                    int64_t rows, int64_t usual, hipStream_t s);
+hipError_t launch_expert_matmul_i8_few(int groups, int64_t rows, int N, int K, const void* x, const float* x_scale,
+                                       const void* w, const float* w_scale, const int32_t* offsets, void* y,
+                                       hipStream_t s);
 // per-row e4m3 quantisation of the BF16 rows [c*P_c, c*P_c + N_c) of chunks c0..c0+nc-1
 hipError_t launch_quantize_segments_fp8(const char* name, const void* src, void* codes, float* scale,
                                         const int32_t* offsets, int El, int c0, int nc, int64_t P_c,

@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "common.h"
+#include "i8.h"
 #include "launch.h"
 #include "trace.h"
 
@@ -34,28 +35,6 @@ MOE_DEV uint32_t wave_max_u32(uint32_t v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, kWave));
   return v;
-}
-
-struct RowScale { float inv, scale; };
-MOE_DEV RowScale row_scale(uint32_t magnitude) {
-  if (magnitude >= 0x7f800000u) return {0.f, __uint_as_float(0x7fc00000u)};
-  if (magnitude == 0) return {0.f, 1.0f};
-  const float amax = __uint_as_float(magnitude);
-  // below 127 / FLT_MAX the multiplier overflows: such a row is a row of zeros
-  const float inv = 127.0f / amax;
-  return inv <= 3.402823466e38f ? RowScale{inv, amax / 127.0f} : RowScale{0.f, 1.0f};
-}
-
-// inv == 0: codes 0, whatever the values are
-MOE_DEV uint32_t codes4(float a, float b, float c, float d, float inv) {
-  if (inv == 0.f) return 0;
-  const int i = (int)rintf(a * inv), j = (int)rintf(b * inv), k = (int)rintf(c * inv), l = (int)rintf(d * inv);
-  auto cl = [](int v) { return (uint32_t)(max(-127, min(127, v)) & 0xff); };
-  return cl(i) | (cl(j) << 8) | (cl(k) << 16) | (cl(l) << 24);
-}
-MOE_DEV uint2 codes8(const u32x4& v, float inv) {
-  return make_uint2(codes4(bf2f(v.x & 0xffff), bf2f(v.x >> 16), bf2f(v.y & 0xffff), bf2f(v.y >> 16), inv),
-                    codes4(bf2f(v.z & 0xffff), bf2f(v.z >> 16), bf2f(v.w & 0xffff), bf2f(v.w >> 16), inv));
 }
 
 // One wave: the row's scale, its codes handed out vector by vector. NV > 0: the row stays in
@@ -98,23 +77,57 @@ __global__ __launch_bounds__(256) void quantize_rows_i8_kernel(const u32x4* __re
   if (lane == 0) scale[r] = q.scale;
 }
 
-// Dispatch: x[t] quantised once and stored to every local slot's row.
-template <int NV>
-__global__ __launch_bounds__(256) void dispatch_i8_kernel(const u32x4* __restrict__ x, const int32_t* __restrict__ row_of,
-                                                          uint2* __restrict__ xd, float* __restrict__ xd_scale, int64_t t0,
-                                                          int64_t t1, int K, int64_t nvec) {
+// Dispatch: x[t] quantised once and stored to every local slot's row, one block per token (many short
+// blocks keep more loads in flight than a wave per row: 21 -> 16 us at 16K tokens of 2048). Thread i
+// holds vectors i, i + 256, ...; NV = 0: read twice. kSkip: a token without a local slot is not read; the
+// check waits for its slots, so a few tokens (bound by latency) load without it.
+constexpr int kDispThreads = 256;
+template <int NV, bool kSkip>
+__global__ __launch_bounds__(kDispThreads) void dispatch_i8_kernel(const u32x4* __restrict__ x, const int32_t* __restrict__ row_of,
+                                                                   uint2* __restrict__ xd, float* __restrict__ xd_scale,
+                                                                   int64_t t0, int K, int64_t nvec) {
+  __shared__ uint32_t part[kDispThreads / 64];
   const int lane = threadIdx.x & 63;
-  const int64_t t = t0 + (int64_t)blockIdx.x * kI8RowsPerBlock + (threadIdx.x >> 6);
-  if (t >= t1) return;
+  const int64_t t = t0 + blockIdx.x;
   const int32_t myrow = lane < K ? row_of[t * K + lane] : -1;
-  if (__ballot(myrow >= 0) == 0) return;
-  const RowScale q = quantize_row<NV>(x + t * nvec, nvec, lane, [&](int64_t i, uint2 c) {
+  if (kSkip && __ballot(myrow >= 0) == 0) return;
+  const u32x4* src = x + t * nvec;
+  u32x4 v[NV > 0 ? NV : 1];
+  uint32_t m = 0;
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int b = 0; b < NV; ++b) {
+      const int64_t i = threadIdx.x + b * kDispThreads;
+      v[b] = i < nvec ? src[i] : u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int b = 0; b < NV; ++b) m = max(m, magnitude8(v[b]));
+  } else {
+    for (int64_t i = threadIdx.x; i < nvec; i += kDispThreads) m = max(m, magnitude8(src[i]));
+  }
+  m = wave_max_u32(m);
+  if (lane == 0) part[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = part[0];
+#pragma unroll
+  for (int w = 1; w < kDispThreads / 64; ++w) m = max(m, part[w]);
+  const RowScale q = row_scale(m);
+  auto store = [&](int64_t i, uint2 c) {
     for (int j = 0; j < K; ++j) {
       const int32_t r = __builtin_amdgcn_readlane(myrow, j);
       if (r >= 0) xd[(int64_t)r * nvec + i] = c;
     }
-  });
-  if (myrow >= 0) xd_scale[myrow] = q.scale;
+  };
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int b = 0; b < NV; ++b) {
+      const int64_t i = threadIdx.x + b * kDispThreads;
+      if (i < nvec) store(i, codes8(v[b], q.inv));
+    }
+  } else {
+    for (int64_t i = threadIdx.x; i < nvec; i += kDispThreads) store(i, codes8(src[i], q.inv));
+  }
+  if (threadIdx.x < 64 && myrow >= 0) xd_scale[myrow] = q.scale;
 }
 
 // The FP32 rows of h of each chunk (the row count is on the device): 4 values a vector.
@@ -189,8 +202,13 @@ hipError_t launch_dispatch_i8(const void* x, const int32_t* row_of, void* xd, fl
   const int64_t nvec = H / 8;
   {
     MOE_TRACE("dispatch_i8", s);
-    MOE_I8_NV(nvec, MOE_LAUNCH(dispatch_i8_kernel<NV>, row_grid(t1 - t0), dim3(256), 0, s, (const u32x4*)x, row_of,
-                               (uint2*)xd, xd_scale, t0, t1, K, nvec));
+    const bool skip = t1 - t0 > 1024;
+    auto k = skip ? dispatch_i8_kernel<0, true> : dispatch_i8_kernel<0, false>;
+    if (nvec <= kDispThreads) k = skip ? dispatch_i8_kernel<1, true> : dispatch_i8_kernel<1, false>;
+    else if (nvec <= 2 * kDispThreads) k = skip ? dispatch_i8_kernel<2, true> : dispatch_i8_kernel<2, false>;
+    else if (nvec <= 4 * kDispThreads) k = skip ? dispatch_i8_kernel<4, true> : dispatch_i8_kernel<4, false>;
+    MOE_LAUNCH(k, dim3((unsigned)(t1 - t0)), dim3(kDispThreads), 0, s, (const u32x4*)x, row_of, (uint2*)xd, xd_scale, t0, K,
+               nvec);
   }
   return hipGetLastError();
 }

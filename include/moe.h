@@ -177,7 +177,9 @@ moe_status moe_dispatch(const moe_desc* d, int chunk, const void* x, const int32
  * the codes half of the h buffer with its scale in h_scale, and the down projection reads the
  * codes. gu is unused for FP8. INT8: both products are exact int32 sums of 8-bit codes, dequantised by
  * s_row*s_col in FP32; h is written in FP32 at the start of the h buffer and quantised per row as
- * moe_quantize_rows_i8 does (codes after the FP32 values, scale in h_scale); gu is unused. */
+ * moe_quantize_rows_i8 does; gu is unused. h and h_scale are scratch then: with few tokens per expert
+ * the call streams the weights in kernels that keep neither codes nor scale (yd is bit for bit the
+ * same). */
 moe_status moe_expert_ffn(const moe_desc* d, int chunk, const void* xd, const float* xd_scale,
                           const void* w1, const float* w1_scale, const void* w2,
                           const float* w2_scale, const int32_t* offsets, void* gu, void* h,
