@@ -52,6 +52,7 @@ int64_t min_pc(const moe_desc* d) {
 }
 int elem_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }  // payload rows (FP8, INT8: BF16 x/yd)
 bool one_byte(const moe_desc* d) { return d->dtype == MOE_FP8_E4M3 || d->dtype == MOE_INT8; }  // forward only
+constexpr int kI8MaxN = 1 << 21;  // 256 rows of BF16 outputs within 2^30 bytes (one tile's buffer descriptor)
 constexpr int kI8MaxK = 131008;  // 128 * 128 * K <= 2^31 - 1, K a multiple of 64
 constexpr int64_t kRsrcMax = 0x7fffffff;  // bytes one raw buffer descriptor addresses
 
@@ -626,7 +627,8 @@ moe_status moe_expert_matmul_i8(int32_t groups, int64_t rows, int32_t N, int32_t
   if (groups < 0 || rows < 0) return fail(MOE_ERR_ARG, "%s: negative groups or rows", __func__);
   if (groups > 1024) return fail(MOE_ERR_UNSUPPORTED, "%s: groups = %d above 1024", __func__, groups);
   if (rows > INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: row indices exceed int32", __func__);
-  if (N <= 0 || N % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: N = %d must be a positive multiple of 8", __func__, N);
+  if (N <= 0 || N % 8 || N > kI8MaxN)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: N = %d must be a positive multiple of 8, at most %d", __func__, N, kI8MaxN);
   if (K <= 0 || K % 64 || K > kI8MaxK)
     return fail(MOE_ERR_UNSUPPORTED, "%s: K = %d must be a positive multiple of 64, at most %d", __func__, K, kI8MaxK);
   if ((int64_t)N * K > kRsrcMax)

@@ -1,5 +1,5 @@
 // Shared engine of the grouped expert GEMMs on CDNA4 matrix cores (BF16 and FP8 e4m3 MFMA with
-// FP32 accumulation, 8-bit integer MFMA with int32 accumulation): LDS operand ring, fragments, K loop, output staging, the row-grouped
+// FP32 accumulation): LDS operand ring, fragments, K loop, output staging, the row-grouped
 // GEMM's tile walk, and the host-side launch helpers.
 //
 // Engine (one 512-thread workgroup = 8 waves in a 2 x 4 grid over a BM x BN output tile, two
@@ -44,7 +44,7 @@ constexpr int kRowB = 64;           // K bytes per MN row per stage
 constexpr int kKRows = 32;          // K rows per stage for 16-bit K-slow operands
 constexpr int kMaxGroups = 1024;
 
-// Operand element of a GEMM (the template arguments named DT): BF16, FP8 e4m3 or 8-bit integers.
+// Operand element of a stage's products (stage_mma): BF16, FP8 e4m3 or 8-bit integers (int32 sums).
 enum Elem { kElBF16 = 0, kElFP8 = 1, kElI8 = 2 };
 typedef __attribute__((ext_vector_type(16))) int i32x16_t;
 // accumulator of one 32 x 32 block
@@ -212,7 +212,7 @@ MOE_DEV i32x8_t frag_km8_2(const char* st, int mb, int lane) {
 }
 
 // One 32 x 32 x (32 bytes of K) product of 16-byte fragments. 8-bit integers sit in a stage row like
-// BF16 values (two steps of two 16-byte halves), with twice the values and exact int32 sums.
+// BF16 values (two steps of two 16-byte halves), with twice the values.
 template <int DT>
 MOE_DEV acc_t<DT> mma16(bf16x8_t b, bf16x8_t a, acc_t<DT> c) {
   if constexpr (DT == kElI8)
@@ -314,9 +314,9 @@ MOE_DEV void stage_mma(const char* sa, const char* sb, int arow0, int brow0, int
 // s + kNst - 1; past the last stage they fetch masked (zero) or unused data into a ring slot that
 // is never read again, so every iteration waits with the same count. On return all loads have
 // completed and every wave has passed a barrier after its last LDS read, so the ring is free.
-template <int DT, bool AKS, bool BKS, int RA, int RB, int TM, int TN, int TMA, class LA, class LB>
+template <bool FP8, bool AKS, bool BKS, int RA, int RB, int TM, int TN, int TMA, class LA, class LB>
 MOE_DEV void kloop(const LA& la, const LB& lb, char* ring, int nks, int arow0, int brow0, int lane,
-                   acc_t<DT> (&acc)[TM][TN]) {
+                   f32x16_t (&acc)[TM][TN]) {
   constexpr int SA = RA * kRowB, SS = (RA + RB) * kRowB;
   constexpr int NL = LA::NI + LB::NI;  // load instructions per wave per stage
   constexpr bool kAsm = AKS || BKS;    // transposing reads follow: loads written in assembly
@@ -338,7 +338,7 @@ MOE_DEV void kloop(const LA& la, const LB& lb, char* ring, int nks, int arow0, i
     const uint32_t st = rl + (ld % kNst) * SS;
     const char* cur = ring + (s % kNst) * SS;
     if constexpr (kAll) {
-      stage_mma<DT, AKS, BKS, RA, RB, TM, TN, TMA, NL>(cur, cur + SA, arow0, brow0, lane, acc, [&] {
+      stage_mma<FP8, AKS, BKS, RA, RB, TM, TN, TMA, NL>(cur, cur + SA, arow0, brow0, lane, acc, [&] {
         la.template issue<kAsm>(st, ld);
         lb.template issue<kAsm>(st + SA, ld);
       });
@@ -349,22 +349,22 @@ MOE_DEV void kloop(const LA& la, const LB& lb, char* ring, int nks, int arow0, i
         la.template issue<kAsm>(st, ld);
         lb.template issue<kAsm>(st + SA, ld);
       }
-      stage_mma<DT, AKS, BKS, RA, RB, TM, TN, TMA, 0>(cur, cur + SA, arow0, brow0, lane, acc, [] {});
+      stage_mma<FP8, AKS, BKS, RA, RB, TM, TN, TMA, 0>(cur, cur + SA, arow0, brow0, lane, acc, [] {});
     }
   }
   wait_vm<0>();
   __syncthreads();
 }
 
-// K loop for two K-major operands over pair slots: the LDS ring holds two slots of
+// K loop for two K-major operands (BF16 or FP8) over pair slots: the LDS ring holds two slots of
 // two stages each (rows of 128 bytes), and each load brings a whole 128-byte line per row, half the
 // load requests per byte of 64-byte stage rows (the loads' issue limits the 64-byte K loop when
 // every CU runs one). Pair p+1's loads go out during the first half of pair p, into the other
 // slot, which every wave finished reading before pair p's barrier; pair p+1 then waits for all of
 // them. Past the last pair they fetch masked or unused data into the slot no one reads again.
-template <int DT, int RA, int RB, int TM, int TN, int TMA, class LA, class LB>
+template <bool FP8, int RA, int RB, int TM, int TN, int TMA, class LA, class LB>
 MOE_DEV void kloop_pairs(const LA& la, const LB& lb, char* ring, int nks, int arow0, int brow0, int lane,
-                         acc_t<DT> (&acc)[TM][TN]) {
+                         f32x16_t (&acc)[TM][TN]) {
   constexpr int SA = RA * 2 * kRowB, SS = (RA + RB) * 2 * kRowB;
   constexpr int NL = LA::NI + LB::NI;  // load instructions per wave per pair
   const uint32_t rl = lds_addr(ring);
@@ -377,11 +377,11 @@ MOE_DEV void kloop_pairs(const LA& la, const LB& lb, char* ring, int nks, int ar
     const int ld = p + 1;
     const uint32_t st = rl + (ld & 1) * SS;
     const char* cur = ring + (p & 1) * SS;
-    stage_mma<DT, false, false, RA, RB, TM, TN, TMA, NL, 0>(cur, cur + SA, arow0, brow0, lane, acc, [&] {
+    stage_mma<FP8, false, false, RA, RB, TM, TN, TMA, NL, 0>(cur, cur + SA, arow0, brow0, lane, acc, [&] {
       la.template issue<false>(st, ld);
       lb.template issue<false>(st + SA, ld);
     });
-    if (2 * p + 1 < nks) stage_mma<DT, false, false, RA, RB, TM, TN, TMA, 0, 1>(cur, cur + SA, arow0, brow0, lane, acc, [] {});
+    if (2 * p + 1 < nks) stage_mma<FP8, false, false, RA, RB, TM, TN, TMA, 0, 1>(cur, cur + SA, arow0, brow0, lane, acc, [] {});
   }
   wait_vm<0>();
   __syncthreads();
@@ -509,16 +509,16 @@ MOE_DEV void store_staged_q(const char* lds, uint8_t* dst, int64_t ld, float* sc
 enum Mode { kGateUp = 0, kDown = 1, kDownBwd = 2, kGateUpBwd = 3 };
 
 struct RowsArgs {
-  const void* A;          // [P, K] dispatch-ordered rows (BF16, or e4m3 / 8-bit integer codes)
+  const void* A;          // [P, K] dispatch-ordered rows (BF16, or e4m3 codes)
   const void* B;          // expert weights, strideB elements per expert
-  uint16_t* C;            // [P, ldc] BF16 output rows (8-bit integer kGateUp: h as FP32 rows)
+  uint16_t* C;            // [P, ldc] BF16 output rows
   uint16_t* C2;           // kGateUp: G/U save [P, 2I] (nullable)
   const uint16_t* aux;    // kDownBwd: G/U [P, 2I]
-  const float* scale_a;   // FP8, 8-bit integers: per dispatch row
-  const float* scale_b;   // FP8, 8-bit integers: per weight row, strideSB per expert
+  const float* scale_a;   // FP8: per dispatch row
+  const float* scale_b;   // FP8: per weight row, strideSB per expert
   int64_t lda, ldc, strideB, strideSB;
   int K, N, I;
-  const int32_t* offsets;  // 8-bit integer kDown: null for one group of P_c rows
+  const int32_t* offsets;
   int El, c0, nc;
   int64_t P_c;
   // QOUT launches (block-scaled FP8 output instead of C): e4m3 codes [P, ldc] and one FP32 scale
@@ -571,20 +571,17 @@ MOE_DEV int first_slot(int first) {
 
 // The tiles of one row-grouped GEMM from per-XCD slot `first` on; returns the slot after its
 // last. Every thread of the workgroup calls it (it contains barriers).
-template <int BM, int BN, int MODE, int DT, bool QOUT = false, bool GATHER = false>
+template <int BM, int BN, int MODE, bool FP8, bool QOUT = false, bool GATHER = false>
 MOE_DEV int rows_list(const RowsArgs& a, int first, RowsShared& sh, char* ring) {
   constexpr int WTM = BM / kWM, WTN = BN / kWN, TM = WTM / 32, TN = WTN / 32;
   constexpr bool kSwiGLU = (MODE == kGateUp);
-  constexpr bool FP8 = DT == kElFP8, I8 = DT == kElI8;
-  constexpr bool kScaled = FP8 || I8;  // one-byte operands with a scale per row of each
-  static_assert(!I8 || MODE == kGateUp || MODE == kDown, "8-bit integers: forward");
   // BF16 input gradients read W_e as stored (K-slow); FP8 ones read a transposed copy (K-major)
-  constexpr bool kBKS = !kScaled && (MODE == kDownBwd || MODE == kGateUpBwd);
-  constexpr int ES = kScaled ? 1 : 2;  // element bytes
+  constexpr bool kBKS = !FP8 && (MODE == kDownBwd || MODE == kGateUpBwd);
+  constexpr int ES = FP8 ? 1 : 2;      // element bytes
   constexpr int OUTN = kSwiGLU ? BN / 2 : BN;
   static_assert(!(FP8 && MODE == kGateUpBwd), "FP8 gate/up dgrad runs as kDown on the transposed W1");
   static_assert(!QOUT || ((MODE == kDown || MODE == kGateUpBwd) && BN == 256), "FP8 output: plain 256-wide tiles");
-  static_assert(!GATHER || (MODE == kGateUp && DT == kElBF16), "row gather: the BF16 gate/up GEMM");
+  static_assert(!GATHER || (MODE == kGateUp && !FP8), "row gather: the BF16 gate/up GEMM");
   int* s_pre = sh.pre;
   int64_t* s_r0 = sh.r0;
   int* s_len = sh.len;
@@ -601,22 +598,10 @@ MOE_DEV int rows_list(const RowsArgs& a, int first, RowsShared& sh, char* ring) 
   // MFMA). Large tiles are dealt first, so the small ones fill a second round where one is needed.
   for (int g = tid; g < G; g += kThreads) {
     const int c = a.c0 + g / a.El, e = g % a.El;
-    int o0, o1;
-    if (I8 && !a.offsets) {
-      o0 = 0;
-      o1 = (int)a.P_c;
-    } else {
-      const int32_t* off = a.offsets + (int64_t)c * (a.El + 1);
-      o0 = off[e];
-      o1 = off[e + 1];
-      if constexpr (I8) {  // the caller's table (moe_expert_matmul_i8): nothing outside its rows
-        o0 = max(0, min(o0, (int)a.P_c));
-        o1 = max(o0, min(o1, (int)a.P_c));
-      }
-    }
-    const int len = o1 - o0;
+    const int32_t* off = a.offsets + (int64_t)c * (a.El + 1);
+    const int len = off[e + 1] - off[e];
     const int rem = len % BM;
-    s_r0[g] = (int64_t)c * a.P_c + o0;
+    s_r0[g] = (int64_t)c * a.P_c + off[e];
     s_len[g] = len;
     s_pre[g + 1] = (len / BM + (rem > BM / 2 ? 1 : 0)) * ntiles;
     s_preb[g + 1] = (rem > 0 && rem <= BM / 2 ? 1 : 0) * ntiles;
@@ -673,7 +658,7 @@ MOE_DEV int rows_list(const RowsArgs& a, int first, RowsShared& sh, char* ring) 
       // whose short FP8 stages need the ring's three stages of loads ahead (pairs: 8% slower);
       // the BF16 input gradients take their K-major A operand in pairs as well
       constexpr bool kPair = !kBKS && !(FP8 && MODE == kGateUp);
-      constexpr bool kAPair = kBKS;
+      constexpr bool kAPair = !FP8 && kBKS;
       Loader<BM, false, kWaves, kPair || kAPair> la;
       if constexpr (GATHER) {
         // tile row r reads token row gather[r0 + r]; rows past the segment point one row past the
@@ -696,7 +681,7 @@ MOE_DEV int rows_list(const RowsArgs& a, int first, RowsShared& sh, char* ring) 
                          const int q = r % WTN, hw = WTN / 2, j = (r / WTN) * hw + (q < hw ? q : q - hw);
                          return q < hw ? j : I + j;
                        });
-      } else if constexpr (MODE == kDown || kScaled) {
+      } else if constexpr (MODE == kDown || FP8) {
         lb.init_kmajor(Be + (int64_t)n0 * a.K * ES, (int64_t)a.K * ES, ((int64_t)a.N - n0) * a.K * ES, wave, lane,
                        [](int r) { return r; });
       } else {
@@ -704,26 +689,26 @@ MOE_DEV int rows_list(const RowsArgs& a, int first, RowsShared& sh, char* ring) 
         lb.init_kslow(Be + (int64_t)n0 * 2, (int64_t)a.N * 2, ((int64_t)a.K * a.N - n0) * 2, wave, lane);
       }
 
-      acc_t<DT> acc[TM][TN];
+      f32x16_t acc[TM][TN];
 #pragma unroll
       for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
-          for (int q = 0; q < 16; ++q) acc[tm][tn][q] = 0;
+          for (int q = 0; q < 16; ++q) acc[tm][tn][q] = 0.f;
 
-      const int nks = a.K / (kScaled ? 64 : 32);
+      const int nks = a.K / (FP8 ? 64 : 32);
       const int tma = __builtin_amdgcn_readfirstlane(max(0, min(TM, (mvalid - wm * WTM + 31) / 32)));
       const int arow0 = wm * WTM, brow0 = wn * WTN;
       static_assert(TM <= 4, "TM > 4");
       switch (tma) {
 #define MOE_KL(T_)                                                                                        \
   if constexpr (kPair)                                                                                     \
-    kloop_pairs<DT, BM, BN, TM, TN, (T_ <= TM ? T_ : TM)>(la, lb, ring, nks, arow0, brow0, lane, acc);    \
+    kloop_pairs<FP8, BM, BN, TM, TN, (T_ <= TM ? T_ : TM)>(la, lb, ring, nks, arow0, brow0, lane, acc);    \
   else if constexpr (kAPair)                                                                               \
     kloop_apairs<BM, BN, TM, TN, (T_ <= TM ? T_ : TM)>(la, lb, ring, nks, arow0, brow0, lane, acc);        \
   else                                                                                                     \
-    kloop<DT, false, kBKS, BM, BN, TM, TN, (T_ <= TM ? T_ : TM)>(la, lb, ring, nks, arow0, brow0, lane, acc)
+    kloop<FP8, false, kBKS, BM, BN, TM, TN, (T_ <= TM ? T_ : TM)>(la, lb, ring, nks, arow0, brow0, lane, acc)
         case 4: MOE_KL(4); break;
         case 3: MOE_KL(3); break;
         case 2: MOE_KL(2); break;
@@ -744,34 +729,8 @@ MOE_DEV int rows_list(const RowsArgs& a, int first, RowsShared& sh, char* ring) 
         float sr[TM];
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm)
-          sr[tm] = (kScaled && mrow + tm * 32 < mvalid) ? a.scale_a[r0 + mrow + tm * 32] : 1.f;
-        const float* sb = kScaled ? a.scale_b + (int64_t)e * a.strideSB : nullptr;
-        if constexpr (I8) {
-          // h in FP32: it is quantised per row next, and a BF16 rounding before that would move
-          // codes by whole steps. G and U are not kept.
-          constexpr int WP = 2 * W;  // the staged tile and the rows in 16-bit units
-          static_assert(stage_bytes<BM, WP>() <= rows_lds_bytes<BM, BN, MODE>(), "FP32 staging tile");
-#pragma unroll
-          for (int tm = 0; tm < TM; ++tm)
-#pragma unroll
-            for (int tn = 0; tn < TN / 2; ++tn)
-#pragma unroll
-              for (int gq = 0; gq < 4; ++gq) {
-                const int jl = wn * (WTN / 2) + tn * 32 + out_col(gq, lane);
-                float hv[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const int j = min(n0 + jl + q, a.N - 1);
-                  const float gv = (float)acc[tm][tn][4 * gq + q] * (sr[tm] * sb[j]);
-                  const float uv = (float)acc[tm][tn + TN / 2][4 * gq + q] * (sr[tm] * sb[a.I + j]);
-                  hv[q] = gv * sigmoidf_(gv) * uv;
-                }
-                *(float4*)(sg + (mrow + tm * 32) * pitch<WP>() + 4 * jl) = make_float4(hv[0], hv[1], hv[2], hv[3]);
-              }
-          lds_barrier();
-          store_staged<BM, WP>(sg, a.C + (r0 * a.ldc + n0) * 2, 2 * a.ldc, mvalid, 2 * nvalid, tid);
-          lds_barrier();
-        } else {
+          sr[tm] = (FP8 && mrow + tm * 32 < mvalid) ? a.scale_a[r0 + mrow + tm * 32] : 1.f;
+        const float* sb = FP8 ? a.scale_b + (int64_t)e * a.strideSB : nullptr;
         // G and U (dequantised) into the two staging tiles
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm)
@@ -826,7 +785,6 @@ MOE_DEV int rows_list(const RowsArgs& a, int first, RowsShared& sh, char* ring) 
         lds_barrier();
         store_staged<BM, W>(sg, a.C + r0 * a.ldc + n0, a.ldc, mvalid, nvalid, tid);
         lds_barrier();
-        }
       } else if constexpr (MODE == kDownBwd) {
         // G and U of the tile's rows and columns, staged coalesced; dG and dU overwrite them in place
         constexpr int W = BN;
@@ -839,7 +797,7 @@ MOE_DEV int rows_list(const RowsArgs& a, int first, RowsShared& sh, char* ring) 
         float sr[TM];
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm)
-          sr[tm] = (kScaled && mrow + tm * 32 < mvalid) ? a.scale_a[r0 + mrow + tm * 32] : 1.f;
+          sr[tm] = (FP8 && mrow + tm * 32 < mvalid) ? a.scale_a[r0 + mrow + tm * 32] : 1.f;
         lds_barrier();
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm)
@@ -874,7 +832,7 @@ MOE_DEV int rows_list(const RowsArgs& a, int first, RowsShared& sh, char* ring) 
         float sr[TM];
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm)
-          sr[tm] = (kScaled && mrow + tm * 32 < mvalid) ? a.scale_a[r0 + mrow + tm * 32] : 1.f;
+          sr[tm] = (FP8 && mrow + tm * 32 < mvalid) ? a.scale_a[r0 + mrow + tm * 32] : 1.f;
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
@@ -885,8 +843,8 @@ MOE_DEV int rows_list(const RowsArgs& a, int first, RowsShared& sh, char* ring) 
               float v[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                v[q] = (float)acc[tm][tn][4 * gq + q];
-                if constexpr (kScaled) v[q] *= sr[tm] * a.scale_b[(int64_t)e * a.strideSB + min(n0 + nl + q, a.N - 1)];
+                v[q] = acc[tm][tn][4 * gq + q];
+                if constexpr (FP8) v[q] *= sr[tm] * a.scale_b[(int64_t)e * a.strideSB + min(n0 + nl + q, a.N - 1)];
               }
               *(uint2*)(ring + (mrow + tm * 32) * pitch<W>() + 2 * nl) = pack4(v[0], v[1], v[2], v[3]);
             }

@@ -20,11 +20,11 @@
 namespace moe {
 namespace gg {
 
-template <int BM, int BN, int MODE, int DT, bool QOUT, bool GATHER>
+template <int BM, int BN, int MODE, bool FP8, bool QOUT, bool GATHER>
 __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a) {
   __shared__ RowsShared sh;
   extern __shared__ __attribute__((aligned(1024))) char ring[];
-  rows_list<BM, BN, MODE, DT, QOUT, GATHER>(a, 0, sh, ring);
+  rows_list<BM, BN, MODE, FP8, QOUT, GATHER>(a, 0, sh, ring);
 }
 
 // Two independent row-grouped GEMMs in one persistent launch: the second's tiles fill the
@@ -135,14 +135,14 @@ __global__ __launch_bounds__(kThreads) void wgrad_fp8_kernel(WgradFp8Args a, Wgr
 // Grid bound: per chunk at most floor(P_c / BM) + E_local row tiles (every expert adds at most
 // one partial tile) times the column tiles; the device-side count decides the work.
 // QOUT: a.Cq set (block-scaled FP8 output, plain-store modes only).
-template <int BM, int BN, int MODE, int DT>
+template <int BM, int BN, int MODE, bool FP8>
 hipError_t run_rows(const char* name, const RowsArgs& a, hipStream_t s) {
   const size_t lds = rows_lds_bytes<BM, BN, MODE>();
-  constexpr bool kQ = (MODE == kDown || MODE == kGateUpBwd) && BN == 256 && DT != kElI8;
-  constexpr bool kG = MODE == kGateUp && DT == kElBF16;
-  auto k = (kQ && a.Cq)       ? rows_kernel<BM, BN, MODE, DT, kQ, false>
-           : (kG && a.gather) ? rows_kernel<BM, BN, MODE, DT, false, kG>
-                              : rows_kernel<BM, BN, MODE, DT, false, false>;
+  constexpr bool kQ = (MODE == kDown || MODE == kGateUpBwd) && BN == 256;
+  constexpr bool kG = MODE == kGateUp && !FP8;
+  auto k = (kQ && a.Cq)       ? rows_kernel<BM, BN, MODE, FP8, kQ, false>
+           : (kG && a.gather) ? rows_kernel<BM, BN, MODE, FP8, false, kG>
+                              : rows_kernel<BM, BN, MODE, FP8, false, false>;
   hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
   const int outn = (MODE == kGateUp) ? BN / 2 : BN;
@@ -276,45 +276,6 @@ hipError_t launch_expert_fwd_fp8(const void* xd, const float* xd_scale, const vo
   b.lda = I; b.ldc = H; b.strideB = (int64_t)H * I; b.K = I; b.N = H; b.I = I;
   b.offsets = offsets; b.El = El; b.c0 = c0; b.nc = nc; b.P_c = P_c;
   return run_rows<256, 256, kDown, true>("gemm_down_fp8", b, s);
-}
-
-// 8-bit integer forward: gate/up with exact int32 sums, dequantised by s_row * s_col, SwiGLU -> h
-// (FP32 rows at the start of the h buffer); h quantised per row (codes after the FP32 values); down
-// -> yd (BF16).
-hipError_t launch_expert_fwd_i8(const void* xd, const float* xd_scale, const void* w1, const float* w1_scale,
-                                const void* w2, const float* w2_scale, const int32_t* offsets, void* h,
-                                float* h_scale, void* yd, int H, int I, int El, int c0, int nc, int64_t P_c,
-                                int64_t P, hipStream_t s) {
-  if (nc <= 0 || El <= 0) return hipSuccess;
-  int8_t* hq = (int8_t*)h + P * (int64_t)I * 4;
-  RowsArgs a{};
-  a.A = xd; a.B = w1; a.C = (uint16_t*)h;
-  a.scale_a = xd_scale; a.scale_b = w1_scale; a.strideSB = 2 * (int64_t)I;
-  a.lda = H; a.ldc = I; a.strideB = (int64_t)2 * I * H; a.K = H; a.N = I; a.I = I;
-  a.offsets = offsets; a.El = El; a.c0 = c0; a.nc = nc; a.P_c = P_c;
-  hipError_t e = run_rows<256, 256, kGateUp, kElI8>("gemm_gateup_swiglu_i8", a, s);
-  if (e != hipSuccess) return e;
-  e = launch_quantize_h_i8((const float*)h, hq, h_scale, offsets, El, c0, nc, P_c, I, s);
-  if (e != hipSuccess) return e;
-  RowsArgs b{};
-  b.A = hq; b.B = w2; b.C = (uint16_t*)yd;
-  b.scale_a = h_scale; b.scale_b = w2_scale; b.strideSB = H;
-  b.lda = I; b.ldc = H; b.strideB = (int64_t)H * I; b.K = I; b.N = H; b.I = I;
-  b.offsets = offsets; b.El = El; b.c0 = c0; b.nc = nc; b.P_c = P_c;
-  return run_rows<256, 256, kDown, kElI8>("gemm_down_i8", b, s);
-}
-
-// y = dequantised x w^T for the rows of each group (moe_expert_matmul_i8).
-hipError_t launch_expert_matmul_i8(int groups, int64_t rows, int N, int K, const void* x, const float* x_scale,
-                                   const void* w, const float* w_scale, const int32_t* offsets, void* y,
-                                   hipStream_t s) {
-  if (groups <= 0 || rows <= 0) return hipSuccess;
-  RowsArgs b{};
-  b.A = x; b.B = w; b.C = (uint16_t*)y;
-  b.scale_a = x_scale; b.scale_b = w_scale; b.strideSB = N;
-  b.lda = K; b.ldc = N; b.strideB = (int64_t)N * K; b.K = K; b.N = N;
-  b.offsets = offsets; b.El = groups; b.c0 = 0; b.nc = 1; b.P_c = rows;
-  return run_rows<256, 256, kDown, kElI8>("gemm_matmul_i8", b, s);
 }
 
 // The weight gradients' FP8 operands that do not wait for the input gradients: dyd, h and xd.

@@ -15,12 +15,20 @@ MOE_DEV RowScale row_scale(uint32_t magnitude) {
   return inv <= 3.402823466e38f ? RowScale{inv, amax / 127.0f} : RowScale{0.f, 1.0f};
 }
 
-// inv == 0: codes 0, whatever the values are
+// Codes of four values. Each product is rounded to FP32 and then to the nearest integer, halves to even, by
+// adding 1.5 * 2^23: the sum's last bits are the integer in two's complement, so three byte permutes
+// pack four codes (rounding, converting, clamping and shifting each value takes three times the
+// instructions). |v| <= amax keeps the rounded product within 127. The two steps must not be fused: a
+// product that FP32 rounds onto a half belongs to the even code. inv == 0: codes 0, whatever the values
+// are.
 MOE_DEV uint32_t codes4(float a, float b, float c, float d, float inv) {
-  if (inv == 0.f) return 0;
-  const int i = (int)rintf(a * inv), j = (int)rintf(b * inv), k = (int)rintf(c * inv), l = (int)rintf(d * inv);
-  auto cl = [](int v) { return (uint32_t)(max(-127, min(127, v)) & 0xff); };
-  return cl(i) | (cl(j) << 8) | (cl(k) << 16) | (cl(l) << 24);
+#pragma clang fp contract(off)
+  constexpr float kShift = 12582912.0f;
+  const float p = a * inv, q = b * inv, r = c * inv, s = d * inv;
+  const uint32_t i = __float_as_uint(p + kShift), j = __float_as_uint(q + kShift);
+  const uint32_t k = __float_as_uint(r + kShift), l = __float_as_uint(s + kShift);
+  const uint32_t lo = __builtin_amdgcn_perm(j, i, 0x0c0c0400), hi = __builtin_amdgcn_perm(l, k, 0x04000c0c);
+  return inv == 0.f ? 0u : lo | hi;
 }
 MOE_DEV uint2 codes8(const u32x4& v, float inv) {
   return make_uint2(codes4(bf2f(v.x & 0xffff), bf2f(v.x >> 16), bf2f(v.y & 0xffff), bf2f(v.y >> 16), inv),

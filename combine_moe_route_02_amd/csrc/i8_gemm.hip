@@ -1,0 +1,340 @@
+// Grouped GEMMs of the 8-bit integer experts: v_mfma_i32_32x32x32_i8 on the shared engine's tiles (256 x 256,
+// 8 waves of 128 x 64, operands by direct-to-LDS loads into two slots of 128-byte rows).
+//
+// Integer products take half the time of BF16 ones, so what surrounds a tile's K loop weighs double: run
+// as the other GEMMs, a tile spent 16 us outside its K loop against 0.6 us per 64 bytes of K (first
+// loads, sums through LDS into rows, a barrier on each side, stores), more than half of the down
+// projection's 23 us. Here the list of tiles is one stream instead:
+//   * during a tile's last pair of stages its workgroup already loads the next tile's first pair, into
+//     the slot that pair would have had;
+//   * the sums go from registers to HBM without LDS: swapping lane halves gives every lane 8 columns of a
+//     row (16 bytes), so neither ring slot nor barrier is needed. Each wave issues exactly kStores buffer
+//     stores per tile, rows and columns outside it dropped by the descriptor's extent, and the
+//     next tile waits for its loads with those stores still in flight.
+// The sums are exact in int32 and rounded once to FP32; scales multiply in FP32 and BF16 rounds once.
+#include <type_traits>
+
+#include "gg_engine.h"
+
+namespace moe {
+namespace gg {
+namespace {
+
+constexpr int kTile = 256;
+constexpr int kSlotA = kTile * 2 * kRowB, kSlot = 2 * kSlotA;  // pair slot: rows of A, then of B
+constexpr int kRing = 2 * kSlot;
+constexpr int kStores = 16;  // buffer stores of a wave per tile
+constexpr int kMN = 4, kNN = 2;  // 32 x 32 blocks of a wave
+constexpr int kOutside = 0x7ffffff0;  // past every output descriptor's extent (at most 2^30 bytes)
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
+
+struct I8Args {
+  const int8_t* A;         // [P, K]
+  const float* scale_a;    // [P]
+  const int8_t* B;         // per expert [N, K], gate/up [2 N, K]
+  const float* scale_b;    // per expert [N], [2 N]
+  void* C;                 // gate/up: h [P, N] FP32; else [P, N] BF16
+  int K, N;
+  const int32_t* offsets;  // null: one group of P_c rows
+  int El, c0, nc;
+  int64_t P_c;
+};
+
+struct Groups {
+  int pre[kMaxGroups + 1], preb[kMaxGroups + 1];  // tiles before group g: large, small
+  int64_t r0[kMaxGroups];
+  int len[kMaxGroups];
+  float scale[2 * kTile];
+};
+static_assert(kThreads == 2 * kTile, "one scale per thread");
+
+struct I8Tile {
+  const char* a;  // first byte of its rows, and their extent
+  const char* b;
+  int64_t abytes, bbytes, r0;
+  int mvalid, n0, e;
+};
+
+MOE_DEV int64_t uniform64(int64_t v) {
+  return ((int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+
+// Running sums of v[1 .. G] in place, by one wave.
+MOE_DEV void scan(int* v, int G, int lane) {
+  int before = 0;
+  if (lane == 0) v[0] = 0;
+  for (int g0 = 0; g0 < G; g0 += 64) {
+    int x = g0 + lane < G ? v[g0 + lane + 1] : 0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(x, o, 64);
+      if (lane >= o) x += y;
+    }
+    if (g0 + lane < G) v[g0 + lane + 1] = before + x;
+    before += __builtin_amdgcn_readlane(x, 63);
+  }
+}
+
+// Group of a tile: the groups whose tiles end at or before it.
+MOE_DEV int group_of(const int* pre, int G, int tile, int lane) {
+  int g = 0;
+  for (int g0 = 0; g0 < G; g0 += 64) g += __popcll(__ballot(g0 + lane < G && pre[g0 + lane + 1] <= tile));
+  return __builtin_amdgcn_readfirstlane(g);
+}
+
+// A lane's scales of a tile from LDS: its four rows, and eight groups of four columns (the second four GAP
+// bytes further on). Written in assembly because the compiler would first wait for every direct-to-LDS
+// load in flight, those of the next tile's first stages here, which fill another part of LDS.
+template <int GAP>
+MOE_DEV void read_scales(uint32_t rows, uint32_t cols, float (&r)[4], f32x4_t (&c)[8]) {
+  asm volatile(
+      "ds_read_b32 %0, %12\n\tds_read_b32 %1, %12 offset:128\n\t"
+      "ds_read_b32 %2, %12 offset:256\n\tds_read_b32 %3, %12 offset:384\n\t"
+      "ds_read_b128 %4, %13\n\tds_read_b128 %5, %13 offset:32\n\t"
+      "ds_read_b128 %6, %13 offset:64\n\tds_read_b128 %7, %13 offset:96\n\t"
+      "ds_read_b128 %8, %13 offset:%14\n\tds_read_b128 %9, %13 offset:%14+32\n\t"
+      "ds_read_b128 %10, %13 offset:%14+64\n\tds_read_b128 %11, %13 offset:%14+96\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(c[0]), "=&v"(c[1]), "=&v"(c[2]), "=&v"(c[3]),
+        "=&v"(c[4]), "=&v"(c[5]), "=&v"(c[6]), "=&v"(c[7])
+      : "v"(rows), "v"(cols), "n"(GAP)
+      : "memory");
+}
+
+template <bool GU>
+__global__ __launch_bounds__(kThreads) void i8_gemm_kernel(I8Args a) {
+  constexpr int OUTN = GU ? kTile / 2 : kTile;  // output columns of a tile
+  __shared__ Groups sh;
+  extern __shared__ __attribute__((aligned(1024))) char ring[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / kWN, wn = wave % kWN;
+  const int G = a.nc * a.El, ntiles = (a.N + OUTN - 1) / OUTN;
+  // "large" row tiles (full, or a last one of more than half the rows) come before the "small" last ones,
+  // which fill a last round where one is needed
+  for (int g = tid; g < G; g += kThreads) {
+    const int c = a.c0 + g / a.El, e = g % a.El;
+    int o0 = 0, o1 = (int)a.P_c;
+    if (a.offsets) {  // nothing outside the rows, whatever the table holds
+      const int32_t* off = a.offsets + (int64_t)c * (a.El + 1);
+      o0 = max(0, min(off[e], (int)a.P_c));
+      o1 = max(o0, min(off[e + 1], (int)a.P_c));
+    }
+    const int len = o1 - o0, rem = len % kTile;
+    sh.r0[g] = (int64_t)c * a.P_c + o0;
+    sh.len[g] = len;
+    sh.pre[g + 1] = (len / kTile + (rem > kTile / 2 ? 1 : 0)) * ntiles;
+    sh.preb[g + 1] = (rem > 0 && rem <= kTile / 2 ? 1 : 0) * ntiles;
+  }
+  __syncthreads();
+  if (wave == 0) scan(sh.pre, G, lane);
+  if (wave == 1) scan(sh.preb, G, lane);
+  __syncthreads();
+  const int total_l = sh.pre[G], total_s = sh.preb[G];
+  // each XCD (block % 8) owns a contiguous range of the large and one of the small tiles
+  const int pxl = (total_l + 7) / 8, pxs = (total_s + 7) / 8;
+  const int xcd = blockIdx.x % 8, per_xcd = gridDim.x / 8;
+  int slot = blockIdx.x / 8;
+
+  auto find = [&](I8Tile& t) -> bool {  // the tile of `slot`, or of the next slot that has one
+    for (; slot < pxl + pxs; slot += per_xcd) {
+      const bool large = slot < pxl;
+      const int tile = large ? xcd * pxl + slot : xcd * pxs + (slot - pxl);
+      if (tile >= (large ? total_l : total_s)) continue;
+      const int* pre = large ? sh.pre : sh.preb;
+      const int g = group_of(pre, G, tile, lane);
+      const int at = tile - __builtin_amdgcn_readfirstlane(pre[g]), len = __builtin_amdgcn_readfirstlane(sh.len[g]);
+      const int mt = large ? at / ntiles : len / kTile;
+      t.e = g % a.El;
+      t.n0 = (at % ntiles) * OUTN;
+      t.r0 = uniform64(sh.r0[g]) + (int64_t)mt * kTile;
+      t.mvalid = min(kTile, len - mt * kTile);
+      const int64_t wrows = GU ? 2 * (int64_t)a.N : a.N;
+      t.a = (const char*)a.A + t.r0 * a.K;
+      t.abytes = (int64_t)t.mvalid * a.K;
+      t.b = (const char*)a.B + (t.e * wrows + t.n0) * a.K;
+      t.bbytes = (wrows - t.n0) * a.K;
+      slot += per_xcd;
+      return true;
+    }
+    return false;
+  };
+
+  // loads of a pair of stages: 8 rows of 128 bytes per wave instruction, chunks swizzled as km2_off reads them
+  constexpr int NI = kTile / (8 * kWaves);
+  uint32_t va[NI], vb[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int r = 8 * (wave * NI + i) + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+    // gate/up: each wave's 64 tile rows are 32 gate rows and the 32 up rows of the same columns
+    const int q = r % 64, br = GU ? (r / 64) * 32 + (q < 32 ? q : a.N + q - 32) : r;
+    va[i] = (uint32_t)(r * a.K) + 16u * c;
+    vb[i] = (uint32_t)((int64_t)br * a.K) + 16u * c;
+  }
+  const uint32_t rl = lds_addr(ring);
+  auto issue = [&](const I8Tile& t, bool any, int pair, uint32_t at) {
+    const auto ra = make_rsrc(t.a, any ? t.abytes : 0), rb = make_rsrc(t.b, any ? t.bbytes : 0);
+    const uint32_t l0 = at + (uint32_t)(wave * NI * 1024);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(uintptr_t)(l0 + i * 1024), 16, (int)va[i], pair * 2 * kRowB, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t*)(uintptr_t)(l0 + kSlotA + i * 1024), 16, (int)vb[i], pair * 2 * kRowB, 0, 0);
+  };
+
+  I8Tile cur, next;
+  if (!find(cur)) return;
+  issue(cur, true, 0, rl);
+  const int nks = a.K / 64, np = (nks + 1) / 2;
+  const int arow0 = wm * 128, brow0 = wn * 64;
+  int buf = 0;
+  for (bool first = true;; first = false) {
+    const bool more = find(next);
+    if (!more) next = cur;
+    acc_t<kElI8> acc[kMN][kNN];
+#pragma unroll
+    for (int tm = 0; tm < kMN; ++tm)
+#pragma unroll
+      for (int tn = 0; tn < kNN; ++tn)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[tm][tn][q] = 0;
+    // the tile's scales, one per thread (rows, then columns; gate/up: gate columns, then up), on their way
+    // through the K loop and handed over in LDS: held per lane they would take 36 registers
+    float scale = 0.f;
+    auto load_scale = [&] {
+      const int i = tid - kTile, c = GU ? i % OUTN : i;
+      scale = tid < kTile ? a.scale_a[cur.r0 + min(tid, cur.mvalid - 1)]
+                          : a.scale_b[(int64_t)cur.e * (GU ? 2 * a.N : a.N) + (GU && i >= OUTN ? a.N : 0) + min(cur.n0 + c, a.N - 1)];
+    };
+    // One pair of stages; the next pair's loads, or the next tile's first, fill the other slot, which
+    // every wave has read before this pair's barrier.
+    auto kloop = [&](auto tma) {
+      constexpr int TMA = decltype(tma)::value;
+      for (int p = 0; p < np; ++p) {
+        if (p == 0 && !first) wait_vm<kStores>();  // loads complete in order: the last tile's stores are younger
+        else wait_vm<0>();
+        __builtin_amdgcn_s_barrier();
+        if (p == 0) load_scale();
+        const char* st = ring + buf * kSlot;
+        buf ^= 1;
+        const uint32_t fill = rl + (uint32_t)(buf * kSlot);
+        const bool inside = p + 1 < np;
+        stage_mma<kElI8, false, false, kTile, kTile, kMN, kNN, TMA, 2 * NI, 0>(
+            st, st + kSlotA, arow0, brow0, lane, acc,
+            [&] { issue(inside ? cur : next, inside || more, inside ? p + 1 : 0, fill); });
+        if (2 * p + 1 < nks)
+          stage_mma<kElI8, false, false, kTile, kTile, kMN, kNN, TMA, 0, 1>(st, st + kSlotA, arow0, brow0, lane, acc, [] {});
+      }
+    };
+    switch (__builtin_amdgcn_readfirstlane(max(0, min(kMN, (cur.mvalid - arow0 + 31) / 32)))) {
+      case 4: kloop(std::integral_constant<int, 4>()); break;
+      case 3: kloop(std::integral_constant<int, 3>()); break;
+      case 2: kloop(std::integral_constant<int, 2>()); break;
+      case 1: kloop(std::integral_constant<int, 1>()); break;
+      default: kloop(std::integral_constant<int, 0>()); break;
+    }
+    sh.scale[tid] = scale;
+    lds_barrier();  // (their last readers passed the barrier at the head of this tile)
+    // out: lane l holds row l & 31 of a block and columns 8 g + 4 (l >> 5) .. + 3 of its group g
+    const int col0 = GU ? wn * 32 : wn * 64;  // the wave's first output column in the tile
+    const int nvalid = min(OUTN, a.N - cur.n0);
+    float sa[kMN];
+    f32x4_t sb[8];  // gate/up: four groups of gate columns, four of up; else those of the two column blocks
+    const uint32_t at = lds_addr(sh.scale);
+    read_scales<GU ? OUTN * 4 : 128>(at + 4 * (arow0 + out_row(lane)), at + 4 * (kTile + col0 + 4 * (lane >> 5)), sa, sb);
+    constexpr int ES = GU ? 4 : 2;
+    const int64_t ld = (int64_t)a.N * ES;
+    const auto rc = make_rsrc((char*)a.C + cur.r0 * ld + (int64_t)cur.n0 * ES, (cur.mvalid - 1) * ld + (int64_t)nvalid * ES);
+#pragma unroll
+    for (int tm = 0; tm < kMN; ++tm) {
+      const int m = arow0 + tm * 32 + out_row(lane);
+      const uint32_t row = (uint32_t)(m * ld);
+      if constexpr (GU) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          f32x4_t h;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float gv = (float)acc[tm][0][4 * g + q] * (sa[tm] * sb[g][q]);
+            const float uv = (float)acc[tm][1][4 * g + q] * (sa[tm] * sb[4 + g][q]);
+            h[q] = gv * sigmoidf_(gv) * uv;
+          }
+          const int c = col0 + out_col(g, lane);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, h), rc, c < nvalid ? (int)(row + 4 * c) : kOutside, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int tn = 0; tn < kNN; ++tn)
+#pragma unroll
+          for (int g = 0; g < 4; g += 2) {
+            uint2 p[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float v[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[q] = (float)acc[tm][tn][4 * (g + k) + q] * (sa[tm] * sb[4 * tn + g + k][q]);
+              p[k] = pack4(v[0], v[1], v[2], v[3]);
+            }
+            // the halves' lanes exchange: lanes 0..31 get all 8 columns of group g, lanes 32..63 of g + 1
+            const auto x = __builtin_amdgcn_permlane32_swap(p[0].x, p[1].x, false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(p[0].y, p[1].y, false, false);
+            const u32x4_t o{x[0], y[0], x[1], y[1]};
+            const int c = col0 + tn * 32 + 8 * (g + (lane >> 5));
+            __builtin_amdgcn_raw_buffer_store_b128(o, rc, c < nvalid ? (int)(row + 2 * c) : kOutside, 0, 0);
+          }
+      }
+    }
+    if (!more) break;
+    cur = next;
+  }
+  wait_vm<0>();  // the last pair's loads (of nothing) still write zeros to this workgroup's LDS
+}
+
+template <bool GU>
+hipError_t run_i8(const char* name, const I8Args& a, hipStream_t s) {
+  auto k = i8_gemm_kernel<GU>;
+  hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, kRing);
+  if (e != hipSuccess) return e;
+  const int outn = GU ? kTile / 2 : kTile;
+  // per chunk at most floor(P_c / 256) + El row tiles; the device-side count decides the work
+  const int64_t grid = persistent_grid((int64_t)a.nc * (a.P_c / kTile + a.El) * ((a.N + outn - 1) / outn));
+  if (grid <= 0) return hipSuccess;
+  {
+    MOE_TRACE(name, s);
+    MOE_LAUNCH(k, dim3((unsigned)grid), dim3(kThreads), kRing, s, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace gg
+
+// Gate/up with exact int32 sums, dequantised by s_row * s_col, SwiGLU -> h (FP32 rows at the start of the h
+// buffer: it is quantised per row next, and a BF16 rounding before that would move codes by whole steps);
+// h quantised per row (codes after the FP32 values); down -> yd (BF16).
+hipError_t launch_expert_fwd_i8(const void* xd, const float* xd_scale, const void* w1, const float* w1_scale,
+                                const void* w2, const float* w2_scale, const int32_t* offsets, void* h,
+                                float* h_scale, void* yd, int H, int I, int El, int c0, int nc, int64_t P_c,
+                                int64_t P, hipStream_t s) {
+  if (nc <= 0 || El <= 0) return hipSuccess;
+  int8_t* hq = (int8_t*)h + P * (int64_t)I * 4;
+  gg::I8Args a{(const int8_t*)xd, xd_scale, (const int8_t*)w1, w1_scale, h, H, I, offsets, El, c0, nc, P_c};
+  hipError_t e = gg::run_i8<true>("gemm_gateup_swiglu_i8", a, s);
+  if (e != hipSuccess) return e;
+  e = launch_quantize_h_i8((const float*)h, hq, h_scale, offsets, El, c0, nc, P_c, I, s);
+  if (e != hipSuccess) return e;
+  gg::I8Args b{hq, h_scale, (const int8_t*)w2, w2_scale, yd, I, H, offsets, El, c0, nc, P_c};
+  return gg::run_i8<false>("gemm_down_i8", b, s);
+}
+
+// y = dequantised x w^T for the rows of each group (moe_expert_matmul_i8).
+hipError_t launch_expert_matmul_i8(int groups, int64_t rows, int N, int K, const void* x, const float* x_scale,
+                                   const void* w, const float* w_scale, const int32_t* offsets, void* y,
+                                   hipStream_t s) {
+  if (groups <= 0 || rows <= 0) return hipSuccess;
+  gg::I8Args a{(const int8_t*)x, x_scale, (const int8_t*)w, w_scale, y, K, N, offsets, groups, 0, 1, rows};
+  return gg::run_i8<false>("gemm_matmul_i8", a, s);
+}
+
+}  // namespace moe

@@ -77,7 +77,7 @@ hipError_t launch_expert_fwd_fp8(const void* xd, const float* xd_scale, const vo
                                  const float* w1_scale, const void* w2, const float* w2_scale,
                                  const int32_t* offsets, void* h, float* h_scale, void* yd, int H,
                                  int I, int El, int c0, int nc, int64_t P_c, int64_t P, hipStream_t s);
-// 8-bit integers (rows_i8.hip, grouped_gemm.hip). h holds [P, I] FP32 values followed by [P, I] codes
+// 8-bit integers (rows_i8.hip, i8_gemm.hip). h holds [P, I] FP32 values followed by [P, I] codes
 // (P = n_chunks * P_c).
 hipError_t launch_quantize_rows_i8(const void* src, void* codes, float* scale, int64_t rows, int cols, hipStream_t s);
 hipError_t launch_dispatch_i8(const void* x, const int32_t* row_of, void* xd, float* xd_scale, int64_t t0, int64_t t1,

@@ -21,12 +21,12 @@ constexpr int kI8MaxVec = 16;       // 16-byte vectors of a row that a lane hold
 
 // Magnitude bits of a row's values, compared as integers: monotone, and NaN ranks above infinity, so
 // the maximum also says whether every value is finite.
-MOE_DEV uint32_t magnitude8(const u32x4& v) {  // 8 BF16 values
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
-  return m;
+MOE_DEV uint32_t magnitude8(const u32x4& v) {  // 8 BF16 values, both halves of a word at once
+  typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
+  auto half = [](uint32_t w) { return __builtin_bit_cast(u16x2, w & 0x7fff7fffu); };
+  const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(half(v.x), half(v.y)),
+                                            __builtin_elementwise_max(half(v.z), half(v.w)));
+  return (uint32_t)max(m.x, m.y) << 16;
 }
 MOE_DEV uint32_t magnitude4(const u32x4& v) {  // 4 FP32 values
   return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
@@ -77,20 +77,38 @@ __global__ __launch_bounds__(256) void quantize_rows_i8_kernel(const u32x4* __re
   if (lane == 0) scale[r] = q.scale;
 }
 
-// Dispatch: x[t] quantised once and stored to every local slot's row, one block per token (many short
-// blocks keep more loads in flight than a wave per row: 21 -> 16 us at 16K tokens of 2048). Thread i
-// holds vectors i, i + 256, ...; NV = 0: read twice. kSkip: a token without a local slot is not read; the
-// check waits for its slots, so a few tokens (bound by latency) load without it.
+// Dispatch: x[t] quantised once and stored to every local slot's row. Many tokens: one wave per token,
+// a token without a local slot is not read (19 us at 16K tokens of 2048 with 16 of 128 experts local; a
+// block per token 22 us).
+template <int NV>
+__global__ __launch_bounds__(256) void dispatch_i8_kernel(const u32x4* __restrict__ x, const int32_t* __restrict__ row_of,
+                                                          uint2* __restrict__ xd, float* __restrict__ xd_scale, int64_t t0,
+                                                          int64_t t1, int K, int64_t nvec) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = t0 + (int64_t)blockIdx.x * kI8RowsPerBlock + (threadIdx.x >> 6);
+  if (t >= t1) return;
+  const int32_t myrow = lane < K ? row_of[t * K + lane] : -1;
+  if (__ballot(myrow >= 0) == 0) return;
+  const RowScale q = quantize_row<NV>(x + t * nvec, nvec, lane, [&](int64_t i, uint2 c) {
+    for (int j = 0; j < K; ++j) {
+      const int32_t r = __builtin_amdgcn_readlane(myrow, j);
+      if (r >= 0) xd[(int64_t)r * nvec + i] = c;
+    }
+  });
+  if (myrow >= 0) xd_scale[myrow] = q.scale;
+}
+
+// Few tokens are bound by latency (one token 4.5 -> 2.6 us): one block per token, whose values load beside
+// its slots without a check; thread i holds vectors i, i + 256, ... (NV = 0: read twice).
 constexpr int kDispThreads = 256;
-template <int NV, bool kSkip>
-__global__ __launch_bounds__(kDispThreads) void dispatch_i8_kernel(const u32x4* __restrict__ x, const int32_t* __restrict__ row_of,
+template <int NV>
+__global__ __launch_bounds__(kDispThreads) void dispatch_few_i8_kernel(const u32x4* __restrict__ x, const int32_t* __restrict__ row_of,
                                                                    uint2* __restrict__ xd, float* __restrict__ xd_scale,
                                                                    int64_t t0, int K, int64_t nvec) {
   __shared__ uint32_t part[kDispThreads / 64];
   const int lane = threadIdx.x & 63;
   const int64_t t = t0 + blockIdx.x;
   const int32_t myrow = lane < K ? row_of[t * K + lane] : -1;
-  if (kSkip && __ballot(myrow >= 0) == 0) return;
   const u32x4* src = x + t * nvec;
   u32x4 v[NV > 0 ? NV : 1];
   uint32_t m = 0;
@@ -202,13 +220,17 @@ hipError_t launch_dispatch_i8(const void* x, const int32_t* row_of, void* xd, fl
   const int64_t nvec = H / 8;
   {
     MOE_TRACE("dispatch_i8", s);
-    const bool skip = t1 - t0 > 1024;
-    auto k = skip ? dispatch_i8_kernel<0, true> : dispatch_i8_kernel<0, false>;
-    if (nvec <= kDispThreads) k = skip ? dispatch_i8_kernel<1, true> : dispatch_i8_kernel<1, false>;
-    else if (nvec <= 2 * kDispThreads) k = skip ? dispatch_i8_kernel<2, true> : dispatch_i8_kernel<2, false>;
-    else if (nvec <= 4 * kDispThreads) k = skip ? dispatch_i8_kernel<4, true> : dispatch_i8_kernel<4, false>;
-    MOE_LAUNCH(k, dim3((unsigned)(t1 - t0)), dim3(kDispThreads), 0, s, (const u32x4*)x, row_of, (uint2*)xd, xd_scale, t0, K,
-               nvec);
+    if (t1 - t0 > 1024) {
+      MOE_I8_NV(nvec, MOE_LAUNCH(dispatch_i8_kernel<NV>, row_grid(t1 - t0), dim3(256), 0, s, (const u32x4*)x, row_of,
+                                 (uint2*)xd, xd_scale, t0, t1, K, nvec));
+    } else {
+      auto k = nvec <= kDispThreads       ? dispatch_few_i8_kernel<1>
+               : nvec <= 2 * kDispThreads ? dispatch_few_i8_kernel<2>
+               : nvec <= 4 * kDispThreads ? dispatch_few_i8_kernel<4>
+                                          : dispatch_few_i8_kernel<0>;
+      MOE_LAUNCH(k, dim3((unsigned)(t1 - t0)), dim3(kDispThreads), 0, s, (const u32x4*)x, row_of, (uint2*)xd, xd_scale, t0,
+                 K, nvec);
+    }
   }
   return hipGetLastError();
 }

@@ -299,7 +299,7 @@ moe_status moe_quantize_rows_i8(int64_t rows, int32_t cols, const void* src_bf16
  * [0, rows]); NULL with groups = 1 is one group of every row (a dense product). x [rows, K] and w
  * [groups, N, K] are codes in [-128, 127], x_scale [rows], w_scale [groups, N] FP32, y [rows, N] BF16.
  * The sum is exact in int32 and rounded once to FP32. Rows in no group are not written. groups up to
- * 1024, N a multiple of 8, K a multiple of 64 up to 131008, N * K below 2^31 (MOE_ERR_UNSUPPORTED);
+ * 1024, N a multiple of 8 up to 2097152, K a multiple of 64 up to 131008, N * K below 2^31 (MOE_ERR_UNSUPPORTED);
  * x, w and y 16-byte aligned (MOE_ERR_ARG). */
 moe_status moe_expert_matmul_i8(int32_t groups, int64_t rows, int32_t N, int32_t K, const void* x,
                                 const float* x_scale, const void* w, const float* w_scale,
