@@ -22,6 +22,7 @@ using gg::ks_off;
 constexpr int kDT = 32;        // tokens per tile
 constexpr int kDThreads = 256;
 constexpr int kStageK = 64;    // W_r rows staged at once
+constexpr int kAhead = 3;      // dxd rows of a token loaded a tile ahead
 
 // KS: K steps of 16 experts (E <= 16 KS); CW: columns per wave
 template <int KS, int CW>
@@ -34,18 +35,20 @@ struct DenseLds {
   static constexpr int kSums = kDT * kPitchC;
   static constexpr int kW = (KS * 16 < kStageK ? KS * 16 : kStageK) * kSlice * 2;  // W_r staging, before the first tile
   static constexpr int kRows = kC + (kSums > kW ? kSums : kW);
-  static constexpr int kBytes = kRows + 2 * kDT * 8 * 4;  // slot rows of two tiles
+  static constexpr int kBytes = kRows + 3 * kDT * 8 * 4;  // slot rows of three tiles
 };
 
-// One vector of 8 columns of a dispatch row: BF16 values, or (Q) e4m3 codes with their block's scale.
+// One vector of 8 columns of a dispatch row: BF16 values, or (Q) e4m3 codes with their block's scale. Loads
+// and adds carry no branch (a row that is absent loads row 0 and adds zeros): the compiler counts
+// loads in flight only in straight code, and behind branches waits for all of them.
 template <bool Q> struct RowVec;
 template <> struct RowVec<false> {
   u32x4 v;
   MOE_DEV void load(const void* dxd, const float*, int64_t r, int64_t nvec, int vec, int) {
     v = ((const u32x4*)dxd)[r * nvec + vec];
   }
-  MOE_DEV void add(float (&f)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  MOE_DEV void add(float (&f)[8], bool on) const {
+    const uint32_t m = on ? 0xffffffffu : 0u, w[4] = {v.x & m, v.y & m, v.z & m, v.w & m};
 #pragma unroll
     for (int i = 0; i < 4; ++i) { f[2 * i] += bf2f(w[i] & 0xffff); f[2 * i + 1] += bf2f(w[i] >> 16); }
   }
@@ -57,9 +60,10 @@ template <> struct RowVec<true> {
     v = ((const uint2*)dxd)[r * nvec + vec];
     s = dxs[r * nblk + (vec >> 5)];
   }
-  MOE_DEV void add(float (&f)[8]) const {
+  MOE_DEV void add(float (&f)[8], bool on) const {
     float g[8];
-    deq8(v, s, g);
+    const uint32_t m = on ? 0xffffffffu : 0u;
+    deq8(make_uint2(v.x & m, v.y & m), on ? s : 0.f, g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] += g[i];
   }
@@ -77,7 +81,7 @@ struct DenseArgs {
 };
 
 template <int KS, int CW, bool Q>
-__global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_kernel(DenseArgs a) {
+__global__ __launch_bounds__(kDThreads, KS <= 8 ? 2 : 1) void dispatch_bwd_dense_kernel(DenseArgs a) {
   using L = DenseLds<KS, CW>;
   constexpr int TN = CW / 32, SL = L::kSlice;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
@@ -96,23 +100,44 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_kernel(DenseArgs
   constexpr int NI = kDT * VPR / kDThreads;     // of them per thread: tokens tid / VPR + it * (256 / VPR)
   const int c = tid % VPR, rt = tid / VPR, n = n0 + 8 * c;
   const bool in_cols = n < a.H;
+  const int vec = min(n, a.H - 8) / 8;
+  const void* const dxd = a.dxd ? a.dxd : a.w_r;  // no local expert: any readable row
   float4 dl[ND];
   int slots[8];
-  // dlogits of the tile (one contiguous block; columns past E and tokens past the chunk are zeros) and the
-  // slot rows of token tid: issued one tile ahead
+  // dlogits of a tile (one contiguous block; columns past E and tokens past the chunk are zeros): issued one
+  // tile ahead
   auto fetch = [&](int64_t tile) {
     const int64_t r0 = a.t0 + tile * kDT;
     const int nt = (int)(a.t1 - r0 < kDT ? a.t1 - r0 : kDT);
 #pragma unroll
-    for (int u = 0; u < ND; ++u) {
-      const int i = tid + u * kDThreads, r = i / (KS * 4), e4 = i % (KS * 4);
-      dl[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < nt && e4 < evec) dl[u] = *(const float4*)(a.dlogits + (r0 + r) * a.E + 4 * e4);
+    for (int u = 0; u < ND; ++u) {  // unconditional (so that later waits can count them); zeroed where it is used
+      const int i = tid + u * kDThreads, r = min(i / (KS * 4), nt - 1), e4 = min(i % (KS * 4), evec - 1);
+      dl[u] = *(const float4*)(a.dlogits + (r0 + r) * a.E + 4 * e4);
     }
-    if (tid < kDT)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) slots[k] = k < a.K && tid < nt ? a.row_of[(r0 + tid) * a.K + k] : -1;
   };
+  // slots of token tid (tid < kDT) of the XCD's tile l: issued two tiles ahead, put into LDS one tile ahead,
+  // the token's local rows first, in slot order (none past the end)
+  auto token = [&](int64_t l) { return a.t0 + (xcd * px + l) * kDT + min(tid, kDT - 1); };
+  auto inside = [&](int64_t l) { return l < px && token(l) < a.t1; };
+  auto fetch_slots = [&](int64_t l) {
+    if (wave > 0) return;
+    const int32_t* p = a.row_of + (inside(l) ? token(l) : a.t0) * a.K;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) slots[k] = p[min(k, a.K - 1)];
+  };
+  auto put_slots = [&](int buf, int64_t l) {
+    if (wave > 0 || tid >= kDT) return;
+    int* const srow = (int*)(lds + L::kRows) + buf * (kDT * 8) + tid * 8;
+    const bool in = inside(l);
+    int m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      srow[m] = slots[k];  // kept if it is a local slot, else overwritten
+      m += in && k < a.K && slots[k] >= 0 ? 1 : 0;
+    }
+    for (; m < 8; ++m) srow[m] = -1;
+  };
+  fetch_slots(first);
   fetch(xcd * px + first);
 
   // the slice of W_r as fragments: rows of W_r through LDS, transposed by the fragment reads; two
@@ -149,18 +174,37 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_kernel(DenseArgs
       }
     }
   }
-  // Two barriers per tile. A wave may start the next tile while others still add rows of this one, so
-  // the slot rows alternate between two buffers; the parts and the sums are separate areas.
-  int par = 0;
-  for (int64_t l = first; l < px; l += a.lanes, par ^= 1) {
+  // The tokens' first kAhead dxd rows are loaded a tile ahead.
+  RowVec<Q> v[kAhead][NI];
+  int row[kAhead][NI];
+  auto fetch_rows = [&](int buf) {
+    const int* const srow = (const int*)(lds + L::kRows) + buf * (kDT * 8);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+      for (int u = 0; u < NI; ++u) {
+        row[s][u] = srow[(rt + u * (kDThreads / VPR)) * 8 + s];
+        v[s][u].load(dxd, a.dxs, max(row[s][u], 0), nvec, vec, nblk);
+      }
+  };
+  put_slots(0, first);
+  fetch_slots(first + a.lanes);
+  gg::lds_barrier();
+  fetch_rows(0);
+  // Two barriers per tile. A wave may start the next tile while others still add rows of this one or look
+  // up the next one's, so the slot rows go round three buffers; the parts and the sums are separate areas.
+  int buf = 0;
+  for (int64_t l = first; l < px; l += a.lanes) {
     const int64_t tile = xcd * px + l;
     if (tile >= tiles) break;
-    int* const srow = (int*)(lds + L::kRows) + par * (kDT * 8);
+    const int* const srow = (const int*)(lds + L::kRows) + buf * (kDT * 8);
+    buf = buf == 2 ? 0 : buf + 1;
     const int64_t r0 = a.t0 + tile * kDT;
     const int nt = (int)(a.t1 - r0 < kDT ? a.t1 - r0 : kDT);
 #pragma unroll
     for (int u = 0; u < ND; ++u) {
       const int i = tid + u * kDThreads, r = i / (KS * 4), e4 = i % (KS * 4);
+      if (r >= nt || e4 >= evec) dl[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       const uint2 h = gg::pack4(dl[u].x, dl[u].y, dl[u].z, dl[u].w);
       float hf[4];
       gg::unpack4(h, hf);
@@ -168,26 +212,10 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_kernel(DenseArgs
       *(uint2*)(lds + L::kPartA + r * L::kPitchA + 8 * e4) =
           gg::pack4(dl[u].x - hf[0], dl[u].y - hf[1], dl[u].z - hf[2], dl[u].w - hf[3]);
     }
-    if (tid < kDT) {  // the token's local rows first, in slot order
-      int m = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (slots[k] >= 0) srow[tid * 8 + m++] = slots[k];
-      for (; m < 8; ++m) srow[tid * 8 + m] = -1;
-    }
-    __syncthreads();
-
-    // the tokens' first two rows and the next tile's inputs travel behind the products
-    RowVec<Q> v[2][NI];
-    int row[2][NI];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int u = 0; u < NI; ++u) {
-        row[s][u] = srow[(rt + u * (kDThreads / VPR)) * 8 + s];
-        if (row[s][u] >= 0 && in_cols) v[s][u].load(a.dxd, a.dxs, row[s][u], nvec, n / 8, nblk);
-      }
-    if (l + a.lanes < px && tile + a.lanes < tiles) fetch(tile + a.lanes);
+    put_slots(buf, l + a.lanes);  // the next tile's
+    gg::lds_barrier();  // (loads stay in flight)
+    fetch(tile + a.lanes < tiles ? tile + a.lanes : tile);  // (unused behind the last tile)
+    fetch_slots(l + 2 * a.lanes);
 
     f32x16_t acc[TN];
 #pragma unroll
@@ -212,8 +240,8 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_kernel(DenseArgs
         *(float4*)(sc + (lane & 31) * L::kPitchC + 4 * (wave * CW + 32 * tn + gg::out_col(g, lane))) =
             make_float4(acc[tn][4 * g], acc[tn][4 * g + 1], acc[tn][4 * g + 2], acc[tn][4 * g + 3]);
     gg::lds_barrier();  // the loads above stay in flight
+    __builtin_amdgcn_sched_barrier(0);  // nothing that waits for the rows moves in front of the products
 
-    if (!in_cols) continue;
     float f[NI][8];
 #pragma unroll
     for (int u = 0; u < NI; ++u) {
@@ -223,32 +251,32 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_kernel(DenseArgs
       f[u][4] = y.x; f[u][5] = y.y; f[u][6] = y.z; f[u][7] = y.w;
     }
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < kAhead; ++s)
 #pragma unroll
       for (int u = 0; u < NI; ++u)
-        if (row[s][u] >= 0) v[s][u].add(f[u]);
+        v[s][u].add(f[u], row[s][u] >= 0);
     // tokens with more local slots: the next slot of every token in flight together
-    for (int s = 2; s < a.K; ++s) {
+    for (int s = kAhead; s < a.K; ++s) {
       bool any = false;
 #pragma unroll
       for (int u = 0; u < NI; ++u) {
-        row[0][u] = row[1][u] < 0 ? -1 : srow[(rt + u * (kDThreads / VPR)) * 8 + s];
-        row[1][u] = row[0][u];
+        row[0][u] = srow[(rt + u * (kDThreads / VPR)) * 8 + s];
         any |= row[0][u] >= 0;
-        if (row[0][u] >= 0) v[0][u].load(a.dxd, a.dxs, row[0][u], nvec, n / 8, nblk);
       }
-      if (!any) break;
+      if (__ballot(any) == 0) break;
 #pragma unroll
-      for (int u = 0; u < NI; ++u)
-        if (row[0][u] >= 0) v[0][u].add(f[u]);
+      for (int u = 0; u < NI; ++u) v[0][u].load(dxd, a.dxs, max(row[0][u], 0), nvec, vec, nblk);
+#pragma unroll
+      for (int u = 0; u < NI; ++u) v[0][u].add(f[u], row[0][u] >= 0);
     }
 #pragma unroll
     for (int u = 0; u < NI; ++u) {
       const int r = rt + u * (kDThreads / VPR);
-      if (r < nt)
+      if (r < nt && in_cols)
         *(u32x4*)(a.dx + (r0 + r) * a.H + n) = u32x4{pack_bf2(f[u][0], f[u][1]), pack_bf2(f[u][2], f[u][3]),
                                                      pack_bf2(f[u][4], f[u][5]), pack_bf2(f[u][6], f[u][7])};
     }
+    fetch_rows(buf);
   }
 }
 

@@ -7,9 +7,9 @@
 //   loss = a L_bal + b L_z.
 // Counts carry no gradient, so with w_se = a E c_se / (S' n_s^2 k)
 //   dlogits_te = g p_te (w_se - sum_j w_sj p_tj + 2 b lse_t / N).
-// The bracket does not change when w_s is shifted, so the kernel takes w_se - a / (S' n_s), formed
-// in FP64: near a balanced load every w_se is almost that constant and the difference would lose
-// its digits.
+// The bracket does not change when w_s is shifted, so the kernel takes w_se - a / (S' n_s) =
+// a (c_se E - n_s k) / (S' n_s^2 k), the difference in integers: near a balanced load every w_se is almost
+// that constant and a difference of the two in floating point would lose its digits.
 //
 // Everything is bound by reading the logits once forward and once more (with one write of the
 // gradient) backward. A row of E logits is held by 16 to 64 lanes in registers: one pass gives the
@@ -289,7 +289,7 @@ __global__ __launch_bounds__(kRedThreads) void router_loss_reduce_kernel(
   double p = 0.0, z = 0.0;
   int c = 0, n = 0;
   if (e < E)
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t i = first + grp; i < end; i += kRedGroups) {
       p += (double)ws.p[i * E + e];
       c += ws.c[i * E + e];
@@ -333,13 +333,14 @@ __global__ __launch_bounds__(kRedThreads) void router_loss_reduce_kernel(
   int full = 0;
   for (int i = tid; i < pc.S; i += kRedThreads) {
     const int ns = ld_device(&seg_tokens[i]);
-    if (ns <= 0) continue;
+    const double zs = ld_device(&ws.zs[i]);  // an empty segment's sums are zeros
     double cp = 0.0;
+#pragma unroll 8
     for (int j = 0; j < nb; ++j) cp += ld_device(&ws.cp[(int64_t)i * nb + j]);
-    bal += cp * (double)E / ((double)ns * (double)ns * (double)K);
-    z += ld_device(&ws.zs[i]);
+    bal += ns > 0 ? cp * (double)E / ((double)ns * (double)ns * (double)K) : 0.0;
+    z += zs;
     n += ns;
-    full += 1;
+    full += ns > 0 ? 1 : 0;
   }
   bal = lanes_sum<1>(bal);
   z = lanes_sum<1>(z);
@@ -362,6 +363,58 @@ __global__ __launch_bounds__(kRedThreads) void router_loss_reduce_kernel(
   }
 }
 
+// One segment of few tiles: one block adds them all, columns side by side in `ec` threads (E rounded up to a
+// power of two), and forms the losses with no exchange between blocks (512 tokens: 7 us with it).
+__global__ __launch_bounds__(kRedThreads) void router_loss_reduce_one_kernel(
+    Pieces pc, LossWs ws, int64_t slots, int E, int K, int ec, float balance_coef, float z_coef,
+    int32_t* __restrict__ seg_counts, int32_t* __restrict__ seg_tokens, float* __restrict__ seg_probs,
+    float* __restrict__ loss) {
+  constexpr int NW = kRedThreads / kWave;
+  __shared__ double redp[kRedThreads], red[NW], redz[NW];
+  __shared__ int redc[kRedThreads], redn[NW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = tid & (ec - 1), grp = tid / ec, groups = kRedThreads / ec;
+  const int64_t b0 = pc.bound(1), b1 = pc.bound(2), first = b0 / pc.R + 1;
+  int64_t end = b1 > b0 ? first + (b1 - b0 + pc.R - 1) / pc.R : first;
+  if (end > slots) end = slots;
+  double p = 0.0, z = 0.0;
+  int c = 0, n = 0;
+  if (col < E)
+#pragma unroll 8
+    for (int64_t i = first + grp; i < end; i += groups) {
+      p += (double)ws.p[i * E + col];
+      c += ws.c[i * E + col];
+    }
+  for (int64_t i = first + tid; i < end; i += kRedThreads) { z += ws.z[i]; n += ws.n[i]; }
+  redp[tid] = p;
+  redc[tid] = c;
+  z = lanes_sum<1>(z);
+  n = lanes_sum<1>(n);
+  if (lane == 0) { redz[wave] = z; redn[wave] = n; }
+  __syncthreads();
+  double cp = 0.0;
+  if (tid < E) {
+    for (int k = 1; k < groups; ++k) { p += redp[k * ec + tid]; c += redc[k * ec + tid]; }
+    seg_probs[tid] = (float)p;
+    seg_counts[tid] = c;
+    cp = p * (double)c;
+  }
+  cp = lanes_sum<1>(cp);
+  if (lane == 0) red[wave] = cp;
+  __syncthreads();
+  if (tid == 0) {
+    cp = z = 0.0;
+    n = 0;
+    for (int w = 0; w < NW; ++w) { cp += red[w]; z += redz[w]; n += redn[w]; }
+    const double lb = n ? cp * (double)E / ((double)n * (double)n * (double)K) : 0.0, lz = n ? z / n : 0.0;
+    loss[0] = (float)((double)balance_coef * lb + (z_coef != 0.f ? (double)z_coef * lz : 0.0));
+    loss[1] = (float)lb;
+    loss[2] = (float)lz;
+    seg_tokens[0] = n;
+    seg_tokens[1] = n;
+    seg_tokens[2] = n > 0 ? 1 : 0;
+  }
+}
+
 template <int G, int NV, int W>
 __global__ __launch_bounds__(kLossThreads) void router_loss_bwd_kernel(
     const float* __restrict__ logits, const float* __restrict__ lse_in, const uint8_t* __restrict__ mask,
@@ -376,9 +429,9 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_bwd_kernel(
   const bool outside = t.piece == 0 || t.piece == pc.S + 1;
   const int ns = outside ? 0 : seg_tokens[s];
   const int N = seg_tokens[pc.S], full = seg_tokens[pc.S + 1];
-  const double per = ns > 0 && full > 0 ? (double)balance_coef / ((double)full * (double)ns) : 0.0;
-  const double share = ns > 0 ? (double)E / ((double)ns * (double)K) : 0.0;
-  const float zc = N > 0 ? (float)(2.0 * (double)z_coef / (double)N) : 0.f;
+  const int64_t even = (int64_t)ns * K;  // slots of the segment
+  const float per = ns > 0 && full > 0 ? balance_coef / ((float)full * (float)ns * (float)even) : 0.f;
+  const float zc = N > 0 ? 2.f * z_coef / (float)N : 0.f;
   const float gl = dloss ? *dloss : 1.f;
   constexpr int U = kLossBatch;
   float w[C];
@@ -406,7 +459,7 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_bwd_kernel(
 #pragma unroll
         for (int j = 0; j < W; ++j) {
           const int e = W * (i * G + q) + j;
-          w[i * W + j] = ns > 0 && e < E ? (float)(per * ((double)seg_counts[(int64_t)s * E + e] * share - 1.0)) : 0.f;
+          w[i * W + j] = ns > 0 && e < E ? per * (float)((int64_t)seg_counts[(int64_t)s * E + e] * E - even) : 0.f;
         }
     }
     // lse keeps only the digits that its size leaves, up to log E is lost where the logits are huge,
@@ -470,7 +523,13 @@ hipError_t launch_router_loss(const float* logits, const int32_t* topk_idx, cons
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  {
+  if (S == 1 && slots <= 70) {  // at most 64 tiles of 32 rows and the pieces' edges
+    int ec = 64;
+    while (ec < E) ec *= 2;
+    MOE_TRACE("router_loss_reduce", s);
+    MOE_LAUNCH(router_loss_reduce_one_kernel, dim3(1), dim3(kRedThreads), 0, s, pc, ws, slots, E, K, ec, balance_coef, z_coef,
+               seg_counts, seg_tokens, seg_probs, loss);
+  } else {
     MOE_TRACE("router_loss_reduce", s);
     MOE_LAUNCH(router_loss_reduce_kernel, dim3((unsigned)((int64_t)S * red_blocks(E))), dim3(kRedThreads), 0, s, pc, ws,
                slots, E, K, balance_coef, z_coef, seg_counts, seg_tokens, seg_probs, loss);
