@@ -382,11 +382,10 @@ moe_status moe_expert_ffn(const moe_desc* d, int chunk, const void* xd, const fl
   }
   if (d->dtype == MOE_INT8) {
     MOE_NEED(xd_scale); MOE_NEED(w1_scale); MOE_NEED(w2_scale); MOE_NEED(h_scale);
-    const int64_t slots = min_pc(d) * r.nc;  // the rows that routing can make, whatever P_c is
     const int64_t usual = cdiv(tokens_per_chunk(d) * d->k, d->E);
     if (few_rows(d->E_local, usual, 2 * (int64_t)d->I)) {
       MOE_HIP(moe::launch_expert_fwd_i8_few(xd, xd_scale, w1, w1_scale, w2, w2_scale, offsets, h, yd, d->H, d->I,
-                                            d->E_local, r.c0, r.nc, d->P_c, rows_of(d), slots, usual,
+                                            d->E_local, r.c0, r.nc, d->P_c, rows_of(d), d->P_c * r.nc, usual,
                                             (hipStream_t)stream),
               "expert_ffn_i8");
       return MOE_OK;
@@ -616,7 +615,7 @@ moe_status moe_quantize_rows_i8(int64_t rows, int32_t cols, const void* src_bf16
   MOE_NEED(src_bf16); MOE_NEED(codes); MOE_NEED(scale);
   if (((uintptr_t)src_bf16 & 15) || ((uintptr_t)codes & 7))
     return fail(MOE_ERR_ARG, "%s: the rows must be 16-byte aligned and the codes 8-byte aligned", __func__);
-  if (rows > 4 * (int64_t)INT32_MAX) return fail(MOE_ERR_UNSUPPORTED, "%s: rows = %lld above 4 (2^31 - 1)", __func__, (long long)rows);
+  if (rows >= 1 << 26) return fail(MOE_ERR_UNSUPPORTED, "%s: rows = %lld above 2^26 - 1", __func__, (long long)rows);
   MOE_HIP(moe::launch_quantize_rows_i8(src_bf16, codes, scale, rows, cols, (hipStream_t)stream), "quantize_rows_i8");
   return MOE_OK;
 }

@@ -150,8 +150,8 @@ moe_status moe_route_noalloc(const moe_desc* d, int chunk, const float* logits, 
 /* Routing from the token activations (the router projection fused into routing): logits =
  * x . W_r^T with BF16 x [T,H] and W_r [E,H], FP32 accumulation on MFMA, then the top-k of
  * moe_route on those logits, which stay in registers and LDS; `logits` (nullable, FP32 [T,E])
- * receives them. Every other argument and output is moe_route's. Needs a BF16 or FP8 descriptor
- * (x is BF16 in both) and E a multiple of 32, at most 256 (MOE_ERR_UNSUPPORTED otherwise). */
+ * receives them. Every other argument and output is moe_route's. Needs a BF16, FP8 or INT8 descriptor
+ * (x is BF16 in each) and E a multiple of 32, at most 256 (MOE_ERR_UNSUPPORTED otherwise). */
 moe_status moe_route_x(const moe_desc* d, int chunk, const void* x, const void* w_r, float* logits,
                        int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets, int32_t* row_of,
                        int32_t* src_token, void* workspace, void* stream);
@@ -289,7 +289,7 @@ moe_status moe_quantize_rows_fp8(int64_t rows, int32_t cols, const void* src_bf1
  * activations per token): codes = RNE(v * (127/amax)) in [-127, 127] and scale = amax/127, each step
  * rounded once in FP32; a row of zeros (or of values so small that 127/amax overflows) has codes 0
  * and scale 1; a row with a NaN or an infinity has codes 0 and scale NaN. cols a multiple of 8, src
- * 16-byte and codes 8-byte aligned (MOE_ERR_ARG). */
+ * 16-byte and codes 8-byte aligned (MOE_ERR_ARG); rows below 2^26 (MOE_ERR_UNSUPPORTED). */
 moe_status moe_quantize_rows_i8(int64_t rows, int32_t cols, const void* src_bf16, void* codes,
                                 float* scale, void* stream);
 
@@ -394,7 +394,7 @@ moe_status moe_stash_load(const void* pool, const float* pool_scale, int64_t liv
  * run on `compute`, which waits on `aux` only where it consumes aux work. On return
  * all work is ordered before later work on `compute`. Both streams at the default priority;
  * with compute == aux everything runs in issue order on that one stream. With `logits` NULL the
- * forward routes from x and `w_r` (moe_route_x; BF16 or FP8 descriptor, E % 32 == 0, E <= 256).
+ * forward routes from x and `w_r` (moe_route_x; BF16, FP8 or INT8 descriptor, E % 32 == 0, E <= 256).
  * The schedule's cross-stream dependencies use HIP events from a pool that the library creates
  * per host thread and device on first use and keeps until the process ends, so layer calls
  * issued from different threads never share events. Calls that share `workspace` or any saved-

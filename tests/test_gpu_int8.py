@@ -93,6 +93,25 @@ def test_grouped_product(off, N, K):
     _assert_product(*_product(torch, mh, rows, N, K, 4, off, len(off) + N))
 
 
+# More tiles than CUs, so that workgroups run several tiles in a row: one, two, three and four stages of K, a last
+# row tile of few rows and a last column tile of 8 columns
+@pytest.mark.parametrize("rows,N,K", [(4400, 4616, 64), (4400, 4616, 128), (4500, 4616, 192), (4608, 4616, 256)])
+def test_many_tiles_per_workgroup(rows, N, K):
+    torch, mh = _gpu()
+    _assert_product(*_product(torch, mh, rows, N, K, 1, None, K))
+
+
+def test_many_uneven_groups():
+    """Sixty groups of 0 to 900 rows: large and small row tiles of many groups, several per workgroup."""
+    torch, mh = _gpu()
+    rng = np.random.default_rng(12)
+    lens = rng.integers(0, 900, 60)
+    lens[[3, 17, 59]] = 0
+    lens[[4, 30]] = [256, 1]
+    off = [7] + list(7 + np.cumsum(lens))
+    _assert_product(*_product(torch, mh, int(off[-1]) + 9, 264, 192, 60, off, 13))
+
+
 def test_product_of_the_extreme_codes():
     """-128 everywhere at a long K: the int32 sum is 2^14 K."""
     torch, mh = _gpu()
@@ -185,6 +204,48 @@ def test_layer_forward(cfg):
     _, _, e = _layer(torch, mh, cfg, stages=False, two_streams=False)
     for o in (c, e):
         assert torch.equal(b["out"], o["out"]) and torch.equal(b["yd"], o["yd"])
+
+
+def test_layer_routes_from_x():
+    torch, mh = _gpu()
+    cfg = MoeConfig("i8_from_x", T=65, H=256, I=64, E=32, E_local=32, k=4, n_chunks=2, dtype="int8", seed_base=970)
+    inp, d, b = _layer(torch, mh, cfg, stages=True)
+    w_r = moe_inputs.make_inputs(cfg, parts=("w_r",))
+    b["w_r"] = harness.to_dev(w_r, "w_r", "bf16")
+    logits = torch.empty(cfg.T, cfg.E, device="cuda")
+    mh.moe_route_x(d, -1, b["x"], b["w_r"], logits, b["topk_idx"], b["gates"], b["counts"], b["offsets"], b["row_of"],
+                   b["src_token"], b["workspace"])
+    b["logits"] = logits
+    cs = torch.cuda.current_stream()
+    mh.moe_layer_forward(d, b, cs, cs)
+    torch.cuda.synchronize()
+    want = b["out"][:cfg.T].clone()
+    b["logits"] = None
+    mh.moe_layer_forward(d, b, cs, torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert torch.equal(b["out"][:cfg.T], want)
+
+
+def test_rows_region_wider_than_routing_needs():
+    """A caller's P_c above the static worst case, and its own table of rows that fills it: more experts have rows than
+    the descriptor's tokens could reach."""
+    torch, mh = _gpu()
+    T, H, I, El, k = 2, 128, 64, 24, 1
+    d = mh.make_desc(T=T, H=H, I=I, E=El, E_local=El, k=k, n_chunks=1, dtype="int8", P_c=48, P_out=4)
+    rng = np.random.default_rng(3)
+    xq, xs = rng.integers(-127, 128, (48, H)).astype(np.int8), (rng.random(48) + 0.1).astype(np.float32) * 0.01
+    w1, w2 = rng.integers(-127, 128, (El, 2 * I, H)).astype(np.int8), rng.integers(-127, 128, (El, H, I)).astype(np.int8)
+    w1s, w2s = np.full((El, 2 * I), 0.01, np.float32), np.full((El, H), 0.01, np.float32)
+    off = np.arange(0, 2 * El + 1, 2, dtype=np.int32)
+    dev = [torch.from_numpy(a).cuda() for a in (xq, xs, w1, w1s, w2, w2s, off)]
+    h, hs = torch.empty(5 * 48 * I, dtype=torch.uint8, device="cuda"), torch.empty(48, device="cuda")
+    yd = torch.zeros(48, H, dtype=torch.bfloat16, device="cuda")
+    mh.moe_expert_ffn(d, 0, dev[0], dev[1], dev[2], dev[3], dev[4], dev[5], dev[6], None, h, hs, yd)
+    torch.cuda.synchronize()
+    gu = oi8.matmul(xq, xs, w1, w1s, off)
+    hq, hsc = oi8.quantize_rows((gu[:, :I] / (1 + np.exp(-gu[:, :I])) * gu[:, I:]).astype(np.float32))
+    want = oi8.matmul(hq, hsc, w2, w2s, off)
+    assert np.linalg.norm(harness.to_np(yd) - want) <= OUT_TOL * np.linalg.norm(want)
 
 
 def test_a_row_that_is_not_finite_stays_visible_and_alone():

@@ -57,6 +57,7 @@ def test_quantize_rows_arguments():
     assert _status(q, 4, 16, None, 16, 16, 0) == -1 and _status(q, 4, 16, 16, None, 16, 0) == -1
     assert _status(q, 4, 16, 16, 16, None, 0) == -1
     assert _status(q, 4, 16, 24, 16, 16, 0) == -1 and _status(q, 4, 16, 16, 20, 16, 0) == -1
+    assert _status(q, 2 ** 26, 16, 16, 16, 16, 0) == -3
     assert _status(q, 0, 16, None, None, None, 0) == 0
 
 
@@ -68,7 +69,7 @@ def test_matmul_arguments():
     assert _mm(groups=-1) == -1 and _mm(rows=-1) == -1
     assert _mm(groups=1025) == -3 and _mm(rows=2 ** 31) == -3
     assert _mm(N=60) == -3 and _mm(N=0) == -3 and _mm(K=96) == -3 and _mm(K=0) == -3 and _mm(K=131072) == -3
-    assert _mm(N=65536, K=65536) == -3
+    assert _mm(N=65536, K=65536) == -3 and _mm(N=2 ** 21 + 8, K=64) == -3
     assert _mm(off=None) == -1 and _mm(groups=1, off=None, y=None) == -1
     for name in ("x", "xs", "w", "ws", "y"):
         assert _mm(**{name: None}) == -1
