@@ -57,16 +57,14 @@ constexpr int kI8MaxK = 131008;  // 128 * 128 * K <= 2^31 - 1, K a multiple of 6
 constexpr int64_t kRsrcMax = 0x7fffffff;  // bytes one raw buffer descriptor addresses
 
 // Whether an 8-bit integer product of `groups` groups with `rows` rows each on average and N columns goes
-// to the few-rows kernels. They stream the weights whatever the rows are, but load the rows again for every
-// column slice; the GEMM's time is that of a 256 x 256 tile's K loop times its rounds over the CUs.
-// Measured (few-rows / GEMM, us): 128 groups of K = 2048 and 768, 2 rows 126 / 168, 16 rows 182 / 183, 32
-// rows 236 / 194; 16 groups, 4 rows 29 / 44, 32 rows 43 / 46, 64 rows 65 / 47; one group of K = 2048, N =
-// 2048, 16 rows 9 / 21, 256 rows 25 / 33, 512 rows 44 / 33; N = 7168, 77 rows 14 / 23, 256 rows 29 / 33, 512
-// rows 52 / 34; K = 7168, N = 4096, 128 rows 39 / 66, 512 rows 127 / 92.
+// to the few-rows kernels. They stream the weights on every CU however few columns there are, but load the rows
+// again for every column slice; the GEMM needs some tiles (128 x 128 here) for its CUs and keeps its rows in LDS.
+// Measured (few-rows / GEMM, us): experts of K = 2048 and 768, 128 of them with 1 row 98 / 95, 2 rows 122 / 124, 8
+// rows 146 / 140, 32 rows 222 / 156; 16 experts, 4 rows 25 / 30, 16 rows 30 / 30, 64 rows 59 / 34; 2 experts, 32
+// rows 21 / 27, 128 rows 44 / 30; one group of K = 2048, N = 1536, 48 rows 7 / 11, 128 rows 11 / 12, 192 rows 17 /
+// 13; K = 7168, N = 4096, 64 rows 19 / 24, 96 rows 26 / 28, 128 rows 33 / 29.
 bool few_rows(int64_t groups, int64_t rows, int64_t N) {
-  if (rows <= 16) return true;
-  const int64_t tiles = groups * cdiv(N, 256) * cdiv(rows, 256);
-  return rows <= 320 && rows * groups * N <= 1000000 * cdiv(tiles, 256);
+  return rows <= 4 || (rows <= 128 && rows * groups * cdiv(N, 128) < 4608);
 }
 
 moe_status validate(const moe_desc* d) {
@@ -391,7 +389,7 @@ moe_status moe_expert_ffn(const moe_desc* d, int chunk, const void* xd, const fl
       return MOE_OK;
     }
     MOE_HIP(moe::launch_expert_fwd_i8(xd, xd_scale, w1, w1_scale, w2, w2_scale, offsets, h, h_scale, yd, d->H, d->I,
-                                      d->E_local, r.c0, r.nc, d->P_c, rows_of(d), (hipStream_t)stream),
+                                      d->E_local, r.c0, r.nc, d->P_c, rows_of(d), usual, (hipStream_t)stream),
             "expert_ffn_i8");
     return MOE_OK;
   }

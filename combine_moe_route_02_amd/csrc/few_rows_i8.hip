@@ -349,13 +349,17 @@ hipError_t run_few_nb(const char* name, FewArgs a, int64_t active, hipStream_t s
 template <int MODE, int KW>
 hipError_t run_few_kw(const char* name, const FewArgs& a, int cap, bool wide, int64_t active, hipStream_t s) {
   if (cap <= 16) return run_few_nb<MODE, KW, 1>(name, a, active, s);
-  if (cap <= 32) return run_few_nb<MODE, KW, 2>(name, a, active, s);
-  if constexpr (MODE == kFewCodes) {
-    if (wide && cap <= 64) return run_few_nb<MODE, KW, 4, true>(name, a, active, s);
-    if (wide) return run_few_nb<MODE, KW, 8, true>(name, a, active, s);
+  if constexpr (MODE != kFewDown && KW < 4) {
+    return run_few_nb<MODE, KW, 2>(name, a, active, s);  // cap <= 32
+  } else {
+    if (cap <= 32) return run_few_nb<MODE, KW, 2>(name, a, active, s);
+    if constexpr (MODE == kFewCodes) {
+      if (wide && cap <= 64) return run_few_nb<MODE, KW, 4, true>(name, a, active, s);
+      if (wide) return run_few_nb<MODE, KW, 8, true>(name, a, active, s);
+    }
+    if (cap <= 64) return run_few_nb<MODE, KW, 4>(name, a, active, s);
+    return run_few_nb<MODE, KW, 8>(name, a, active, s);
   }
-  if (cap <= 64) return run_few_nb<MODE, KW, 4>(name, a, active, s);
-  return run_few_nb<MODE, KW, 8>(name, a, active, s);
 }
 
 // rows: a bound of the rows of all groups; usual: the rows that one group has on average
@@ -374,8 +378,10 @@ hipError_t run_few(const char* name, FewArgs a, int64_t rows, int64_t usual, hip
   const bool wide = MODE == kFewCodes && cap >= 64 && active * ((a.N + 2 * kCols - 1) / (2 * kCols)) >= 192;
   const int per = wide ? 2 : 1;
   const int64_t cols = (a.N + per * kCols - 1) / (per * kCols), want = 2 * 256;
-  if (active * ((cols + 3) / 4) >= want) return run_few_kw<MODE, 1>(name, a, cap, wide, active, s);
-  if (active * ((cols + 1) / 2) >= want) return run_few_kw<MODE, 2>(name, a, cap, wide, active, s);
+  // (more than 32 rows on so many columns go to the GEMM, down's apart, whose columns are not the ones that decide)
+  const bool apart = MODE == kFewDown || cap <= 32;
+  if (apart && active * ((cols + 3) / 4) >= want) return run_few_kw<MODE, 1>(name, a, cap, wide, active, s);
+  if (apart && active * ((cols + 1) / 2) >= want) return run_few_kw<MODE, 2>(name, a, cap, wide, active, s);
   return run_few_kw<MODE, 4>(name, a, cap, wide, active, s);
 }
 

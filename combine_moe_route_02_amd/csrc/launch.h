@@ -78,7 +78,7 @@ hipError_t launch_expert_fwd_fp8(const void* xd, const float* xd_scale, const vo
                                  const int32_t* offsets, void* h, float* h_scale, void* yd, int H,
                                  int I, int El, int c0, int nc, int64_t P_c, int64_t P, hipStream_t s);
 // 8-bit integers (rows_i8.hip, i8_gemm.hip). h holds [P, I] FP32 values followed by [P, I] codes
-// (P = n_chunks * P_c).
+// (P = n_chunks * P_c); usual: rows of one expert in one chunk on average.
 hipError_t launch_quantize_rows_i8(const void* src, void* codes, float* scale, int64_t rows, int cols, hipStream_t s);
 hipError_t launch_dispatch_i8(const void* x, const int32_t* row_of, void* xd, float* xd_scale, int64_t t0, int64_t t1,
                               int K, int H, hipStream_t s);
@@ -87,7 +87,7 @@ hipError_t launch_quantize_h_i8(const float* h, void* codes, float* scale, const
 hipError_t launch_expert_fwd_i8(const void* xd, const float* xd_scale, const void* w1, const float* w1_scale,
                                 const void* w2, const float* w2_scale, const int32_t* offsets, void* h,
                                 float* h_scale, void* yd, int H, int I, int El, int c0, int nc, int64_t P_c,
-                                int64_t P, hipStream_t s);
+                                int64_t P, int64_t usual, hipStream_t s);
 // offsets null: one group of all rows
 hipError_t launch_expert_matmul_i8(int groups, int64_t rows, int N, int K, const void* x, const float* x_scale,
                                    const void* w, const float* w_scale, const int32_t* offsets, void* y,

@@ -101,6 +101,38 @@ def test_many_tiles_per_workgroup(rows, N, K):
     _assert_product(*_product(torch, mh, rows, N, K, 1, None, K))
 
 
+# Small tiles (128 x 128): rows past a few tiles, and tiles enough for two rounds with fewer stages than a tile's loads
+# run ahead
+@pytest.mark.parametrize("rows", [130, 200, 321, 513, 1025])
+@pytest.mark.parametrize("N,K", [(8, 64), (520, 192), (1032, 1088), (264, 2112)])
+def test_dense_product_of_many_rows(rows, N, K):
+    torch, mh = _gpu()
+    _assert_product(*_product(torch, mh, rows, N, K, 1, None, rows + N + K))
+
+
+@pytest.mark.parametrize("K", [64, 128, 192, 256, 320, 384, 448, 576])
+def test_small_tiles_in_a_row(K):
+    torch, mh = _gpu()
+    _assert_product(*_product(torch, mh, 2007, 2312, K, 1, None, K))
+
+
+# Few rows per group: whole K per wave (128 groups on 256 columns), halves of it (on 128), quarters; more groups than a
+# workgroup has threads, most of them empty; groups of more rows than a pass holds
+@pytest.mark.parametrize("G,N,K,low,high", [(128, 256, 320, 0, 9), (128, 136, 192, 0, 9), (128, 256, 64, 3, 4), (64, 128, 448, 0, 33),
+                                            (600, 72, 128, 0, 2), (16, 512, 320, 10, 40), (16, 512, 320, 20, 140),
+                                            (4, 200, 192, 60, 130), (2, 520, 1088, 100, 128)])
+def test_few_rows_of_many_groups(G, N, K, low, high):
+    torch, mh = _gpu()
+    rng = np.random.default_rng(G + N + K)
+    lens = rng.integers(low, high, G)
+    if G == 600:
+        lens *= rng.integers(0, 12, G) == 0
+    if G == 16:
+        lens[5] = 300 if high > 100 else 200
+    off = [3] + list(3 + np.cumsum(lens))
+    _assert_product(*_product(torch, mh, int(off[-1]) + 5, N, K, G, off, 17))
+
+
 def test_many_uneven_groups():
     """Sixty groups of 0 to 900 rows: large and small row tiles of many groups, several per workgroup."""
     torch, mh = _gpu()
@@ -154,6 +186,10 @@ CASES = [
     MoeConfig("i8_t1000", T=1000, H=256, I=192, E=32, E_local=8, e0=4, k=4, n_chunks=2, dtype="int8", seed_base=940),
     MoeConfig("i8_zipf", T=3000, H=512, I=256, E=32, E_local=8, k=8, n_chunks=2, dtype="int8", seed_base=950,
               zipf_s=1.2, n_empty=2),
+    MoeConfig("i8_small_tiles", T=700, H=448, I=192, E=8, E_local=5, e0=3, k=4, n_chunks=2, dtype="int8", seed_base=980),
+    MoeConfig("i8_large_tiles", T=4100, H=128, I=512, E=8, E_local=8, k=4, n_chunks=1, dtype="int8", seed_base=985),
+    MoeConfig("i8_down_wide", T=64, H=1024, I=64, E=32, E_local=32, k=8, n_chunks=1, dtype="int8", seed_base=990),
+    MoeConfig("i8_down_wide_rows", T=250, H=1088, I=64, E=32, E_local=32, k=8, n_chunks=1, dtype="int8", seed_base=995),
     MoeConfig("i8_wide", T=20, H=9216, I=64, E=8, E_local=4, k=2, n_chunks=1, dtype="int8", seed_base=960),
 ]
 
