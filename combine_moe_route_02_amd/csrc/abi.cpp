@@ -59,12 +59,20 @@ constexpr int64_t kRsrcMax = 0x7fffffff;  // bytes one raw buffer descriptor add
 // Whether an 8-bit integer product of `groups` groups with `rows` rows each on average and N columns goes
 // to the few-rows kernels. They stream the weights on every CU however few columns there are, but load the rows
 // again for every column slice; the GEMM needs some tiles (128 x 128 here) for its CUs and keeps its rows in LDS.
-// Measured (few-rows / GEMM, us): experts of K = 2048 and 768, 128 of them with 1 row 98 / 95, 2 rows 122 / 124, 8
-// rows 146 / 140, 32 rows 222 / 156; 16 experts, 4 rows 25 / 30, 16 rows 30 / 30, 64 rows 59 / 34; 2 experts, 32
-// rows 21 / 27, 128 rows 44 / 30; one group of K = 2048, N = 1536, 48 rows 7 / 11, 128 rows 11 / 12, 192 rows 17 /
-// 13; K = 7168, N = 4096, 64 rows 19 / 24, 96 rows 26 / 28, 128 rows 33 / 29.
+// Measured (few-rows / GEMM, us): one group of K = 2048, N = 1536, 48 rows 7 / 11, 128 rows 11 / 12, 192 rows 17 /
+// 13; K = 7168, N = 4096, 64 rows 19 / 24, 96 rows 26 / 28, 128 rows 33 / 29; 16 groups of K = 2048, N = 1536, 24
+// rows 15 / 12; of K = N = 512, 96 rows 6 / 8, 192 rows 9 / 8.
 bool few_rows(int64_t groups, int64_t rows, int64_t N) {
   return rows <= 4 || (rows <= 128 && rows * groups * cdiv(N, 128) < 4608);
+}
+
+// The same for both products of an expert layer: few rows save a launch (h is quantised inside down), but gate/up
+// and down load rows in proportion to all their products. Measured (few-rows / GEMM, us, the whole layer): H = 2048, I =
+// 768, 128 experts with 1 row 98 / 95, 2 rows 122 / 124, 8 rows 146 / 140, 32 rows 222 / 156; 16 experts, 4 rows
+// 25 / 30, 16 rows 30 / 30, 64 rows 59 / 34; 2 experts, 32 rows 21 / 27, 64 rows 32 / 29; H = 512, I = 256, 16
+// experts, 64 rows 23 / 24, 128 rows 35 / 25; H = 1024, I = 64, 128 experts, 16 rows 28 / 34, 64 rows 58 / 40.
+bool few_rows_layer(int64_t groups, int64_t rows, int64_t H, int64_t I) {
+  return rows <= 4 || (rows <= 64 && rows * groups * I * H <= 200000000);
 }
 
 moe_status validate(const moe_desc* d) {
@@ -381,7 +389,7 @@ moe_status moe_expert_ffn(const moe_desc* d, int chunk, const void* xd, const fl
   if (d->dtype == MOE_INT8) {
     MOE_NEED(xd_scale); MOE_NEED(w1_scale); MOE_NEED(w2_scale); MOE_NEED(h_scale);
     const int64_t usual = cdiv(tokens_per_chunk(d) * d->k, d->E);
-    if (few_rows(d->E_local, usual, 2 * (int64_t)d->I)) {
+    if (few_rows_layer(d->E_local, usual, d->H, d->I)) {
       MOE_HIP(moe::launch_expert_fwd_i8_few(xd, xd_scale, w1, w1_scale, w2, w2_scale, offsets, h, yd, d->H, d->I,
                                             d->E_local, r.c0, r.nc, d->P_c, rows_of(d), d->P_c * r.nc, usual,
                                             (hipStream_t)stream),
@@ -584,7 +592,8 @@ moe_status moe_dispatch_bwd(const moe_desc* d, int chunk, const void* dxd, const
   MOE_NEED(row_of); MOE_NEED(topk_idx); MOE_NEED(dlogits); MOE_NEED(w_r); MOE_NEED(dx);
   if (rows_of(d) > 0) MOE_NEED(dxd);
   if (d->flags & MOE_FLAG_ROUTER_LOSS) {
-    MOE_HIP(moe::launch_dispatch_bwd_dense(is_bf16_rows(d), dxd, dxd_scales(d, dxd), row_of, dlogits, w_r, dx, r.t0,
+    if (rows_of(d) == 0) dxd = nullptr;  // no row is read, whatever was passed
+    MOE_HIP(moe::launch_dispatch_bwd_dense(is_bf16_rows(d), dxd, dxd ? dxd_scales(d, dxd) : nullptr, row_of, dlogits, w_r, dx, r.t0,
                                            r.t1, d->k, d->E, d->H, (hipStream_t)stream),
             "dispatch_bwd_dense");
     return MOE_OK;

@@ -378,7 +378,8 @@ hipError_t run_few(const char* name, FewArgs a, int64_t rows, int64_t usual, hip
   const bool wide = MODE == kFewCodes && cap >= 64 && active * ((a.N + 2 * kCols - 1) / (2 * kCols)) >= 192;
   const int per = wide ? 2 : 1;
   const int64_t cols = (a.N + per * kCols - 1) / (per * kCols), want = 2 * 256;
-  // (more than 32 rows on so many columns go to the GEMM, down's apart, whose columns are not the ones that decide)
+  // (more than 32 rows on so many columns: a product goes to the GEMM, and gate/up comes here with a small H only;
+  // down has its own columns)
   const bool apart = MODE == kFewDown || cap <= 32;
   if (apart && active * ((cols + 3) / 4) >= want) return run_few_kw<MODE, 1>(name, a, cap, wide, active, s);
   if (apart && active * ((cols + 1) / 2) >= want) return run_few_kw<MODE, 2>(name, a, cap, wide, active, s);

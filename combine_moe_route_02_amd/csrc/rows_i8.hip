@@ -155,7 +155,7 @@ __global__ __launch_bounds__(256) void quantize_h_i8_kernel(const u32x4* __restr
                                                             int El, int c0, int64_t P_c, int64_t nvec) {
   const int lane = threadIdx.x & 63;
   const int c = c0 + (int)blockIdx.y;
-  const int64_t n = offsets[(int64_t)c * (El + 1) + El];
+  const int64_t n = min((int64_t)offsets[(int64_t)c * (El + 1) + El], P_c);  // no row past the chunk, whatever the table holds
   for (int64_t r = (int64_t)blockIdx.x * kI8RowsPerBlock + (threadIdx.x >> 6); r < n;
        r += (int64_t)gridDim.x * kI8RowsPerBlock) {
     const int64_t row = (int64_t)c * P_c + r;

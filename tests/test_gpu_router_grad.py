@@ -88,6 +88,13 @@ def test_dispatch_bwd(T, H, E, El, k, n, dtype):
         assert (again[min(T, (c + 1) * tc):] == -5.0).all()
 
 
+# FP32 takes any number of experts: around the chunks of 64, odd ones, a single one
+@pytest.mark.parametrize("T,H,E,El,k,n", [(33, 64, 1, 1, 1, 1), (5, 192, 3, 2, 2, 1), (64, 128, 63, 7, 8, 1), (65, 320, 65, 65, 8, 2),
+                                          (97, 192, 131, 40, 5, 1), (300, 1088, 127, 30, 6, 3)])
+def test_dispatch_bwd_f32_any_experts(T, H, E, El, k, n):
+    test_dispatch_bwd(T, H, E, El, k, n, "f32")
+
+
 @pytest.mark.parametrize("T,H,E,El,k,n", [SHAPES[2], SHAPES[3], SHAPES[5], SHAPES[8]])
 def test_dispatch_bwd_fp8_rows(T, H, E, El, k, n):
     torch, mh = _gpu()
