@@ -24,7 +24,6 @@
 namespace moe {
 
 constexpr int kLossThreads = 256;
-constexpr int kLossBatch = 4;                         // rows of a lane group in flight
 constexpr int kRedThreads = 1024;
 constexpr int kRedCols = 16;                          // columns per reduce block
 constexpr int kRedGroups = kRedThreads / kRedCols;    // tiles read side by side
@@ -80,7 +79,8 @@ int64_t router_loss_ws_bytes(int64_t T, int S, int E) {
 struct Pieces {
   const int32_t* off;  // [S + 1] or null: one segment of every row
   int64_t T;
-  int S, R;
+  int S, R;  // R rows per tile, 2^shift
+  int shift;
   MOE_DEV int64_t bound(int i) const {
     if (i == 0 || T == 0) return 0;
     if (i >= S + 2) return T;
@@ -88,7 +88,7 @@ struct Pieces {
     const int64_t o = off[i - 1];
     return o < 0 ? 0 : (o > T ? T : o);
   }
-  MOE_DEV int64_t base(int i) const { return bound(i) / R + i; }
+  MOE_DEV int64_t base(int i) const { return (bound(i) >> shift) + i; }
 };
 
 // The block's piece and rows. Every thread of the block calls it.
@@ -121,7 +121,7 @@ MOE_DEV float group_reduce(float v, Op&& op) {
   v = op(v, dpp<0xB1>(v));   // lane ^ 1
   v = op(v, dpp<0x4E>(v));   // lane ^ 2
   v = op(v, dpp<0x141>(v));  // mirror of 8 lanes
-  v = op(v, dpp<0x140>(v));  // mirror of 16 lanes
+  if constexpr (G >= 16) v = op(v, dpp<0x140>(v));  // mirror of 16 lanes
   if constexpr (G >= 32) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
@@ -137,21 +137,29 @@ MOE_DEV float group_sum(float v) { return group_reduce<G>(v, [](float a, float b
 template <int G>
 MOE_DEV float group_max(float v) { return group_reduce<G>(v, [](float a, float b) { return fmaxf(a, b); }); }
 
-// One row in a group of G lanes: lane q holds columns W * (i * G + q) .. + W of i < NV; columns past
-// E hold -inf.
+// One row in a group of G lanes: lane q holds columns W * (i * G + q) .. + W of i < NV. Loads carry no branch
+// (behind one the compiler waits for every load in flight): columns past E load the last ones, and
+// `keep` puts -inf there and everywhere in a row that does not count, whatever it holds.
 template <int G, int NV, int W>
 MOE_DEV void load_row(const float* row, int E, int q, float (&v)[NV * W]) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = W * (i * G + q);
+    const int e = min(W * (i * G + q), E - W);
     if constexpr (W == 4) {
-      const float inf = __builtin_huge_valf();
-      const float4 f = e < E ? *(const float4*)(row + e) : make_float4(-inf, -inf, -inf, -inf);
+      const float4 f = *(const float4*)(row + e);
       v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
     } else {
-      v[i] = e < E ? row[e] : -__builtin_huge_valf();
+      v[i] = row[e];
     }
   }
+}
+template <int G, int NV, int W>
+MOE_DEV void keep(float (&v)[NV * W], int E, int q, bool counted) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      v[i * W + w] = counted && W * (i * G + q) < E ? v[i * W + w] : -__builtin_huge_valf();
 }
 
 template <int G, int NV, int W>
@@ -178,24 +186,32 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_stats_kernel(
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
   double z = 0.0;  // lse reaches 1e38 where a row holds the lowest value: its square passes FP32
   int n = 0;
-  // U rows of a group are loaded together: a short input is bound by the latency of its loads. Every lane
-  // runs the same trip count, so the reductions are never divergent.
-  constexpr int U = kLossBatch;
+  // U rows of a group are loaded together (a short input is bound by the latency of its loads), and the next U while
+  // these are summed. Every lane runs the same trip count, so the reductions are never divergent.
+  constexpr int U = G >= 32 ? 4 : G / 8;  // (with 8 lanes a row, one pass is the smallest tile)
+  const uint8_t* const mk = mask ? mask : (const uint8_t*)logits;  // no mask: any readable byte, not looked at
+  struct Rows { float v[U][C]; int k[U]; uint8_t m[U]; };
+  auto load = [&](Rows& b, int64_t rb) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = min(rb + u * RP + g, t.r1 - 1);
+      load_row<G, NV, W>(logits + r * E, E, q, b.v[u]);
+      b.m[u] = mk[r];
+      b.k[u] = idx[r * K + min(q, K - 1)];
+    }
+  };
+  Rows next;
+  load(next, t.r0);
   for (int64_t rb = t.r0; rb < t.r1; rb += RP * U) {
-    float v[U][C];
+    Rows cur = next;
+    if (rb + RP * U < t.r1) load(next, rb + RP * U);
+    float (&v)[U][C] = cur.v;
     int my[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t r = rb + u * RP + g;
-      const bool counted = r < t.r1 && (!mask || mask[r] != 0);
-      my[u] = -1;
-      if (counted) {
-        load_row<G, NV, W>(logits + r * E, E, q, v[u]);
-        if (q < K) my[u] = idx[r * K + q];
-      } else {
-#pragma unroll
-        for (int c = 0; c < C; ++c) v[u][c] = -__builtin_huge_valf();
-      }
+      const bool counted = rb + u * RP + g < t.r1 && (!mask || cur.m[u] != 0);
+      keep<G, NV, W>(v[u], E, q, counted);
+      my[u] = counted && q < K ? cur.k[u] : -1;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -282,8 +298,8 @@ __global__ __launch_bounds__(kRedThreads) void router_loss_reduce_kernel(
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = tid % kRedCols, grp = tid / kRedCols;
   const int e = cb * kRedCols + col;
   const int64_t b0 = pc.bound(s + 1), b1 = pc.bound(s + 2);
-  const int64_t first = b0 / pc.R + s + 1;
-  int64_t end = b1 > b0 ? first + (b1 - b0 + pc.R - 1) / pc.R : first;
+  const int64_t first = (b0 >> pc.shift) + s + 1;
+  int64_t end = b1 > b0 ? first + ((b1 - b0 + pc.R - 1) >> pc.shift) : first;
   if (end > slots) end = slots;
 
   double p = 0.0, z = 0.0;
@@ -373,8 +389,8 @@ __global__ __launch_bounds__(kRedThreads) void router_loss_reduce_one_kernel(
   __shared__ double redp[kRedThreads], red[NW], redz[NW];
   __shared__ int redc[kRedThreads], redn[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = tid & (ec - 1), grp = tid / ec, groups = kRedThreads / ec;
-  const int64_t b0 = pc.bound(1), b1 = pc.bound(2), first = b0 / pc.R + 1;
-  int64_t end = b1 > b0 ? first + (b1 - b0 + pc.R - 1) / pc.R : first;
+  const int64_t b0 = pc.bound(1), b1 = pc.bound(2), first = (b0 >> pc.shift) + 1;
+  int64_t end = b1 > b0 ? first + ((b1 - b0 + pc.R - 1) >> pc.shift) : first;
   if (end > slots) end = slots;
   double p = 0.0, z = 0.0;
   int c = 0, n = 0;
@@ -429,28 +445,36 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_bwd_kernel(
   const bool outside = t.piece == 0 || t.piece == pc.S + 1;
   const int ns = outside ? 0 : seg_tokens[s];
   const int N = seg_tokens[pc.S], full = seg_tokens[pc.S + 1];
-  const int64_t even = (int64_t)ns * K;  // slots of the segment
+  const double even = (double)ns * K;  // slots of the segment (whole numbers below 2^53: exact)
   const float per = ns > 0 && full > 0 ? balance_coef / ((float)full * (float)ns * (float)even) : 0.f;
   const float zc = N > 0 ? 2.f * z_coef / (float)N : 0.f;
   const float gl = dloss ? *dloss : 1.f;
-  constexpr int U = kLossBatch;
+  constexpr int U = 4;
+  const uint8_t* const mk = mask ? mask : (const uint8_t*)logits;  // no mask: any readable byte, not looked at
+  struct Rows { float v[U][C], lse[U]; uint8_t m[U]; };
+  auto load = [&](Rows& b, int64_t rb) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = min(rb + u * RP + g, t.r1 - 1);
+      load_row<G, NV, W>(logits + r * E, E, q, b.v[u]);
+      b.lse[u] = lse_in[r];
+      b.m[u] = mk[r];
+    }
+  };
+  Rows next;
+  load(next, t.r0);
   float w[C];
   bool have_w = false;
   for (int64_t rb = t.r0; rb < t.r1; rb += RP * U) {
-    float v[U][C], lse[U];
+    Rows cur = next;
+    if (rb + RP * U < t.r1) load(next, rb + RP * U);
+    float (&v)[U][C] = cur.v, (&lse)[U] = cur.lse;
     bool counted[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t r = rb + u * RP + g;
-      counted[u] = r < t.r1 && !outside && (!mask || mask[r] != 0);
-      lse[u] = 0.f;
-      if (counted[u]) {
-        load_row<G, NV, W>(logits + r * E, E, q, v[u]);
-        lse[u] = lse_in[r];
-      } else {
-#pragma unroll
-        for (int c = 0; c < C; ++c) v[u][c] = -__builtin_huge_valf();
-      }
+      counted[u] = rb + u * RP + g < t.r1 && !outside && (!mask || cur.m[u] != 0);
+      keep<G, NV, W>(v[u], E, q, counted[u]);
+      lse[u] = counted[u] ? lse[u] : 0.f;
     }
     if (!have_w) {  // the segment's coefficients, behind the first rows' loads
       have_w = true;
@@ -459,7 +483,7 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_bwd_kernel(
 #pragma unroll
         for (int j = 0; j < W; ++j) {
           const int e = W * (i * G + q) + j;
-          w[i * W + j] = ns > 0 && e < E ? per * (float)((int64_t)seg_counts[(int64_t)s * E + e] * E - even) : 0.f;
+          w[i * W + j] = ns > 0 && e < E ? per * (float)((double)seg_counts[(int64_t)s * E + e] * E - even) : 0.f;
         }
     }
     // lse keeps only the digits that its size leaves, up to log E is lost where the logits are huge,
@@ -493,16 +517,18 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_bwd_kernel(
   }
 }
 
-// Lanes per row and registers per lane by E: a row of 16-byte vectors in as few lanes as leave one or
-// two vectors each (four above 512 experts); rows that are not whole aligned 16-byte vectors go by
-// single values.
-#define MOE_LOSS_SHAPE(E, vec, ...)                                                             \
+// Lanes per row and registers per lane by E; rows that are not whole aligned 16-byte vectors go by single values.
+// Forward: four vectors a lane where they fill them (two up to 64 experts), so that the steps of a row's
+// reductions serve more rows at once (35K tokens of 96 experts 10 us with one vector a lane, 7 us so).
+// Backward: one or two, because every lane forms the coefficients of its own columns first (512 tokens
+// of 128 experts 7.4 us with four vectors a lane, 5.3 us so).
+#define MOE_LOSS_SHAPE(E, vec, FWD, ...)                                                        \
   do {                                                                                          \
     if (vec) {                                                                                  \
-      if ((E) <= 64) { constexpr int G = 16, NV = 1, W = 4; __VA_ARGS__; }                      \
-      else if ((E) <= 128) { constexpr int G = 32, NV = 1, W = 4; __VA_ARGS__; }                \
-      else if ((E) <= 256) { constexpr int G = 32, NV = 2, W = 4; __VA_ARGS__; }                \
-      else if ((E) <= 512) { constexpr int G = 64, NV = 2, W = 4; __VA_ARGS__; }                \
+      if ((E) <= 64) { constexpr int G = FWD ? 8 : 16, NV = FWD ? 2 : 1, W = 4; __VA_ARGS__; }   \
+      else if ((E) <= 128) { constexpr int G = FWD ? 8 : 32, NV = FWD ? 4 : 1, W = 4; __VA_ARGS__; }  \
+      else if ((E) <= 256) { constexpr int G = FWD ? 16 : 32, NV = FWD ? 4 : 2, W = 4; __VA_ARGS__; } \
+      else if ((E) <= 512) { constexpr int G = FWD ? 32 : 64, NV = FWD ? 4 : 2, W = 4; __VA_ARGS__; } \
       else { constexpr int G = 64, NV = 4, W = 4; __VA_ARGS__; }                                \
     } else if ((E) <= 128) { constexpr int G = 64, NV = 2, W = 1; __VA_ARGS__; }                \
     else { constexpr int G = 64, NV = 16, W = 1; __VA_ARGS__; }                                 \
@@ -513,12 +539,13 @@ hipError_t launch_router_loss(const float* logits, const int32_t* topk_idx, cons
                               float* seg_probs, float* loss, void* workspace, int64_t T, int E, int K, int S,
                               float balance_coef, float z_coef, hipStream_t s) {
   const LossWs ws = loss_ws(workspace, T, S, E, nullptr);
-  const Pieces pc{seg_offsets, T, S, router_loss_tile(T)};
+  const int R = router_loss_tile(T);
+  const Pieces pc{seg_offsets, T, S, R, __builtin_ctz(R)};
   const int64_t slots = loss_slots(T, S);
   if (T > 0) {
     const bool vec = E % 4 == 0 && (uintptr_t)logits % 16 == 0;
     MOE_TRACE("router_loss_stats", s);
-    MOE_LOSS_SHAPE(E, vec, MOE_LAUNCH((router_loss_stats_kernel<G, NV, W>), dim3((unsigned)slots), dim3(kLossThreads), 0, s,
+    MOE_LOSS_SHAPE(E, vec, true, MOE_LAUNCH((router_loss_stats_kernel<G, NV, W>), dim3((unsigned)slots), dim3(kLossThreads), 0, s,
                                       logits, topk_idx, mask, lse, pc, ws, E, K));
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -542,11 +569,12 @@ hipError_t launch_router_loss_bwd(const float* logits, const float* lse, const i
                                   const float* dloss, float* dlogits, int64_t T, int E, int K, int S,
                                   float balance_coef, float z_coef, hipStream_t s) {
   if (T <= 0) return hipSuccess;
-  const Pieces pc{seg_offsets, T, S, router_loss_tile(T)};
+  const int R = router_loss_tile(T);
+  const Pieces pc{seg_offsets, T, S, R, __builtin_ctz(R)};
   const bool vec = E % 4 == 0 && (uintptr_t)logits % 16 == 0 && (uintptr_t)dlogits % 16 == 0;
   {
     MOE_TRACE("router_loss_bwd", s);
-    MOE_LOSS_SHAPE(E, vec, MOE_LAUNCH((router_loss_bwd_kernel<G, NV, W>), dim3((unsigned)loss_slots(T, S)),
+    MOE_LOSS_SHAPE(E, vec, false, MOE_LAUNCH((router_loss_bwd_kernel<G, NV, W>), dim3((unsigned)loss_slots(T, S)),
                                       dim3(kLossThreads), 0, s, logits, lse, mask, seg_counts, seg_tokens, dloss, dlogits,
                                       pc, E, K, balance_coef, z_coef));
   }
