@@ -109,6 +109,25 @@ def test_segments_and_masks(off, masked):
     _check(b, orl.router_loss(lg, idx, k, a, z, off, mask), k, a, z, 1.0)
 
 
+# Few tiles in several segments (one block adds them), at each lane shape, and just past that
+@pytest.mark.parametrize("T,E,k,S", [(12, 80, 3, 22), (1, 4, 1, 2), (40, 7, 2, 5), (65, 64, 8, 3), (300, 128, 8, 17), (200, 256, 4, 9),
+                                     (90, 512, 2, 8), (64, 1024, 8, 3), (33, 333, 5, 6), (2000, 60, 6, 40), (1400, 160, 3, 2),
+                                     (700, 512, 8, 30)])
+def test_few_tiles_in_segments(T, E, k, S):
+    torch, mh = _gpu()
+    rng, lg, idx = _draw(T, E, k, T + E + S, std=2.0)
+    mask = (rng.random(T) < 0.7).astype(np.uint8)
+    lg[mask == 0] = np.nan
+    off = np.sort(rng.integers(0, T + 1, S + 1)).astype(np.int32)
+    a, z, g = 0.7, 0.01, -0.6
+    d = _desc(mh, T, E, k)
+    b = _buffers(torch, mh, d, S)
+    _call(mh, d, S, a, z, torch.from_numpy(lg).cuda(), torch.from_numpy(idx).cuda(), torch.from_numpy(off).cuda(),
+          torch.from_numpy(mask).cuda(), torch.tensor([g], device="cuda"), b)
+    torch.cuda.synchronize()
+    _check(b, orl.router_loss(lg, idx, k, a, z, off.tolist(), mask), k, a, z, g)
+
+
 def test_rows_of_the_lowest_value():
     """A row that holds the type's lowest value everywhere is an even row; its lse squared passes FP32, so the z part
     is infinite and a loss that does not use it stays finite."""
