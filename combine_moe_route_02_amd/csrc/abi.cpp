@@ -54,6 +54,7 @@ int elem_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }  // payload rows (
 bool one_byte(const moe_desc* d) { return d->dtype == MOE_FP8_E4M3 || d->dtype == MOE_INT8; }  // forward only
 constexpr int kI8MaxN = 1 << 21;  // 256 rows of BF16 outputs within 2^30 bytes (one tile's buffer descriptor)
 constexpr int kI8MaxK = 131008;  // 128 * 128 * K <= 2^31 - 1, K a multiple of 64
+constexpr int64_t kFewMaxColumns = 1 << 28;  // of all groups: at most 2^24 workgroups of the few-rows kernels
 constexpr int64_t kRsrcMax = 0x7fffffff;  // bytes one raw buffer descriptor addresses
 
 // Whether an 8-bit integer product of `groups` groups with `rows` rows each on average and N columns goes
@@ -63,6 +64,7 @@ constexpr int64_t kRsrcMax = 0x7fffffff;  // bytes one raw buffer descriptor add
 // 13; K = 7168, N = 4096, 64 rows 19 / 24, 96 rows 26 / 28, 128 rows 33 / 29; 16 groups of K = 2048, N = 1536, 24
 // rows 15 / 12; of K = N = 512, 96 rows 6 / 8, 192 rows 9 / 8.
 bool few_rows(int64_t groups, int64_t rows, int64_t N) {
+  if (groups * N >= kFewMaxColumns) return false;
   return rows <= 4 || (rows <= 128 && rows * groups * cdiv(N, 128) < 4608);
 }
 
@@ -72,6 +74,7 @@ bool few_rows(int64_t groups, int64_t rows, int64_t N) {
 // 25 / 30, 16 rows 30 / 30, 64 rows 59 / 34; 2 experts, 32 rows 21 / 27, 64 rows 32 / 29; H = 512, I = 256, 16
 // experts, 64 rows 23 / 24, 128 rows 35 / 25; H = 1024, I = 64, 128 experts, 16 rows 28 / 34, 64 rows 58 / 40.
 bool few_rows_layer(int64_t groups, int64_t rows, int64_t H, int64_t I) {
+  if (groups * (I > H ? I : H) >= kFewMaxColumns) return false;
   return rows <= 4 || (rows <= 64 && rows * groups * I * H <= 200000000);
 }
 
@@ -593,7 +596,7 @@ moe_status moe_dispatch_bwd(const moe_desc* d, int chunk, const void* dxd, const
   if (rows_of(d) > 0) MOE_NEED(dxd);
   if (d->flags & MOE_FLAG_ROUTER_LOSS) {
     if (rows_of(d) == 0) dxd = nullptr;  // no row is read, whatever was passed
-    MOE_HIP(moe::launch_dispatch_bwd_dense(is_bf16_rows(d), dxd, dxd ? dxd_scales(d, dxd) : nullptr, row_of, dlogits, w_r, dx, r.t0,
+    MOE_HIP(moe::launch_dispatch_bwd_dense(is_bf16_rows(d), dxd, dxd_scales(d, dxd), row_of, dlogits, w_r, dx, r.t0,
                                            r.t1, d->k, d->E, d->H, (hipStream_t)stream),
             "dispatch_bwd_dense");
     return MOE_OK;
@@ -805,7 +808,8 @@ static moe_status route_any(const moe_desc* d, int c, const moe_tensors* t, hipS
   if (t->logits || d->T == 0)
     return moe_route(d, c, t->logits, t->topk_idx, t->gates, t->counts, t->offsets, t->row_of, t->src_token,
                      t->workspace, s);
-  return moe_route_x(d, c, t->x, t->w_r, (d->flags & MOE_FLAG_ROUTER_LOSS) ? t->router_logits : nullptr, t->topk_idx, t->gates, t->counts, t->offsets, t->row_of,
+  float* keep = (d->flags & MOE_FLAG_ROUTER_LOSS) ? t->router_logits : nullptr;
+  return moe_route_x(d, c, t->x, t->w_r, keep, t->topk_idx, t->gates, t->counts, t->offsets, t->row_of,
                      t->src_token, t->workspace, s);
 }
 

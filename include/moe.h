@@ -322,7 +322,7 @@ moe_status moe_quantize_cols_fp8(int64_t batch, int64_t rows, int32_t cols, cons
  * ascending; entries are clamped to [0, T]); NULL with n_segments = 1 is one segment of all T
  * tokens. Tokens before the first and behind the last segment, tokens whose token_mask entry
  * (device uint8 [T], nullable) is 0, and tokens whose logits are all -inf are left out: their
- * logits may hold anything (a masked row is not read) and reach no sum. For the counted tokens,
+ * logits may hold anything (they may be read, but reach no sum and no output). For the counted tokens,
  * with p_t = softmax(logits_t) over all E experts:
  *   seg_tokens[s] = n_s, seg_tokens[n_segments] = N = sum n_s, seg_tokens[n_segments + 1] = S',
  *     the segments with n_s > 0;                              int32 [n_segments + 2]

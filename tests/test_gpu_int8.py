@@ -284,6 +284,45 @@ def test_rows_region_wider_than_routing_needs():
     assert np.linalg.norm(harness.to_np(yd) - want) <= OUT_TOL * np.linalg.norm(want)
 
 
+def test_layer_without_tokens():
+    torch, mh = _gpu()
+    d = mh.make_desc(T=0, H=128, I=64, E=8, E_local=4, k=2, n_chunks=2, dtype="int8")
+    b = mh.allocate(d)
+    b["x"] = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    b["logits"] = torch.empty(0, 8, device="cuda")
+    for name, shape in (("w1", (4, 128, 128)), ("w2", (4, 128, 64))):
+        b[name], b[name + "_scale"] = torch.ones(shape, dtype=torch.int8, device="cuda"), torch.ones(shape[:2], device="cuda")
+    mh.moe_layer_forward(d, b, torch.cuda.current_stream(), torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert not b["offsets"].any().item()
+
+
+def test_products_side_by_side_on_two_streams():
+    """Two calls at once, each on its own stream and of another kind, give what each gives alone."""
+    torch, mh = _gpu()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    shapes = [(1, 40, 1024, 2048), (1, 900, 1032, 1088), (1, 5000, 2056, 320)]
+    data, want = [], []
+    for G, rows, N, K in shapes:
+        x = torch.randint(-127, 128, (rows, K), dtype=torch.int8, device="cuda", generator=g)
+        w = torch.randint(-127, 128, (G, N, K), dtype=torch.int8, device="cuda", generator=g)
+        xs, ws = torch.rand(rows, device="cuda", generator=g) + 0.1, torch.rand(G, N, device="cuda", generator=g) + 0.1
+        data.append((G, rows, N, K, x, xs, w, ws, None))
+        want.append(torch.empty(rows, N, dtype=torch.bfloat16, device="cuda"))
+        mh.moe_expert_matmul_i8(*data[-1], want[-1])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in shapes]
+    got = [[torch.empty_like(w) for w in want] for _ in range(4)]
+    torch.cuda.synchronize()
+    for ys in got:
+        for a, y, s in zip(data, ys, streams):
+            mh.moe_expert_matmul_i8(*a, y, s)
+    torch.cuda.synchronize()
+    for ys in got:
+        for y, w in zip(ys, want):
+            assert torch.equal(y, w)
+
+
 def test_a_row_that_is_not_finite_stays_visible_and_alone():
     torch, mh = _gpu()
     cfg = CASES[3]
@@ -297,7 +336,7 @@ def test_a_row_that_is_not_finite_stays_visible_and_alone():
     assert torch.equal(b["out"][keep], want[keep])
 
 
-@pytest.mark.parametrize("cfg", [CASES[0], CASES[3], CASES[6]], ids=["t1", "t33", "t1000"])
+@pytest.mark.parametrize("cfg", [CASES[0], CASES[3], CASES[6], CASES[7], CASES[9]], ids=["t1", "t33", "t1000", "small_tiles", "large_tiles"])
 def test_replays_of_a_graph(cfg):
     torch, mh = _gpu()
     inp, d, b = _layer(torch, mh, cfg, stages=True)

@@ -223,6 +223,22 @@ def test_layer_with_fp8_backward(flags):
     _check(*_layer(torch, mh, LAYERS[1], flags, "fused"), mh)
 
 
+def test_layer_without_tokens():
+    torch, mh = _gpu()
+    d = mh.make_desc(T=0, H=128, I=64, E=8, E_local=4, k=2, n_chunks=2, flags=mh.FLAG_ROUTER_LOSS)
+    b = mh.allocate(d, n_segments=2)
+    for name, shape in (("w1", (4, 128, 128)), ("w2", (4, 128, 64)), ("w_r", (8, 128))):
+        b[name] = torch.ones(shape, dtype=torch.bfloat16, device="cuda")
+    for name in ("x", "dy"):
+        b[name] = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    b.update(logits=torch.empty(0, 8, device="cuda"), seg_offsets=torch.zeros(3, dtype=torch.int32, device="cuda"), balance_coef=A, z_coef=Z)
+    b["router_loss"].fill_(9.0)
+    mh.moe_layer_forward_backward(d, b, torch.cuda.current_stream(), torch.cuda.Stream())
+    torch.cuda.synchronize()
+    for name in ("router_loss", "seg_tokens", "seg_counts", "seg_probs", "dwr", "dw1", "dw2"):
+        assert not b[name].float().any().item(), name
+
+
 def test_layer_is_the_same_on_one_stream_and_as_stages():
     torch, mh = _gpu()
     cfg = LAYERS[1]
