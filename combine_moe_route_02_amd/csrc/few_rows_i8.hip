@@ -157,7 +157,7 @@ MOE_DEV void few_pass(const FewArgs& a, int e, int64_t r0, int m0, int n, int n0
   constexpr int CW = kFewWaves / KW;              // waves side by side in columns
   constexpr int CS = chunk_k<NB>() / 64;          // K steps of a staged chunk
   // K steps of a batch (two in flight): about 16 KiB of weights and rows a wave
-  constexpr int UM = kStaged ? 8 : NB == 1 ? 8 / CB : NB == 2 ? 4 : NB <= 4 ? 2 : 1;
+  constexpr int UM = kStaged ? 8 / CB : NB == 1 ? 8 / CB : NB == 2 ? 4 : NB <= 4 ? 2 : 1;
   constexpr int U = kStaged && CS / KW < UM ? CS / KW : UM;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -302,8 +302,8 @@ MOE_DEV void few_pass(const FewArgs& a, int e, int64_t r0, int m0, int n, int n0
   }
 }
 
-// Weight operands of a wave, and columns of a workgroup. WIDE: a wave of the plain product takes 32 columns, so
-// that each load of rows serves two operands. NBM: blocks of 16 rows that a pass holds at most.
+// Weight operands of a wave, and columns of a workgroup. WIDE: a wave of the plain product or of down takes 32
+// columns, so that each load of rows serves two operands. NBM: blocks of 16 rows that a pass holds at most.
 template <int MODE, bool WIDE> constexpr int wave_operands() { return MODE == kFewGateUp || WIDE ? 2 : 1; }
 template <int KW, bool WIDE> constexpr int wg_cols() { return (WIDE ? 2 : 1) * kCols * kFewWaves / KW; }
 
@@ -342,8 +342,10 @@ hipError_t run_few_nb(const char* name, FewArgs a, int64_t active, hipStream_t s
   }
   lds += kScaleBytes;
   auto k = few_rows_i8_kernel<MODE, KW, NBM, WIDE>;
-  hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (e != hipSuccess) return e;
+  if (lds > 64 * 1024) {  // (the call is a good part of a small launch's host time)
+    hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
   {
     MOE_TRACE(name, s);
     MOE_LAUNCH(k, dim3((unsigned)(active * a.ctiles)), dim3(kFewThreads), lds, s, a);
@@ -382,6 +384,12 @@ hipError_t run_few(const char* name, FewArgs a, int64_t rows, int64_t usual, hip
   const bool wide = MODE == kFewCodes && cap >= 64 && active * ((a.N + 2 * kCols - 1) / (2 * kCols)) >= 192;
   const int per = wide ? 2 : 1;
   const int64_t cols = (a.N + per * kCols - 1) / (per * kCols), want = 2 * 256;
+  // Down with many columns: 32 a wave too, since every workgroup stages the rows first (33 tokens of 128 experts, H =
+  // 512, I = 256: the layer 25 -> 21 us; 4 tokens, H = 2048, I = 768 38 -> 34.5 us)
+  if constexpr (MODE == kFewDown) {
+    if (cap <= 32 && active * ((cols + 7) / 8) >= want)
+      return cap <= 16 ? run_few_nb<MODE, 1, 1, true>(name, a, active, s) : run_few_nb<MODE, 1, 2, true>(name, a, active, s);
+  }
   // (more than 32 rows on so many columns: a product goes to the GEMM, and gate/up comes here with a small H only;
   // down has its own columns)
   const bool apart = MODE == kFewDown || cap <= 32;

@@ -190,6 +190,8 @@ CASES = [
     MoeConfig("i8_large_tiles", T=4100, H=128, I=512, E=8, E_local=8, k=4, n_chunks=1, dtype="int8", seed_base=985),
     MoeConfig("i8_down_wide", T=64, H=1024, I=64, E=32, E_local=32, k=8, n_chunks=1, dtype="int8", seed_base=990),
     MoeConfig("i8_down_wide_rows", T=250, H=1088, I=64, E=32, E_local=32, k=8, n_chunks=1, dtype="int8", seed_base=995),
+    MoeConfig("i8_down_32_columns", T=8, H=2048, I=64, E=32, E_local=32, k=8, n_chunks=1, dtype="int8", seed_base=1000),
+    MoeConfig("i8_down_32_columns_rows", T=41, H=2112, I=128, E=32, E_local=32, k=8, n_chunks=1, dtype="int8", seed_base=1005),
     MoeConfig("i8_wide", T=20, H=9216, I=64, E=8, E_local=4, k=2, n_chunks=1, dtype="int8", seed_base=960),
 ]
 
