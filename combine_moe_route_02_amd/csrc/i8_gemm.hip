@@ -55,8 +55,7 @@ struct I8Args {
 
 struct Groups {
   int pre[kMaxGroups + 1], preb[kMaxGroups + 1];  // tiles before group g: large, small
-  int64_t r0[kMaxGroups];
-  int len[kMaxGroups];
+  int o0[kMaxGroups], len[kMaxGroups];
 };
 
 struct I8Tile {
@@ -65,10 +64,6 @@ struct I8Tile {
   int64_t abytes, bbytes, r0;
   int mvalid, n0, e;
 };
-
-MOE_DEV int64_t uniform64(int64_t v) {
-  return ((int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
-}
 
 // Running sums of v[1 .. G] in place, by one wave.
 MOE_DEV void scan(int* v, int G, int lane) {
@@ -84,6 +79,17 @@ MOE_DEV void scan(int* v, int G, int lane) {
     if (g0 + lane < G) v[g0 + lane + 1] = before + x;
     before += __builtin_amdgcn_readlane(x, 63);
   }
+}
+
+// The same of one value per lane, in registers (a chain of DPP steps).
+MOE_DEV int scan64(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8: sums inside 16 lanes
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // lane 15 to lanes 16 .. 31, 47 to 48 .. 63
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // lane 31 to lanes 32 .. 63
+  return x;
 }
 
 // Group of a tile: the groups whose tiles end at or before it.
@@ -126,25 +132,39 @@ __global__ __launch_bounds__(I8Shape<SMALL>::kThreads) void i8_gemm_kernel(I8Arg
   const int G = a.nc * a.El, ntiles = (a.N + OUTN - 1) / OUTN;
   // "large" row tiles (full, or a last one of more than half the rows) come before the "small" last ones,
   // which fill a last round where one is needed
-  for (int g = tid; g < G; g += kThreads) {
+  auto rows_of = [&](int g, int& o0, int& len, int& large, int& small) {
     const int c = a.c0 + g / a.El, e = g % a.El;
-    int o0 = 0, o1 = (int)a.P_c;
+    o0 = 0;
+    int o1 = (int)a.P_c;
     if (a.offsets) {  // nothing outside the rows, whatever the table holds
       const int32_t* off = a.offsets + (int64_t)c * (a.El + 1);
       o0 = max(0, min(off[e], (int)a.P_c));
       o1 = max(o0, min(off[e + 1], (int)a.P_c));
     }
-    const int len = o1 - o0, rem = len % kTile;
-    sh.r0[g] = (int64_t)c * a.P_c + o0;
-    sh.len[g] = len;
-    sh.pre[g + 1] = (len / kTile + (rem > kTile / 2 ? 1 : 0)) * ntiles;
-    sh.preb[g + 1] = (rem > 0 && rem <= kTile / 2 ? 1 : 0) * ntiles;
+    len = o1 - o0;
+    const int rem = len % kTile;
+    large = (len / kTile + (rem > kTile / 2 ? 1 : 0)) * ntiles;
+    small = (rem > 0 && rem <= kTile / 2 ? 1 : 0) * ntiles;
+  };
+  // Up to 64 groups stay in registers, one per lane of every wave: the first tile's loads then wait for
+  // neither LDS nor a barrier.
+  const bool in_lanes = G <= 64;
+  int l_o0 = 0, l_len = 0, l_pre = 0, l_preb = 0, total_l, total_s;
+  if (in_lanes) {
+    if (lane < G) rows_of(lane, l_o0, l_len, l_pre, l_preb);
+    l_pre = scan64(l_pre);
+    l_preb = scan64(l_preb);
+    total_l = __builtin_amdgcn_readlane(l_pre, 63);
+    total_s = __builtin_amdgcn_readlane(l_preb, 63);
+  } else {
+    for (int g = tid; g < G; g += kThreads) rows_of(g, sh.o0[g], sh.len[g], sh.pre[g + 1], sh.preb[g + 1]);
+    __syncthreads();
+    if (wave == 0) scan(sh.pre, G, lane);
+    if (wave == 1) scan(sh.preb, G, lane);
+    __syncthreads();
+    total_l = __builtin_amdgcn_readfirstlane(sh.pre[G]);
+    total_s = __builtin_amdgcn_readfirstlane(sh.preb[G]);
   }
-  __syncthreads();
-  if (wave == 0) scan(sh.pre, G, lane);
-  if (wave == 1) scan(sh.preb, G, lane);
-  __syncthreads();
-  const int total_l = sh.pre[G], total_s = sh.preb[G];
   // each XCD (block % 8) owns a contiguous range of the large and one of the small tiles
   const int pxl = (total_l + 7) / 8, pxs = (total_s + 7) / 8;
   const int xcd = blockIdx.x % 8, per_xcd = gridDim.x / 8;
@@ -154,13 +174,25 @@ __global__ __launch_bounds__(I8Shape<SMALL>::kThreads) void i8_gemm_kernel(I8Arg
       const bool large = slot < pxl;
       const int tile = large ? xcd * pxl + slot : xcd * pxs + (slot - pxl);
       if (tile >= (large ? total_l : total_s)) continue;
-      const int* pre = large ? sh.pre : sh.preb;
-      const int g = group_of(pre, G, tile, lane);
-      const int at = tile - __builtin_amdgcn_readfirstlane(pre[g]), len = __builtin_amdgcn_readfirstlane(sh.len[g]);
+      int g, before, len, o0;
+      if (in_lanes) {
+        const int pre = large ? l_pre : l_preb;
+        g = __popcll(__ballot(pre <= tile));  // (lanes past the groups hold the total)
+        before = g > 0 ? __builtin_amdgcn_readlane(pre, g - 1) : 0;
+        len = __builtin_amdgcn_readlane(l_len, g);
+        o0 = __builtin_amdgcn_readlane(l_o0, g);
+      } else {
+        const int* pre = large ? sh.pre : sh.preb;
+        g = group_of(pre, G, tile, lane);
+        before = __builtin_amdgcn_readfirstlane(pre[g]);
+        len = __builtin_amdgcn_readfirstlane(sh.len[g]);
+        o0 = __builtin_amdgcn_readfirstlane(sh.o0[g]);
+      }
+      const int at = tile - before;
       const int mt = large ? at / ntiles : len / kTile;
       t.e = g % a.El;
       t.n0 = (at % ntiles) * OUTN;
-      t.r0 = uniform64(sh.r0[g]) + (int64_t)mt * kTile;
+      t.r0 = (int64_t)(a.c0 + g / a.El) * a.P_c + o0 + (int64_t)mt * kTile;
       t.mvalid = min(kTile, len - mt * kTile);
       const int64_t wrows = GU ? 2 * (int64_t)a.N : a.N;
       t.a = (const char*)a.A + t.r0 * a.K;
