@@ -27,8 +27,7 @@ namespace moe {
 
 constexpr int kLossThreads = 256;
 constexpr int kRedThreads = 1024;
-constexpr int kRedCols = 16;                          // columns per reduce block
-constexpr int kRedGroups = kRedThreads / kRedCols;    // tiles read side by side
+constexpr int kRedCols = 16;  // columns per reduce block (the fewest)
 
 // Rows per tile: about 1024 tiles for long inputs (four 256-thread blocks per CU), down to 32 rows.
 int router_loss_tile(int64_t T) {
@@ -285,20 +284,23 @@ MOE_DEV int lanes_sum(int v) {
   return v;
 }
 
-// Adds the tiles of each segment in a fixed order: one block per segment and 16 columns, 64 tiles side
-// by side (a wave holds 4 tiles x 16 columns), one barrier. With more than one block the last to
-// arrive forms the losses from the segments' sums.
-__global__ __launch_bounds__(kRedThreads) void router_loss_reduce_kernel(
+// Adds the tiles of each segment in a fixed order: one block of RT threads per segment and RC columns, RT / RC
+// tiles side by side, one barrier. The last block to arrive forms the losses from the segments' sums. 1024
+// threads on 16 columns (64 tiles at once), or, for segments of a few tiles, 256 on 32: fewer lanes
+// without a tile and half the arrivals (267 tokens of 212 experts in 57 segments, with their gradient, 26 -> 20 us,
+// 11973 of 184 in 63 29 -> 23 us; one wide segment of 1000 tiles 10 us of its own).
+template <int RT, int RC>
+__global__ __launch_bounds__(RT) void router_loss_reduce_kernel(
     Pieces pc, LossWs ws, int64_t slots, int E, int K, float balance_coef, float z_coef, int32_t* __restrict__ seg_counts,
     int32_t* __restrict__ seg_tokens, float* __restrict__ seg_probs, float* __restrict__ loss) {
-  constexpr int NW = kRedThreads / kWave;
-  __shared__ double red[NW][kRedCols + 1];
-  __shared__ int redc[NW][kRedCols + 1];
+  constexpr int NW = RT / kWave;
+  __shared__ double red[NW][RC + 1];
+  __shared__ int redc[NW][RC + 1];
   __shared__ bool last;
-  const int nb = (E + kRedCols - 1) / kRedCols;
+  const int nb = (E + RC - 1) / RC;
   const int s = blockIdx.x / nb, cb = blockIdx.x % nb;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = tid % kRedCols, grp = tid / kRedCols;
-  const int e = cb * kRedCols + col;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = tid % RC, grp = tid / RC;
+  const int e = cb * RC + col;
   const int64_t b0 = pc.bound(s + 1), b1 = pc.bound(s + 2);
   const int64_t first = (b0 >> pc.shift) + s + 1;
   int64_t end = b1 > b0 ? first + ((b1 - b0 + pc.R - 1) >> pc.shift) : first;
@@ -308,36 +310,36 @@ __global__ __launch_bounds__(kRedThreads) void router_loss_reduce_kernel(
   int c = 0, n = 0;
   if (e < E)
 #pragma unroll 8
-    for (int64_t i = first + grp; i < end; i += kRedGroups) {
+    for (int64_t i = first + grp; i < end; i += (RT / RC)) {
       p += (double)ws.p[i * E + e];
       c += ws.c[i * E + e];
     }
   if (cb == 0)
-    for (int64_t i = first + tid; i < end; i += kRedThreads) { z += ws.z[i]; n += ws.n[i]; }
-  p = lanes_sum<kRedCols>(p);
-  c = lanes_sum<kRedCols>(c);
-  if (lane < kRedCols) { red[wave][lane] = p; redc[wave][lane] = c; }
+    for (int64_t i = first + tid; i < end; i += RT) { z += ws.z[i]; n += ws.n[i]; }
+  p = lanes_sum<RC>(p);
+  c = lanes_sum<RC>(c);
+  if (lane < RC) { red[wave][lane] = p; redc[wave][lane] = c; }
   if (cb == 0) {
     z = lanes_sum<1>(z);
     n = lanes_sum<1>(n);
-    if (lane == 0) { red[wave][kRedCols] = z; redc[wave][kRedCols] = n; }
+    if (lane == 0) { red[wave][RC] = z; redc[wave][RC] = n; }
   }
   __syncthreads();
   if (wave == 0) {
     p = 0.0;
     c = 0;
-    if (lane < kRedCols || (cb == 0 && lane == kRedCols))
+    if (lane < RC || (cb == 0 && lane == RC))
 #pragma unroll
       for (int w = 0; w < NW; ++w) { p += red[w][lane]; c += redc[w][lane]; }
-    if (lane < kRedCols && e < E) {
+    if (lane < RC && e < E) {
       seg_probs[(int64_t)s * E + e] = (float)p;
       seg_counts[(int64_t)s * E + e] = c;
     }
-    const double cp = lanes_sum<1>(lane < kRedCols && e < E ? p * (double)c : 0.0);
+    const double cp = lanes_sum<1>(lane < RC && e < E ? p * (double)c : 0.0);
     // What the last block reads is stored and loaded past the XCD's L2 (device-scope atomics), so the
     // stores need only be complete before the arrival: a fence would write the whole L2 back.
     if (lane == 0) st_device(&ws.cp[(int64_t)s * nb + cb], cp);
-    if (cb == 0 && lane == kRedCols) { st_device(&ws.zs[s], p); st_device(&seg_tokens[s], c); }
+    if (cb == 0 && lane == RC) { st_device(&ws.zs[s], p); st_device(&seg_tokens[s], c); }
     asm volatile("" ::: "memory");
     wait_vm<0>();
     asm volatile("" ::: "memory");
@@ -349,7 +351,7 @@ __global__ __launch_bounds__(kRedThreads) void router_loss_reduce_kernel(
   z = 0.0;
   n = 0;
   int full = 0;
-  for (int i = tid; i < pc.S; i += kRedThreads) {
+  for (int i = tid; i < pc.S; i += RT) {
     const int ns = ld_device(&seg_tokens[i]);
     const double zs = ld_device(&ws.zs[i]);  // an empty segment's sums are zeros
     double cp = 0.0;
@@ -436,7 +438,7 @@ __global__ __launch_bounds__(kRedThreads) void router_loss_reduce_one_kernel(
 // Several segments of few tiles: one block loads all their partials into LDS at once and adds each segment's in tile
 // order (12 tokens in 22 segments 4.8 us, 7 us with the exchange between blocks; in the forward's last block, which
 // has to wait for the others' stores, 6 us). One segment by the kernel above is 0.5 us faster than here.
-constexpr size_t kSmallLds = 60 * 1024;
+constexpr size_t kSmallLds = 30 * 1024;  // (more takes as long here as with the exchange)
 struct SmallSlot { double z; int n, first, end; };  // a tile's sums; the tiles of segment i (there are more tiles than segments)
 static size_t small_lds(int64_t slots, int E) { return (size_t)(slots * (sizeof(SmallSlot) + 8 * (int64_t)E)); }
 
@@ -637,8 +639,11 @@ hipError_t launch_router_loss(const float* logits, const int32_t* topk_idx, cons
                balance_coef, z_coef, seg_counts, seg_tokens, seg_probs, loss);
   } else {
     MOE_TRACE("router_loss_reduce", s);
-    MOE_LAUNCH(router_loss_reduce_kernel, dim3((unsigned)((int64_t)S * red_blocks(E))), dim3(kRedThreads), 0, s, pc, ws,
-               slots, E, K, balance_coef, z_coef, seg_counts, seg_tokens, seg_probs, loss);
+    const bool narrow = slots <= 40 * (int64_t)S;
+    const int rc = narrow ? 2 * kRedCols : kRedCols, rt = narrow ? 256 : kRedThreads;
+    MOE_LAUNCH(narrow ? (router_loss_reduce_kernel<256, 2 * kRedCols>) : (router_loss_reduce_kernel<kRedThreads, kRedCols>),
+               dim3((unsigned)((int64_t)S * ((E + rc - 1) / rc))), dim3(rt), 0, s, pc, ws, slots, E, K, balance_coef, z_coef,
+               seg_counts, seg_tokens, seg_probs, loss);
   }
   return hipGetLastError();
 }

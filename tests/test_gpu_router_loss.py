@@ -112,7 +112,7 @@ def test_segments_and_masks(off, masked):
 # Few tiles in several segments (one block adds them), at each lane shape, and just past that
 @pytest.mark.parametrize("T,E,k,S", [(12, 80, 3, 22), (1, 4, 1, 2), (40, 7, 2, 5), (65, 64, 8, 3), (300, 128, 8, 17), (200, 256, 4, 9),
                                      (90, 512, 2, 8), (64, 1024, 8, 3), (33, 333, 5, 6), (2000, 60, 6, 40), (1400, 160, 3, 2),
-                                     (700, 512, 8, 30)])
+                                     (700, 512, 8, 30), (5, 136, 4, 58), (267, 212, 8, 57), (3000, 64, 4, 2), (4000, 100, 3, 40)])
 def test_few_tiles_in_segments(T, E, k, S):
     torch, mh = _gpu()
     rng, lg, idx = _draw(T, E, k, T + E + S, std=2.0)
