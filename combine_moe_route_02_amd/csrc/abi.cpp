@@ -57,25 +57,28 @@ constexpr int kI8MaxK = 131008;  // 128 * 128 * K <= 2^31 - 1, K a multiple of 6
 constexpr int64_t kFewMaxColumns = 1 << 28;  // of all groups: at most 2^24 workgroups of the few-rows kernels
 constexpr int64_t kRsrcMax = 0x7fffffff;  // bytes one raw buffer descriptor addresses
 
-// Whether an 8-bit integer product of `groups` groups with `rows` rows each on average and N columns goes
+// Whether an 8-bit integer product of `groups` groups with `rows` rows each on average, N columns and K terms goes
 // to the few-rows kernels. They stream the weights on every CU however few columns there are, but load the rows
-// again for every column slice; the GEMM needs some tiles (128 x 128 here) for its CUs and keeps its rows in LDS.
-// Measured (few-rows / GEMM, us): one group of K = 2048, N = 1536, 48 rows 7 / 11, 128 rows 11 / 12, 192 rows 17 /
-// 13; K = 7168, N = 4096, 64 rows 19 / 24, 96 rows 26 / 28, 128 rows 33 / 29; 16 groups of K = 2048, N = 1536, 24
-// rows 15 / 12; of K = N = 512, 96 rows 6 / 8, 192 rows 9 / 8.
-bool few_rows(int64_t groups, int64_t rows, int64_t N) {
+// again for every column slice; the GEMM needs some tiles for its CUs and keeps its rows in LDS.
+// Measured (few-rows / GEMM, us): one group of K = 2048, N = 1536, 48 rows 6.6 / 8.9, 96 rows 9.2 / 9.1, 128 rows
+// 11.4 / 9.1; N = 7168, 32 rows 8.0 / 8.6, 80 rows 10.1 / 9.1; K = 7168, N = 4096, 32 rows 12.5 / 16.4, 64 rows 18.8 /
+// 17.5; 8 groups of K = 2048, N = 1536, 17 rows 9.4 / 9.2, 32 rows 10.8 / 9.2; of K = 768, N = 2048, 32 rows 6.7 / 7.0,
+// 64 rows 9.5 / 7.2; 16 groups of K = N = 512, 96 rows 5.9 / 6.3. Long sums favour the few-rows kernels, whose waves
+// share them: K counts to 2048.
+bool few_rows(int64_t groups, int64_t rows, int64_t N, int64_t K) {
   if (groups * N >= kFewMaxColumns) return false;
-  return rows <= 4 || (rows <= 128 && rows * groups * cdiv(N, 128) < 4608);
+  return rows <= 4 || (rows <= 96 && rows * groups * cdiv(N, 128) * (K < 2048 ? K : 2048) <= 3200000);
 }
 
-// The same for both products of an expert layer: few rows save a launch (h is quantised inside down), but gate/up
-// and down load rows in proportion to all their products. Measured (few-rows / GEMM, us, the whole layer): H = 2048, I =
-// 768, 128 experts with 1 row 98 / 95, 2 rows 122 / 124, 8 rows 146 / 140, 32 rows 222 / 156; 16 experts, 4 rows
-// 25 / 30, 16 rows 30 / 30, 64 rows 59 / 34; 2 experts, 32 rows 21 / 27, 64 rows 32 / 29; H = 512, I = 256, 16
-// experts, 64 rows 23 / 24, 128 rows 35 / 25; H = 1024, I = 64, 128 experts, 16 rows 28 / 34, 64 rows 58 / 40.
+// The same for both products of an expert layer: few rows save a launch (h is quantised inside down), but their
+// workgroups read rows again and again; next to the weights' 3 H I bytes an expert that is hidden up to a point. Measured
+// (few-rows / GEMM, us, the whole layer): H = 2048, I = 768, 128 experts with 1 row 96 / 96, 2 rows 121 / 125, 16 rows
+// 165 / 145; 16 experts, 4 rows 26 / 29, 16 rows 30 / 29, 64 rows 59 / 33; 2 experts, 32 rows 21 / 24, 64 rows 32 / 25;
+// H = 512, I = 256, 128 experts, 16 rows 25 / 33, 32 rows 44 / 34; 16 experts, 32 rows 19 / 22, 128 rows 36 / 25; H =
+// 256, I = 640, 56 experts, 22 rows 45 / 29; H = 1024, I = 64, 128 experts, 32 rows 35 / 36, 64 rows 58 / 40.
 bool few_rows_layer(int64_t groups, int64_t rows, int64_t H, int64_t I) {
   if (groups * (I > H ? I : H) >= kFewMaxColumns) return false;
-  return rows <= 4 || (rows <= 64 && rows * groups * I * H <= 200000000);
+  return rows <= 4 || (rows <= 48 && moe::few_rows_i8_traffic(groups, rows, H, I) <= 40000000 + 3 * groups * H * I / 5);
 }
 
 moe_status validate(const moe_desc* d) {
@@ -648,7 +651,7 @@ moe_status moe_expert_matmul_i8(int32_t groups, int64_t rows, int32_t N, int32_t
   MOE_NEED(x); MOE_NEED(x_scale); MOE_NEED(w); MOE_NEED(w_scale); MOE_NEED(y);
   if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)y) & 15)
     return fail(MOE_ERR_ARG, "%s: x, w and y must be 16-byte aligned", __func__);
-  const bool few = few_rows(groups, cdiv(rows, groups), N);
+  const bool few = few_rows(groups, cdiv(rows, groups), N, K);
   MOE_HIP((few ? moe::launch_expert_matmul_i8_few : moe::launch_expert_matmul_i8)(groups, rows, N, K, x, x_scale, w,
                                                                                   w_scale, offsets, y, (hipStream_t)stream),
           "expert_matmul_i8");

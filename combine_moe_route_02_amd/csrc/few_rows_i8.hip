@@ -369,13 +369,26 @@ hipError_t run_few_kw(const char* name, const FewArgs& a, int cap, bool wide, in
 }
 
 // rows: a bound of the rows of all groups; usual: the rows that one group has on average
+// Rows of a pass: enough for nearly every group when rows spread by chance (their deviation is the square root
+// of the mean), so that weights are read once; a fuller group takes more passes.
+int pass_rows(int64_t usual, bool spread) {
+  const double most = (double)usual + (spread ? 4.0 * std::sqrt((double)usual) : 0.0);
+  int cap = 16;
+  while (cap < kMaxRows && cap < most) cap *= 2;
+  return cap;
+}
+constexpr int64_t kWant = 2 * 256;  // workgroups: one or two for every CU
+// Column slices of 16 that a workgroup of down takes. With many columns 32 a wave, since every workgroup stages
+// the rows first (33 tokens of 128 experts, H = 512, I = 256: the layer 25 -> 21 us; 4 tokens, H = 2048, I =
+// 768 38 -> 34.5 us); then the widest slice that gives every CU a workgroup or two.
+int down_slices(int64_t active, int64_t cols, int cap) {
+  if (cap <= 32 && active * ((cols + 7) / 8) >= kWant) return 8;
+  return active * ((cols + 3) / 4) >= kWant ? 4 : active * ((cols + 1) / 2) >= kWant ? 2 : 1;
+}
+
 template <int MODE>
 hipError_t run_few(const char* name, FewArgs a, int64_t rows, int64_t usual, hipStream_t s) {
-  // Rows of a pass: enough for nearly every group when rows spread by chance (their deviation is the
-  // square root of the mean), so that weights are read once; a fuller group takes more passes.
-  const double most = (double)usual + 4.0 * std::sqrt((double)usual);
-  int cap = 16;
-  while (cap < kMaxRows && cap < (a.offsets ? most : (double)usual)) cap *= 2;
+  const int cap = pass_rows(usual, a.offsets != nullptr);
   a.listed = a.offsets && rows < a.groups;  // fewer rows than groups: list the groups that have some
   const int64_t active = a.listed ? rows : a.groups;
   // Plain products of more than 32 rows take 32 columns a wave where that leaves most CUs a workgroup (77 rows x
@@ -383,22 +396,30 @@ hipError_t run_few(const char* name, FewArgs a, int64_t rows, int64_t usual, hip
   // slice that still gives every CU a workgroup or two.
   const bool wide = MODE == kFewCodes && cap >= 64 && active * ((a.N + 2 * kCols - 1) / (2 * kCols)) >= 192;
   const int per = wide ? 2 : 1;
-  const int64_t cols = (a.N + per * kCols - 1) / (per * kCols), want = 2 * 256;
-  // Down with many columns: 32 a wave too, since every workgroup stages the rows first (33 tokens of 128 experts, H =
-  // 512, I = 256: the layer 25 -> 21 us; 4 tokens, H = 2048, I = 768 38 -> 34.5 us)
+  const int64_t cols = (a.N + per * kCols - 1) / (per * kCols);
   if constexpr (MODE == kFewDown) {
-    if (cap <= 32 && active * ((cols + 7) / 8) >= want)
-      return cap <= 16 ? run_few_nb<MODE, 1, 1, true>(name, a, active, s) : run_few_nb<MODE, 1, 2, true>(name, a, active, s);
+    switch (down_slices(active, cols, cap)) {
+      case 8: return cap <= 16 ? run_few_nb<MODE, 1, 1, true>(name, a, active, s) : run_few_nb<MODE, 1, 2, true>(name, a, active, s);
+      case 4: return run_few_kw<MODE, 1>(name, a, cap, false, active, s);
+      case 2: return run_few_kw<MODE, 2>(name, a, cap, false, active, s);
+      default: return run_few_kw<MODE, 4>(name, a, cap, false, active, s);
+    }
+  } else {
+    // (more than 32 rows on so many columns: a product goes to the GEMM, and gate/up comes here with a small H only)
+    if (cap <= 32 && active * ((cols + 3) / 4) >= kWant) return run_few_kw<MODE, 1>(name, a, cap, wide, active, s);
+    if (cap <= 32 && active * ((cols + 1) / 2) >= kWant) return run_few_kw<MODE, 2>(name, a, cap, wide, active, s);
+    return run_few_kw<MODE, 4>(name, a, cap, wide, active, s);
   }
-  // (more than 32 rows on so many columns: a product goes to the GEMM, and gate/up comes here with a small H only;
-  // down has its own columns)
-  const bool apart = MODE == kFewDown || cap <= 32;
-  if (apart && active * ((cols + 3) / 4) >= want) return run_few_kw<MODE, 1>(name, a, cap, wide, active, s);
-  if (apart && active * ((cols + 1) / 2) >= want) return run_few_kw<MODE, 2>(name, a, cap, wide, active, s);
-  return run_few_kw<MODE, 4>(name, a, cap, wide, active, s);
 }
 
 }  // namespace
+
+// Bytes of rows that an expert layer's workgroups read here: gate/up every row of H codes for each 16 columns, down
+// every row of I FP32 values for each workgroup.
+int64_t few_rows_i8_traffic(int64_t groups, int64_t usual, int64_t H, int64_t I) {
+  const int64_t cols = (H + kCols - 1) / kCols, per = down_slices(groups, cols, pass_rows(usual, true));
+  return groups * usual * (I / kCols * H + (cols + per - 1) / per * I * 4);
+}
 
 // rows: a bound of the rows of chunks c0 .. c0 + nc - 1 together; usual: one expert's in one chunk on average
 hipError_t launch_expert_fwd_i8_few(const void* xd, const float* xd_scale, const void* w1, const float* w1_scale,

@@ -1,6 +1,6 @@
 // Grouped GEMMs of the 8-bit integer experts: v_mfma_i32_32x32x32_i8 on tiles of 256 x 256 (8 waves of 128 x 64,
 // operands by direct-to-LDS loads into two slots of 128-byte rows) or, where those are too few for the CUs, of
-// 128 x 128 (4 waves of 64 x 64, four slots).
+// 128 x 128 (4 waves of 64 x 64, four slots) or 64 x 64 (4 waves of 32 x 32, eight slots).
 //
 // Integer products take half the time of BF16 ones, so what surrounds a tile's K loop (its first loads, sums
 // through LDS into rows with a barrier on each side, stores) weighs double. Here the list of tiles is one
@@ -18,7 +18,10 @@
 // 90 us, down 59 us).
 // Small tiles: 0.5 us a pair of stages, bound by LDS (a pair's 64 fragment reads take as long as its products, and
 // the loads' writes come on top: the same time with loads of nothing). They stream weights at HBM's rate
-// (128 groups of 24 rows x 2048 on 1536 columns 81 us, 5.0 TB/s). Eight waves of 32 x 64 take the same time.
+// (128 groups of 24 rows x 2048 on 1536 columns 81 us, 5.0 TB/s). Eight waves of 32 x 64 take the same time. Tiny
+// tiles: 0.3 us a pair, so four of them on four CUs beat a small one (256 rows x 7168 on 4096 columns 28 -> 21 us).
+// Tiles of 256 x 192 gain with even groups (gate/up of 16 x 1024 rows 60 -> 55 us) and lose with uneven ones,
+// whose small last tiles then make a third round (65 -> 83 us).
 // The sums are exact in int32 and rounded once to FP32; scales multiply in FP32 and BF16 rounds once.
 #include <type_traits>
 
@@ -29,14 +32,15 @@ namespace gg {
 namespace {
 
 // Tiles of kTile x kTile, waves kWM x kWN, each with kMN x kNN blocks of 32 x 32
-template <bool SMALL> struct I8Shape {
-  static constexpr int kTile = SMALL ? 128 : 256, kWM = 2, kWN = SMALL ? 2 : 4;
+enum { kLarge = 256, kSmall = 128, kTiny = 64 };
+template <int TILE> struct I8Shape {
+  static constexpr int kTile = TILE, kWM = 2, kWN = TILE == kLarge ? 4 : 2;
   static constexpr int kThreads = 64 * kWM * kWN;
   static constexpr int kMN = kTile / kWM / 32, kNN = kTile / kWN / 32;
   static constexpr int kSlotA = kTile * 2 * kRowB, kSlot = 2 * kSlotA;  // pair slot: rows of A, then of B
-  static constexpr int kSlots = SMALL ? 4 : 2, kRing = kSlots * kSlot;
-  static constexpr int kStores = 4 * kMN;                               // buffer stores of a wave per tile
-  static_assert(kNN == 2 && kThreads == 2 * kTile, "64 columns per wave; one scale per thread");
+  static constexpr int kSlots = 512 / kTile, kRing = kSlots * kSlot;    // 128 KB
+  static constexpr int kStores = 2 * kMN * kNN;                         // buffer stores of a wave per tile
+  static_assert(kThreads >= 2 * kTile, "one scale per thread");
 };
 constexpr int kOutside = 0x7ffffff0;  // past every output descriptor's extent (at most 2^30 bytes)
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
@@ -99,32 +103,39 @@ MOE_DEV int group_of(const int* pre, int G, int tile, int lane) {
   return __builtin_amdgcn_readfirstlane(g);
 }
 
-// A lane's scales of a tile from LDS: its four rows, and eight groups of four columns (the second four GAP
-// bytes further on). Written in assembly because the compiler would first wait for every direct-to-LDS
+// A lane's scales of a tile from LDS: its rows (of four blocks, or one), and four groups of four columns of
+// each column block. Written in assembly because the compiler would first wait for every direct-to-LDS
 // load in flight, those of the next tile's first stages here, which fill another part of LDS.
-template <int GAP>
 MOE_DEV void read_scales(uint32_t rows, uint32_t cols, float (&r)[4], f32x4_t (&c)[8]) {
   asm volatile(
       "ds_read_b32 %0, %12\n\tds_read_b32 %1, %12 offset:128\n\t"
       "ds_read_b32 %2, %12 offset:256\n\tds_read_b32 %3, %12 offset:384\n\t"
       "ds_read_b128 %4, %13\n\tds_read_b128 %5, %13 offset:32\n\t"
       "ds_read_b128 %6, %13 offset:64\n\tds_read_b128 %7, %13 offset:96\n\t"
-      "ds_read_b128 %8, %13 offset:%14\n\tds_read_b128 %9, %13 offset:%14+32\n\t"
-      "ds_read_b128 %10, %13 offset:%14+64\n\tds_read_b128 %11, %13 offset:%14+96\n\t"
+      "ds_read_b128 %8, %13 offset:128\n\tds_read_b128 %9, %13 offset:160\n\t"
+      "ds_read_b128 %10, %13 offset:192\n\tds_read_b128 %11, %13 offset:224\n\t"
       "s_waitcnt lgkmcnt(0)"
       : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(c[0]), "=&v"(c[1]), "=&v"(c[2]), "=&v"(c[3]),
         "=&v"(c[4]), "=&v"(c[5]), "=&v"(c[6]), "=&v"(c[7])
-      : "v"(rows), "v"(cols), "n"(GAP)
+      : "v"(rows), "v"(cols)
+      : "memory");
+}
+MOE_DEV void read_scales(uint32_t rows, uint32_t cols, float (&r)[4], f32x4_t (&c)[4]) {
+  asm volatile(
+      "ds_read_b32 %0, %5\n\tds_read_b128 %1, %6\n\tds_read_b128 %2, %6 offset:32\n\t"
+      "ds_read_b128 %3, %6 offset:64\n\tds_read_b128 %4, %6 offset:96\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(r[0]), "=&v"(c[0]), "=&v"(c[1]), "=&v"(c[2]), "=&v"(c[3])
+      : "v"(rows), "v"(cols)
       : "memory");
 }
 
-template <bool GU, bool SMALL>
-__global__ __launch_bounds__(I8Shape<SMALL>::kThreads) void i8_gemm_kernel(I8Args a) {
-  using S = I8Shape<SMALL>;
+template <bool GU, int TILE>
+__global__ __launch_bounds__(I8Shape<TILE>::kThreads) void i8_gemm_kernel(I8Args a) {
+  using S = I8Shape<TILE>;
   constexpr int kTile = S::kTile, kWN = S::kWN, kThreads = S::kThreads, kMN = S::kMN, kNN = S::kNN, kSlots = S::kSlots;
   constexpr int OUTN = GU ? kTile / 2 : kTile;  // output columns of a tile
   __shared__ Groups sh;
-  __shared__ float scales[kSlots][2 * kTile];  // rows, then columns (gate/up: gate columns, then up)
+  __shared__ float scales[kSlots][2 * kTile];  // rows, then columns in the order of the tile's rows of B
   extern __shared__ __attribute__((aligned(1024))) char ring[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -207,14 +218,15 @@ __global__ __launch_bounds__(I8Shape<SMALL>::kThreads) void i8_gemm_kernel(I8Arg
 
   // loads of a pair of stages: 8 rows of 128 bytes per wave instruction, chunks swizzled as km2_off reads them
   constexpr int NI = kTile / (kThreads / 8);
+  // gate/up: 32 rows of the tile are 16 gate rows and the 16 up rows of the same columns, so that a lane's sums
+  // of one block hold both
+  auto brow = [&](int r) { return !GU ? r : r / 32 * 16 + (r % 32 < 16 ? r % 32 : a.N + r % 32 - 16); };
   uint32_t va[NI], vb[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int r = 8 * (wave * NI + i) + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
-    // gate/up: each wave's 64 tile rows are 32 gate rows and the 32 up rows of the same columns
-    const int q = r % 64, br = GU ? (r / 64) * 32 + (q < 32 ? q : a.N + q - 32) : r;
     va[i] = (uint32_t)(r * a.K) + 16u * c;
-    vb[i] = (uint32_t)((int64_t)br * a.K) + 16u * c;
+    vb[i] = (uint32_t)((int64_t)brow(r) * a.K) + 16u * c;
   }
   const uint32_t rl = lds_addr(ring);
   auto issue = [&](const I8Tile& t, bool any, int pair, uint32_t at) {
@@ -230,12 +242,13 @@ __global__ __launch_bounds__(I8Shape<SMALL>::kThreads) void i8_gemm_kernel(I8Arg
 
   // A tile's scales, one per thread, through LDS: held per lane they would take 36 registers
   auto issue_scales = [&](const I8Tile& t, int buf) {
+    if (wave >= 2 * kTile / 64) return;
     const uint32_t l0 = lds_addr(scales[0]) + (uint32_t)(buf * (2 * kTile * 4) + wave * 256);
-    const int wrows = GU ? 2 * a.N : a.N, c = tid - kTile;
+    const int wrows = GU ? 2 * a.N : a.N;
     const bool rows = wave < kTile / 64;
     const auto r = rows ? make_rsrc(a.scale_a + t.r0, (int64_t)t.mvalid * 4)
                         : make_rsrc(a.scale_b + (int64_t)t.e * wrows + t.n0, (int64_t)(wrows - t.n0) * 4);
-    const int at = rows ? tid : GU && c >= OUTN ? a.N + c - OUTN : c;
+    const int at = rows ? tid : brow(tid - kTile);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(uintptr_t)l0, 4, 4 * at, 0, 0, 0);
   };
 
@@ -265,7 +278,7 @@ __global__ __launch_bounds__(I8Shape<SMALL>::kThreads) void i8_gemm_kernel(I8Arg
     issue_ld(i);
     if (++ldp == np) next_ld();
   }
-  const int arow0 = wm * (kTile / 2), brow0 = wn * 64;
+  const int arow0 = wm * (kTile / 2), brow0 = wn * 32 * kNN;
   const int inside = max(0, np - kAhead);  // pairs whose loads are of the same tile
   int buf = 0, tbuf = 0;
   bool first = true;
@@ -311,20 +324,20 @@ __global__ __launch_bounds__(I8Shape<SMALL>::kThreads) void i8_gemm_kernel(I8Arg
       }
     };
     const int blocks = __builtin_amdgcn_readfirstlane(max(0, min(kMN, (cur.mvalid - arow0 + 31) / 32)));
-    if (!SMALL && blocks == 4) kloop(std::integral_constant<int, kMN>());
-    else if (!SMALL && blocks == 3) kloop(std::integral_constant<int, kMN - 1>());
-    else if (blocks == 2) kloop(std::integral_constant<int, 2>());
+    if (kMN == 4 && blocks == 4) kloop(std::integral_constant<int, kMN == 4 ? 4 : 0>());
+    else if (kMN == 4 && blocks == 3) kloop(std::integral_constant<int, kMN == 4 ? 3 : 0>());
+    else if (kMN >= 2 && blocks == 2) kloop(std::integral_constant<int, kMN >= 2 ? 2 : 0>());
     else if (blocks == 1) kloop(std::integral_constant<int, 1>());
     else kloop(std::integral_constant<int, 0>());
     first = false;
     // out: lane l holds row l & 31 of a block and columns 8 g + 4 (l >> 5) .. + 3 of its group g
-    const int col0 = GU ? wn * 32 : wn * 64;  // the wave's first output column in the tile
+    const int col0 = wn * (OUTN / kWN);  // the wave's first output column in the tile
     const int nvalid = min(OUTN, a.N - cur.n0);
-    float sa[4];  // (two of a small tile's are not used)
-    f32x4_t sb[8];  // gate/up: four groups of gate columns, four of up; else those of the two column blocks
+    float sa[4];  // (those past the wave's blocks are not used)
+    f32x4_t sb[4 * kNN];
     const uint32_t at = lds_addr(scales[0]) + (uint32_t)(tbuf * (2 * kTile * 4));
     tbuf = (tbuf + 1) % kSlots;
-    read_scales<GU ? OUTN * 4 : 128>(at + 4 * (arow0 + out_row(lane)), at + 4 * (kTile + col0 + 4 * (lane >> 5)), sa, sb);
+    read_scales(at + 4 * (arow0 + out_row(lane)), at + 4 * (kTile + brow0 + 4 * (lane >> 5)), sa, sb);
     constexpr int ES = GU ? 4 : 2;
     const int64_t ld = (int64_t)a.N * ES;
     const auto rc = make_rsrc((char*)a.C + cur.r0 * ld + (int64_t)cur.n0 * ES, (cur.mvalid - 1) * ld + (int64_t)nvalid * ES);
@@ -334,17 +347,19 @@ __global__ __launch_bounds__(I8Shape<SMALL>::kThreads) void i8_gemm_kernel(I8Arg
       const uint32_t row = (uint32_t)(m * ld);
       if constexpr (GU) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          f32x4_t h;
+        for (int tn = 0; tn < kNN; ++tn)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float gv = (float)acc[tm][0][4 * g + q] * (sa[tm] * sb[g][q]);
-            const float uv = (float)acc[tm][1][4 * g + q] * (sa[tm] * sb[4 + g][q]);
-            h[q] = gv * sigmoidf_(gv) * uv;
+          for (int g = 0; g < 2; ++g) {
+            f32x4_t h;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float gv = (float)acc[tm][tn][4 * g + q] * (sa[tm] * sb[4 * tn + g][q]);
+              const float uv = (float)acc[tm][tn][8 + 4 * g + q] * (sa[tm] * sb[4 * tn + 2 + g][q]);
+              h[q] = gv * sigmoidf_(gv) * uv;
+            }
+            const int c = col0 + 16 * tn + out_col(g, lane);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, h), rc, c < nvalid ? (int)(row + 4 * c) : kOutside, 0, 0);
           }
-          const int c = col0 + out_col(g, lane);
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, h), rc, c < nvalid ? (int)(row + 4 * c) : kOutside, 0, 0);
-        }
       } else {
 #pragma unroll
         for (int tn = 0; tn < kNN; ++tn)
@@ -371,17 +386,17 @@ __global__ __launch_bounds__(I8Shape<SMALL>::kThreads) void i8_gemm_kernel(I8Arg
   wait_vm<0>();  // the last loads (of nothing) still write zeros to this workgroup's LDS
 }
 
-template <bool GU, bool SMALL>
+template <bool GU, int TILE>
 hipError_t run_i8_tiles(const char* name, const I8Args& a, int64_t tiles, hipStream_t s) {
-  auto k = i8_gemm_kernel<GU, SMALL>;
-  hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, I8Shape<SMALL>::kRing);
+  auto k = i8_gemm_kernel<GU, TILE>;
+  hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, I8Shape<TILE>::kRing);
   if (e != hipSuccess) return e;
   if (tiles <= 0) return hipSuccess;
   // (large and small tiles are shared out to the XCDs apart, each with up to 7 places over)
   const int64_t grid = persistent_grid(tiles + 14);
   {
     MOE_TRACE(name, s);
-    MOE_LAUNCH(k, dim3((unsigned)grid), dim3(I8Shape<SMALL>::kThreads), I8Shape<SMALL>::kRing, s, a);
+    MOE_LAUNCH(k, dim3((unsigned)grid), dim3(I8Shape<TILE>::kThreads), I8Shape<TILE>::kRing, s, a);
   }
   return hipGetLastError();
 }
@@ -389,9 +404,12 @@ hipError_t run_i8_tiles(const char* name, const I8Args& a, int64_t tiles, hipStr
 // usual: rows of one group on average
 template <bool GU>
 hipError_t run_i8(const char* name, const I8Args& a, int64_t usual, hipStream_t s) {
-  // per chunk at most floor(P_c / tile) + El row tiles; the device-side count decides the work
+  // per chunk at most floor(P_c / tile) + El row tiles; the device-side count decides the work. Of groups of uneven
+  // length every second or so has a row tile more than the average fills.
+  const int64_t uneven = a.offsets ? 1 : 0;
   auto tiles = [&](int64_t tile, bool bound) {
-    const int64_t outn = GU ? tile / 2 : tile, mt = bound ? a.P_c / tile + a.El : a.El * ((usual + tile - 1) / tile);
+    const int64_t outn = GU ? tile / 2 : tile;
+    const int64_t mt = bound ? a.P_c / tile + a.El : a.El * ((usual + uneven * (tile / 2) + tile - 1) / tile);
     return a.nc * mt * ((a.N + outn - 1) / outn);
   };
   const int64_t cus = cu_count();
@@ -399,8 +417,11 @@ hipError_t run_i8(const char* name, const I8Args& a, int64_t usual, hipStream_t 
   // A round of large tiles takes two to three times as long as one of small ones (the same once they leave CUs
   // idle): 2000 rows x 4096 on 4096 columns 49 (one round) against 47 us (two), 3000 rows 52 (one) against 69
   // (three), 336 rows x 6848 on 2848 columns 66 against 31 us (one of each).
-  if (rounds(128) <= 2 * rounds(256)) return run_i8_tiles<GU, true>(name, a, tiles(128, true), s);
-  return run_i8_tiles<GU, false>(name, a, tiles(256, true), s);
+  // A round of tiny tiles takes about 0.65 of one of small ones: 518 rows x 5568 on 448 columns 15 (one round) against
+  // 23 us (one), 336 rows x 6848 on 2848 columns 33 (two) against 31 us (one).
+  if (rounds(64) <= rounds(128)) return run_i8_tiles<GU, kTiny>(name, a, tiles(64, true), s);
+  if (rounds(128) <= 2 * rounds(256)) return run_i8_tiles<GU, kSmall>(name, a, tiles(128, true), s);
+  return run_i8_tiles<GU, kLarge>(name, a, tiles(256, true), s);
 }
 
 }  // namespace

@@ -94,6 +94,7 @@ hipError_t launch_expert_matmul_i8(int groups, int64_t rows, int N, int K, const
                                    hipStream_t s);
 // the same products for a few rows per group (few_rows_i8.hip); rows: a bound of the rows of all groups,
 // usual: one group's on average
+int64_t few_rows_i8_traffic(int64_t groups, int64_t usual, int64_t H, int64_t I);
 hipError_t launch_expert_fwd_i8_few(const void* xd, const float* xd_scale, const void* w1, const float* w1_scale,
                                     const void* w2, const float* w2_scale, const int32_t* offsets, void* h,
                                     void* yd, int H, int I, int El, int c0, int nc, int64_t P_c, int64_t P,

@@ -120,7 +120,8 @@ def test_small_tiles_in_a_row(K):
 # workgroup has threads, most of them empty; groups of more rows than a pass holds
 @pytest.mark.parametrize("G,N,K,low,high", [(128, 256, 320, 0, 9), (128, 136, 192, 0, 9), (128, 256, 64, 3, 4), (64, 128, 448, 0, 33),
                                             (600, 72, 128, 0, 2), (16, 512, 320, 10, 40), (16, 512, 320, 20, 140),
-                                            (4, 200, 192, 60, 130), (2, 520, 1088, 100, 128)])
+                                            (4, 200, 192, 60, 130), (2, 520, 1088, 100, 128), (2, 520, 192, 60, 96),
+                                            (300, 64, 576, 20, 60), (80, 56, 1088, 30, 70)])
 def test_few_rows_of_many_groups(G, N, K, low, high):
     torch, mh = _gpu()
     rng = np.random.default_rng(G + N + K)
