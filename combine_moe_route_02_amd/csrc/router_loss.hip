@@ -639,7 +639,7 @@ hipError_t launch_router_loss(const float* logits, const int32_t* topk_idx, cons
                balance_coef, z_coef, seg_counts, seg_tokens, seg_probs, loss);
   } else {
     MOE_TRACE("router_loss_reduce", s);
-    const bool narrow = slots <= 40 * (int64_t)S;
+    const bool narrow = slots <= 30 * (int64_t)S;
     const int rc = narrow ? 2 * kRedCols : kRedCols, rt = narrow ? 256 : kRedThreads;
     MOE_LAUNCH(narrow ? (router_loss_reduce_kernel<256, 2 * kRedCols>) : (router_loss_reduce_kernel<kRedThreads, kRedCols>),
                dim3((unsigned)((int64_t)S * ((E + rc - 1) / rc))), dim3(rt), 0, s, pc, ws, slots, E, K, balance_coef, z_coef,
