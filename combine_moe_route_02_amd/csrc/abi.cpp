@@ -421,7 +421,7 @@ moe_status moe_combine(const moe_desc* d, int chunk, const void* yd, const float
   MOE_NEED(gates); MOE_NEED(row_of); MOE_NEED(out);
   if (rows_of(d) > 0) MOE_NEED(yd);
   MOE_HIP(moe::launch_combine(is_bf16_rows(d), yd, gates, row_of, out, r.t0, r.t1, d->k,
-                              (int64_t)d->H * elem_size(d->dtype), (hipStream_t)stream), "combine");
+                              (int64_t)d->H * elem_size(d->dtype), (hipStream_t)stream, d->dtype == MOE_INT8), "combine");
   return MOE_OK;
 }
 

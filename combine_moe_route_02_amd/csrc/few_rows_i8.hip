@@ -50,7 +50,7 @@ struct FewArgs {
   const int8_t* w;          // per group [N, K] (gate/up: [2 N, K], gate rows first)
   const float* w_scale;     // per group [N] ([2 N])
   float* out_h;             // kFewGateUp: [P, N]
-  uint16_t* y;              // else: [P, N] BF16
+  uint16_t* y;              // kFewCodes: [P, N] BF16; kFewDown: rows of yd (i8.h)
   const int32_t* offsets;   // null: one group of P_c rows
   int64_t P_c;
   int K, N, El, c0, groups; // groups = El * chunks
@@ -247,7 +247,7 @@ MOE_DEV void few_pass(const FewArgs& a, int e, int64_t r0, int m0, int n, int n0
   auto finish = [&](int b, float srow, const i32x4_t (&v)[CB]) {
     const int m = m0 + 16 * b + lr;
     const int64_t row = r0 + min(m, n - 1);
-    if constexpr (MODE == kFewDown) srow = scales[2 * (min(m, n - 1) - m0) + 1];
+    if constexpr (MODE == kFewDown) srow = scales[2 * (min(m, n - 1) - m0) + 1] * kYdUnit;
     float o[4];
     if constexpr (MODE == kFewGateUp) {
       uint32_t big = 0;
@@ -267,7 +267,9 @@ MOE_DEV void few_pass(const FewArgs& a, int e, int64_t r0, int m0, int n, int n0
 #pragma unroll
         for (int q = 0; q < 4; ++q) o[q] = (float)v[cb][q] * (srow * sb[cb][q]);
         const int at = c + kCols * cb;
-        if (m < n && at < a.N) *(uint2*)(a.y + row * a.N + at) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+        const uint2 p = MODE == kFewDown ? make_uint2(pack_yd(o[0], o[1]), pack_yd(o[2], o[3]))
+                                         : make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+        if (m < n && at < a.N) *(uint2*)(a.y + row * a.N + at) = p;
       }
     }
   };

@@ -35,4 +35,21 @@ MOE_DEV uint2 codes8(const u32x4& v, float inv) {
                     codes4(bf2f(v.z & 0xffff), bf2f(v.z >> 16), bf2f(v.w & 0xffff), bf2f(v.w >> 16), inv));
 }
 
+// Rows of yd between the experts and combine: 16 bits of sign, 7 exponent bits (bias 63) and 8 mantissa bits. With
+// BF16 there, its rounding and the output's are two of the same size in a row (sqrt(2) of one); with one bit more
+// the first is half (1.12). Magnitudes from 2^-62, gradually less to 2^-70, to just under 2^65; what is larger, or
+// not finite, is code 0x7fff and comes out as NaN. The encoder takes values times 2^-64, so that the exponent's top
+// bit is clear and the code is FP32's upper half without it; halves round away from zero.
+constexpr float kYdUnit = 0x1p-64f;
+MOE_DEV uint32_t pack_yd(float lo, float hi) {
+  const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
+  const uint32_t u = min(a << 1, 0x7ffeffffu) + 0x8000u, v = min(b << 1, 0x7ffeffffu) + 0x8000u;
+  return __builtin_amdgcn_perm(v | (b & 0x80000000u), u | (a & 0x80000000u), 0x07060302);
+}
+MOE_DEV float unpack_yd(uint32_t high) {  // the code in the upper half
+  const uint32_t m = high & 0x7fff0000u;
+  const float v = __uint_as_float((high & 0x80000000u) | (m >> 1)) * 0x1p64f;
+  return m == 0x7fff0000u ? __uint_as_float(0x7fc00000u) : v;
+}
+
 }  // namespace moe

@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "gg_engine.h"
+#include "i8.h"
 
 namespace moe {
 namespace gg {
@@ -50,7 +51,7 @@ struct I8Args {
   const float* scale_a;    // [P]
   const int8_t* B;         // per expert [N, K], gate/up [2 N, K]
   const float* scale_b;    // per expert [N], [2 N]
-  void* C;                 // gate/up: h [P, N] FP32; else [P, N] BF16
+  void* C;                 // gate/up: h [P, N] FP32; product [P, N] BF16; down: rows of yd (i8.h)
   int K, N;
   const int32_t* offsets;  // null: one group of P_c rows
   int El, c0, nc;
@@ -129,9 +130,11 @@ MOE_DEV void read_scales(uint32_t rows, uint32_t cols, float (&r)[4], f32x4_t (&
       : "memory");
 }
 
-template <bool GU, int TILE>
+enum I8Out { kProduct, kGateUp8, kDown8 };  // BF16 rows; h in FP32; rows of yd (i8.h)
+template <int OUT, int TILE>
 __global__ __launch_bounds__(I8Shape<TILE>::kThreads) void i8_gemm_kernel(I8Args a) {
   using S = I8Shape<TILE>;
+  constexpr bool GU = OUT == kGateUp8;
   constexpr int kTile = S::kTile, kWN = S::kWN, kThreads = S::kThreads, kMN = S::kMN, kNN = S::kNN, kSlots = S::kSlots;
   constexpr int OUTN = GU ? kTile / 2 : kTile;  // output columns of a tile
   __shared__ Groups sh;
@@ -338,6 +341,9 @@ __global__ __launch_bounds__(I8Shape<TILE>::kThreads) void i8_gemm_kernel(I8Args
     const uint32_t at = lds_addr(scales[0]) + (uint32_t)(tbuf * (2 * kTile * 4));
     tbuf = (tbuf + 1) % kSlots;
     read_scales(at + 4 * (arow0 + out_row(lane)), at + 4 * (kTile + brow0 + 4 * (lane >> 5)), sa, sb);
+    if constexpr (OUT == kDown8)
+#pragma unroll
+      for (int tm = 0; tm < kMN; ++tm) sa[tm] *= kYdUnit;
     constexpr int ES = GU ? 4 : 2;
     const int64_t ld = (int64_t)a.N * ES;
     const auto rc = make_rsrc((char*)a.C + cur.r0 * ld + (int64_t)cur.n0 * ES, (cur.mvalid - 1) * ld + (int64_t)nvalid * ES);
@@ -371,7 +377,7 @@ __global__ __launch_bounds__(I8Shape<TILE>::kThreads) void i8_gemm_kernel(I8Args
               float v[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) v[q] = (float)acc[tm][tn][4 * (g + k) + q] * (sa[tm] * sb[4 * tn + g + k][q]);
-              p[k] = pack4(v[0], v[1], v[2], v[3]);
+              p[k] = OUT == kDown8 ? make_uint2(pack_yd(v[0], v[1]), pack_yd(v[2], v[3])) : pack4(v[0], v[1], v[2], v[3]);
             }
             // the halves' lanes exchange: lanes 0..31 get all 8 columns of group g, lanes 32..63 of g + 1
             const auto x = __builtin_amdgcn_permlane32_swap(p[0].x, p[1].x, false, false);
@@ -386,9 +392,9 @@ __global__ __launch_bounds__(I8Shape<TILE>::kThreads) void i8_gemm_kernel(I8Args
   wait_vm<0>();  // the last loads (of nothing) still write zeros to this workgroup's LDS
 }
 
-template <bool GU, int TILE>
+template <int OUT, int TILE>
 hipError_t run_i8_tiles(const char* name, const I8Args& a, int64_t tiles, hipStream_t s) {
-  auto k = i8_gemm_kernel<GU, TILE>;
+  auto k = i8_gemm_kernel<OUT, TILE>;
   hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, I8Shape<TILE>::kRing);
   if (e != hipSuccess) return e;
   if (tiles <= 0) return hipSuccess;
@@ -402,13 +408,13 @@ hipError_t run_i8_tiles(const char* name, const I8Args& a, int64_t tiles, hipStr
 }
 
 // usual: rows of one group on average
-template <bool GU>
+template <int OUT>
 hipError_t run_i8(const char* name, const I8Args& a, int64_t usual, hipStream_t s) {
   // per chunk at most floor(P_c / tile) + El row tiles; the device-side count decides the work. Of groups of uneven
   // length every second or so has a row tile more than the average fills.
   const int64_t uneven = a.offsets ? 1 : 0;
   auto tiles = [&](int64_t tile, bool bound) {
-    const int64_t outn = GU ? tile / 2 : tile;
+    const int64_t outn = OUT == kGateUp8 ? tile / 2 : tile;
     const int64_t mt = bound ? a.P_c / tile + a.El : a.El * ((usual + uneven * (tile / 2) + tile - 1) / tile);
     return a.nc * mt * ((a.N + outn - 1) / outn);
   };
@@ -419,9 +425,9 @@ hipError_t run_i8(const char* name, const I8Args& a, int64_t usual, hipStream_t 
   // (three), 336 rows x 6848 on 2848 columns 66 against 31 us (one of each).
   // A round of tiny tiles takes about 0.65 of one of small ones: 518 rows x 5568 on 448 columns 15 (one round) against
   // 23 us (one), 336 rows x 6848 on 2848 columns 33 (two) against 31 us (one).
-  if (rounds(64) <= rounds(128)) return run_i8_tiles<GU, kTiny>(name, a, tiles(64, true), s);
-  if (rounds(128) <= 2 * rounds(256)) return run_i8_tiles<GU, kSmall>(name, a, tiles(128, true), s);
-  return run_i8_tiles<GU, kLarge>(name, a, tiles(256, true), s);
+  if (rounds(64) <= rounds(128)) return run_i8_tiles<OUT, kTiny>(name, a, tiles(64, true), s);
+  if (rounds(128) <= 2 * rounds(256)) return run_i8_tiles<OUT, kSmall>(name, a, tiles(128, true), s);
+  return run_i8_tiles<OUT, kLarge>(name, a, tiles(256, true), s);
 }
 
 }  // namespace
@@ -429,7 +435,7 @@ hipError_t run_i8(const char* name, const I8Args& a, int64_t usual, hipStream_t 
 
 // Gate/up with exact int32 sums, dequantised by s_row * s_col, SwiGLU -> h (FP32 rows at the start of the h
 // buffer: it is quantised per row next, and a BF16 rounding before that would move codes by whole steps);
-// h quantised per row (codes after the FP32 values); down -> yd (BF16).
+// h quantised per row (codes after the FP32 values); down -> yd.
 hipError_t launch_expert_fwd_i8(const void* xd, const float* xd_scale, const void* w1, const float* w1_scale,
                                 const void* w2, const float* w2_scale, const int32_t* offsets, void* h,
                                 float* h_scale, void* yd, int H, int I, int El, int c0, int nc, int64_t P_c,
@@ -437,12 +443,12 @@ hipError_t launch_expert_fwd_i8(const void* xd, const float* xd_scale, const voi
   if (nc <= 0 || El <= 0) return hipSuccess;
   int8_t* hq = (int8_t*)h + P * (int64_t)I * 4;
   gg::I8Args a{(const int8_t*)xd, xd_scale, (const int8_t*)w1, w1_scale, h, H, I, offsets, El, c0, nc, P_c};
-  hipError_t e = gg::run_i8<true>("gemm_gateup_swiglu_i8", a, usual, s);
+  hipError_t e = gg::run_i8<gg::kGateUp8>("gemm_gateup_swiglu_i8", a, usual, s);
   if (e != hipSuccess) return e;
   e = launch_quantize_h_i8((const float*)h, hq, h_scale, offsets, El, c0, nc, P_c, I, s);
   if (e != hipSuccess) return e;
   gg::I8Args b{hq, h_scale, (const int8_t*)w2, w2_scale, yd, I, H, offsets, El, c0, nc, P_c};
-  return gg::run_i8<false>("gemm_down_i8", b, usual, s);
+  return gg::run_i8<gg::kDown8>("gemm_down_i8", b, usual, s);
 }
 
 // y = dequantised x w^T for the rows of each group (moe_expert_matmul_i8).
@@ -451,7 +457,7 @@ hipError_t launch_expert_matmul_i8(int groups, int64_t rows, int N, int K, const
                                    hipStream_t s) {
   if (groups <= 0 || rows <= 0) return hipSuccess;
   gg::I8Args a{(const int8_t*)x, x_scale, (const int8_t*)w, w_scale, y, K, N, offsets, groups, 0, 1, rows};
-  return gg::run_i8<false>("gemm_matmul_i8", a, (rows + groups - 1) / groups, s);
+  return gg::run_i8<gg::kProduct>("gemm_matmul_i8", a, (rows + groups - 1) / groups, s);
 }
 
 }  // namespace moe

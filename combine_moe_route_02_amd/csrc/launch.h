@@ -44,7 +44,7 @@ hipError_t launch_dispatch_fp8(const void* x, const int32_t* row_of, void* xd, f
 hipError_t launch_quantize_rows_fp8(const void* src, void* codes, float* scale, int64_t rows,
                                     int cols, hipStream_t s);
 hipError_t launch_combine(bool bf16, const void* yd, const float* gates, const int32_t* row_of,
-                          void* out, int64_t t0, int64_t t1, int K, int64_t row_bytes, hipStream_t s);
+                          void* out, int64_t t0, int64_t t1, int K, int64_t row_bytes, hipStream_t s, bool i8);
 constexpr int kCombineQMaxH = 8192;  // combine backward quantises dyd rows up to this H
 hipError_t launch_combine_bwd(bool bf16, const void* dy, const void* yd, const float* gates,
                               const int32_t* row_of, void* dyd, float* dgates, int64_t t0,

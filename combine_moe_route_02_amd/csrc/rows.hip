@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "i8.h"
 #include "launch.h"
 #include "trace.h"
 
@@ -246,9 +247,19 @@ template <> struct Vec<uint16_t> {
   }
 };
 
+struct YdI8 {};  // the integer experts' rows (i8.h)
+template <> struct Vec<YdI8> {
+  static constexpr int N = 8;
+  MOE_DEV static void to_f(const u32x4& v, float* f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { f[2 * i] = unpack_yd(w[i] << 16); f[2 * i + 1] = unpack_yd(w[i] & 0xffff0000u); }
+  }
+};
+
 // Combine: out[t] = RNE(sum_j g_tj * yd[row_of[t][j]]), FP32 accumulation, j ascending; a token
-// without a local expert gets a zero row.
-template <typename T, int K>
+// without a local expert gets a zero row. Y: the rows' type where it is not the output's.
+template <typename T, int K, typename Y = T>
 __global__ __launch_bounds__(kBlockThreads) void combine_kernel(
     const u32x4* __restrict__ yd, const float* __restrict__ gates, const int32_t* __restrict__ row_of,
     u32x4* __restrict__ out, int64_t t0, int64_t t1, int64_t nvec) {
@@ -272,7 +283,7 @@ __global__ __launch_bounds__(kBlockThreads) void combine_kernel(
       if (bcast_i(myrow, j) < 0) continue;
       const float g = bcast_f(mygate, j);
       float f[V::N];
-      V::to_f(v[j], f);
+      Vec<Y>::to_f(v[j], f);
 #pragma unroll
       for (int q = 0; q < V::N; ++q) acc[q] = fmaf(g, f[q], acc[q]);
     }
@@ -823,8 +834,14 @@ hipError_t launch_quantize_expert_cols_fp8(const char* name, const void* src, vo
 }
 
 hipError_t launch_combine(bool bf16, const void* yd, const float* gates, const int32_t* row_of,
-                          void* out, int64_t t0, int64_t t1, int K, int64_t row_bytes, hipStream_t s) {
+                          void* out, int64_t t0, int64_t t1, int K, int64_t row_bytes, hipStream_t s, bool i8) {
   if (t1 <= t0) return hipSuccess;
+  if (i8) {
+    MOE_TRACE("combine", s);
+    MOE_SWITCH_K(K, MOE_LAUNCH((combine_kernel<uint16_t, KK, YdI8>), dim3((unsigned)(t1 - t0)), dim3(kBlockThreads), 0, s,
+                       (const u32x4*)yd, gates, row_of, (u32x4*)out, t0, t1, row_bytes / 16));
+    return hipGetLastError();
+  }
   if (bf16)
     {
       MOE_TRACE("combine", s);

@@ -44,7 +44,10 @@
  *        out                            f32       bf16       bf16
  *        dw1, dw2                       f32       bf16       -
  *     MOE_INT8 (forward only) is laid out like MOE_FP8_E4M3 with 8-bit integer codes (xd, W1, W2),
- *     except h: [P,I] f32 then [P,I] codes (5*P*I bytes).
+ *     except h: [P,I] f32 then [P,I] codes (5*P*I bytes), and yd: 16-bit values of sign, 7 exponent
+ *     bits (bias 63) and 8 mantissa bits, subnormal below 2^-62, code 0x7fff for NaN and for magnitudes
+ *     past the last one (0x7ffe, just under 2^65); they pass from moe_expert_ffn to moe_combine, whose sum then is
+ *     within 1.12 of one BF16 rounding (two BF16 roundings in a row: 1.41).
  *     logits, gates, dgates, dlogits, dwr_acc are always f32; every index array is int32.
  *   - Shapes: logits [T,E]; topk_idx, gates, row_of, dgates [T,k]; counts [n,E];
  *     offsets [n,E_l+1]; src_token [P]; xd, yd, dyd, dxd [P,H]; gu, dgu [P,2I]; h [P,I];

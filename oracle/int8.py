@@ -38,6 +38,16 @@ def matmul(xq, xs, wq, ws, offsets=None):
     return y
 
 
+def decode_yd(codes):
+    """Values of the 16-bit rows between the experts and combine: sign, 7 exponent bits (bias 63), 8 mantissa bits,
+    subnormal below 2^-62; 0x7fff is NaN."""
+    c = codes.astype(np.int64) & 0xffff
+    e, m = (c >> 8) & 0x7f, c & 0xff
+    v = np.where(e > 0, np.ldexp(1.0 + m / 256.0, e - 63), np.ldexp(m / 256.0, -62))
+    v = np.where(c >> 15, -v, v)
+    return np.where((c & 0x7fff) == 0x7fff, np.nan, v)
+
+
 def forward(x, logits, w1q, w1s, w2q, w2s, *, k, e0, E_local, n_chunks, P_c):
     """Layer forward on integer codes. Returns the routing state and h, yd, out in FP64 (h quantised from its FP32
     rounding, the value that the kernel holds)."""

@@ -3,8 +3,8 @@
 Codes and scales are compared bit for bit (both sides take the same FP32 steps); so are products of the same codes
 computed by different calls, since the sums are exact. A product's value is an exact integer, rounded once to FP32
 (2^-24), times the rounded product of two scales (two more), rounded once to BF16: 2^-8 of the value plus 3 * 2^-24.
-The layer's output differs from the oracle's by the BF16 rounding of yd and of out (2^-8 / sqrt(3) rms each at most)
-and by codes of h that fall on the other side of a half because h carries FP32 rounding (a relative 1e-6 moves a share
+The layer's output differs from the oracle's by the rounding of yd (2^-9 / sqrt(3) rms at most) and the BF16 rounding of
+out (2^-8 / sqrt(3)), together under the 2^-8 sqrt(2 / 3) of two BF16 roundings that the bound allows, and by codes of h that fall on the other side of a half because h carries FP32 rounding (a relative 1e-6 moves a share
 2e-6 / step of the codes, under 1e-3 of the norm): 2^-8 * sqrt(2 / 3) + 1e-3 = 4.2e-3 of the norm."""
 import numpy as np
 import pytest
@@ -284,7 +284,75 @@ def test_rows_region_wider_than_routing_needs():
     gu = oi8.matmul(xq, xs, w1, w1s, off)
     hq, hsc = oi8.quantize_rows((gu[:, :I] / (1 + np.exp(-gu[:, :I])) * gu[:, I:]).astype(np.float32))
     want = oi8.matmul(hq, hsc, w2, w2s, off)
-    assert np.linalg.norm(harness.to_np(yd) - want) <= OUT_TOL * np.linalg.norm(want)
+    got = oi8.decode_yd(yd.view(torch.int16).cpu().numpy())
+    assert np.linalg.norm(got - want) <= OUT_TOL * np.linalg.norm(want)
+
+
+def _ffn(torch, mh, T, H, I, xq, xs, w1, w1s, w2, w2s):
+    """yd codes of T rows through one expert: few rows, or with more the GEMM."""
+    d = mh.make_desc(T=T, H=H, I=I, E=1, E_local=1, k=1, n_chunks=1, dtype="int8")
+    dev = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (xq, xs, w1, w1s, w2, w2s)]
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    h, hs = torch.empty(5 * d.P_c * I, dtype=torch.uint8, device="cuda"), torch.empty(d.P_c, device="cuda")
+    yd = torch.zeros(d.P_c, H, dtype=torch.int16, device="cuda")
+    mh.moe_expert_ffn(d, 0, dev[0], dev[1], dev[2], dev[3], dev[4], dev[5], off, None, h, hs, yd)
+    torch.cuda.synchronize()
+    return yd.cpu().numpy()[:T]
+
+
+def test_rows_between_the_experts_and_combine_are_the_same_from_either_kernel():
+    torch, mh = _gpu()
+    rng = np.random.default_rng(8)
+    T, H, I = 700, 320, 192
+    xq, xs = rng.integers(-127, 128, (T, H)).astype(np.int8), (rng.random(T) + 0.1).astype(np.float32) * 0.01
+    w = [rng.integers(-127, 128, (1, 2 * I, H)).astype(np.int8), (rng.random((1, 2 * I)) * 0.01).astype(np.float32),
+         rng.integers(-127, 128, (1, H, I)).astype(np.int8), (rng.random((1, H)) * 0.01).astype(np.float32)]
+    many = _ffn(torch, mh, T, H, I, xq, xs, *w)
+    for n in (1, 16, 30, 47, 130):
+        np.testing.assert_array_equal(_ffn(torch, mh, n, H, I, xq[:n], xs[:n], *w), many[:n])
+
+
+@pytest.mark.parametrize("T", [8, 400])
+def test_rows_between_the_experts_and_combine_at_the_ends_of_their_range(T):
+    """Every column of h is equal, so its codes are 127 and y = 127 sum(w2) (h / 127) w2_scale: column scales take y
+    through subnormal, smallest, ordinary, largest and too large values, and NaN. 2^-9 is the rounding, 1e-5 covers h's
+    sigmoid and scales; a subnormal is off by half a step, 2^-71, at most."""
+    torch, mh = _gpu()
+    H, I = 128, 64
+    xq, xs = np.full((T, H), 100, np.int8), np.full(T, 1e-3, np.float32)
+    w1, w1s = np.full((1, 2 * I, H), 20, np.int8), np.full((1, 2 * I), 1e-3, np.float32)
+    w2 = np.ones((1, H, I), np.int8)
+    w2[0, 1::2] = -1
+    scale = np.array([1e-38, 1e-30, 1e-24, 1e-21, 1e-20, 1e-18, 1e-9, 1e-3, 1.0, 1e9, 1e16, 2e18, 5e18, 1e20, 1e36, 0.0],
+                     np.float32)
+    w2s = np.tile(scale, H // len(scale))[None].copy()
+    w2s[0, 32], w2s[0, 34] = np.nan, np.inf
+    w2s[0, 33:34].view(np.uint32)[:] = 0xffffffff   # a NaN whose every bit is set
+    got = oi8.decode_yd(_ffn(torch, mh, T, H, I, xq, xs, w1, w1s, w2, w2s))
+    g = 20.0 * 100 * H * 1e-6
+    y = g / (1 + np.exp(-g)) * g * I * w2[0, :, 0] * w2s[0].astype(np.float64)
+    big = ~(np.abs(y) < 2.0 ** 65 * (1 - 1.5 * 2.0 ** -9))
+    near = np.abs(np.abs(y) / 2.0 ** 65 - 1) < 0.01    # (no column falls there: either side would do)
+    assert not near.any() and big.any() and (np.abs(y[~big]) > 2.0 ** 63).any() and ((0 < np.abs(y)) & (np.abs(y) < 2.0 ** -63)).any()
+    assert np.isnan(got[:, big]).all()
+    assert np.all(np.abs(got - y)[:, ~big] <= (2.0 ** -9 + 1e-5) * np.abs(y[~big]) + 2.0 ** -71)
+
+
+def test_combine_reads_every_code_of_the_rows():
+    torch, mh = _gpu()
+    T, H = 1024, 64
+    codes = np.arange(T * H, dtype=np.int64).astype(np.uint16).reshape(T, H)
+    d = mh.make_desc(T=T, H=H, I=64, E=1, E_local=1, k=1, n_chunks=1, dtype="int8")
+    out = torch.empty(d.P_out, H, dtype=torch.bfloat16, device="cuda")
+    row = torch.arange(T, dtype=torch.int32, device="cuda").reshape(T, 1)
+    mh.moe_combine(d, 0, torch.from_numpy(codes.view(np.int16)).cuda(), torch.ones(T, 1, device="cuda"), row, out)
+    torch.cuda.synchronize()
+    val = oi8.decode_yd(codes.view(np.int16))
+    nan = np.isnan(val)
+    want = moe_inputs.bf16_bits_to_f32(moe_inputs.f32_to_bf16_bits(np.where(nan, 0, val).astype(np.float32)))
+    got = harness.to_np(out[:T])
+    assert np.isnan(got[nan]).all() and nan.sum() == 2
+    np.testing.assert_array_equal(got[~nan], want[~nan])
 
 
 def test_layer_without_tokens():

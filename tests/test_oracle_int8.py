@@ -45,3 +45,9 @@ def test_forward_is_near_the_unquantised_layer():
     want = oracle.forward(x, lg, w1, w2, **kw)["out"]
     # each of the four quantisations is off by up to half of amax / 127, about 1% of an element's size
     assert np.linalg.norm(got["out"] - want) <= 0.04 * np.linalg.norm(want)
+
+
+def test_rows_between_the_experts_and_combine_decode():
+    c = np.array([0x0000, 0x8000, 0x0001, 0x00ff, 0x0100, 0x3f00, 0xbf80, 0x4001, 0x7ffe, 0x7fff, 0xffff], np.uint16)
+    want = [0.0, 0.0, 2.0 ** -70, 255 * 2.0 ** -70, 2.0 ** -62, 1.0, -1.5, 2.0 + 2.0 ** -7, 2.0 ** 65 - 2.0 ** 57, np.nan, np.nan]
+    np.testing.assert_array_equal(oi8.decode_yd(c.view(np.int16)), want)
