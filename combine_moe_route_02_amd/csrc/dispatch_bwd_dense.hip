@@ -285,56 +285,52 @@ __global__ __launch_bounds__(kDThreads, KS <= 8 ? 2 : 1) void dispatch_bwd_dense
   }
 }
 
-// FP32 payloads: FP32 MFMA (32 x 32 x 2), so that the sums keep FP32 products. A workgroup takes 32 or 64 tokens and
-// 128 columns, a wave 32 of them; dlogits and W_r pass through LDS in chunks of 64 experts, the next chunk's loads in
+// FP32 payloads: FP32 MFMA (32 x 32 x 2), so that the sums keep FP32 products. A workgroup takes 32 tokens and 128
+// columns, a wave 32 of them; dlogits and W_r pass through LDS in chunks of 64 experts, the next chunk's loads in
 // registers meanwhile, and a token's first rows of dxd are on their way from the start. Experts e and e + half of a
-// chunk make one step, so that the dlogits reads of both lane halves fall on different banks. Two or three workgroups
-// per CU cover one another's loads. 16000 tokens x 2048: 244 us with 32 experts, all local, 8 per token (the bytes
-// alone 241 us at the rate of a copy); 167 us with 160 experts of which 20 are local, 63 TFLOP/s (57 us of bytes and
-// 69 us of FP32 products).
+// chunk make one step, so that the dlogits reads of both lane halves fall on different banks. Three workgroups per CU
+// (LDS; 168 registers) cover one another's loads: 3731 tokens x 1088 with 116 experts 23 us, 27 us with two. 16000
+// tokens x 2048: 241 us with 32 experts, all local, 8 per token (the rate of a copy); 165 us with 160 experts of which
+// 20 are local, 64 TFLOP/s (57 us of bytes and 69 us of FP32 products; 64 tokens a workgroup 158 us, but 3731 tokens
+// 28 us).
 constexpr int kFCols = 128, kFE = 64;
-template <int DT> struct alignas(16) F32Lds {
+struct alignas(16) F32Lds {
   union {
     float w[kFE][kFCols];
-    float sums[DT][kFCols + 4];
+    float sums[kDT][kFCols + 4];
   };
-  float dl[DT][kFE + 1];
-  int32_t row[DT][8];
+  float dl[kDT][kFE + 1];
+  int32_t row[kDT][8];
 };
 
-template <int TB>
-__global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_f32_kernel(
+__global__ __launch_bounds__(kDThreads, 3) void dispatch_bwd_dense_f32_kernel(
     const float* __restrict__ dxd, const int32_t* __restrict__ row_of, const float* __restrict__ dlogits,
     const float* __restrict__ w_r, float* __restrict__ dx, int64_t t0, int64_t t1, int K, int E, int H, int nct) {
-  constexpr int DT = 32 * TB, NO = 4 * TB, kAhead = TB == 1 ? 2 : 1;
-  __shared__ F32Lds<DT> sh;
+  constexpr int NO = 4, kAheadF = 2;  // output vectors of a thread; rows of a token loaded from the start
+  __shared__ F32Lds sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t tiles = (t1 - t0 + DT - 1) / DT, px = (tiles + 7) / 8;
+  const int64_t tiles = (t1 - t0 + kDT - 1) / kDT, px = (tiles + 7) / 8;
   const int64_t tile = blockIdx.x % 8 * px + blockIdx.x / 8 / nct;  // an XCD's tokens are one range
   if (tile >= tiles) return;
-  const int64_t r0 = t0 + tile * DT;
-  const int nt = (int)(t1 - r0 < DT ? t1 - r0 : DT), n0 = blockIdx.x / 8 % nct * kFCols;
+  const int64_t r0 = t0 + tile * kDT;
+  const int nt = (int)(t1 - r0 < kDT ? t1 - r0 : kDT), n0 = blockIdx.x / 8 % nct * kFCols;
 
-  // chunk loads: 8 vectors of W_r (rows tid / 32 + 8 u), 8 TB values of dlogits (tokens tid / 64 + 4 u); loads carry no
+  // chunk loads: 8 vectors of W_r (rows tid / 32 + 8 u), 8 values of dlogits (tokens tid / 64 + 4 u); loads carry no
   // branch (the compiler would wait behind each), and experts past the last one are zeroed as they go to LDS
   float4 wv[8];
-  float dv[8 * TB];
+  float dv[8];
   const int wc = n0 + 4 * (tid % 32);
   auto fetch = [&](int e0) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int e = e0 + tid / 32 + 8 * u;
+      const int e = e0 + tid / 32 + 8 * u, d = e0 + lane, t = wave + 4 * u;
       wv[u] = *(const float4*)(w_r + (int64_t)min(e, E - 1) * H + min(wc, H - 4));
-    }
-#pragma unroll
-    for (int u = 0; u < 8 * TB; ++u) {
-      const int d = e0 + lane, t = wave + 4 * u;
       dv[u] = dlogits[(r0 + min(t, nt - 1)) * E + min(d, E - 1)];
     }
   };
   fetch(0);
   // a token's local rows first, in slot order
-  if (tid < DT) {
+  if (tid < kDT) {
     int32_t slots[8];
     const int32_t* p = row_of + (r0 + min(tid, nt - 1)) * K;
 #pragma unroll
@@ -352,8 +348,8 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_f32_kernel(
   const int oc = 4 * (tid % 32), ot = tid / 32;
   const bool in_cols = n0 + oc < H;
   const float* const rows = dxd ? dxd : w_r;  // no local expert: any readable row
-  float4 v[kAhead][NO];
-  bool on[kAhead][NO];
+  float4 v[kAheadF][NO];
+  bool on[kAheadF][NO];
   auto load_rows = [&](float4 (&d)[NO], bool (&on)[NO], int s) {
 #pragma unroll
     for (int u = 0; u < NO; ++u) {
@@ -363,20 +359,18 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_f32_kernel(
     }
   };
 #pragma unroll
-  for (int s = 0; s < kAhead; ++s) load_rows(v[s], on[s], s);
+  for (int s = 0; s < kAheadF; ++s) load_rows(v[s], on[s], s);
 
-  f32x16_t acc[TB];
+  f32x16_t acc;
 #pragma unroll
-  for (int b = 0; b < TB; ++b)
-#pragma unroll
-    for (int q = 0; q < 16; ++q) acc[b][q] = 0.f;
+  for (int q = 0; q < 16; ++q) acc[q] = 0.f;
   for (int e0 = 0; e0 < E; e0 += kFE) {
     if (e0 > 0) gg::lds_barrier();  // the chunk before this one has been read
 #pragma unroll
     for (int u = 0; u < 8; ++u)
       *(float4*)&sh.w[tid / 32 + 8 * u][4 * (tid % 32)] = e0 + tid / 32 + 8 * u < E ? wv[u] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int u = 0; u < 8 * TB; ++u) sh.dl[wave + 4 * u][lane] = e0 + lane < E ? dv[u] : 0.f;
+    for (int u = 0; u < 8; ++u) sh.dl[wave + 4 * u][lane] = e0 + lane < E ? dv[u] : 0.f;
     gg::lds_barrier();
     if (e0 + kFE < E) fetch(e0 + kFE);
     const int half = (min(kFE, E - e0) + 1) / 2, eh = (lane >> 5) * half;
@@ -384,17 +378,11 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_f32_kernel(
     const float* pd = &sh.dl[lane & 31][eh];
     auto steps = [&](int i, auto n) {
       constexpr int N = decltype(n)::value;
-      float w[N], d[N][TB];
+      float w[N], d[N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        w[j] = pw[(i + j) * kFCols];
+      for (int j = 0; j < N; ++j) { w[j] = pw[(i + j) * kFCols]; d[j] = pd[i + j]; }
 #pragma unroll
-        for (int b = 0; b < TB; ++b) d[j][b] = pd[32 * b * (kFE + 1) + i + j];
-      }
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-#pragma unroll
-        for (int b = 0; b < TB; ++b) acc[b] = __builtin_amdgcn_mfma_f32_32x32x2f32(w[j], d[j][b], acc[b], 0, 0, 0);
+      for (int j = 0; j < N; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(w[j], d[j], acc, 0, 0, 0);
     };
     int i = 0;
     for (; i + 4 <= half; i += 4) steps(i, std::integral_constant<int, 4>());
@@ -403,11 +391,9 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_f32_kernel(
   gg::lds_barrier();
   // lane: token lane & 31, four consecutive columns per accumulator group
 #pragma unroll
-  for (int b = 0; b < TB; ++b)
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      *(float4*)&sh.sums[32 * b + (lane & 31)][32 * wave + gg::out_col(g, lane)] =
-          make_float4(acc[b][4 * g], acc[b][4 * g + 1], acc[b][4 * g + 2], acc[b][4 * g + 3]);
+  for (int g = 0; g < 4; ++g)
+    *(float4*)&sh.sums[lane & 31][32 * wave + gg::out_col(g, lane)] =
+        make_float4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
   gg::lds_barrier();
   float4 f[NO];
 #pragma unroll
@@ -420,8 +406,8 @@ __global__ __launch_bounds__(kDThreads) void dispatch_bwd_dense_f32_kernel(
     }
   };
 #pragma unroll
-  for (int s = 0; s < kAhead; ++s) add(v[s], on[s]);
-  for (int s = kAhead; s < K; ++s) {
+  for (int s = 0; s < kAheadF; ++s) add(v[s], on[s]);
+  for (int s = kAheadF; s < K; ++s) {
     bool any = false;
 #pragma unroll
     for (int u = 0; u < NO; ++u) any |= sh.row[ot + 8 * u][s] >= 0;
@@ -466,12 +452,9 @@ hipError_t launch_dispatch_bwd_dense(bool bf16, const void* dxd, const float* dx
   if (!bf16) {
     MOE_TRACE("dispatch_bwd_dense_f32", s);
     const int nct = (H + kFCols - 1) / kFCols;
-    // 64 tokens halve the reads of W_r from L2: 16000 tokens x 2048 with 160 experts 167 against 193 us. Fewer than
-    // three workgroups per CU leave CUs waiting: 3731 tokens x 1088 28 against 26 us.
-    const int dt = (t1 - t0) / 64 * nct >= 3 * gg::cu_count() ? 64 : 32;
-    const int64_t px = ((t1 - t0 + dt - 1) / dt + 7) / 8;
-    MOE_LAUNCH(dt == 64 ? dispatch_bwd_dense_f32_kernel<2> : dispatch_bwd_dense_f32_kernel<1>, dim3((unsigned)(8 * px * nct)),
-               dim3(kDThreads), 0, s, (const float*)dxd, row_of, dlogits, (const float*)w_r, (float*)dx, t0, t1, K, E, H, nct);
+    const int64_t px = ((t1 - t0 + kDT - 1) / kDT + 7) / 8;
+    MOE_LAUNCH(dispatch_bwd_dense_f32_kernel, dim3((unsigned)(8 * px * nct)), dim3(kDThreads), 0, s, (const float*)dxd,
+               row_of, dlogits, (const float*)w_r, (float*)dx, t0, t1, K, E, H, nct);
     return hipGetLastError();
   }
   DenseArgs a{dxd, dxd_scales, row_of, dlogits, (const uint16_t*)w_r, (uint16_t*)dx, t0, t1, K, E, H, 0, 0};
