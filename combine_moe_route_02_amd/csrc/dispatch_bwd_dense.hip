@@ -11,8 +11,9 @@
 // multiplies its columns, the FP32 sums go through LDS into rows of 16-byte vectors, and there the
 // slots' dxd rows are added as they are loaded. Each XCD owns a range of tokens, so that the tile's
 // dlogits, which every slice reads, come from its L2. A slot's dxd rows and the next tile's dlogits are loaded a
-// tile ahead. 16384 tokens x 2048, 128 experts of which 16 are local: 40 us for 144 MB (3.6 TB/s; 29 us at the rate
-// of a copy), bound by the rows' gather behind two barriers per tile; 1000 tokens x 256: 5.5 us, one tile per
+// tile ahead. dx is stored past the L2, which keeps the rows and dlogits (44 -> 39 us; loads of
+// the rows marked the same way 48 us). 16384 tokens x 2048, 128 experts of which 16 are local: 37 us for 144 MB (3.9 TB/s;
+// 29 us at the rate of a copy), bound by the rows' gather behind two barriers per tile; 1000 tokens x 256: 5.5 us, one tile per
 // workgroup, latency. Slices of 128 columns (three workgroups per CU) 57 us, two rows ahead 48 us.
 #include <type_traits>
 
@@ -278,8 +279,9 @@ __global__ __launch_bounds__(kDThreads, KS <= 8 ? 2 : 1) void dispatch_bwd_dense
     for (int u = 0; u < NI; ++u) {
       const int r = rt + u * (kDThreads / VPR);
       if (r < nt && in_cols)
-        *(u32x4*)(a.dx + (r0 + r) * a.H + n) = u32x4{pack_bf2(f[u][0], f[u][1]), pack_bf2(f[u][2], f[u][3]),
-                                                     pack_bf2(f[u][4], f[u][5]), pack_bf2(f[u][6], f[u][7])};
+        __builtin_nontemporal_store(i32x4_t{(int)pack_bf2(f[u][0], f[u][1]), (int)pack_bf2(f[u][2], f[u][3]),
+                                            (int)pack_bf2(f[u][4], f[u][5]), (int)pack_bf2(f[u][6], f[u][7])},
+                                    (i32x4_t*)(a.dx + (r0 + r) * a.H + n));
     }
     fetch_rows(buf);
   }
@@ -418,7 +420,7 @@ __global__ __launch_bounds__(kDThreads, 3) void dispatch_bwd_dense_f32_kernel(
 #pragma unroll
   for (int u = 0; u < NO; ++u) {
     const int t = ot + 8 * u;
-    if (t < nt && in_cols) *(float4*)(dx + (r0 + t) * H + n0 + oc) = f[u];
+    if (t < nt && in_cols) __builtin_nontemporal_store(f32x4_t{f[u].x, f[u].y, f[u].z, f[u].w}, (f32x4_t*)(dx + (r0 + t) * H + n0 + oc));
   }
 }
 

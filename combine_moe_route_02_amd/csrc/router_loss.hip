@@ -587,7 +587,8 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_bwd_kernel(
         float o[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) o[j] = counted[u] ? scale * v[u][i * W + j] * (w[i * W + j] + add) : 0.f;
-        if constexpr (W == 4) *(float4*)(dlogits + r * E + e) = make_float4(o[0], o[1], o[2], o[3]);
+        // (whole lines past the L2: 40000 tokens of 160 experts with the forward 33 -> 30 us, 131072 of 256 84 -> 80.5)
+        if constexpr (W == 4) __builtin_nontemporal_store(f32x4_t{o[0], o[1], o[2], o[3]}, (f32x4_t*)(dlogits + r * E + e));
         else dlogits[r * E + e] = o[0];
       }
     }
