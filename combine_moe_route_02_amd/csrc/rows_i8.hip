@@ -38,6 +38,13 @@ MOE_DEV uint32_t wave_max_u32(uint32_t v) {
   return v;
 }
 
+// A row is read once and its codes are read next: the row's lines need not stay in the L2 (8192 rows of 7168 values with
+// the L2 cold 36 -> 34 us, dispatch of 16K tokens 20 -> 18.6 us; codes stored past the L2 cost the GEMM more).
+MOE_DEV u32x4 load_once(const u32x4* p) {
+  const i32x4_t v = __builtin_nontemporal_load((const i32x4_t*)p);
+  return u32x4{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
+}
+
 // One wave: the row's scale, its codes handed out vector by vector. NV > 0: the row stays in
 // registers (nvec <= 64 NV); NV = 0: it is read twice.
 template <int NV, class Out>
@@ -48,7 +55,7 @@ MOE_DEV RowScale quantize_row(const u32x4* src, int64_t nvec, int lane, Out&& ou
 #pragma unroll
     for (int b = 0; b < NV; ++b) {
       const int64_t i = b * 64 + lane;
-      v[b] = i < nvec ? src[i] : u32x4{0u, 0u, 0u, 0u};
+      v[b] = i < nvec ? load_once(src + i) : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int b = 0; b < NV; ++b) m = max(m, magnitude8(v[b]));
