@@ -1089,21 +1089,25 @@ static moe_status forward_sched_merged(const moe_desc* d, const moe_tensors* t, 
 }
 
 //   compute: CB0 DDG0 | wait(cb1) [DDG1 GUDG0] | ... | [GUDG n-1, dW2], dW1, wait(done)
-//   aux:     CB1 (C n-1) wait(cb0) RB0 | CB2 RB1 wait(dg0) DB0 | CB3 RB2 wait(dg1) DB1 | ... | wait(dg n-1) DB n-1
+//   aux:     wait(begin) CB1 (C n-1) wait(cb0) RB0 | CB2 RB1 wait(dg0) DB0 | CB3 RB2 wait(dg1) DB1 | ... | wait(dg n-1) DB n-1
 // (C n-1: the fused primitive's deferred last combine of the forward)
 // deferred_combine: the forward left its last chunk's combine to this schedule (fused primitive);
 // it runs on aux after chunk 1's combine backward.
+// after_forward: the forward was issued by the same call, so aux has already waited for the last chunk's GEMMs.
+// Otherwise aux first waits for what the compute stream holds: dy, or the forward's last yd, may still be on its way
+// there, and chunk 1's combine backward reads both.
 static moe_status backward_sched_merged(const moe_desc* d, const moe_tensors* t, hipStream_t cs, hipStream_t as,
-                                        bool deferred_combine = false) {
+                                        bool after_forward, bool deferred_combine = false) {
   const int n = d->n_chunks;
   const bool two = cs != as;
   const hipStream_t side = two ? as : cs;
   const moe::ExpertGemm g = expert_gemm(d, t);
   hipEvent_t* ev = nullptr;
-  MOE_TRY(events(4 * n + 2, &ev));
+  MOE_TRY(events(4 * n + 3, &ev));
   hipEvent_t* cb = ev + 2 * n + 1;
   hipEvent_t* dg = ev + 3 * n + 1;
   hipEvent_t done = ev[4 * n + 1];
+  hipEvent_t begin = ev[4 * n + 2];
   auto combine_bwd = [&](int c, hipStream_t s) {
     return moe_combine_bwd(d, c, t->dy, t->yd, t->gates, t->row_of, t->dyd, t->dgates, s);
   };
@@ -1111,6 +1115,10 @@ static moe_status backward_sched_merged(const moe_desc* d, const moe_tensors* t,
     return moe_route_bwd(d, c, t->dgates, t->gates, t->topk_idx, t->x, t->dlogits, t->dwr_acc, t->dwr,
                          t->workspace, side);
   };
+  if (two && n > 1 && !after_forward) {
+    MOE_HIP(hipEventRecord(begin, cs), "hipEventRecord");
+    MOE_HIP(hipStreamWaitEvent(as, begin, 0), "hipStreamWaitEvent");
+  }
   MOE_TRY(combine_bwd(0, cs));
   if (two) MOE_HIP(hipEventRecord(cb[0], cs), "hipEventRecord");
   // chunk 1's combine backward does not need chunk 0's: aux starts it at once (the compute stream
@@ -1164,7 +1172,8 @@ moe_status moe_layer_backward(const moe_desc* d, const moe_tensors* t, void* com
   MOE_TRY(check_fwd_tensors(d, t));
   MOE_TRY(check_loss_tensors(d, t, true));
   MOE_TRY(check_bwd_tensors(d, t));
-  if (merged_bwd(d)) return backward_sched_merged(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream);
+  if (merged_bwd(d))
+    return backward_sched_merged(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream, false);
   return backward_sched(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream);
 }
 
@@ -1185,7 +1194,7 @@ moe_status moe_layer_forward_backward(const moe_desc* d, const moe_tensors* t, v
   else
     MOE_TRY(forward_sched(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream, false));
   if (merged_bwd(d))
-    return backward_sched_merged(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream, defer);
+    return backward_sched_merged(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream, true, defer);
   return backward_sched(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream);
 }
 

@@ -394,7 +394,8 @@ moe_status moe_stash_load(const void* pool, const float* pool_scale, int64_t liv
  * expert GEMMs of chunk c on `compute`, and combine of chunk c runs on `aux` after them. The
  * first chunk's routing and dispatch, the last chunk's combine (on `aux` in the fused
  * forward+backward, where nothing after it reads `out`) and the first chunk's combine backward
- * run on `compute`, which waits on `aux` only where it consumes aux work. On return
+ * run on `compute`, which waits on `aux` only where it consumes aux work; `aux` first waits for the
+ * work that `compute` holds when the call is made, so inputs may still be on their way there. On return
  * all work is ordered before later work on `compute`. Both streams at the default priority;
  * with compute == aux everything runs in issue order on that one stream. With `logits` NULL the
  * forward routes from x and `w_r` (moe_route_x; BF16, FP8 or INT8 descriptor, E % 32 == 0, E <= 256).

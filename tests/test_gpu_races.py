@@ -140,3 +140,28 @@ def test_one_stream_equals_two_streams():
     mh.moe_layer_forward_backward(d, b, cs, cs)
     torch.cuda.synchronize()
     _assert_same(ref, _snapshot(b, cfg), "one stream")
+
+
+@pytest.mark.parametrize("flags", [0, 4, 16, 1 | 2])
+@pytest.mark.parametrize("late", ["dy", "yd"])
+def test_backward_waits_for_what_the_compute_stream_still_writes(late, flags):
+    """The caller's dy, or the forward's yd, reaches its buffer on the compute stream behind a delay, right before the
+    backward is called: no stream of the backward may read the buffer earlier."""
+    cfg = CASES[0]
+    torch, mh, d, b = _setup(cfg, flags)
+    if flags & mh.FLAG_ROUTER_LOSS:
+        b.update(balance_coef=0.5, z_coef=0.01)
+    cs, aux = torch.cuda.current_stream(), torch.cuda.Stream()
+    mh.moe_layer_forward(d, b, cs, aux)
+    mh.moe_layer_backward(d, b, cs, cs)
+    torch.cuda.synchronize()
+    ref, whole = _snapshot(b, cfg), b[late].clone()
+    b[late].zero_()
+    for name in ("dgates", "dx", "dyd"):
+        b[name].zero_()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(DELAY_CYCLES)
+    b[late].copy_(whole)
+    mh.moe_layer_backward(d, b, cs, aux)
+    torch.cuda.synchronize()
+    _assert_same(ref, _snapshot(b, cfg), f"{late} late")
