@@ -247,7 +247,7 @@ MOE_DEV void few_pass(const FewArgs& a, int e, int64_t r0, int m0, int n, int n0
   auto finish = [&](int b, float srow, const i32x4_t (&v)[CB]) {
     const int m = m0 + 16 * b + lr;
     const int64_t row = r0 + min(m, n - 1);
-    if constexpr (MODE == kFewDown) srow = scales[2 * (min(m, n - 1) - m0) + 1] * kYdUnit;
+    if constexpr (MODE == kFewDown) srow = scales[2 * (min(m, n - 1) - m0) + 1];
     float o[4];
     if constexpr (MODE == kFewGateUp) {
       uint32_t big = 0;
@@ -265,7 +265,7 @@ MOE_DEV void few_pass(const FewArgs& a, int e, int64_t r0, int m0, int n, int n0
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = (float)v[cb][q] * (srow * sb[cb][q]);
+        for (int q = 0; q < 4; ++q) o[q] = (MODE == kFewDown ? kYdUnit * (float)v[cb][q] : (float)v[cb][q]) * (srow * sb[cb][q]);
         const int at = c + kCols * cb;
         const uint2 p = MODE == kFewDown ? make_uint2(pack_yd(o[0], o[1]), pack_yd(o[2], o[3]))
                                          : make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));

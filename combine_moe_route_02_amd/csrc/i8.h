@@ -39,7 +39,9 @@ MOE_DEV uint2 codes8(const u32x4& v, float inv) {
 // BF16 there, its rounding and the output's are two of the same size in a row (sqrt(2) of one); with one bit more
 // the first is half (1.12). Magnitudes from 2^-62, gradually less to 2^-70, to just under 2^65; what is larger, or
 // not finite, is code 0x7fff and comes out as NaN. The encoder takes values times 2^-64, so that the exponent's top
-// bit is clear and the code is FP32's upper half without it; halves round away from zero.
+// bit is clear and the code is FP32's upper half without it; halves round away from zero. The unit multiplies the
+// integer sum: ahead of it, the product of two small scales would become subnormal and lose bits that a long sum brings
+// back into the format's range.
 constexpr float kYdUnit = 0x1p-64f;
 MOE_DEV uint32_t pack_yd(float lo, float hi) {
   const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);

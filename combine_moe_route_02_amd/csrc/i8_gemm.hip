@@ -341,9 +341,6 @@ __global__ __launch_bounds__(I8Shape<TILE>::kThreads) void i8_gemm_kernel(I8Args
     const uint32_t at = lds_addr(scales[0]) + (uint32_t)(tbuf * (2 * kTile * 4));
     tbuf = (tbuf + 1) % kSlots;
     read_scales(at + 4 * (arow0 + out_row(lane)), at + 4 * (kTile + brow0 + 4 * (lane >> 5)), sa, sb);
-    if constexpr (OUT == kDown8)
-#pragma unroll
-      for (int tm = 0; tm < kMN; ++tm) sa[tm] *= kYdUnit;
     constexpr int ES = GU ? 4 : 2;
     const int64_t ld = (int64_t)a.N * ES;
     const auto rc = make_rsrc((char*)a.C + cur.r0 * ld + (int64_t)cur.n0 * ES, (cur.mvalid - 1) * ld + (int64_t)nvalid * ES);
@@ -376,7 +373,10 @@ __global__ __launch_bounds__(I8Shape<TILE>::kThreads) void i8_gemm_kernel(I8Args
             for (int k = 0; k < 2; ++k) {
               float v[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) v[q] = (float)acc[tm][tn][4 * (g + k) + q] * (sa[tm] * sb[4 * tn + g + k][q]);
+              for (int q = 0; q < 4; ++q) {
+                const float sum = (float)acc[tm][tn][4 * (g + k) + q];
+                v[q] = (OUT == kDown8 ? kYdUnit * sum : sum) * (sa[tm] * sb[4 * tn + g + k][q]);
+              }
               p[k] = OUT == kDown8 ? make_uint2(pack_yd(v[0], v[1]), pack_yd(v[2], v[3])) : pack4(v[0], v[1], v[2], v[3]);
             }
             // the halves' lanes exchange: lanes 0..31 get all 8 columns of group g, lanes 32..63 of g + 1

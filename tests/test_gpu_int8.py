@@ -424,3 +424,23 @@ def test_replays_of_a_graph(cfg):
         harness.run_stages(mh, d, b, False, torch.cuda.current_stream())
         torch.cuda.synchronize()
         assert torch.equal(got[:cfg.T], b["out"][:cfg.T]), i
+
+
+@pytest.mark.parametrize("T", [8, 400])
+def test_rows_between_the_experts_and_combine_of_long_sums_and_small_scales(T):
+    """The row's and the column's scale are small and the integer sum is long, so that the product of the scales is far
+    below y. Every column of h is equal (codes 127), so y = sum(w2) h w2_scale; 2^-9 is the rounding, 1e-5 covers h's sigmoid
+    and the FP32 steps, 2^-71 is half a subnormal step."""
+    torch, mh = _gpu()
+    H, I = 128, 2048
+    xq, xs = np.full((T, H), 100, np.int8), np.full(T, 1e-3, np.float32)
+    w1, w1s = np.full((1, 2 * I, H), 20, np.int8), np.full((1, 2 * I), 1e-3, np.float32)
+    w1s[0, I:] = 1e-3 * 2.0 ** -38
+    w2 = np.full((1, H, I), 127, np.int8)
+    w2[0, 1::2] = -127
+    w2s = (np.float32(1.3) * 2.0 ** -(np.arange(H) % 32).astype(np.float32) * 2.0 ** -14)[None].astype(np.float32)
+    got = oi8.decode_yd(_ffn(torch, mh, T, H, I, xq, xs, w1, w1s, w2, w2s))
+    g, u = 256e3 * float(xs[0]) * float(w1s[0, 0]), 256e3 * float(xs[0]) * float(w1s[0, I])
+    y = g / (1 + np.exp(-g)) * u * I * w2[0, :, 0].astype(np.float64) * w2s[0].astype(np.float64)
+    assert np.abs(y).max() < 2.0 ** -35 and np.abs(y).min() > 2.0 ** -70 and np.abs(y).min() < 2.0 ** -60
+    assert np.all(np.abs(got - y) <= (2.0 ** -9 + 1e-5) * np.abs(y) + 2.0 ** -71)
