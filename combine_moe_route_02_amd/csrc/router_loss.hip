@@ -578,7 +578,9 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_bwd_kernel(
       sum = group_sum<G>(sum);
       d = group_sum<G>(d);
       if (r >= t.r1) continue;
-      const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+      // no finite logit: left out like a masked row, with zeros whatever dloss and the coefficients are
+      const bool live = counted[u] && sum != 0.f;
+      const float inv = live ? 1.0f / sum : 0.f;
       const float add = zc * lse[u] - d * inv, scale = gl * inv;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -586,7 +588,7 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_bwd_kernel(
         if (e >= E) continue;
         float o[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) o[j] = counted[u] ? scale * v[u][i * W + j] * (w[i * W + j] + add) : 0.f;
+        for (int j = 0; j < W; ++j) o[j] = live ? scale * v[u][i * W + j] * (w[i * W + j] + add) : 0.f;
         // (whole lines past the L2: 40000 tokens of 160 experts with the forward 33 -> 30 us, 131072 of 256 84 -> 80.5)
         if constexpr (W == 4) __builtin_nontemporal_store(f32x4_t{o[0], o[1], o[2], o[3]}, (f32x4_t*)(dlogits + r * E + e));
         else dlogits[r * E + e] = o[0];

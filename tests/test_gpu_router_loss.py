@@ -241,3 +241,27 @@ def test_repeats_bit_for_bit_on_streams_and_in_a_graph():
         for n in ref:
             if n != "ws":
                 assert torch.equal(ref[n], b[n]), (i, n)
+
+
+@pytest.mark.parametrize("E", [64, 256, 100, 333])
+@pytest.mark.parametrize("g", [np.inf, np.nan])
+def test_tokens_left_out_have_zero_gradient_whatever_the_upstream_gradient_is(E, g):
+    """A step whose upstream gradient has overflowed (a loss scaler sees that from the counted rows): masked tokens,
+    tokens outside every segment and tokens without a finite logit still get rows of zeros."""
+    torch, mh = _gpu()
+    T, k = 90, 4
+    _, lg, idx = _draw(T, E, k, 11)
+    mask = np.ones(T, np.uint8)
+    mask[10:20] = 0
+    lg[30:40] = -np.inf
+    off = torch.tensor([5, 50, 80], dtype=torch.int32, device="cuda")
+    d = _desc(mh, T, E, k)
+    b = _buffers(torch, mh, d, 2)
+    _call(mh, d, 2, 0.5, 0.1, torch.from_numpy(lg).cuda(), torch.from_numpy(idx).cuda(), off, torch.from_numpy(mask).cuda(),
+          torch.tensor([g], dtype=torch.float32, device="cuda"), b)
+    torch.cuda.synchronize()
+    got = b["dlogits"].cpu().numpy()
+    out = np.zeros(T, bool)
+    out[:5] = out[10:20] = out[30:40] = out[80:] = True
+    assert np.all(got[out] == 0.0)
+    assert not np.isfinite(got[~out]).any(axis=1).all()
