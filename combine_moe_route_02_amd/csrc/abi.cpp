@@ -628,7 +628,8 @@ moe_status moe_quantize_rows_i8(int64_t rows, int32_t cols, const void* src_bf16
   MOE_NEED(src_bf16); MOE_NEED(codes); MOE_NEED(scale);
   if (((uintptr_t)src_bf16 & 15) || ((uintptr_t)codes & 7))
     return fail(MOE_ERR_ARG, "%s: the rows must be 16-byte aligned and the codes 8-byte aligned", __func__);
-  if (rows >= 1 << 26) return fail(MOE_ERR_UNSUPPORTED, "%s: rows = %lld above 2^26 - 1", __func__, (long long)rows);
+  // four rows to a workgroup of 256 threads, and a launch holds fewer than 2^32 threads
+  if (rows > (1 << 26) - 4) return fail(MOE_ERR_UNSUPPORTED, "%s: rows = %lld above 2^26 - 4", __func__, (long long)rows);
   MOE_HIP(moe::launch_quantize_rows_i8(src_bf16, codes, scale, rows, cols, (hipStream_t)stream), "quantize_rows_i8");
   return MOE_OK;
 }

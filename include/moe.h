@@ -292,7 +292,7 @@ moe_status moe_quantize_rows_fp8(int64_t rows, int32_t cols, const void* src_bf1
  * activations per token): codes = RNE(v * (127/amax)) in [-127, 127] and scale = amax/127, each step
  * rounded once in FP32; a row of zeros (or of values so small that 127/amax overflows) has codes 0
  * and scale 1; a row with a NaN or an infinity has codes 0 and scale NaN. cols a multiple of 8, src
- * 16-byte and codes 8-byte aligned (MOE_ERR_ARG); rows below 2^26 (MOE_ERR_UNSUPPORTED). */
+ * 16-byte and codes 8-byte aligned (MOE_ERR_ARG); rows up to 2^26 - 4 (MOE_ERR_UNSUPPORTED). */
 moe_status moe_quantize_rows_i8(int64_t rows, int32_t cols, const void* src_bf16, void* codes,
                                 float* scale, void* stream);
 

@@ -444,3 +444,16 @@ def test_rows_between_the_experts_and_combine_of_long_sums_and_small_scales(T):
     y = g / (1 + np.exp(-g)) * u * I * w2[0, :, 0].astype(np.float64) * w2s[0].astype(np.float64)
     assert np.abs(y).max() < 2.0 ** -35 and np.abs(y).min() > 2.0 ** -70 and np.abs(y).min() < 2.0 ** -60
     assert np.all(np.abs(got - y) <= (2.0 ** -9 + 1e-5) * np.abs(y) + 2.0 ** -71)
+
+
+def test_quantize_the_most_rows():
+    torch, mh = _gpu()
+    rows, cols = 2 ** 26 - 4, 8
+    src = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+    src[-1] = torch.arange(8, device="cuda").to(torch.bfloat16)
+    codes, scale = torch.zeros(rows, cols, dtype=torch.int8, device="cuda"), torch.zeros(rows, device="cuda")
+    mh.moe_quantize_rows_i8(rows, cols, src, codes, scale)
+    torch.cuda.synchronize()
+    q, s = oi8.quantize_rows(np.arange(8, dtype=np.float32)[None])
+    assert codes[-1].tolist() == q[0].tolist() and scale[-1].item() == s[0]
+    assert (codes[:-1] == 127).all() and (scale[:-1] == float(np.float32(1) / np.float32(127))).all()

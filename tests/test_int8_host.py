@@ -76,3 +76,8 @@ def test_matmul_arguments():
     for name in ("x", "w", "y"):
         assert _mm(**{name: 24}) == -1
     assert _mm(groups=0, x=None) == 0 and _mm(rows=0, x=None) == 0
+
+
+def test_quantize_rows_refuses_what_a_launch_cannot_hold():
+    for rows in (2 ** 26 - 3, 2 ** 26 - 2, 2 ** 26 - 1):
+        assert _status(mh.moe_quantize_rows_i8, rows, 8, 16, 16, 16, 0) == -3
