@@ -457,3 +457,82 @@ def test_quantize_the_most_rows():
     q, s = oi8.quantize_rows(np.arange(8, dtype=np.float32)[None])
     assert codes[-1].tolist() == q[0].tolist() and scale[-1].item() == s[0]
     assert (codes[:-1] == 127).all() and (scale[:-1] == float(np.float32(1) / np.float32(127))).all()
+
+
+# More than 2048 tokens: a wave per token, the row in 1, 2, 4, 8 or 16 vectors a lane, or read twice
+@pytest.mark.parametrize("H", [64, 512, 576, 1024, 2048, 2112, 4096, 8192, 8256, 16384])
+def test_dispatch_of_many_tokens_bitwise(H):
+    torch, mh = _gpu()
+    T, E, El, k = 2049, 8, 3, 2
+    rng = np.random.default_rng(H)
+    a = rng.standard_normal((T, H)).astype(np.float32) * 10.0 ** rng.uniform(-3, 3, (T, 1)).astype(np.float32)
+    a[5], a[6, -1], a[7, 0] = 0.0, np.nan, -np.inf
+    dev, val = _bf16(torch, a)
+    d = mh.make_desc(T=T, H=H, I=64, E=E, E_local=El, k=k, n_chunks=1, dtype="int8")
+    row = np.full((T, k), -1, np.int32)
+    local = rng.random((T, k)) < El / E
+    local[5:8] = True
+    row[local] = rng.permutation(d.P_c)[:local.sum()]
+    xd, xds = torch.full((d.P_c, H), 77, dtype=torch.int8, device="cuda"), torch.full((d.P_c,), 7.0, device="cuda")
+    mh.moe_dispatch(d, -1, dev, torch.from_numpy(row).cuda(), xd, xds, None)
+    torch.cuda.synchronize()
+    q, s = oi8.quantize_rows(val)
+    want, wants = np.full((d.P_c, H), 77, np.int8), np.full(d.P_c, 7.0, np.float32)
+    for j in range(k):
+        m = row[:, j] >= 0
+        want[row[m, j]], wants[row[m, j]] = q[m], s[m]
+    np.testing.assert_array_equal(xd.cpu().numpy(), want)
+    np.testing.assert_array_equal(xds.cpu().numpy(), wants)
+
+
+# The GEMM's path stage by stage, each against 64 bits from what the stage before it left: 256 x 256 tiles for both
+# products (the first two: several tiles a workgroup, last row tiles of uneven experts, odd numbers of stages; the third
+# takes them for gate/up), and every length of h's quantisation (1, 2, 4, 8 or 16 vectors a lane, or read twice)
+@pytest.mark.parametrize("T,H,I,E,El,k", [(3000, 832, 448, 8, 8, 6), (8200, 2112, 832, 16, 8, 4), (5001, 576, 1344, 8, 5, 7),
+                                          (300, 64, 256, 2, 2, 1), (301, 128, 512, 2, 2, 1), (302, 64, 1024, 2, 2, 2),
+                                          (303, 128, 1088, 2, 2, 1), (304, 64, 2112, 2, 2, 1), (305, 64, 4096, 2, 1, 2),
+                                          (306, 64, 4160, 2, 2, 1)])
+def test_expert_stages_one_by_one(T, H, I, E, El, k):
+    torch, mh = _gpu()
+    print(f"[int8] stages {T, H, I, E, El, k}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(T + I)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    d = mh.make_desc(T=T, H=H, I=I, E=E, E_local=El, k=k, n_chunks=1, dtype="int8")
+    b = mh.allocate(d)
+    b["x"] = rn(T, H).to(torch.bfloat16)
+    b["logits"] = rn(T, E) + 0.7 * rn(1, E)     # experts of uneven length
+    for name, rows, cols in (("w1", 2 * I, H), ("w2", H, I)):
+        b[name], b[name + "_scale"] = torch.empty(El, rows, cols, dtype=torch.int8, device="cuda"), torch.empty(El, rows, device="cuda")
+        mh.moe_quantize_rows_i8(El * rows, cols, (rn(El, rows, cols) * 0.05).to(torch.bfloat16), b[name], b[name + "_scale"])
+    b["yd"].view(torch.int16).fill_(0x1234)
+    harness.run_stages(mh, d, b, False, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    off, P, f64 = b["offsets"][0].tolist(), d.P_c, torch.float64
+    n = off[-1]
+    h = b["h"][:4 * P * I].view(torch.float32).reshape(P, I)
+    hq, hs = b["h"][4 * P * I:5 * P * I].view(torch.int8).reshape(P, I), b["h_scale"]
+    yd = torch.from_numpy(oi8.decode_yd(b["yd"].view(torch.int16).cpu().numpy())).cuda()
+    assert (b["yd"].view(torch.int16)[n:] == 0x1234).all()
+
+    def product(rows, s, w, ws):
+        return (rows.to(f64) @ w.to(f64).t().contiguous()) * s.to(f64).unsqueeze(1) * ws.to(f64)
+    for e in range(El):
+        r = slice(off[e], off[e + 1])
+        gu = product(b["xd"][r], b["xd_scale"][r], b["w1"][e], b["w1_scale"][e])
+        G, U = gu[:, :I], gu[:, I:]
+        want = G / (1 + torch.exp(-G)) * U
+        # G and U: three FP32 roundings each, of which the sigmoid feels |G| more; its exponential's argument |G| 2^-23, the
+        # exponential and the reciprocal 2^-23 each, one sum and two products
+        bad = (h[r].to(f64) - want).abs() > (16 + 6 * G.abs()) * 2.0 ** -24 * want.abs()
+        assert not bad.any(), (e, torch.nonzero(bad)[:4].tolist())
+        # a product is exact in int32, three FP32 roundings, and half a step of 8 mantissa bits
+        want = product(hq[r], hs[r], b["w2"][e], b["w2_scale"][e])
+        bad = (yd[r] - want).abs() > (2.0 ** -9 + 2.0 ** -20) * want.abs() + 2.0 ** -71
+        assert not bad.any(), (e, torch.nonzero(bad)[:4].tolist())
+    q, s = oi8.quantize_rows(h[:n].cpu().numpy())
+    np.testing.assert_array_equal(hq[:n].cpu().numpy(), q)
+    np.testing.assert_array_equal(hs[:n].cpu().numpy(), s)
+    row = b["row_of"].long()
+    part = yd[row.clamp(min=0)] * (b["gates"].to(f64) * (row >= 0)).unsqueeze(2)
+    want, terms = part.sum(1), part.abs().sum(1)
+    assert ((b["out"][:T].to(f64) - want).abs() <= 2.0 ** -8 * want.abs() + 2 * k * 2.0 ** -24 * terms).all()
