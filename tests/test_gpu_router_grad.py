@@ -289,3 +289,48 @@ def test_layer_replays_in_a_graph():
         torch.cuda.synchronize()
         for n in names:
             assert torch.equal(got[n][:run.cfg.T] if n == "out" else got[n], b[n][:run.cfg.T] if n == "out" else b[n]), (i, n)
+
+
+# Workgroups that walk many tiles (the slots' rows go round three buffers, rows and dlogits load a tile ahead), at each
+# number of expert fragments, with tokens that hold more local slots than are loaded ahead; FP8 rows; FP32
+@pytest.mark.parametrize("T,H,E,El,k,kind", [(16390, 2048, 128, 100, 8, "bf16"), (9001, 2112, 32, 9, 4, "bf16"), (9001, 2048, 64, 64, 8, "fp8"),
+                                             (7003, 2304, 200, 150, 7, "bf16"), (5000, 2048, 260, 40, 8, "fp8"), (5005, 2048, 1000, 900, 8, "bf16"),
+                                             (16390, 1088, 128, 16, 8, "f32"), (5003, 2048, 157, 157, 8, "f32")])
+def test_dispatch_bwd_of_many_tiles(T, H, E, El, k, kind):
+    torch, mh = _gpu()
+    print(f"[router_grad] many tiles {T, H, E, El, k, kind}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(T + H + E)
+    f32, f64 = torch.float32, torch.float64
+    dt = f32 if kind == "f32" else torch.bfloat16
+    d = mh.make_desc(T=T, H=H, I=64, E=E, E_local=El, k=k, n_chunks=1, dtype="f32" if kind == "f32" else "bf16",
+                     flags=mh.FLAG_ROUTER_LOSS | (mh.FLAG_FP8_DXD if kind == "fp8" else 0))
+    P, nb = d.P_c, (H + 255) // 256
+    idx = torch.rand(T, E, generator=g, device="cuda").topk(k, 1).indices.to(torch.int32)
+    local = idx < El
+    row = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    row[local] = torch.randperm(P, generator=g, device="cuda")[:int(local.sum())].to(torch.int32)
+    w = (torch.randn(E, H, generator=g, device="cuda") * 0.1).to(dt)
+    dl = torch.randn(T, E, generator=g, device="cuda") * 10.0 ** (4 * torch.rand(T, 1, generator=g, device="cuda") - 3)
+    val = torch.randn(P, H, generator=g, device="cuda").to(dt)
+    dxd = val
+    if kind == "fp8":
+        codes = torch.randint(0, 127, (P, H), generator=g, device="cuda", dtype=torch.uint8)
+        codes |= torch.randint(0, 2, (P, H), generator=g, device="cuda", dtype=torch.uint8) << 7
+        sc = torch.rand(P, nb, generator=g, device="cuda") * 0.01 + 0.001
+        val = codes.view(torch.float8_e4m3fn).to(f32) * sc.repeat_interleave(256, 1)[:, :H]
+        dxd = torch.zeros(P * H * 2, dtype=torch.uint8, device="cuda")
+        dxd[:P * H] = codes.reshape(-1)
+        dxd[P * H:P * H + 4 * P * nb] = sc.view(torch.uint8).reshape(-1)
+    dx = torch.full((T + 1, H), -5.0, dtype=dt, device="cuda")
+    mh.moe_dispatch_bwd(d, -1, dxd, row, idx, dl, w, dx)
+    torch.cuda.synchronize()
+    want, mag = dl.to(f64) @ w.to(f64), dl.to(f64).abs() @ w.to(f64).abs()
+    for j in range(k):
+        part = val[row[:, j].clamp(min=0).long()].to(f64) * (row[:, j:j + 1] >= 0)
+        want += part
+        mag += part.abs()
+    # (FP8 rows: the values above are the FP32 products that the kernel forms; one more rounding covers another order)
+    lim = (E + k) * F * mag if kind == "f32" else 2.0 ** -8 * want.abs() + ((E + 2 * k) * F + 2.0 ** -17) * mag * (1 + 2.0 ** -8)
+    bad = (dx[:T].to(f64) - want).abs() > lim
+    assert not bad.any(), torch.nonzero(bad)[:4].tolist()
+    assert (dx[T] == -5.0).all()

@@ -265,3 +265,23 @@ def test_tokens_left_out_have_zero_gradient_whatever_the_upstream_gradient_is(E,
     out[:5] = out[10:20] = out[30:40] = out[80:] = True
     assert np.all(got[out] == 0.0)
     assert not np.isfinite(got[~out]).any(axis=1).all()
+
+
+# As many segments as the call takes, of a few tokens or of none; many experts with many segments
+@pytest.mark.parametrize("T,E,k,S", [(70000, 8, 2, 65536), (500, 12, 3, 65536), (9000, 1024, 8, 3000), (40000, 33, 4, 20000)])
+def test_very_many_segments(T, E, k, S):
+    torch, mh = _gpu()
+    print(f"[router_loss] {T, E, k, S}", flush=True)
+    rng, lg, idx = _draw(T, E, k, S)
+    mask = (rng.random(T) < 0.9).astype(np.uint8)
+    lg[mask == 0] = np.nan
+    off = np.sort(rng.integers(0, T + 1, S + 1)).astype(np.int32)
+    a, z, g = 0.7, 0.01, -0.6
+    d = _desc(mh, T, E, k)
+    b = _buffers(torch, mh, d, S)
+    args = (torch.from_numpy(lg).cuda(), torch.from_numpy(idx).cuda(), torch.from_numpy(off).cuda(), torch.from_numpy(mask).cuda(),
+            torch.tensor([g], device="cuda"))
+    for _ in range(2):  # (the second call finds the arrival counter as the first left it)
+        _call(mh, d, S, a, z, *args, b)
+    torch.cuda.synchronize()
+    _check(b, orl.router_loss(lg, idx, k, a, z, off.tolist(), mask), k, a, z, g)
