@@ -37,7 +37,9 @@ MOE_DEV uint2 codes8(const u32x4& v, float inv) {
 
 // Rows of yd between the experts and combine: 16 bits of sign, 7 exponent bits (bias 63) and 8 mantissa bits. With
 // BF16 there, its rounding and the output's are two of the same size in a row (sqrt(2) of one); with one bit more
-// the first is half (1.12). Magnitudes from 2^-62, gradually less to 2^-70, to just under 2^65; what is larger, or
+// the first is half (sqrt(1.25) = 1.12 of one). That holds where the gates spread the values; times a gate of 1 (k = 1)
+// or another power of two, codes with the last bit set are ties of the output's rounding, off by half a step whichever
+// way they go: sqrt(1.75) = 1.32 of one, where BF16 rows would have been exact. Magnitudes from 2^-62, gradually less to 2^-70, to just under 2^65; what is larger, or
 // not finite, is code 0x7fff and comes out as NaN. The encoder takes values times 2^-64, so that the exponent's top
 // bit is clear and the code is FP32's upper half without it; halves round away from zero. The unit multiplies the
 // integer sum: ahead of it, the product of two small scales would become subnormal and lose bits that a long sum brings

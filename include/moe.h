@@ -46,8 +46,10 @@
  *     MOE_INT8 (forward only) is laid out like MOE_FP8_E4M3 with 8-bit integer codes (xd, W1, W2),
  *     except h: [P,I] f32 then [P,I] codes (5*P*I bytes), and yd: 16-bit values of sign, 7 exponent
  *     bits (bias 63) and 8 mantissa bits, subnormal below 2^-62, code 0x7fff for NaN and for magnitudes
- *     past the last one (0x7ffe, just under 2^65); they pass from moe_expert_ffn to moe_combine, whose sum then is
- *     within 1.12 of one BF16 rounding (two BF16 roundings in a row: 1.41).
+ *     past the last one (0x7ffe, just under 2^65); they pass from moe_expert_ffn to moe_combine. The error of
+ *     out, in the root mean square, is 1.12 times that of one BF16 rounding where the gates spread the values
+ *     (with BF16 rows: 1.41), and 1.32 times where a gate is a power of two, as the gate 1 of k = 1: half of
+ *     the codes are then halfway between two BF16 values (with BF16 rows: 1).
  *     logits, gates, dgates, dlogits, dwr_acc are always f32; every index array is int32.
  *   - Shapes: logits [T,E]; topk_idx, gates, row_of, dgates [T,k]; counts [n,E];
  *     offsets [n,E_l+1]; src_token [P]; xd, yd, dyd, dxd [P,H]; gu, dgu [P,2I]; h [P,I];

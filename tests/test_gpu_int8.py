@@ -536,3 +536,37 @@ def test_expert_stages_one_by_one(T, H, I, E, El, k):
     part = yd[row.clamp(min=0)] * (b["gates"].to(f64) * (row >= 0)).unsqueeze(2)
     want, terms = part.sum(1), part.abs().sum(1)
     assert ((b["out"][:T].to(f64) - want).abs() <= 2.0 ** -8 * want.abs() + 2 * k * 2.0 ** -24 * terms).all()
+
+
+# The error that the rows of yd add to the output's own rounding, as a root mean square in units of that rounding. A code's
+# error is uniform over a step half as long as BF16's: sqrt(1 + 1/4) = 1.118 together, where the gates spread the values. With
+# k = 1 the gate is 1: an even code is a BF16 value (only the code's own 1/4), an odd one a tie (half a step, 3 in these units,
+# and the 1/4): the mean is 7/4, 1.323. The squares of 300 thousand errors or more average to 1% here (their own spread is
+# of the size of their mean): 1% on the ratio is more than five deviations.
+@pytest.mark.parametrize("k,El,factor", [(1, 8, 1.323), (2, 8, 1.118), (8, 8, 1.118), (4, 3, 1.118)])
+def test_error_of_the_layer_in_units_of_the_outputs_rounding(k, El, factor):
+    torch, mh = _gpu()
+    T, H, I, E, f64 = 1500, 512, 256, 8, torch.float64
+    g = torch.Generator(device="cuda").manual_seed(k)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    d = mh.make_desc(T=T, H=H, I=I, E=E, E_local=El, k=k, n_chunks=1, dtype="int8")
+    b = mh.allocate(d)
+    b["x"], b["logits"] = rn(T, H).to(torch.bfloat16), rn(T, E)
+    for name, rows, cols in (("w1", 2 * I, H), ("w2", H, I)):
+        b[name], b[name + "_scale"] = torch.empty(El, rows, cols, dtype=torch.int8, device="cuda"), torch.empty(El, rows, device="cuda")
+        mh.moe_quantize_rows_i8(El * rows, cols, (rn(El, rows, cols) * 0.05).to(torch.bfloat16), b[name], b[name + "_scale"])
+    mh.moe_layer_forward(d, b, torch.cuda.current_stream(), torch.cuda.Stream())
+    torch.cuda.synchronize()
+    P, off = d.P_c, b["offsets"][0].tolist()
+    y = torch.zeros(P, H, dtype=f64, device="cuda")
+    hq = b["h"][4 * P * I:5 * P * I].view(torch.int8).reshape(P, I)
+    for e in range(El):
+        r = slice(off[e], off[e + 1])
+        y[r] = (hq[r].to(f64) @ b["w2"][e].to(f64).t().contiguous()) * b["h_scale"][r].to(f64).unsqueeze(1) * b["w2_scale"][e].to(f64)
+    row = b["row_of"].long()
+    want = (y[row.clamp(min=0)] * (b["gates"].to(f64) * (row >= 0)).unsqueeze(2)).sum(1)
+    assert (want != 0).sum() >= 300000
+    one = (want.to(torch.bfloat16).to(f64) - want).norm()
+    both = (b["out"][:T].to(f64) - want).norm()
+    print(f"[int8] k {k}: {both / one:.4f} of one rounding, {both / want.norm():.3e} of the norm", flush=True)
+    assert both <= 1.01 * factor * one
