@@ -310,3 +310,25 @@ def test_noalloc_route_size_limit_is_checked_on_the_host():
     st, msg = _status_of(mh.moe_route_noalloc, d, -1, 1, 1, 1, 1, 1, 1, 1, 0)
     assert st == -3 and "scratch" in msg, msg
     assert _status_of(mh.moe_route_noalloc, _desc(), 0, None, None, None, None, None, None, None, 0)[0] == -1
+
+
+def test_stream_of_a_call_without_one(monkeypatch):
+    """A call without a stream takes torch's current one, anew each time: also where torch has no raw accessors."""
+    import types
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=now["stream"]))
+    now = {"stream": 5}
+    for raw in (True, False):
+        if raw:
+            monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: now["stream"] + 100 * dev, raising=False)
+            monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now.get("dev", 0), raising=False)
+        else:
+            monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+        monkeypatch.setattr(mh, "_raw_stream", None)
+        for stream in (5, 0, 8):
+            now["stream"] = stream
+            assert mh._stream(None) == stream
+        if raw:
+            now["dev"] = 1
+            assert mh._stream(None) == 108
+    assert mh._stream(17) == 17 and mh._stream(types.SimpleNamespace(cuda_stream=3)) == 3

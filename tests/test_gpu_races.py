@@ -165,3 +165,13 @@ def test_backward_waits_for_what_the_compute_stream_still_writes(late, flags):
     mh.moe_layer_backward(d, b, cs, aux)
     torch.cuda.synchronize()
     _assert_same(ref, _snapshot(b, cfg), f"{late} late")
+
+
+def test_a_call_without_a_stream_takes_torchs_current_one(monkeypatch):
+    torch, mh = _require_gpu()
+    monkeypatch.setattr(mh, "_raw_stream", None)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (torch.cuda.current_stream(), a, b, a):
+        with torch.cuda.stream(s):
+            assert mh._stream(None) == s.cuda_stream
+    assert mh._stream(None) == torch.cuda.current_stream().cuda_stream
