@@ -64,7 +64,10 @@ constexpr int64_t kRsrcMax = 0x7fffffff;  // bytes one raw buffer descriptor add
 // 11.4 / 9.1; N = 7168, 32 rows 8.0 / 8.6, 80 rows 10.1 / 9.1; K = 7168, N = 4096, 32 rows 12.5 / 16.4, 64 rows 18.8 /
 // 17.5; 8 groups of K = 2048, N = 1536, 17 rows 9.4 / 9.2, 32 rows 10.8 / 9.2; of K = 768, N = 2048, 32 rows 6.7 / 7.0,
 // 64 rows 9.5 / 7.2; 16 groups of K = N = 512, 96 rows 5.9 / 6.3. Long sums favour the few-rows kernels, whose waves
-// share them: K counts to 2048.
+// share them: K counts to 2048. (One of these, 32 rows on N = 7168, goes to the GEMM and loses 0.5 us.)
+// The lengths are on the device, so the average decides, and these are even ones. Uneven lengths cost the few-rows kernels
+// passes over the same weights: 128 groups with 512 rows in all (K = 2048, N = 1536) 73 / 75 where even, 71 / 56 where they
+// fall off as 1 / rank, 122 / 34 as 1 / rank^1.5, 255 / 14 with every row in one group.
 bool few_rows(int64_t groups, int64_t rows, int64_t N, int64_t K) {
   if (groups * N >= kFewMaxColumns) return false;
   return rows <= 4 || (rows <= 96 && rows * groups * cdiv(N, 128) * (K < 2048 ? K : 2048) <= 3200000);
@@ -75,7 +78,9 @@ bool few_rows(int64_t groups, int64_t rows, int64_t N, int64_t K) {
 // (few-rows / GEMM, us, the whole layer): H = 2048, I = 768, 128 experts with 1 row 96 / 96, 2 rows 121 / 125, 16 rows
 // 165 / 145; 16 experts, 4 rows 26 / 29, 16 rows 30 / 29, 64 rows 59 / 33; 2 experts, 32 rows 21 / 24, 64 rows 32 / 25;
 // H = 512, I = 256, 128 experts, 16 rows 25 / 33, 32 rows 44 / 34; 16 experts, 32 rows 19 / 22, 128 rows 36 / 25; H =
-// 256, I = 640, 56 experts, 22 rows 45 / 29; H = 1024, I = 64, 128 experts, 32 rows 35 / 36, 64 rows 58 / 40.
+// 256, I = 640, 56 experts, 22 rows 45 / 29; H = 1024, I = 64, 128 experts, 32 rows 35 / 36, 64 rows 58 / 40. Even routing
+// again; 128 tokens, top-4, of 128 experts (H = 2048, I = 768) 124 / 132 where even, 190 / 52 with experts that fall off as
+// 1 / rank (the fullest has 106 rows); 33 tokens, top-8, 115 / 122 and, as 1 / rank^2, 85 / 41.
 bool few_rows_layer(int64_t groups, int64_t rows, int64_t H, int64_t I) {
   if (groups * (I > H ? I : H) >= kFewMaxColumns) return false;
   return rows <= 4 || (rows <= 48 && moe::few_rows_i8_traffic(groups, rows, H, I) <= 40000000 + 3 * groups * H * I / 5);

@@ -1,9 +1,9 @@
 // 8-bit integer expert products for a few rows per expert (decode batches): the weights of every expert
 // that has rows are streamed once and everything else is small, so the time is the weights' bytes.
 //
-// The grouped GEMM's 256 x 256 tiles leave most CUs idle here (an expert is 6 to 8 tiles) and wait for
-// their operand ring at every tile. These kernels give 16, 32 or 64 columns of one expert to a
-// workgroup of four waves. A wave loads the weights of its 16 columns straight into registers as
+// The grouped GEMM's smallest tiles (64 x 64) walk K pair by pair at 0.3 us however few rows they hold, a few experts
+// fill few CUs with them, and h takes a launch of its own to be quantised. These kernels give 16, 32 or 64 columns of one
+// expert to a workgroup of four waves. A wave loads the weights of its 16 columns straight into registers as
 // v_mfma_i32_16x16x64_i8 operands (16 columns x 64 bytes, no LDS: no weight is used by two waves), one
 // batch of K steps ahead. With 64 columns each wave runs the whole of K; with fewer, 2 or 4 waves share
 // the columns and take the K steps in turn, so that a few experts still fill the CUs, and their int32
@@ -16,7 +16,10 @@
 // codes half of the h buffer, unused here), and down forms each row's scale from them and quantises h
 // once per workgroup, with the FP32 steps of the quantisation kernels.
 //
-// H = 2048, I = 768, 128 experts, top-8: one token (8 experts, 38 MB of weights) 9 us gate/up and 7 us down, of which a
+// Both products and h's codes, H = 2048, I = 768, 128 experts, top-8 (here / GEMM path, us): 1 token 15 / 23, 4 tokens 29 /
+// 40, 16 tokens 93 / 104, 33 tokens 115 / 122. A pass holds the rows that even routing gives an expert; one with many more takes
+// its weights through again for every pass (the figures of uneven routing stand at few_rows_layer).
+// The same layer: one token (8 experts, 38 MB of weights) 9 us gate/up and 7 us down, of which a
 // launch's first loads and the sums' exchange are half; 33 tokens (all but a few experts) 72 and 47 us, 4.8 and 3.8
 // TB/s. Twice the loads in flight are slower (16 rows x 7168 on 4096 columns 10.5 -> 11.0 us, 32 rows 12.5 -> 15).
 #include <algorithm>
@@ -370,7 +373,6 @@ hipError_t run_few_kw(const char* name, const FewArgs& a, int cap, bool wide, in
   }
 }
 
-// rows: a bound of the rows of all groups; usual: the rows that one group has on average
 // Rows of a pass: enough for nearly every group when rows spread by chance (their deviation is the square root
 // of the mean), so that weights are read once; a fuller group takes more passes.
 int pass_rows(int64_t usual, bool spread) {
@@ -388,6 +390,7 @@ int down_slices(int64_t active, int64_t cols, int cap) {
   return active * ((cols + 3) / 4) >= kWant ? 4 : active * ((cols + 1) / 2) >= kWant ? 2 : 1;
 }
 
+// rows: a bound of the rows of all groups; usual: the rows that one group has on average
 template <int MODE>
 hipError_t run_few(const char* name, FewArgs a, int64_t rows, int64_t usual, hipStream_t s) {
   const int cap = pass_rows(usual, a.offsets != nullptr);

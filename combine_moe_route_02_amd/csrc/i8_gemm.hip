@@ -11,14 +11,14 @@
 //     row (16 bytes), so neither ring slot nor barrier is needed. Each wave issues exactly kStores buffer
 //     stores per tile, rows and columns outside it dropped by the descriptor's extent, and the
 //     next tile waits for its loads with those stores still in flight.
-// Measured at 8192 x 4096 x 7168: 198 us (2.43 POPS; MFMA busy 65% of the cycles, clock near 1.8 GHz under
-// this load, LDS bank conflicts 0) against 220 us tile by tile; four slots of single stages, loaded three
-// ahead, 222 us. The expert products of the 16K-token share take two rounds of 35 us (gate/up) and two and
-// a part of 22 us (down): 128-row tiles lose more in the K loop than they gain in the last round (gate/up
+// Measured at 8192 x 4096 x 7168: 195 us (2.47 POPS; MFMA busy 65% of the cycles, clock 1.8 GHz under
+// this load, LDS bank conflicts 0; 210 us on a slower card) against 220 us tile by tile on a card of 198; four slots of single
+// stages, loaded three ahead, 222 us. The expert products of the 16K-token share take two rounds of 33 us (gate/up, 66) and
+// two and a part of 22 us (down, 51): 128-row tiles lose more in the K loop than they gain in the last round (gate/up
 // 90 us, down 59 us).
-// Small tiles: 0.5 us a pair of stages, bound by LDS (a pair's 64 fragment reads take as long as its products, and
-// the loads' writes come on top: the same time with loads of nothing). They stream weights at HBM's rate
-// (128 groups of 24 rows x 2048 on 1536 columns 81 us, 5.0 TB/s). Eight waves of 32 x 64 take the same time. Tiny
+// Small tiles: 0.5 us a pair of stages. One wave a SIMD does its fragment reads, its products and its waits one after the
+// other: on a CU that has a tile MFMA is busy 28% and LDS 15% of the cycles, and loads of nothing take the same time. They
+// stream weights at HBM's rate (128 groups of 24 rows x 2048 on 1536 columns 82 us, 4.9 TB/s). Eight waves of 32 x 64 take the same time. Tiny
 // tiles: 0.3 us a pair, so four of them on four CUs beat a small one (256 rows x 7168 on 4096 columns 28 -> 21 us).
 // Tiles of 256 x 192 gain with even groups (gate/up of 16 x 1024 rows 60 -> 55 us) and lose with uneven ones,
 // whose small last tiles then make a third round (65 -> 83 us).

@@ -92,7 +92,9 @@ struct Pieces {
   MOE_DEV int64_t base(int i) const { return (bound(i) >> shift) + i; }
 };
 
-// The block's piece and rows. Every thread of the block calls it.
+// The block's piece and rows. Every thread of the block calls it. Every block scans the segments, so the time grows with
+// their square once they are many: 131072 tokens of 128 experts, forward and backward, 53 us with up to 64 segments, 118 us
+// with 1024, 0.7 ms with 8192, 15 ms with 65536.
 struct Tile { int piece; int64_t r0, r1; };
 MOE_DEV Tile find_tile(const Pieces& q) {
   const int64_t blk = blockIdx.x;

@@ -6,8 +6,8 @@
 // with one FP32 rounding per step; a row of zeros has codes 0 and scale 1. A row that holds a NaN or
 // an infinity has codes 0 and scale NaN, so what is computed from it is NaN. All are bound by their
 // bytes: one wave per row, 16-byte loads, and the row stays in registers between its absmax and its
-// codes where it fits (up to 16 vectors a lane), so it is read once. 8192 rows of 7168 values 32 us (5.4 TB/s), 16K rows
-// of 768 FP32 values 11.5 us.
+// codes where it fits (up to 16 vectors a lane), so it is read once. 8192 rows of 7168 values 34 us (5.2 TB/s; 32 to
+// 36 from card to card), 16K rows of 768 FP32 values 11.2 us.
 #include <algorithm>
 
 #include "common.h"
@@ -39,7 +39,7 @@ MOE_DEV uint32_t wave_max_u32(uint32_t v) {
 }
 
 // A row is read once and its codes are read next: the row's lines need not stay in the L2 (8192 rows of 7168 values with
-// the L2 cold 36 -> 34 us, dispatch of 16K tokens 20 -> 18.6 us; codes stored past the L2 cost the GEMM more).
+// the L2 cold 36 -> 34 us on one card, dispatch of 16K tokens 20 -> 18.6 us; codes stored past the L2 cost the GEMM more).
 MOE_DEV u32x4 load_once(const u32x4* p) {
   const i32x4_t v = __builtin_nontemporal_load((const i32x4_t*)p);
   return u32x4{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
