@@ -570,3 +570,26 @@ def test_error_of_the_layer_in_units_of_the_outputs_rounding(k, El, factor):
     both = (b["out"][:T].to(f64) - want).norm()
     print(f"[int8] k {k}: {both / one:.4f} of one rounding, {both / want.norm():.3e} of the norm", flush=True)
     assert both <= 1.01 * factor * one
+
+
+# Chunks without a token, no local expert, one expert in all, every expert chosen by every token
+@pytest.mark.parametrize("cfg", [
+    MoeConfig("i8_empty_chunks", T=2, H=128, I=64, E=8, E_local=8, k=3, n_chunks=5, dtype="int8", seed_base=1010),
+    MoeConfig("i8_one_expert", T=37, H=192, I=128, E=1, E_local=1, k=1, n_chunks=2, dtype="int8", seed_base=1020),
+    MoeConfig("i8_all_chosen", T=400, H=256, I=128, E=8, E_local=5, e0=3, k=8, n_chunks=3, dtype="int8", seed_base=1030),
+    MoeConfig("i8_top1", T=900, H=320, I=192, E=16, E_local=16, k=1, n_chunks=1, dtype="int8", seed_base=1040),
+], ids=lambda c: c.name)
+def test_layer_forward_at_the_edges(cfg):
+    test_layer_forward(cfg)
+
+
+def test_layer_without_a_local_expert():
+    torch, mh = _gpu()
+    for T in (3, 3000):
+        d = mh.make_desc(T=T, H=128, I=64, E=8, E_local=0, e0=8, k=2, n_chunks=2, dtype="int8")
+        b = mh.allocate(d)
+        b["x"], b["logits"] = torch.randn(T, 128, device="cuda").to(torch.bfloat16), torch.randn(T, 8, device="cuda")
+        b["out"].fill_(3.0)
+        mh.moe_layer_forward(d, b, torch.cuda.current_stream(), torch.cuda.Stream())
+        torch.cuda.synchronize()
+        assert not b["out"][:T].any() and (b["out"][T:] == 3.0).all() and (b["row_of"] == -1).all()

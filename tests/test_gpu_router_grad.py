@@ -334,3 +334,48 @@ def test_dispatch_bwd_of_many_tiles(T, H, E, El, k, kind):
     bad = (dx[:T].to(f64) - want).abs() > lim
     assert not bad.any(), torch.nonzero(bad)[:4].tolist()
     assert (dx[T] == -5.0).all()
+
+
+# FP32 in several chunks, chunks without a token, every expert local and chosen by every token
+@pytest.mark.parametrize("how", ["fused", "apart"])
+@pytest.mark.parametrize("cfg", [
+    MoeConfig("rl_f32_n3", T=200, H=128, I=64, E=12, E_local=6, e0=3, k=3, n_chunks=3, dtype="f32", seed_base=1000, x_std=0.02, backward=True),
+    MoeConfig("rl_empty_chunks", T=7, H=128, I=64, E=8, E_local=8, k=2, n_chunks=5, dtype="bf16", seed_base=1005, backward=True),
+    MoeConfig("rl_all_chosen", T=260, H=192, I=128, E=8, E_local=8, k=8, n_chunks=2, dtype="bf16", seed_base=1010, backward=True),
+], ids=lambda c: c.name)
+def test_layer_at_the_edges(cfg, how):
+    torch, mh = _gpu()
+    print(f"[router_grad] {cfg} {how}", flush=True)
+    _check(*_layer(torch, mh, cfg, 0, how), mh)
+
+
+@pytest.mark.parametrize("delayed", ["compute", "aux"])
+@pytest.mark.parametrize("flags", [0, 1 | 2 | 4])
+@pytest.mark.parametrize("how", ["fused", "apart", "from_x"])
+def test_layer_with_a_delay_on_one_stream(how, flags, delayed):
+    """Work queued on one of the two streams in front of the call: the loss and its gradient run on either of them and
+    must see every chunk's routing, and every reader of dlogits the loss's gradient."""
+    torch, mh = _gpu()
+    cfg = LAYERS[1]
+    names = ("router_loss", "seg_counts", "seg_probs", "router_lse", "dlogits", "dx", "dwr", "dw1", "dw2")
+    run, _, _ = _layer(torch, mh, cfg, flags, how)
+    b, d = run.bufs, run.desc
+    ref = {n: b[n].clone() for n in names}
+    cs, aux = torch.cuda.current_stream(), torch.cuda.Stream()
+
+    def delay():
+        with torch.cuda.stream(cs if delayed == "compute" else aux):
+            torch.cuda._sleep(2_000_000)
+    for n in names + ("topk_idx", "router_logits"):
+        b[n].zero_()
+    torch.cuda.synchronize()
+    delay()
+    if how == "apart":
+        mh.moe_layer_forward(d, b, cs, aux)
+        delay()
+        mh.moe_layer_backward(d, b, cs, aux)
+    else:
+        mh.moe_layer_forward_backward(d, b, cs, aux)
+    torch.cuda.synchronize()
+    for n in names:
+        assert torch.equal(ref[n], b[n]), n
