@@ -175,3 +175,30 @@ def test_a_call_without_a_stream_takes_torchs_current_one(monkeypatch):
         with torch.cuda.stream(s):
             assert mh._stream(None) == s.cuda_stream
     assert mh._stream(None) == torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("flags", [0, 16, 1 | 2 | 4])
+def test_backward_alone_in_a_graph(flags):
+    """The backward captured without the forward: the auxiliary stream joins the capture through the compute stream."""
+    cfg = CASES[0]
+    torch, mh, d, b = _setup(cfg, flags)
+    if flags & mh.FLAG_ROUTER_LOSS:
+        b.update(balance_coef=0.5, z_coef=0.01)
+    mh.moe_layer_forward(d, b, torch.cuda.current_stream(), torch.cuda.current_stream())
+    main, aux = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=main):
+        mh.moe_layer_backward(d, b, torch.cuda.current_stream(), aux)
+    dy = b["dy"].clone()
+    for i in range(3):
+        b["dy"].copy_(dy * (i + 1))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = _snapshot(b, cfg)
+        for name in ("dgates", "dlogits", "dx", "dw1", "dw2", "dwr"):
+            b[name].fill_(3.0)
+        mh.moe_layer_backward(d, b, torch.cuda.current_stream(), aux)
+        torch.cuda.synchronize()
+        _assert_same(got, _snapshot(b, cfg), f"replay {i}")
