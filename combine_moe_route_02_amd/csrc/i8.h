@@ -39,11 +39,11 @@ MOE_DEV uint2 codes8(const u32x4& v, float inv) {
 // BF16 there, its rounding and the output's are two of the same size in a row (sqrt(2) of one); with one bit more
 // the first is half (sqrt(1.25) = 1.12 of one). That holds where the gates spread the values; times a gate of 1 (k = 1)
 // or another power of two, codes with the last bit set are ties of the output's rounding, off by half a step whichever
-// way they go: sqrt(1.75) = 1.32 of one, where BF16 rows would have been exact. Magnitudes from 2^-62, gradually less to 2^-70, to just under 2^65; what is larger, or
-// not finite, is code 0x7fff and comes out as NaN. The encoder takes values times 2^-64, so that the exponent's top
-// bit is clear and the code is FP32's upper half without it; halves round away from zero. The unit multiplies the
-// integer sum: ahead of it, the product of two small scales would become subnormal and lose bits that a long sum brings
-// back into the format's range.
+// way they go: sqrt(1.75) = 1.32 of one, where BF16 rows would have been exact. Magnitudes from 2^-62, gradually less
+// to 2^-70, to just under 2^65; what is larger, or not finite, is code 0x7fff and comes out as NaN. The encoder takes
+// values times 2^-64, so that the exponent's top bit is clear and the code is FP32's upper half without it; halves round
+// away from zero. The unit multiplies the integer sum: ahead of it, the product of two small scales would become
+// subnormal and lose bits that a long sum brings back into the format's range.
 constexpr float kYdUnit = 0x1p-64f;
 MOE_DEV uint32_t pack_yd(float lo, float hi) {
   const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);

@@ -18,8 +18,9 @@
 // 90 us, down 59 us).
 // Small tiles: 0.5 us a pair of stages. One wave a SIMD does its fragment reads, its products and its waits one after the
 // other: on a CU that has a tile MFMA is busy 28% and LDS 15% of the cycles, and loads of nothing take the same time. They
-// stream weights at HBM's rate (128 groups of 24 rows x 2048 on 1536 columns 82 us, 4.9 TB/s). Eight waves of 32 x 64 take the same time. Tiny
-// tiles: 0.3 us a pair, so four of them on four CUs beat a small one (256 rows x 7168 on 4096 columns 28 -> 21 us).
+// stream weights at HBM's rate (128 groups of 24 rows x 2048 on 1536 columns 82 us, 4.9 TB/s). Eight waves of 32 x 64
+// take the same time. Tiny tiles: 0.3 us a pair, so four of them on four CUs beat a small one (256 rows x 7168 on 4096
+// columns 28 -> 21 us).
 // Tiles of 256 x 192 gain with even groups (gate/up of 16 x 1024 rows 60 -> 55 us) and lose with uneven ones,
 // whose small last tiles then make a third round (65 -> 83 us).
 // The sums are exact in int32 and rounded once to FP32; scales multiply in FP32 and BF16 rounds once.
