@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, c_char_p, c_float, c_int, c_int32, c_int64, c_void_p
+from ctypes import POINTER, Structure, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_uint32, c_void_p
 from typing import Dict, Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +41,42 @@ FLAG_FP8_DXD = 4  # dxd as block-scaled e4m3 rows (codes, then per-256-column sc
 
 
 FLAG_ROUTER_LOSS = 16  # the router logits carry an auxiliary loss: dense dlogits (8 is not a flag)
+FLAG_ROUTER_SCORES = 64  # the layer primitives route by scores (32 is not a flag)
+
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+
+
+class MoeRouterScores(Structure):
+    _fields_ = [("score", c_int32), ("n_groups", c_int32), ("topk_groups", c_int32), ("group_top", c_int32),
+                ("renormalize", c_int32), ("scale", c_float)]
+
+
+def make_router_scores(score="softmax", n_groups=1, topk_groups=1, group_top=1, renormalize=True,
+                       scale=1.0) -> MoeRouterScores:
+    return MoeRouterScores(SCORES[score] if isinstance(score, str) else score, n_groups, topk_groups, group_top,
+                           int(renormalize), scale)
+
+
+class MoeAdamwTensor(Structure):
+    _fields_ = [(f, c_void_p) for f in ("w", "master", "grad", "m", "v", "m_scale", "v_scale")] + \
+        [("n", c_int64), ("w_dtype", c_int32), ("grad_dtype", c_int32), ("lr_scale", c_float), ("weight_decay", c_float)]
+
+
+class MoeAdamwOptions(Structure):
+    _fields_ = [(f, c_double) for f in ("lr", "beta1", "beta2", "eps")] + \
+        [(f, c_void_p) for f in ("lr_dev", "step_dev", "grad_scale")] + \
+        [("step", c_int64), ("state_bits", c_int32), ("seed", c_uint32)]
+
+
+class MoeAdamwState(Structure):
+    _fields_ = [(f, c_void_p) for f in ("master", "m", "v", "m_scale", "v_scale")] + \
+        [("lr_scale", c_float), ("weight_decay", c_float)]
+
+
+class MoeLayerOptimizer(Structure):
+    _fields_ = [("adamw", MoeAdamwOptions), ("w1", MoeAdamwState), ("w2", MoeAdamwState), ("w_r", MoeAdamwState),
+                ("max_norm", c_double), ("norm", c_void_p), ("norm_workspace", c_void_p), ("bias_rate", c_float)]
 
 
 TENSOR_FIELDS = ["x", "logits", "w1", "w1_scale", "w2", "w2_scale", "w_r", "dy",
@@ -57,7 +93,8 @@ LOSS_OPTIONS = {"n_segments": (c_int32, 1), "balance_coef": (c_float, 0.0), "z_c
 
 
 class MoeTensors(Structure):
-    _fields_ = [(f, c_void_p) for f in TENSOR_FIELDS] + [(f, t) for f, (t, _) in LOSS_OPTIONS.items()]
+    _fields_ = [(f, c_void_p) for f in TENSOR_FIELDS] + [(f, t) for f, (t, _) in LOSS_OPTIONS.items()] + \
+        [("router_bias", c_void_p), ("router_scores", MoeRouterScores)]  # FLAG_ROUTER_SCORES
 
 
 SIZE_FIELDS = ["topk_idx", "gates", "counts", "offsets", "row_of", "src_token", "xd", "xd_scale", "gu",
@@ -78,6 +115,15 @@ _SIGS = {
     "moe_route": [POINTER(MoeDesc), c_int] + [c_void_p] * 9,
     "moe_route_x": [POINTER(MoeDesc), c_int] + [c_void_p] * 11,
     "moe_route_noalloc": [POINTER(MoeDesc), c_int] + [c_void_p] * 8,
+    "moe_route_scores": [POINTER(MoeDesc), c_int, POINTER(MoeRouterScores)] + [c_void_p] * 10,
+    "moe_route_scores_bwd": [POINTER(MoeDesc), c_int, POINTER(MoeRouterScores)] + [c_void_p] * 9,
+    "moe_router_bias_update": [c_int32, c_int32, c_void_p, c_float, c_void_p, c_void_p],
+    "moe_adamw_step": [POINTER(MoeAdamwOptions), c_int32, POINTER(MoeAdamwTensor), c_void_p],
+    "moe_grad_norm_bytes": [POINTER(c_int64)],
+    "moe_grad_norm": [c_int32, POINTER(MoeAdamwTensor), c_double] + [c_void_p] * 3,
+    "moe_adamw_unpack": [c_int64] + [c_void_p] * 7,
+    "moe_adamw_pack": [c_int64] + [c_void_p] * 7,
+    "moe_layer_update": [POINTER(MoeDesc), POINTER(MoeTensors), POINTER(MoeLayerOptimizer), c_void_p],
     "moe_dispatch": [POINTER(MoeDesc), c_int] + [c_void_p] * 6,
     "moe_expert_ffn": [POINTER(MoeDesc), c_int] + [c_void_p] * 12,
     "moe_combine": [POINTER(MoeDesc), c_int] + [c_void_p] * 5,
@@ -149,6 +195,10 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
 _raw_stream = None  # torch's current stream of the current device as an integer
 
 
@@ -206,6 +256,25 @@ def moe_route_x(d, chunk, x, w_r, logits, topk_idx, gates, counts, offsets, row_
     _check(lib().moe_route_x(ctypes.byref(d), chunk, _ptr(x), _ptr(w_r), _ptr(logits), _ptr(topk_idx), _ptr(gates),
                              _ptr(counts), _ptr(offsets), _ptr(row_of), _ptr(src_token), _ptr(workspace),
                              _stream(stream)), "moe_route_x")
+
+
+def moe_route_scores(d, chunk, scores, logits, bias, topk_idx, gates, counts, offsets, row_of, src_token, workspace,
+                     stream=None):
+    _check(lib().moe_route_scores(ctypes.byref(d), chunk, _ref(scores), _ptr(logits), _ptr(bias), _ptr(topk_idx),
+                                  _ptr(gates), _ptr(counts), _ptr(offsets), _ptr(row_of), _ptr(src_token),
+                                  _ptr(workspace), _stream(stream)), "moe_route_scores")
+
+
+def moe_route_scores_bwd(d, chunk, scores, logits, dgates, topk_idx, x, dlogits, dwr_acc=None, dwr=None, workspace=None,
+                         stream=None):
+    _check(lib().moe_route_scores_bwd(ctypes.byref(d), chunk, _ref(scores), _ptr(logits), _ptr(dgates),
+                                      _ptr(topk_idx), _ptr(x), _ptr(dlogits), _ptr(dwr_acc), _ptr(dwr),
+                                      _ptr(workspace), _stream(stream)), "moe_route_scores_bwd")
+
+
+def moe_router_bias_update(E, rows, counts, rate, bias, stream=None):
+    _check(lib().moe_router_bias_update(E, rows, _ptr(counts), rate, _ptr(bias), _stream(stream)),
+           "moe_router_bias_update")
 
 
 def moe_dispatch(d, chunk, x, row_of, xd, xd_scale=None, h_scale=None, stream=None):
@@ -322,6 +391,9 @@ def _tensors(bufs: Dict[str, object]) -> MoeTensors:
         setattr(t, f, _ptr(bufs.get(f)))
     for f, (_, default) in LOSS_OPTIONS.items():
         setattr(t, f, bufs.get(f, default))
+    t.router_bias = _ptr(bufs.get("router_bias"))
+    if bufs.get("router_scores") is not None:
+        t.router_scores = bufs["router_scores"]
     return t
 
 
@@ -341,6 +413,121 @@ def moe_layer_forward_backward(d, bufs, compute_stream=None, aux_stream=None):
     t = _tensors(bufs)
     _check(lib().moe_layer_forward_backward(ctypes.byref(d), ctypes.byref(t), _stream(compute_stream),
                                             _stream(aux_stream)), "moe_layer_forward_backward")
+
+
+def moe_layer_update(d, bufs, optimizer, stream=None):
+    t = _tensors(bufs)
+    _check(lib().moe_layer_update(ctypes.byref(d), ctypes.byref(t), _ref(optimizer), _stream(stream)),
+           "moe_layer_update")
+
+
+# ------------------------------------------------------------------ weight update
+
+def _pay(t) -> int:
+    """MOE_F32 or MOE_BF16 of a torch tensor."""
+    name = str(t.dtype)
+    if name not in ("torch.float32", "torch.bfloat16"):
+        raise TypeError(f"weights and gradients are float32 or bfloat16, not {name}")
+    return MOE_F32 if name == "torch.float32" else MOE_BF16
+
+
+def make_adamw_options(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, state_bits=32, seed=0, lr_dev=None, step_dev=None,
+                       grad_scale=None) -> MoeAdamwOptions:
+    """Options of moe_adamw_step. ``step`` counts from 1: set ``options.step`` before each call, or pass ``step_dev`` (and
+    ``lr_dev``), device scalars that the kernels read, where the call is captured into a graph."""
+    return MoeAdamwOptions(lr, beta1, beta2, eps, _ptr(lr_dev), _ptr(step_dev), _ptr(grad_scale), step, state_bits,
+                           seed & 0xffffffff)
+
+
+class AdamwTensors:
+    """The tensors of moe_adamw_step and moe_grad_norm: their table, made once, and the references it needs."""
+
+    def __init__(self, parts):
+        self.parts = [dict(p) for p in parts]
+        self.table = (MoeAdamwTensor * len(self.parts))()
+        for row, p in zip(self.table, self.parts):
+            for f in ("w", "master", "grad", "m", "v", "m_scale", "v_scale"):
+                x = p.get(f)
+                if x is not None and not x.is_contiguous():
+                    raise ValueError(f"{f} must be contiguous")
+                setattr(row, f, _ptr(x))
+            row.n = p["grad"].numel()
+            for f in ("w", "master", "m", "v"):
+                if p.get(f) is not None and p[f].numel() != row.n:
+                    raise ValueError(f"{f} has {p[f].numel()} elements and its gradient {row.n}")
+            row.grad_dtype = _pay(p["grad"])
+            row.w_dtype = _pay(p["w"]) if p.get("w") is not None else MOE_F32
+            row.lr_scale, row.weight_decay = p.get("lr_scale", 1.0), p.get("weight_decay", 0.0)
+
+    def __len__(self):
+        return len(self.parts)
+
+
+def make_adamw_tensors(parts) -> AdamwTensors:
+    """Table of tensors from dicts of torch tensors: ``grad``, ``w``, ``m``, ``v``, with 8-bit averages ``m_scale`` and
+    ``v_scale``, and as wanted ``master``, ``lr_scale`` (1), ``weight_decay`` (0)."""
+    return AdamwTensors(parts)
+
+
+def moe_adamw_step(options, tensors, stream=None):
+    _check(lib().moe_adamw_step(_ref(options), len(tensors), tensors.table, _stream(stream)), "moe_adamw_step")
+
+
+def moe_grad_norm_bytes() -> int:
+    n = c_int64()
+    _check(lib().moe_grad_norm_bytes(ctypes.byref(n)), "moe_grad_norm_bytes")
+    return n.value
+
+
+def moe_grad_norm(tensors, max_norm, norm, workspace, stream=None):
+    _check(lib().moe_grad_norm(len(tensors), tensors.table, max_norm, _ptr(norm), _ptr(workspace), _stream(stream)),
+           "moe_grad_norm")
+
+
+def moe_adamw_unpack(n, m_codes, m_scale, v_codes, v_scale, m, v, stream=None):
+    _check(lib().moe_adamw_unpack(n, _ptr(m_codes), _ptr(m_scale), _ptr(v_codes), _ptr(v_scale), _ptr(m), _ptr(v),
+                                  _stream(stream)), "moe_adamw_unpack")
+
+
+def moe_adamw_pack(n, m, v, m_codes, m_scale, v_codes, v_scale, stream=None):
+    _check(lib().moe_adamw_pack(n, _ptr(m), _ptr(v), _ptr(m_codes), _ptr(m_scale), _ptr(v_codes), _ptr(v_scale),
+                                _stream(stream)), "moe_adamw_pack")
+
+
+def adamw_state(n, state_bits=32, device="cuda"):
+    """Moving averages of a new run for n elements: dict of ``m``, ``v`` and, in 8 bits, their scales; all zeros."""
+    import torch
+    if state_bits == 32:
+        return {f: torch.zeros(n, device=device) for f in ("m", "v")}
+    out = {"m": torch.zeros(n, dtype=torch.int8, device=device), "v": torch.zeros(n, dtype=torch.uint8, device=device)}
+    out.update({f: torch.zeros((n + 255) // 256, device=device) for f in ("m_scale", "v_scale")})
+    return out
+
+
+def make_layer_optimizer(d: MoeDesc, bufs, options, master=True, weight_decay=0.0, max_norm=None, bias_rate=0.0,
+                         device="cuda") -> MoeLayerOptimizer:
+    """Optimizer of moe_layer_update for the layer's ``w1``, ``w2`` and ``w_r`` in ``bufs`` (which must stay the layer's): new
+    moving averages, FP32 masters of BF16 weights (unless ``master`` is false), the norm's buffers where ``max_norm`` is
+    given. The router has no weight decay. The tensors are in ``optimizer.buffers``; set ``optimizer.adamw.step``
+    before each call."""
+    import torch
+    o = MoeLayerOptimizer()
+    o.adamw = options
+    o.buffers = {}
+    for f in ("w1", "w2", "w_r"):
+        w = bufs[f]
+        s = adamw_state(w.numel(), options.state_bits, device)
+        if master and w.dtype == torch.bfloat16:
+            s["master"] = w.detach().float().reshape(-1)
+        o.buffers[f] = s
+        setattr(o, f, MoeAdamwState(*[_ptr(s.get(x)) for x in ("master", "m", "v", "m_scale", "v_scale")], 1.0,
+                                    0.0 if f == "w_r" else weight_decay))
+    if max_norm is not None:
+        o.buffers["norm"] = torch.zeros(2, device=device)
+        o.buffers["norm_workspace"] = torch.empty(moe_grad_norm_bytes(), dtype=torch.uint8, device=device)
+        o.max_norm, o.norm, o.norm_workspace = max_norm, _ptr(o.buffers["norm"]), _ptr(o.buffers["norm_workspace"])
+    o.bias_rate = bias_rate
+    return o
 
 
 # ------------------------------------------------------------------ host-only helpers

@@ -25,7 +25,8 @@ COMMON = [
 ]
 
 SOURCES = ["route.hip", "rows.hip", "gemm.hip", "grouped_gemm.hip", "wgrad.hip", "rows_wgrad.hip", "router_wgrad.hip",
-           "stash.hip", "router_loss.hip", "dispatch_bwd_dense.hip", "rows_i8.hip", "i8_gemm.hip", "few_rows_i8.hip", "abi.cpp", "trace.cpp"]
+           "stash.hip", "router_loss.hip", "dispatch_bwd_dense.hip", "rows_i8.hip", "i8_gemm.hip", "few_rows_i8.hip", "route_scores.hip",
+           "adamw.hip", "abi.cpp", "trace.cpp"]
 
 
 def _compile(src: str) -> str:

@@ -4,12 +4,16 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstdarg>
 #include <cstdio>
+#include <functional>
 #include <map>
+#include <memory>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -88,7 +92,7 @@ bool few_rows_layer(int64_t groups, int64_t rows, int64_t H, int64_t I) {
 
 moe_status validate(const moe_desc* d) {
   if (!d) return fail(MOE_ERR_ARG, "descriptor is NULL");
-  if (d->flags & ~(MOE_FLAG_FP8_DGRAD | MOE_FLAG_FP8_WGRAD | MOE_FLAG_FP8_DXD | MOE_FLAG_ROUTER_LOSS))
+  if (d->flags & ~(MOE_FLAG_FP8_DGRAD | MOE_FLAG_FP8_WGRAD | MOE_FLAG_FP8_DXD | MOE_FLAG_ROUTER_LOSS | MOE_FLAG_ROUTER_SCORES))
     return fail(MOE_ERR_ARG, "descriptor flags 0x%x hold an unknown bit", d->flags);
   if (d->dtype != MOE_F32 && d->dtype != MOE_BF16 && d->dtype != MOE_FP8_E4M3 && d->dtype != MOE_INT8)
     return fail(MOE_ERR_ARG, "unknown dtype %d", d->dtype);
@@ -105,7 +109,7 @@ moe_status validate(const moe_desc* d) {
   if (d->H <= 0 || d->H % 64) return fail(MOE_ERR_UNSUPPORTED, "H = %d must be a positive multiple of 64", d->H);
   if (d->I <= 0 || d->I % 64) return fail(MOE_ERR_UNSUPPORTED, "I = %d must be a positive multiple of 64", d->I);
   if (d->dtype == MOE_BF16 && d->E % 4) return fail(MOE_ERR_UNSUPPORTED, "BF16 path needs E %% 4 == 0 (E = %d)", d->E);
-  if ((d->flags & ~MOE_FLAG_ROUTER_LOSS) && d->dtype != MOE_BF16)
+  if ((d->flags & ~(MOE_FLAG_ROUTER_LOSS | MOE_FLAG_ROUTER_SCORES)) && d->dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "the FP8 backward flags need the BF16 dtype");
   if ((d->flags & MOE_FLAG_ROUTER_LOSS) && one_byte(d))
     return fail(MOE_ERR_UNSUPPORTED, "the router loss flag needs a dtype with a backward (F32 or BF16)");
@@ -338,6 +342,52 @@ moe_status moe_route_noalloc(const moe_desc* d, int chunk, const float* logits, 
   return MOE_OK;
 }
 
+static moe_status check_scores(const char* fn, const moe_desc* d, const moe_router_scores* r) {
+  if (!r) return fail(MOE_ERR_ARG, "%s: argument 'r' is NULL", fn);
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_ARG, "%s: unknown score %d", fn, r->score);
+  if (r->n_groups < 1 || d->E % r->n_groups)
+    return fail(MOE_ERR_ARG, "%s: n_groups = %d does not divide E = %d", fn, r->n_groups, d->E);
+  if (r->n_groups > 64) return fail(MOE_ERR_UNSUPPORTED, "%s: n_groups = %d above 64", fn, r->n_groups);
+  if (r->topk_groups < 1 || r->topk_groups > r->n_groups)
+    return fail(MOE_ERR_ARG, "%s: topk_groups = %d outside 1..%d", fn, r->topk_groups, r->n_groups);
+  if (d->k > r->topk_groups * (d->E / r->n_groups))
+    return fail(MOE_ERR_ARG, "%s: k = %d above the %d experts of the chosen groups", fn, d->k,
+                r->topk_groups * (d->E / r->n_groups));
+  if (r->group_top != 1 && r->group_top != 2) return fail(MOE_ERR_ARG, "%s: group_top = %d is not 1 or 2", fn, r->group_top);
+  if (r->renormalize != 0 && r->renormalize != 1)
+    return fail(MOE_ERR_ARG, "%s: renormalize = %d is not 0 or 1", fn, r->renormalize);
+  if (!std::isfinite(r->scale)) return fail(MOE_ERR_ARG, "%s: scale must be finite", fn);
+  return MOE_OK;
+}
+
+moe_status moe_route_scores(const moe_desc* d, int chunk, const moe_router_scores* r, const float* logits,
+                            const float* bias, int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets,
+                            int32_t* row_of, int32_t* src_token, void* workspace, void* stream) {
+  MOE_TRY(validate(d));
+  MOE_TRY(check_chunk(d, chunk));
+  MOE_TRY(check_scores(__func__, d, r));
+  if (d->T > 0) { MOE_NEED(logits); MOE_NEED(topk_idx); MOE_NEED(gates); MOE_NEED(row_of); }
+  if ((int64_t)d->n_chunks * d->P_c > 0) MOE_NEED(src_token);  // rows past N_c are marked -1
+  MOE_NEED(counts); MOE_NEED(offsets); MOE_NEED(workspace);
+  Range g = range_of(d, chunk);
+  MOE_HIP(moe::launch_route_scores(*r, logits, bias, topk_idx, gates, counts, offsets, row_of, src_token,
+                                   (int32_t*)workspace, d->T, d->E, d->e0, d->E_local, d->k, d->n_chunks, g.c0, g.nc,
+                                   d->P_c, (hipStream_t)stream),
+          "route_scores");
+  return MOE_OK;
+}
+
+moe_status moe_router_bias_update(int32_t E, int32_t rows, const int32_t* counts, float rate, float* bias, void* stream) {
+  if (E < 1 || E > 1024) return fail(MOE_ERR_UNSUPPORTED, "%s: E = %d outside 1..1024", __func__, E);
+  if (rows < 0) return fail(MOE_ERR_ARG, "%s: rows = %d is negative", __func__, rows);
+  if (!std::isfinite(rate)) return fail(MOE_ERR_ARG, "%s: rate must be finite", __func__);
+  if (rows == 0) return MOE_OK;
+  MOE_NEED(counts); MOE_NEED(bias);
+  MOE_HIP(moe::launch_router_bias_update(E, rows, counts, rate, bias, (hipStream_t)stream), "router_bias_update");
+  return MOE_OK;
+}
+
 moe_status moe_route_x(const moe_desc* d, int chunk, const void* x, const void* w_r, float* logits,
                        int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets, int32_t* row_of,
                        int32_t* src_token, void* workspace, void* stream) {
@@ -466,17 +516,11 @@ moe_status moe_combine_bwd(const moe_desc* d, int chunk, const void* dy, const v
   return combine_bwd_impl(d, chunk, dy, yd, gates, row_of, dyd, dgates, nullptr, nullptr, stream);
 }
 
-moe_status moe_route_bwd(const moe_desc* d, int chunk, const float* dgates, const float* gates,
-                         const int32_t* topk_idx, const void* x, float* dlogits, float* dwr_acc, void* dwr,
-                         void* workspace, void* stream) {
-  MOE_TRY(validate(d));
-  MOE_TRY(no_fp8_bwd(d));
-  MOE_TRY(bwd_extent(d));
-  MOE_TRY(check_chunk(d, chunk));
-  MOE_NEED(dwr_acc); MOE_NEED(workspace);
-  if (d->T > 0) { MOE_NEED(dgates); MOE_NEED(gates); MOE_NEED(topk_idx); MOE_NEED(x); MOE_NEED(dlogits); }
+// Route backward of chunks: dlogits by `dlogits_of(range, hi, lo, ldl, pitch)`, then the router weight gradient.
+extern "C++" template <typename Dlogits>
+static moe_status route_bwd_chunks(const moe_desc* d, int chunk, const void* x, const float* dlogits, float* dwr_acc,
+                                   void* dwr, void* workspace, void* stream, Dlogits dlogits_of) {
   const int cfirst = chunk < 0 ? 0 : chunk, clast = chunk < 0 ? d->n_chunks - 1 : chunk;
-  if (clast == d->n_chunks - 1) MOE_NEED(dwr);
   // BF16 rows: the dlogits planes follow the partials (each chunk's router gradient reads them
   // before the next chunk's dlogits kernel, on the same stream, rewrites them)
   uint16_t* hi = nullptr;
@@ -489,14 +533,53 @@ moe_status moe_route_bwd(const moe_desc* d, int chunk, const float* dgates, cons
   }
   for (int c = cfirst; c <= clast; ++c) {
     Range r = range_of(d, c);
-    MOE_HIP(moe::launch_route_bwd_dlogits(dgates, gates, topk_idx, dlogits, r.t0, r.t1, d->k, d->E,
-                                          (hipStream_t)stream, hi, lo, ldl, pitch, d->flags & MOE_FLAG_ROUTER_LOSS),
-            "route_bwd_dlogits");
+    MOE_TRY(dlogits_of(r, hi, lo, ldl, pitch));
     MOE_HIP(moe::launch_router_wgrad(is_bf16_rows(d), dlogits, hi, lo, ldl, x, (float*)workspace, dwr_acc, c == 0,
                                      c == d->n_chunks - 1 ? dwr : nullptr, r.t0, r.t1, d->E, d->H,
                                      (hipStream_t)stream), "router_wgrad");
   }
   return MOE_OK;
+}
+
+moe_status moe_route_bwd(const moe_desc* d, int chunk, const float* dgates, const float* gates,
+                         const int32_t* topk_idx, const void* x, float* dlogits, float* dwr_acc, void* dwr,
+                         void* workspace, void* stream) {
+  MOE_TRY(validate(d));
+  MOE_TRY(no_fp8_bwd(d));
+  MOE_TRY(bwd_extent(d));
+  MOE_TRY(check_chunk(d, chunk));
+  MOE_NEED(dwr_acc); MOE_NEED(workspace);
+  if (d->T > 0) { MOE_NEED(dgates); MOE_NEED(gates); MOE_NEED(topk_idx); MOE_NEED(x); MOE_NEED(dlogits); }
+  if (chunk < 0 || chunk == d->n_chunks - 1) MOE_NEED(dwr);
+  return route_bwd_chunks(d, chunk, x, dlogits, dwr_acc, dwr, workspace, stream,
+                          [&](Range r, uint16_t* hi, uint16_t* lo, int ldl, int64_t pitch) {
+    return hip_check(moe::launch_route_bwd_dlogits(dgates, gates, topk_idx, dlogits, r.t0, r.t1, d->k, d->E,
+                                                   (hipStream_t)stream, hi, lo, ldl, pitch,
+                                                   d->flags & MOE_FLAG_ROUTER_LOSS),
+                     "route_bwd_dlogits");
+  });
+}
+
+moe_status moe_route_scores_bwd(const moe_desc* d, int chunk, const moe_router_scores* r, const float* logits,
+                                const float* dgates, const int32_t* topk_idx, const void* x, float* dlogits,
+                                float* dwr_acc, void* dwr, void* workspace, void* stream) {
+  MOE_TRY(validate(d));
+  MOE_TRY(no_fp8_bwd(d));
+  MOE_TRY(check_chunk(d, chunk));
+  MOE_TRY(check_scores(__func__, d, r));
+  if (d->T > 0) { MOE_NEED(logits); MOE_NEED(dgates); MOE_NEED(topk_idx); MOE_NEED(dlogits); }
+  if (d->T > 0 && dlogits == logits) return fail(MOE_ERR_ARG, "%s: dlogits may not be the logits buffer", __func__);
+  auto launch = [&](Range g, uint16_t* hi, uint16_t* lo, int ldl, int64_t pitch) {
+    return hip_check(moe::launch_route_scores_bwd(*r, logits, dgates, topk_idx, dlogits, g.t0, g.t1, d->k, d->E,
+                                                  (hipStream_t)stream, hi, lo, ldl, pitch,
+                                                  d->flags & MOE_FLAG_ROUTER_LOSS),
+                     "route_scores_bwd");
+  };
+  if (!x && (d->T > 0 || !dwr_acc)) return launch(range_of(d, chunk), nullptr, nullptr, 0, 0);
+  MOE_TRY(bwd_extent(d));
+  MOE_NEED(dwr_acc); MOE_NEED(workspace);
+  if (chunk < 0 || chunk == d->n_chunks - 1) MOE_NEED(dwr);
+  return route_bwd_chunks(d, chunk, x, dlogits, dwr_acc, dwr, workspace, stream, launch);
 }
 
 moe_status moe_expert_wgrad(const moe_desc* d, const void* dyd, const void* dgu, const void* xd, const void* h,
@@ -592,9 +675,10 @@ moe_status moe_expert_wgrad_fp8(const moe_desc* d, const void* dyd, const void* 
                                dw1, dw2, true, stream);
 }
 
-moe_status moe_dispatch_bwd(const moe_desc* d, int chunk, const void* dxd, const int32_t* row_of,
-                            const int32_t* topk_idx, const float* dlogits, const void* w_r, void* dx,
-                            void* stream) {
+// dense: dlogits has a value for every expert
+static moe_status dispatch_bwd_impl(const moe_desc* d, int chunk, const void* dxd, const int32_t* row_of,
+                                    const int32_t* topk_idx, const float* dlogits, const void* w_r, void* dx,
+                                    bool dense, void* stream) {
   MOE_TRY(validate(d));
   MOE_TRY(no_fp8_bwd(d));
   MOE_TRY(check_chunk(d, chunk));
@@ -602,7 +686,7 @@ moe_status moe_dispatch_bwd(const moe_desc* d, int chunk, const void* dxd, const
   if (r.t1 <= r.t0) return MOE_OK;
   MOE_NEED(row_of); MOE_NEED(topk_idx); MOE_NEED(dlogits); MOE_NEED(w_r); MOE_NEED(dx);
   if (rows_of(d) > 0) MOE_NEED(dxd);
-  if (d->flags & MOE_FLAG_ROUTER_LOSS) {
+  if (dense) {
     if (rows_of(d) == 0) dxd = nullptr;  // no row is read, whatever was passed
     MOE_HIP(moe::launch_dispatch_bwd_dense(is_bf16_rows(d), dxd, dxd_scales(d, dxd), row_of, dlogits, w_r, dx, r.t0,
                                            r.t1, d->k, d->E, d->H, (hipStream_t)stream),
@@ -614,6 +698,13 @@ moe_status moe_dispatch_bwd(const moe_desc* d, int chunk, const void* dxd, const
                                    (hipStream_t)stream),
           "dispatch_bwd");
   return MOE_OK;
+}
+
+moe_status moe_dispatch_bwd(const moe_desc* d, int chunk, const void* dxd, const int32_t* row_of,
+                            const int32_t* topk_idx, const float* dlogits, const void* w_r, void* dx,
+                            void* stream) {
+  return dispatch_bwd_impl(d, chunk, dxd, row_of, topk_idx, dlogits, w_r, dx, d && (d->flags & MOE_FLAG_ROUTER_LOSS),
+                           stream);
 }
 
 moe_status moe_quantize_rows_fp8(int64_t rows, int32_t cols, const void* src_bf16, void* codes, float* scale,
@@ -726,6 +817,117 @@ moe_status moe_router_loss_bwd(const moe_desc* d, int32_t n_segments, float bala
   return MOE_OK;
 }
 
+// ----------------------------------------------------------------------------- weight update
+
+static bool misaligned(const void* p, uintptr_t to) { return (uintptr_t)p & (to - 1); }
+
+// Tensors of a call: sizes, types and gradients (norm), and what the update needs besides (update).
+static moe_status check_adamw_tensors(const char* fn, int32_t n, const moe_adamw_tensor* t, bool update, int32_t bits) {
+  if (n < 0) return fail(MOE_ERR_ARG, "%s: n_tensors = %d is negative", fn, n);
+  if (n > 0 && !t) return fail(MOE_ERR_ARG, "%s: argument 'tensors' is NULL", fn);
+  for (int32_t i = 0; i < n; ++i) {
+    const moe_adamw_tensor& x = t[i];
+    if (x.n < 0) return fail(MOE_ERR_ARG, "%s: tensor %d has n = %lld", fn, i, (long long)x.n);
+    if (x.n > ((int64_t)1 << 34)) return fail(MOE_ERR_UNSUPPORTED, "%s: tensor %d has n = %lld above 2^34", fn, i, (long long)x.n);
+    if (x.grad_dtype != MOE_F32 && x.grad_dtype != MOE_BF16)
+      return fail(MOE_ERR_UNSUPPORTED, "%s: tensor %d: gradients are F32 or BF16", fn, i);
+    if (x.n > 0 && !x.grad) return fail(MOE_ERR_ARG, "%s: tensor %d: grad is NULL", fn, i);
+    if (misaligned(x.grad, 16)) return fail(MOE_ERR_ARG, "%s: tensor %d: pointers must be 16-byte aligned", fn, i);
+    if (!update) continue;
+    if (x.w_dtype != MOE_F32 && x.w_dtype != MOE_BF16)
+      return fail(MOE_ERR_UNSUPPORTED, "%s: tensor %d: weights are F32 or BF16", fn, i);
+    if (x.master && x.w_dtype != MOE_BF16) return fail(MOE_ERR_ARG, "%s: tensor %d: a master belongs to BF16 weights", fn, i);
+    if (!std::isfinite(x.lr_scale) || !std::isfinite(x.weight_decay))
+      return fail(MOE_ERR_ARG, "%s: tensor %d: lr_scale and weight_decay must be finite", fn, i);
+    if (x.n == 0) continue;
+    if (!x.w || !x.m || !x.v) return fail(MOE_ERR_ARG, "%s: tensor %d: w, m or v is NULL", fn, i);
+    if (bits == 8 && (!x.m_scale || !x.v_scale)) return fail(MOE_ERR_ARG, "%s: tensor %d: 8-bit averages need their scales", fn, i);
+    if (misaligned(x.w, 16) || misaligned(x.master, 16) || misaligned(x.m, 16) || misaligned(x.v, 16))
+      return fail(MOE_ERR_ARG, "%s: tensor %d: pointers must be 16-byte aligned", fn, i);
+    if (bits == 8 && (misaligned(x.m_scale, 4) || misaligned(x.v_scale, 4)))
+      return fail(MOE_ERR_ARG, "%s: tensor %d: scales must be 4-byte aligned", fn, i);
+  }
+  if (update) {  // a weight listed twice would be updated by two workgroups at once
+    bool ascending = true;
+    for (int32_t i = 1; i < n && ascending; ++i) ascending = t[i - 1].w < t[i].w;
+    if (!ascending) {
+      std::unique_ptr<const void*[]> w(new (std::nothrow) const void*[n]);
+      if (!w) return fail(MOE_ERR_HIP, "%s: no host memory for %d tensors", fn, n);
+      int32_t live = 0;
+      for (int32_t i = 0; i < n; ++i) if (t[i].n > 0) w[live++] = t[i].w;
+      std::sort(w.get(), w.get() + live, std::less<const void*>());
+      if (std::adjacent_find(w.get(), w.get() + live) != w.get() + live)
+        return fail(MOE_ERR_ARG, "%s: a weight is listed twice", fn);
+    }
+  }
+  return MOE_OK;
+}
+
+static moe_status check_adamw(const char* fn, const moe_adamw_options* o) {
+  if (!o) return fail(MOE_ERR_ARG, "%s: the options are NULL", fn);
+  if (!(o->lr >= 0) || !std::isfinite(o->lr) || !(o->eps >= 0) || !std::isfinite(o->eps))
+    return fail(MOE_ERR_ARG, "%s: lr and eps must be finite and not negative", fn);
+  if (!(o->beta1 > 0 && o->beta1 < 1 && o->beta2 > 0 && o->beta2 < 1))
+    return fail(MOE_ERR_ARG, "%s: beta1 and beta2 must lie between 0 and 1", fn);
+  if (!o->step_dev && o->step < 1) return fail(MOE_ERR_ARG, "%s: step = %lld below 1", fn, (long long)o->step);
+  if (o->state_bits != 8 && o->state_bits != 32) return fail(MOE_ERR_UNSUPPORTED, "%s: state_bits = %d is not 8 or 32", fn, o->state_bits);
+  return MOE_OK;
+}
+
+moe_status moe_adamw_step(const moe_adamw_options* o, int32_t n_tensors, const moe_adamw_tensor* tensors, void* stream) {
+  MOE_TRY(check_adamw(__func__, o));
+  MOE_TRY(check_adamw_tensors(__func__, n_tensors, tensors, true, o->state_bits));
+  MOE_HIP(moe::launch_adamw(*o, n_tensors, tensors, (hipStream_t)stream), "adamw");
+  return MOE_OK;
+}
+
+moe_status moe_grad_norm_bytes(int64_t* workspace) {
+  if (!workspace) return fail(MOE_ERR_ARG, "output pointer is NULL");
+  *workspace = moe::grad_norm_ws_bytes();
+  return MOE_OK;
+}
+
+static moe_status check_norm(const char* fn, double max_norm, const float* norm, const void* workspace) {
+  if (!(max_norm > 0)) return fail(MOE_ERR_ARG, "%s: max_norm must be above 0", fn);
+  if (!norm || !workspace) return fail(MOE_ERR_ARG, "%s: norm or its workspace is NULL", fn);
+  if (misaligned(workspace, 8)) return fail(MOE_ERR_ARG, "%s: the workspace must be 8-byte aligned", fn);
+  return MOE_OK;
+}
+
+moe_status moe_grad_norm(int32_t n_tensors, const moe_adamw_tensor* tensors, double max_norm, float* norm,
+                         void* workspace, void* stream) {
+  MOE_TRY(check_adamw_tensors(__func__, n_tensors, tensors, false, 0));
+  MOE_TRY(check_norm(__func__, max_norm, norm, workspace));
+  MOE_HIP(moe::launch_grad_norm(n_tensors, tensors, max_norm, norm, workspace, (hipStream_t)stream), "grad_norm");
+  return MOE_OK;
+}
+
+static moe_status check_pack(const char* fn, int64_t n, const void* m, const void* v, const void* mc, const void* ms,
+                             const void* vc, const void* vs) {
+  if (n < 0) return fail(MOE_ERR_ARG, "%s: n = %lld is negative", fn, (long long)n);
+  if (n > ((int64_t)1 << 34)) return fail(MOE_ERR_UNSUPPORTED, "%s: n = %lld above 2^34", fn, (long long)n);
+  if (n > 0 && (!m || !v || !mc || !ms || !vc || !vs)) return fail(MOE_ERR_ARG, "%s: a pointer is NULL", fn);
+  if (misaligned(m, 16) || misaligned(v, 16) || misaligned(mc, 8) || misaligned(vc, 8))
+    return fail(MOE_ERR_ARG, "%s: values must be 16-byte aligned and codes 8-byte aligned", fn);
+  return MOE_OK;
+}
+
+moe_status moe_adamw_unpack(int64_t n, const void* m_codes, const float* m_scale, const void* v_codes,
+                            const float* v_scale, float* m, float* v, void* stream) {
+  MOE_TRY(check_pack(__func__, n, m, v, m_codes, m_scale, v_codes, v_scale));
+  if (n == 0) return MOE_OK;
+  MOE_HIP(moe::launch_adamw_unpack(n, m_codes, m_scale, v_codes, v_scale, m, v, (hipStream_t)stream), "adamw_unpack");
+  return MOE_OK;
+}
+
+moe_status moe_adamw_pack(int64_t n, const float* m, const float* v, void* m_codes, float* m_scale, void* v_codes,
+                          float* v_scale, void* stream) {
+  MOE_TRY(check_pack(__func__, n, m, v, m_codes, m_scale, v_codes, v_scale));
+  if (n == 0) return MOE_OK;
+  MOE_HIP(moe::launch_adamw_pack(n, m, v, m_codes, m_scale, v_codes, v_scale, (hipStream_t)stream), "adamw_pack");
+  return MOE_OK;
+}
+
 // ----------------------------------------------------------------------------- paged stash
 
 static moe_status check_stash(const char* fn, const void* rows, const void* pool, const void* scale_a,
@@ -811,9 +1013,22 @@ static moe_status check_bwd_tensors(const moe_desc* d, const moe_tensors* t) {
   return MOE_OK;
 }
 
-// Routing of one chunk in a layer primitive: from the given logits, or (logits NULL) from x and
-// the router weight with the projection fused into the top-k.
+// Routing of one chunk in a layer primitive: by scores (MOE_FLAG_ROUTER_SCORES), from the given logits, or (logits
+// NULL) from x and the router weight with the projection fused into the top-k.
+static bool by_scores(const moe_desc* d) { return d->flags & MOE_FLAG_ROUTER_SCORES; }
+static moe_status check_score_tensors(const moe_desc* d, const moe_tensors* t, bool backward) {
+  if (!by_scores(d)) return MOE_OK;
+  MOE_TRY(check_scores(__func__, d, &t->router_scores));
+  if (d->T > 0 && !t->logits)
+    return fail(MOE_ERR_UNSUPPORTED, "layer: routing by scores takes given logits (the projection fused into routing has none)");
+  if (backward && d->T > 0 && t->dlogits == t->logits)
+    return fail(MOE_ERR_ARG, "layer: dlogits may not be the logits buffer");
+  return MOE_OK;
+}
 static moe_status route_any(const moe_desc* d, int c, const moe_tensors* t, hipStream_t s) {
+  if (by_scores(d))
+    return moe_route_scores(d, c, &t->router_scores, t->logits, t->router_bias, t->topk_idx, t->gates, t->counts,
+                            t->offsets, t->row_of, t->src_token, t->workspace, s);
   if (t->logits || d->T == 0)
     return moe_route(d, c, t->logits, t->topk_idx, t->gates, t->counts, t->offsets, t->row_of, t->src_token,
                      t->workspace, s);
@@ -846,6 +1061,18 @@ static moe_status layer_loss_bwd(const moe_desc* d, const moe_tensors* t, hipStr
   if (!(d->flags & MOE_FLAG_ROUTER_LOSS)) return MOE_OK;
   return moe_router_loss_bwd(d, t->n_segments, t->balance_coef, t->z_coef, loss_logits(t), t->router_lse,
                              t->seg_offsets, t->token_mask, t->seg_counts, t->seg_tokens, t->dloss, t->dlogits, s);
+}
+
+static moe_status layer_route_bwd(const moe_desc* d, int c, const moe_tensors* t, hipStream_t s) {
+  if (by_scores(d))
+    return moe_route_scores_bwd(d, c, &t->router_scores, t->logits, t->dgates, t->topk_idx, t->x, t->dlogits, t->dwr_acc,
+                                t->dwr, t->workspace, s);
+  return moe_route_bwd(d, c, t->dgates, t->gates, t->topk_idx, t->x, t->dlogits, t->dwr_acc, t->dwr, t->workspace, s);
+}
+static moe_status layer_dispatch_bwd(const moe_desc* d, int c, const moe_tensors* t, hipStream_t s) {
+  const bool all = by_scores(d) && t->router_scores.score == MOE_SCORE_SOFTMAX && !t->router_scores.renormalize;
+  return dispatch_bwd_impl(d, c, t->dxd, t->row_of, t->topk_idx, t->dlogits, t->w_r, t->dx,
+                           all || (d->flags & MOE_FLAG_ROUTER_LOSS), s);
 }
 
 // Two-stream schedules. A wait of one stream on the other's event costs the waiting stream
@@ -956,8 +1183,7 @@ static moe_status backward_sched(const moe_desc* d, const moe_tensors* t, hipStr
       if (wq8 && c + 2 == n) MOE_TRY(wgrad_operands());
     }
     if (c == 0) MOE_TRY(layer_loss_bwd(d, t, side));
-    MOE_TRY(moe_route_bwd(d, c, t->dgates, t->gates, t->topk_idx, t->x, t->dlogits, t->dwr_acc, t->dwr,
-                          t->workspace, side));
+    MOE_TRY(layer_route_bwd(d, c, t, side));
     if (two && c >= 1) MOE_HIP(hipStreamWaitEvent(cs, cb[c], 0), "hipStreamWaitEvent");
     if (q)
       MOE_TRY(expert_dgrad_fp8_impl(d, c, t->dyd, t->gu, t->w1t, t->w1t_scale, t->w2t, t->w2t_scale, t->offsets,
@@ -969,7 +1195,7 @@ static moe_status backward_sched(const moe_desc* d, const moe_tensors* t, hipStr
       MOE_HIP(hipEventRecord(dg[c], cs), "hipEventRecord");
       MOE_HIP(hipStreamWaitEvent(as, dg[c], 0), "hipStreamWaitEvent");
     }
-    MOE_TRY(moe_dispatch_bwd(d, c, t->dxd, t->row_of, t->topk_idx, t->dlogits, t->w_r, t->dx, side));
+    MOE_TRY(layer_dispatch_bwd(d, c, t, side));
   }
   if (d->flags & MOE_FLAG_FP8_WGRAD) {
     if (wq8 && two) MOE_HIP(hipStreamWaitEvent(cs, wq_done, 0), "hipStreamWaitEvent");
@@ -1008,7 +1234,7 @@ static bool merged_gemms(const moe_desc* d) { return d->dtype == MOE_BF16 && d->
 // the merged backward launches pair BF16 GEMMs; with an FP8 GEMM flag the backward runs per chunk (FP8
 // dxd rows only change the gate/up dgrad's epilogue and dispatch backward, both in the merged launches)
 static bool merged_bwd(const moe_desc* d) {
-  return merged_gemms(d) && (d->flags & ~(MOE_FLAG_FP8_DXD | MOE_FLAG_ROUTER_LOSS)) == 0;
+  return merged_gemms(d) && (d->flags & ~(MOE_FLAG_FP8_DXD | MOE_FLAG_ROUTER_LOSS | MOE_FLAG_ROUTER_SCORES)) == 0;
 }
 
 //   compute: R0 D0 GU0 | wait(disp1) [DN0 GU1] | wait(disp2) [DN1 GU2] | ... | DN n-1, C n-1
@@ -1117,10 +1343,7 @@ static moe_status backward_sched_merged(const moe_desc* d, const moe_tensors* t,
   auto combine_bwd = [&](int c, hipStream_t s) {
     return moe_combine_bwd(d, c, t->dy, t->yd, t->gates, t->row_of, t->dyd, t->dgates, s);
   };
-  auto route_bwd = [&](int c) {
-    return moe_route_bwd(d, c, t->dgates, t->gates, t->topk_idx, t->x, t->dlogits, t->dwr_acc, t->dwr,
-                         t->workspace, side);
-  };
+  auto route_bwd = [&](int c) { return layer_route_bwd(d, c, t, side); };
   if (two && n > 1 && !after_forward) {
     MOE_HIP(hipEventRecord(begin, cs), "hipEventRecord");
     MOE_HIP(hipStreamWaitEvent(as, begin, 0), "hipStreamWaitEvent");
@@ -1155,7 +1378,7 @@ static moe_status backward_sched_merged(const moe_desc* d, const moe_tensors* t,
       MOE_TRY(route_bwd(c + 1));
     }
     if (two) MOE_HIP(hipStreamWaitEvent(as, dg[c], 0), "hipStreamWaitEvent");
-    MOE_TRY(moe_dispatch_bwd(d, c, t->dxd, t->row_of, t->topk_idx, t->dlogits, t->w_r, t->dx, side));
+    MOE_TRY(layer_dispatch_bwd(d, c, t, side));
   }
   MOE_HIP(moe::gg_wgrad1(g, cs), "expert_wgrad");
   if (two) {
@@ -1169,6 +1392,7 @@ moe_status moe_layer_forward(const moe_desc* d, const moe_tensors* t, void* comp
   MOE_TRY(validate(d));
   MOE_TRY(check_fwd_tensors(d, t));
   MOE_TRY(check_loss_tensors(d, t, false));
+  MOE_TRY(check_score_tensors(d, t, false));
   if (merged_gemms(d)) return forward_sched_merged(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream, true);
   return forward_sched(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream, true);
 }
@@ -1177,6 +1401,7 @@ moe_status moe_layer_backward(const moe_desc* d, const moe_tensors* t, void* com
   MOE_TRY(validate(d));
   MOE_TRY(check_fwd_tensors(d, t));
   MOE_TRY(check_loss_tensors(d, t, true));
+  MOE_TRY(check_score_tensors(d, t, true));
   MOE_TRY(check_bwd_tensors(d, t));
   if (merged_bwd(d))
     return backward_sched_merged(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream, false);
@@ -1188,6 +1413,7 @@ moe_status moe_layer_forward_backward(const moe_desc* d, const moe_tensors* t, v
   MOE_TRY(validate(d));
   MOE_TRY(check_fwd_tensors(d, t));
   MOE_TRY(check_loss_tensors(d, t, true));
+  MOE_TRY(check_score_tensors(d, t, true));
   MOE_TRY(check_bwd_tensors(d, t));
   // no join between the two: the backward's first wait of the auxiliary stream follows the
   // whole forward on the compute stream, and its final join covers the forward's aux work
@@ -1202,6 +1428,39 @@ moe_status moe_layer_forward_backward(const moe_desc* d, const moe_tensors* t, v
   if (merged_bwd(d))
     return backward_sched_merged(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream, true, defer);
   return backward_sched(d, t, (hipStream_t)compute_stream, (hipStream_t)aux_stream);
+}
+
+moe_status moe_layer_update(const moe_desc* d, const moe_tensors* t, const moe_layer_optimizer* o, void* stream) {
+  MOE_TRY(validate(d));
+  MOE_TRY(no_fp8_bwd(d));
+  if (!t) return fail(MOE_ERR_ARG, "tensors is NULL");
+  if (!o) return fail(MOE_ERR_ARG, "%s: the optimizer is NULL", __func__);
+  MOE_TRY(check_adamw(__func__, &o->adamw));
+  moe_adamw_tensor list[3];
+  int n = 0;
+  auto add = [&](const void* w, const void* grad, const moe_adamw_state& s, int64_t elements) {
+    list[n++] = moe_adamw_tensor{(void*)w, s.master, grad, s.m, s.v, s.m_scale, s.v_scale, elements, d->dtype, d->dtype,
+                                 s.lr_scale, s.weight_decay};
+  };
+  add(t->w1, t->dw1, o->w1, (int64_t)d->E_local * 2 * d->I * d->H);
+  add(t->w2, t->dw2, o->w2, (int64_t)d->E_local * d->H * d->I);
+  add(t->w_r, t->dwr, o->w_r, (int64_t)d->E * d->H);
+  moe_adamw_options a = o->adamw;
+  MOE_TRY(check_adamw_tensors(__func__, n, list, true, a.state_bits));
+  if (o->norm) {
+    MOE_TRY(check_norm(__func__, o->max_norm, o->norm, o->norm_workspace));
+    if (a.grad_scale) return fail(MOE_ERR_ARG, "%s: grad_scale and norm are both given", __func__);
+    a.grad_scale = o->norm + 1;
+  }
+  const bool bias = by_scores(d) && t->router_bias && o->bias_rate != 0.f;
+  if (bias) {
+    MOE_NEED(t->counts);
+    if (!std::isfinite(o->bias_rate)) return fail(MOE_ERR_ARG, "%s: bias_rate must be finite", __func__);
+  }
+  if (o->norm) MOE_TRY(moe_grad_norm(n, list, o->max_norm, o->norm, o->norm_workspace, stream));
+  MOE_TRY(moe_adamw_step(&a, n, list, stream));
+  if (bias) MOE_TRY(moe_router_bias_update(d->E, d->n_chunks, t->counts, o->bias_rate, t->router_bias, stream));
+  return MOE_OK;
 }
 
 // ----------------------------------------------------------------------------- extent tracker

@@ -1,0 +1,469 @@
+// AdamW over many tensors at once, with moving averages in FP32 or in 8 bits, and the norm of their gradients.
+//
+//   g = grad * grad_scale, m' = b1 m + (1 - b1) g, v' = b2 v + (1 - b2) g^2,
+//   w' = w (1 - lr wd) - lr / (1 - b1^t) * m' / (sqrt(v' / (1 - b2^t)) + eps)
+//
+// Bound by HBM: 28 bytes per parameter with a BF16 gradient, an FP32 master and FP32 averages (gradient 2, master 8,
+// averages 16, BF16 weight 2), 16 with averages in 8 bits. One lane owns 8 consecutive elements (16-byte loads of
+// BF16, 8-byte ones of codes), so 32 lanes own one block of 256 elements that share a scale, and its largest value
+// is a reduction inside half a wave. A workgroup takes tiles of 2048 elements; the tensors of a launch and the tile
+// each starts at are kernel arguments, so no table travels to the device.
+//
+// 8-bit averages. m = s c|c| / 127^2 and v = s c^4 / 255^4 with s the block's largest magnitude: the steps grow with
+// the value, so that entries 10^-4 (m) or 10^-9 (v) of the block's largest keep digits, which equal steps would lose.
+// A step of training moves m and v by some per cent or less, under half a code, and rounding to the nearest code
+// would hold them where they are; so the code above is taken with the chance of how near it is (the expected value
+// is exact), by a hash of the element's place, the step and the seed. v > 0 never rounds to 0: m / sqrt(v) stays bounded.
+// Every FP32 operation that decides a code is rounded once (no contraction), so the codes are defined bit by bit.
+#include <algorithm>
+#include <cmath>
+
+#include "common.h"
+#include "launch.h"
+#include "trace.h"
+
+#pragma clang fp contract(off)
+
+namespace moe {
+
+constexpr int kAdamThreads = 256;
+constexpr int kAdamVec = 8;                          // elements per lane
+constexpr int kAdamTile = kAdamThreads * kAdamVec;   // elements per workgroup
+constexpr int kAdamBlock = 256;                      // elements per scale of an 8-bit average
+constexpr int kAdamBatch = 44;                       // tensors per launch: the arguments stay below 4 KiB
+
+struct AdamTensor {
+  void* w;
+  float* master;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  uint32_t place;   // of element 0 in the random sequence (low 32 bits)
+  uint32_t tile0;   // first tile in this launch
+  float lr_scale, wd;
+};
+struct AdamBatch {
+  AdamTensor t[kAdamBatch];
+  int count;
+};
+struct AdamConst {
+  double lr, beta1, beta2, eps;
+  double unbias1, unbias2;  // 1 / (1 - b1^step), 1 / sqrt(1 - b2^step); from *step_dev on the device where it is given
+  const double* lr_dev;
+  const int64_t* step_dev;
+  const float* grad_scale;
+  int64_t step;
+  uint32_t seed;
+};
+
+// The tensor of a tile: the last one whose first tile is not behind it (tile0 ascends; empty tensors are left out).
+MOE_DEV int tensor_of(const AdamBatch& b, uint32_t tile) {
+  int lo = 0, hi = b.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (b.t[mid].tile0 <= tile) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Random bits of an element: three 16-bit numbers, for m, v and a BF16 weight. Odd multipliers from the digits of the
+// golden ratio, e and pi; shifts carry the high bits down.
+MOE_DEV uint32_t step_key(uint32_t seed, int64_t step) {
+  uint32_t k = (uint32_t)step * 0x243F6A89u + seed;
+  k ^= k >> 16;
+  k *= 0xB7E15163u;
+  return k ^ (k >> 15);
+}
+MOE_DEV uint32_t random_bits(uint32_t place, uint32_t key) {
+  uint32_t x = place * 0x9E3779B9u + key;
+  x = (x ^ (x >> 16)) * 0xB7E15163u;
+  return x ^ (x >> 15);
+}
+MOE_DEV uint32_t more_bits(uint32_t x) { return (x * 0x243F6A89u) >> 16; }
+
+// Values of codes in units of the block's scale.
+constexpr float kInv127 = (float)(1.0 / 127.0), kInv255 = (float)(1.0 / 255.0);
+MOE_DEV float level_m(float c) { const float t = c * kInv127; return t * t; }
+MOE_DEV float level_v(float c) { float t = c * kInv255; t = t * t; return t * t; }
+MOE_DEV float decode_m(int8_t code, float scale) {
+  const float l = level_m((float)code) * scale;
+  return code < 0 ? -l : l;
+}
+MOE_DEV float decode_v(uint8_t code, float scale) { return level_v((float)code) * scale; }
+
+// Code of a in [0, 1]: the level below, or the one above where (a - below) / (above - below) exceeds r. The root only
+// proposes a code, off by one at most; the levels decide.
+template <int TOP, bool FOURTH>
+MOE_DEV int encode(float a, float r) {
+  auto level = [](float c) { return FOURTH ? level_v(c) : level_m(c); };
+  float root = __builtin_amdgcn_sqrtf(a);
+  if (FOURTH) root = __builtin_amdgcn_sqrtf(root);
+  float c = fminf(floorf(root * (float)TOP), (float)(TOP - 1));
+  float lo = level(c), hi = level(c + 1.f);
+  if (lo > a && c > 0.f) {
+    c -= 1.f; hi = lo; lo = level(c);
+  } else if (hi <= a && c < (float)(TOP - 1)) {
+    c += 1.f; lo = hi; hi = level(c + 1.f);
+  }
+  return (int)c + (a - lo > r * (hi - lo) ? 1 : 0);
+}
+
+// Largest magnitude over the 32 lanes of a block, by bits (NaN above infinity above every number).
+MOE_DEV float block_max(uint32_t bits) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) bits = max(bits, (uint32_t)__shfl_xor((int)bits, o, 64));
+  return __uint_as_float(bits);
+}
+// Blocks whose largest value is under 2^-120 count as zeros: its reciprocal would leave the range. An infinite one
+// has no codes: the block becomes NaN, as with a NaN.
+MOE_DEV float block_scale(float big) {
+  return big < 0x1p-120f ? 0.f : big == __builtin_huge_valf() ? __builtin_nanf("") : big;
+}
+MOE_DEV float block_inv(float scale) { return scale > 0.f ? 1.0f / scale : 0.f; }
+MOE_DEV float share(float x, float inv) {
+  return fminf(fabsf(x) * inv, 1.0f);  // never NaN (infinity times 0 gives 1: the scale is NaN then)
+}
+
+template <typename T>
+MOE_DEV void load8(const T* p, int64_t i, int64_t n, float* f) {
+  if (i + kAdamVec <= n) {
+    if constexpr (sizeof(T) == 2) {
+      const u32x4 v = *(const u32x4*)(p + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { f[2 * j] = bf2f(w[j] & 0xffff); f[2 * j + 1] = bf2f(w[j] >> 16); }
+    } else {
+      const float4 a = *(const float4*)(p + i), b = *(const float4*)(p + i + 4);
+      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kAdamVec; ++j) f[j] = i + j < n ? ld_elem(p + i + j) : 0.f;
+  }
+}
+template <typename T>
+MOE_DEV void store8(T* p, int64_t i, int64_t n, const float* f) {
+  if (i + kAdamVec <= n) {
+    if constexpr (sizeof(T) == 2) {
+      *(u32x4*)(p + i) = u32x4{pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7])};
+    } else {
+      *(float4*)(p + i) = make_float4(f[0], f[1], f[2], f[3]);
+      *(float4*)(p + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kAdamVec; ++j) if (i + j < n) st_elem(p + i + j, f[j]);
+  }
+}
+MOE_DEV void load_codes(const uint8_t* p, int64_t i, int64_t n, uint8_t* c) {
+  if (i + kAdamVec <= n) {
+    const uint2 v = *(const uint2*)(p + i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = (uint8_t)((j < 4 ? v.x : v.y) >> (8 * (j & 3)));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = i + j < n ? p[i + j] : 0;
+  }
+}
+MOE_DEV void store_codes(uint8_t* p, int64_t i, int64_t n, const uint32_t* c) {
+  if (i + kAdamVec <= n) {
+    *(uint2*)(p + i) = make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
+                                  c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) if (i + j < n) p[i + j] = (uint8_t)c[j];
+  }
+}
+
+// Eight values of one lane to codes; the block's scale is stored by its first lane. half: r is 1/2 (nearest level).
+template <bool NEAREST>
+MOE_DEV void pack8(const float* m, const float* v, const uint32_t* rnd, int64_t i, int64_t n, uint8_t* mc, float* ms,
+                   uint8_t* vc, float* vs) {
+  uint32_t bm = 0, bv = 0;
+#pragma unroll
+  for (int j = 0; j < kAdamVec; ++j) {
+    bm = max(bm, __float_as_uint(m[j]) & 0x7fffffffu);
+    bv = max(bv, __float_as_uint(v[j]) & 0x7fffffffu);
+  }
+  const float sm = block_scale(block_max(bm)), sv = block_scale(block_max(bv));
+  const float im = block_inv(sm), iv = block_inv(sv);
+  uint32_t cm[8], cv[8];
+#pragma unroll
+  for (int j = 0; j < kAdamVec; ++j) {
+    const float rm = NEAREST ? 0.5f : (float)(rnd[j] & 0xffffu) * 0x1p-16f;
+    const float rv = NEAREST ? 0.5f : (float)(rnd[j] >> 16) * 0x1p-16f;
+    const int c = encode<127, false>(share(m[j], im), rm);
+    cm[j] = (uint32_t)(uint8_t)(int8_t)(m[j] < 0.f ? -c : c);
+    const float a = share(v[j], iv);
+    const int e = encode<255, true>(a, rv);
+    cv[j] = a > 0.f ? (uint32_t)max(e, 1) : 0u;
+  }
+  if (i < n) {
+    store_codes(mc, i, n, cm);
+    store_codes(vc, i, n, cv);
+    if (i % kAdamBlock == 0) { ms[i / kAdamBlock] = sm; vs[i / kAdamBlock] = sv; }
+  }
+}
+
+// W: float, or uint16_t (BF16 bits) with a master or, without one, rounded by chance like the codes: an update under
+// half a step of BF16 (2^-9 of the weight; lr is 10^-4) would otherwise never reach the weight.
+template <typename W, bool MASTER, typename G, bool Q8>
+__global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamBatch b, const AdamConst k) {
+  const AdamTensor& t = b.t[tensor_of(b, blockIdx.x)];
+  const float gs = k.grad_scale ? *k.grad_scale : 1.0f;
+  if (!(fabsf(gs) <= 3.402823466e38f)) return;  // a norm that is not finite: the step is left out
+  int64_t step = k.step;
+  double unbias1 = k.unbias1, unbias2 = k.unbias2;
+  if (k.step_dev) {
+    step = max((int64_t)1, *k.step_dev);
+    unbias1 = -1.0 / expm1((double)step * log(k.beta1));
+    unbias2 = 1.0 / sqrt(-expm1((double)step * log(k.beta2)));
+  }
+  const double lr = (k.lr_dev ? *k.lr_dev : k.lr) * (double)t.lr_scale;
+  const float b1 = (float)k.beta1, o1 = (float)(1.0 - k.beta1), b2 = (float)k.beta2, o2 = (float)(1.0 - k.beta2);
+  const float keep = (float)(1.0 - lr * (double)t.wd);
+  const float c1 = (float)(lr * unbias1), c2 = (float)unbias2;
+  const float eps = (float)k.eps;
+  const int64_t n = t.n;
+  const int64_t i = (int64_t)(blockIdx.x - t.tile0) * kAdamTile + threadIdx.x * kAdamVec;
+  float g[8], w[8], m[8], v[8];
+  load8((const G*)t.grad, i, n, g);
+  if constexpr (MASTER) load8(t.master, i, n, w);
+  else load8((const W*)t.w, i, n, w);
+  if constexpr (Q8) {
+    uint8_t cm[8], cv[8];
+    load_codes((const uint8_t*)t.m, i, n, cm);
+    load_codes((const uint8_t*)t.v, i, n, cv);
+    const float sm = i < n ? t.m_scale[i / kAdamBlock] : 0.f, sv = i < n ? t.v_scale[i / kAdamBlock] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) { m[j] = decode_m((int8_t)cm[j], sm); v[j] = decode_v(cv[j], sv); }
+  } else {
+    load8((const float*)t.m, i, n, m);
+    load8((const float*)t.v, i, n, v);
+  }
+  uint32_t rnd[8];
+  if constexpr (Q8 || (sizeof(W) == 2 && !MASTER)) {
+    const uint32_t key = step_key(k.seed, step);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rnd[j] = random_bits(t.place + (uint32_t)i + j, key);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = g[j] * gs;
+    m[j] = m[j] * b1 + x * o1;
+    v[j] = v[j] * b2 + (x * x) * o2;
+    w[j] = w[j] * keep - c1 * m[j] / (sqrtf(v[j]) * c2 + eps);
+  }
+  if constexpr (MASTER) store8(t.master, i, n, w);
+  if constexpr (sizeof(W) == 2 && !MASTER) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t u = __float_as_uint(w[j]);
+      if ((u & 0x7f800000u) != 0x7f800000u) w[j] = __uint_as_float((u + more_bits(rnd[j])) & 0xffff0000u);
+    }
+  }
+  store8((W*)t.w, i, n, w);
+  if constexpr (Q8) {
+    pack8<false>(m, v, rnd, i, n, (uint8_t*)t.m, t.m_scale, (uint8_t*)t.v, t.v_scale);
+  } else {
+    store8((float*)t.m, i, n, m);
+    store8((float*)t.v, i, n, v);
+  }
+}
+
+// 8-bit averages to FP32 and back (nearest level).
+__global__ __launch_bounds__(kAdamThreads) void adamw_unpack_kernel(int64_t n, const uint8_t* __restrict__ mc,
+                                                                    const float* __restrict__ ms,
+                                                                    const uint8_t* __restrict__ vc,
+                                                                    const float* __restrict__ vs,
+                                                                    float* __restrict__ m, float* __restrict__ v) {
+  const int64_t i = (int64_t)blockIdx.x * kAdamTile + threadIdx.x * kAdamVec;
+  if (i >= n) return;
+  uint8_t cm[8], cv[8];
+  load_codes(mc, i, n, cm);
+  load_codes(vc, i, n, cv);
+  const float sm = ms[i / kAdamBlock], sv = vs[i / kAdamBlock];
+  float fm[8], fv[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) { fm[j] = decode_m((int8_t)cm[j], sm); fv[j] = decode_v(cv[j], sv); }
+  store8(m, i, n, fm);
+  store8(v, i, n, fv);
+}
+
+__global__ __launch_bounds__(kAdamThreads) void adamw_pack_kernel(int64_t n, const float* __restrict__ m,
+                                                                  const float* __restrict__ v, uint8_t* __restrict__ mc,
+                                                                  float* __restrict__ ms, uint8_t* __restrict__ vc,
+                                                                  float* __restrict__ vs) {
+  const int64_t i = (int64_t)blockIdx.x * kAdamTile + threadIdx.x * kAdamVec;
+  float fm[8], fv[8];
+  load8(m, i, n, fm);
+  load8(v, i, n, fv);
+  pack8<true>(fm, fv, nullptr, i, n, mc, ms, vc, vs);
+}
+
+// Norm of all gradients: FP64 sums of squares, one per workgroup (the workgroups of every launch walk the same tiles
+// in the same order, and a later launch adds to the sums of the ones before), then one workgroup adds them.
+constexpr int kNormBlocks = 1024;
+MOE_DEV double wave_sum_d(double x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+  return x;
+}
+MOE_DEV double group_sum_d(double x) {  // of a workgroup of kAdamThreads; in thread 0
+  __shared__ double part[kAdamThreads / 64];
+  x = wave_sum_d(x);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+  __syncthreads();
+  double s = 0.0;
+  for (int w = 0; w < kAdamThreads / 64; ++w) s += part[w];
+  return s;
+}
+
+template <typename G>
+__global__ __launch_bounds__(kAdamThreads) void grad_norm_kernel(const AdamBatch b, uint32_t tiles, bool first,
+                                                                 double* __restrict__ sums) {
+  double s = 0.0;
+  for (uint32_t tile = blockIdx.x; tile < tiles; tile += kNormBlocks) {
+    const AdamTensor& t = b.t[tensor_of(b, tile)];
+    const int64_t i = (int64_t)(tile - t.tile0) * kAdamTile + threadIdx.x * kAdamVec;
+    float g[8];
+    load8((const G*)t.grad, i, t.n, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += (double)g[j] * (double)g[j];
+  }
+  s = group_sum_d(s);
+  if (threadIdx.x == 0) sums[blockIdx.x] = first ? s : sums[blockIdx.x] + s;
+}
+
+__global__ __launch_bounds__(kAdamThreads) void grad_norm_total_kernel(const double* __restrict__ sums, int count,
+                                                                       double max_norm, float* __restrict__ norm) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < count; i += kAdamThreads) s += sums[i];
+  s = group_sum_d(s);
+  if (threadIdx.x == 0) {
+    const double x = sqrt(s);
+    norm[0] = (float)x;
+    // a norm that is no finite FP32 number cannot be scaled by: NaN, which leaves the step out
+    norm[1] = !(fabs(x) <= 3.4028234663852886e38) ? __builtin_nanf("") : x > max_norm ? (float)(max_norm / x) : 1.0f;
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ host
+
+namespace {
+
+int kind_of(const moe_adamw_tensor& t) {
+  return (t.w_dtype == MOE_BF16 ? (t.master ? 2 : 4) : 0) + (t.grad_dtype == MOE_BF16 ? 1 : 0);
+}
+
+// Runs `launch(batch, tiles)` over the tensors for which `pick` holds, kAdamBatch at a time. Elements are placed in
+// the random sequence as if the tensors lay one behind the other in their order, each from a multiple of 256 on.
+template <typename Pick, typename Launch>
+hipError_t over_batches(int n_tensors, const moe_adamw_tensor* t, Pick pick, Launch launch) {
+  AdamBatch b;
+  b.count = 0;
+  int64_t place = 0, tiles = 0;
+  auto flush = [&]() -> hipError_t {
+    if (b.count == 0) return hipSuccess;
+    const hipError_t e = launch(b, (uint32_t)tiles);
+    b.count = 0;
+    tiles = 0;
+    return e;
+  };
+  for (int i = 0; i < n_tensors; ++i) {
+    const int64_t blocks = (t[i].n + kAdamBlock - 1) / kAdamBlock;
+    if (t[i].n > 0 && pick(t[i])) {
+      const int64_t mine = (t[i].n + kAdamTile - 1) / kAdamTile;
+      if (b.count == kAdamBatch || tiles + mine > (1 << 23)) {  // a launch holds fewer than 2^32 threads
+        const hipError_t e = flush();
+        if (e != hipSuccess) return e;
+      }
+      b.t[b.count++] = AdamTensor{t[i].w, t[i].master, t[i].grad, t[i].m, t[i].v, t[i].m_scale, t[i].v_scale, t[i].n,
+                                  (uint32_t)(place * kAdamBlock), (uint32_t)tiles, t[i].lr_scale, t[i].weight_decay};
+      tiles += mine;
+    }
+    place += blocks;
+  }
+  return flush();
+}
+
+template <typename W, bool MASTER, typename G>
+hipError_t launch_kind(const AdamBatch& b, uint32_t tiles, const AdamConst& k, bool q8, hipStream_t s) {
+  MOE_TRACE("adamw", s);
+  if (q8) MOE_LAUNCH((adamw_kernel<W, MASTER, G, true>), dim3(tiles), dim3(kAdamThreads), 0, s, b, k);
+  else MOE_LAUNCH((adamw_kernel<W, MASTER, G, false>), dim3(tiles), dim3(kAdamThreads), 0, s, b, k);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const moe_adamw_options& o, int n_tensors, const moe_adamw_tensor* t, hipStream_t s) {
+  const double step = (double)o.step;
+  const AdamConst k{o.lr, o.beta1, o.beta2, o.eps, -1.0 / std::expm1(step * std::log(o.beta1)),
+                    1.0 / std::sqrt(-std::expm1(step * std::log(o.beta2))), o.lr_dev, o.step_dev, o.grad_scale, o.step, o.seed};
+  const bool q8 = o.state_bits == 8;
+  for (int kind = 0; kind < 6; ++kind) {
+    const hipError_t e = over_batches(
+        n_tensors, t, [&](const moe_adamw_tensor& x) { return kind_of(x) == kind; },
+        [&](const AdamBatch& b, uint32_t tiles) {
+          switch (kind) {
+            case 0: return launch_kind<float, false, float>(b, tiles, k, q8, s);
+            case 1: return launch_kind<float, false, uint16_t>(b, tiles, k, q8, s);
+            case 2: return launch_kind<uint16_t, true, float>(b, tiles, k, q8, s);
+            case 3: return launch_kind<uint16_t, true, uint16_t>(b, tiles, k, q8, s);
+            case 4: return launch_kind<uint16_t, false, float>(b, tiles, k, q8, s);
+            default: return launch_kind<uint16_t, false, uint16_t>(b, tiles, k, q8, s);
+          }
+        });
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+int64_t grad_norm_ws_bytes() { return kNormBlocks * (int64_t)sizeof(double); }
+
+hipError_t launch_grad_norm(int n_tensors, const moe_adamw_tensor* t, double max_norm, float* norm, void* workspace,
+                            hipStream_t s) {
+  double* sums = (double*)workspace;
+  int count = 0;  // sums that hold something
+  for (int bf16 = 0; bf16 < 2; ++bf16) {
+    const hipError_t e = over_batches(
+        n_tensors, t, [&](const moe_adamw_tensor& x) { return (x.grad_dtype == MOE_BF16) == (bf16 == 1); },
+        [&](const AdamBatch& b, uint32_t tiles) {
+          // the first launch writes every sum, later ones add to theirs
+          const bool first = count == 0;
+          const int blocks = first ? kNormBlocks : (int)std::min<uint32_t>(tiles, kNormBlocks);
+          count = kNormBlocks;
+          MOE_TRACE("grad_norm", s);
+          if (bf16) MOE_LAUNCH(grad_norm_kernel<uint16_t>, dim3(blocks), dim3(kAdamThreads), 0, s, b, tiles, first, sums);
+          else MOE_LAUNCH(grad_norm_kernel<float>, dim3(blocks), dim3(kAdamThreads), 0, s, b, tiles, first, sums);
+          return hipGetLastError();
+        });
+    if (e != hipSuccess) return e;
+  }
+  MOE_TRACE("grad_norm_total", s);
+  MOE_LAUNCH(grad_norm_total_kernel, dim3(1), dim3(kAdamThreads), 0, s, sums, count, max_norm, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw_unpack(int64_t n, const void* mc, const float* ms, const void* vc, const float* vs, float* m,
+                               float* v, hipStream_t s) {
+  MOE_TRACE("adamw_unpack", s);
+  MOE_LAUNCH(adamw_unpack_kernel, dim3((unsigned)((n + kAdamTile - 1) / kAdamTile)), dim3(kAdamThreads), 0, s, n,
+             (const uint8_t*)mc, ms, (const uint8_t*)vc, vs, m, v);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw_pack(int64_t n, const float* m, const float* v, void* mc, float* ms, void* vc, float* vs,
+                             hipStream_t s) {
+  MOE_TRACE("adamw_pack", s);
+  MOE_LAUNCH(adamw_pack_kernel, dim3((unsigned)((n + kAdamTile - 1) / kAdamTile)), dim3(kAdamThreads), 0, s, n, m, v,
+             (uint8_t*)mc, ms, (uint8_t*)vc, vs);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/moe.h"
+
 namespace moe {
 
 // routing
@@ -24,6 +26,32 @@ hipError_t launch_route(const float* logits, int32_t* topk_idx, float* gates, in
                         int32_t* offsets, int32_t* row_of, int32_t* src_token, int32_t* scratch,
                         int64_t T, int E, int e0, int El, int K, int n, int chunk0, int nchunks,
                         int64_t P_c, hipStream_t s);
+
+// the permutation from topk_idx and the 16-token histograms of its chunks (at the start of `scratch`)
+hipError_t launch_layout(const int32_t* topk_idx, int32_t* scratch, int32_t* counts, int32_t* offsets, int32_t* row_of,
+                         int32_t* src_token, int64_t T, int E, int e0, int El, int K, int n, int chunk0, int nchunks,
+                         int64_t P_c, hipStream_t s);
+
+// routing by scores (route_scores.hip): choice and gates, then the layout; the gradient to the logits (dl_hi, dl_lo,
+// ldl, pitch, add as launch_route_bwd_dlogits); the bias update
+hipError_t launch_route_scores(const moe_router_scores& r, const float* logits, const float* bias, int32_t* topk_idx,
+                               float* gates, int32_t* counts, int32_t* offsets, int32_t* row_of, int32_t* src_token,
+                               int32_t* scratch, int64_t T, int E, int e0, int El, int K, int n, int chunk0, int nchunks,
+                               int64_t P_c, hipStream_t s);
+hipError_t launch_route_scores_bwd(const moe_router_scores& r, const float* logits, const float* dgates,
+                                   const int32_t* idx, float* dlogits, int64_t t0, int64_t t1, int K, int E,
+                                   hipStream_t s, uint16_t* dl_hi, uint16_t* dl_lo, int ldl, int64_t pitch, bool add);
+hipError_t launch_router_bias_update(int E, int rows, const int32_t* counts, float rate, float* bias, hipStream_t s);
+
+// AdamW (adamw.hip)
+hipError_t launch_adamw(const moe_adamw_options& o, int n_tensors, const moe_adamw_tensor* t, hipStream_t s);
+int64_t grad_norm_ws_bytes();
+hipError_t launch_grad_norm(int n_tensors, const moe_adamw_tensor* t, double max_norm, float* norm, void* workspace,
+                            hipStream_t s);
+hipError_t launch_adamw_unpack(int64_t n, const void* mc, const float* ms, const void* vc, const float* vs, float* m,
+                               float* v, hipStream_t s);
+hipError_t launch_adamw_pack(int64_t n, const float* m, const float* v, void* mc, float* ms, void* vc, float* vs,
+                             hipStream_t s);
 
 // router loss (router_loss.hip): workspace bytes, forward (two launches) and backward
 int64_t router_loss_ws_bytes(int64_t T, int S, int E);

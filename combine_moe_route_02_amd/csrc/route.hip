@@ -29,50 +29,10 @@
 
 #include "common.h"
 #include "launch.h"
+#include "route_keys.h"
 #include "trace.h"
 
 namespace moe {
-
-constexpr int kRouteBlock = 64;     // tokens per route_layout block (one ballot wave)
-constexpr int kRouteThreads = 1024; // route_layout: 16 waves
-constexpr int kGroup = 16;          // lanes per token in route_topk
-constexpr int kTopkThreads = 256;   // route_topk block
-constexpr int kHistTok = kTopkThreads / kGroup;  // tokens per histogram (16)
-constexpr int kSub = kRouteBlock / kHistTok;     // histograms per route_layout block (4)
-
-// Order-preserving map of a logit to 32 bits: larger logit -> larger key; NaN ranks as -inf and
-// -0 equals +0.
-MOE_DEV uint32_t logit_key(float x) {
-  if (x != x) x = -__builtin_huge_valf();
-  if (x == 0.f) x = 0.f;
-  const uint32_t u = __float_as_uint(x);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-MOE_DEV float key_logit(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
-}
-// Full key: logit key above the complemented expert index, so equal logits rank the lower index
-// higher. Every real key is > 0; 0 marks an empty list slot.
-MOE_DEV uint64_t full_key(float x, int e) {
-  return ((uint64_t)logit_key(x) << 32) | (uint32_t)(0xffffffffu - (uint32_t)e);
-}
-
-template <int K>
-MOE_DEV void insert_key(uint64_t (&l)[K], uint64_t key) {
-#pragma unroll
-  for (int s = 0; s < K; ++s) {
-    const uint64_t cur = l[s];
-    const bool take = key > cur;
-    l[s] = take ? key : cur;
-    key = take ? cur : key;
-  }
-}
-
-MOE_DEV uint64_t shfl_xor_u64(uint64_t v, int o) {
-  const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)v, o, kWave);
-  const uint32_t hi = (uint32_t)__shfl_xor((int)(uint32_t)(v >> 32), o, kWave);
-  return ((uint64_t)hi << 32) | lo;
-}
 
 // Top-K of one token's logits row (nullptr: no token) for the 16-lane group of lane q: each lane
 // keeps a sorted list of its share of the experts, then K rounds of a 16-lane max merge the
@@ -462,10 +422,10 @@ int64_t route_scratch_bytes(int64_t T, int n, int E) {
   return (route_hist_ints(T, n, E) + (int64_t)n * route_blocks_per_chunk(T, n) * E) * (int64_t)sizeof(int32_t);
 }
 
-static hipError_t launch_layout(const int32_t* topk_idx, int32_t* scratch, int32_t* counts,
-                               int32_t* offsets, int32_t* row_of, int32_t* src_token, int64_t T, int E,
-                               int e0, int El, int K, int n, int chunk0, int nchunks, int64_t P_c,
-                               hipStream_t s) {
+hipError_t launch_layout(const int32_t* topk_idx, int32_t* scratch, int32_t* counts,
+                         int32_t* offsets, int32_t* row_of, int32_t* src_token, int64_t T, int E,
+                         int e0, int El, int K, int n, int chunk0, int nchunks, int64_t P_c,
+                         hipStream_t s) {
   const int nbpc = route_blocks_per_chunk(T, n);
   int32_t* pre = scratch + route_hist_ints(T, n, E);
   const bool scanned = nbpc > kLayoutDirectBlocks;

@@ -122,6 +122,11 @@ typedef struct moe_desc {
  * writes it over every token once all chunks are routed, and the backward writes its gradient to
  * dlogits first (the loss fields of moe_tensors). */
 #define MOE_FLAG_ROUTER_LOSS 16
+/* (32 is not a flag.) */
+/* The layer primitives route by scores (moe_route_scores with the fields router_scores and router_bias of
+ * moe_tensors, from given logits) and run moe_route_scores_bwd; any dtype, with or without the other flags.
+ * The stage calls do not look at it. */
+#define MOE_FLAG_ROUTER_SCORES 64
 
 /* ---------------------------------------------------------------------------------------
  * Stage calls
@@ -160,6 +165,47 @@ moe_status moe_route_noalloc(const moe_desc* d, int chunk, const float* logits, 
 moe_status moe_route_x(const moe_desc* d, int chunk, const void* x, const void* w_r, float* logits,
                        int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets, int32_t* row_of,
                        int32_t* src_token, void* workspace, void* stream);
+
+/* Routing by scores: a score per expert, a bias that only the choice sees (balance without a loss), groups
+ * of experts, gates from the chosen scores. The pages route by plain top-k; a model that routes
+ * otherwise sets these options.
+ *   score        MOE_SCORE_SOFTMAX: s = softmax(l) over all E experts; MOE_SCORE_SIGMOID: s = 1 / (1 + exp(-l))
+ *   n_groups     groups of E / n_groups experts in a row (1..64, dividing E); 1: no groups
+ *   topk_groups  groups that a token may choose from (1..n_groups, k <= topk_groups * E / n_groups)
+ *   group_top    1 or 2: a group counts as its largest c, or as the sum of its two largest
+ *   renormalize  0: gate_j = scale * s_j; 1: gate_j = scale * s_j / (sum of the chosen s; 0 where that is 0)
+ *   scale        finite
+ * MOE_ERR_ARG outside these, MOE_ERR_UNSUPPORTED for n_groups above 64. */
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef struct moe_router_scores {
+  int32_t score, n_groups, topk_groups, group_top, renormalize;
+  float scale;
+} moe_router_scores;
+
+/* c_e = s_e + bias_e, with s in FP64 and the sum rounded once to FP32 (bias NULL: c_e = s_e rounded); a c of NaN counts
+ * as -inf. Per token the topk_groups groups with the largest group scores (sums rounded once to FP32) are eligible,
+ * and the k largest c among their experts are chosen, slot 0 the largest; ties go to the lower index. Logits: NaN
+ * counts as -inf, +inf as the largest finite value; a row of only -inf has s = 0 everywhere. Gates are FP32,
+ * computed from the logits of the chosen experts. Scores that round to the same FP32 value are ties (sigmoid: logits
+ * above about 17). Every other argument and output is moe_route's; bias [E] FP32. No aliasing. */
+moe_status moe_route_scores(const moe_desc* d, int chunk, const moe_router_scores* r, const float* logits,
+                            const float* bias, int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets,
+                            int32_t* row_of, int32_t* src_token, void* workspace, void* stream);
+
+/* Backward of moe_route_scores (the choice is constant): dlogits from dgates, the logits and topk_idx of the
+ * forward, then the router weight gradient, exactly as moe_route_bwd does with its dlogits. Softmax scores that are
+ * not renormalised give every expert a gradient: set MOE_FLAG_ROUTER_LOSS for moe_dispatch_bwd then (the layer
+ * primitives see to it themselves). With MOE_FLAG_ROUTER_LOSS the gradient is added to what dlogits holds. x NULL:
+ * only dlogits is written, and dwr_acc, dwr and workspace are not used. dlogits may not be the logits buffer. */
+moe_status moe_route_scores_bwd(const moe_desc* d, int chunk, const moe_router_scores* r, const float* logits,
+                                const float* dgates, const int32_t* topk_idx, const void* x, float* dlogits,
+                                float* dwr_acc, void* dwr, void* workspace, void* stream);
+
+/* Balance bias after a step: bias_e += rate * sign(mean load - load_e), load_e the sum of counts[r][e] over the rows r
+ * (counts int32 [rows, E], moe_route's with rows = n_chunks; sum it over GPUs first where the router is shared). E
+ * 1..1024, rate finite. */
+moe_status moe_router_bias_update(int32_t E, int32_t rows, const int32_t* counts, float rate, float* bias,
+                                  void* stream);
 
 /* Dispatch (ChunkedEP "Summary": each token chunk's rows go to the experts before that chunk's
  * expert compute; torchtitan PR 5541 "AI-Generated Details": BF16/FP8 token-row payloads):
@@ -360,6 +406,65 @@ moe_status moe_router_loss_bwd(const moe_desc* d, int32_t n_segments, float bala
                                const float* dloss, float* dlogits, void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Weight update: AdamW over many tensors at once, and the norm of their gradients. The pages train with an
+ * optimizer of their framework; this one takes the gradients that the layer's backward leaves.
+ *
+ * A tensor of n elements (any shape, contiguous; n = 0 is skipped): weight w and gradient grad, each FP32 or BF16
+ * (w_dtype, grad_dtype: MOE_F32, MOE_BF16); master, FP32, with BF16 weights only: the weight that is updated, w
+ * being its BF16 rounding (RNE). BF16 weights without a master are updated in FP32 and rounded to one of the two
+ * BF16 values next to the result, the upper one with the chance of how near it is. lr_scale and weight_decay are the
+ * tensor's own. Every pointer 16-byte aligned, scales 4-byte. Tensors of one call must not overlap (the same w twice
+ * is MOE_ERR_ARG).
+ *
+ * Moving averages, state_bits 32: m and v FP32 [n], scales unused (NULL). state_bits 8: one byte each, blocks of 256
+ * elements in a row with a scale, m_scale and v_scale FP32 [ceil(n / 256)]: m = s c |c| / 127^2 with int8 c, v = s (c /
+ * 255)^4 with uint8 c (each product rounded in FP32; s is the block's largest magnitude, and blocks under 2^-120 are
+ * zeros). A new value lies between two codes and takes the upper one with the chance of how near it is; a v above 0
+ * keeps a code above 0. All zeros (codes and scales) is the state of a new run in either width.
+ *
+ * The chances come from a hash of `seed`, the step and the element's place (tensors one behind the other in the order
+ * of the call, each from a multiple of 256 on): the same call gives the same bits. */
+typedef struct moe_adamw_tensor {
+  void* w; float* master; const void* grad; void* m; void* v; float* m_scale; float* v_scale;
+  int64_t n;
+  int32_t w_dtype, grad_dtype;
+  float lr_scale, weight_decay;
+} moe_adamw_tensor;
+
+/* lr >= 0, 0 < beta < 1, eps >= 0, all finite; step counts from 1. For graphs that are replayed: lr_dev and step_dev
+ * (device FP64 and int64, nullable) take the place of lr and step, read when the kernels run (a step below 1
+ * counts as 1). grad_scale (device FP32, nullable: 1) multiplies every gradient; where it is not finite the call writes
+ * nothing. */
+typedef struct moe_adamw_options {
+  double lr, beta1, beta2, eps;
+  const double* lr_dev; const int64_t* step_dev; const float* grad_scale;
+  int64_t step;
+  int32_t state_bits;
+  uint32_t seed;
+} moe_adamw_options;
+
+/* g = grad * grad_scale; m' = beta1 m + (1 - beta1) g; v' = beta2 v + (1 - beta2) g^2;
+ * w' = w (1 - lr lr_scale weight_decay) - lr lr_scale / (1 - beta1^step) * m' / (sqrt(v' / (1 - beta2^step)) + eps),
+ * in FP32 (m' and v' with each operation rounded once). A gradient that is not finite makes its element
+ * NaN or infinite, and 8-bit averages of its block NaN. One launch per 44 tensors and kind of tensor. */
+moe_status moe_adamw_step(const moe_adamw_options* o, int32_t n_tensors, const moe_adamw_tensor* tensors, void* stream);
+
+/* norm[0] = sqrt of the sum of squares of every gradient (FP64 sums in a fixed order, rounded once), norm[1] = max_norm /
+ * norm where the norm is above max_norm, 1 otherwise, NaN where it is not finite: moe_adamw_step's grad_scale. max_norm >
+ * 0, infinity allowed. Of a tensor only grad, grad_dtype and n are used. workspace: moe_grad_norm_bytes() bytes, 8-byte
+ * aligned, contents undefined before and after; calls that share one must be ordered. norm FP32 [2]. */
+moe_status moe_grad_norm_bytes(int64_t* workspace);
+moe_status moe_grad_norm(int32_t n_tensors, const moe_adamw_tensor* tensors, double max_norm, float* norm,
+                         void* workspace, void* stream);
+
+/* 8-bit averages of n elements to FP32, and FP32 ones to codes (the nearest value; of two as near the lower): to write
+ * or read checkpoints, or to change the width. FP32 pointers 16-byte aligned, codes 8-byte. */
+moe_status moe_adamw_unpack(int64_t n, const void* m_codes, const float* m_scale, const void* v_codes,
+                            const float* v_scale, float* m, float* v, void* stream);
+moe_status moe_adamw_pack(int64_t n, const float* m, const float* v, void* m_codes, float* m_scale, void* v_codes,
+                          float* v_scale, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * Paged activation stash (torchtitan PR 5541, "AI-Generated Details": page-aligned multi-token
  * copy tiles, one page resolved per tile, the first tile of a page records or recycles it,
  * live-prefix and page-tail masks, 64-bit addressing, a bounded copy grid).
@@ -440,6 +545,10 @@ typedef struct moe_tensors {
   int32_t* seg_counts; int32_t* seg_tokens; float* seg_probs; float* router_loss; const float* dloss;
   void* loss_workspace;
   int32_t n_segments; float balance_coef; float z_coef;
+  /* MOE_FLAG_ROUTER_SCORES only, read under that flag alone (see moe_route_scores): the balance bias [E] (nullable;
+   * moe_layer_update writes it) and the options. `logits` must be given. */
+  float* router_bias;
+  moe_router_scores router_scores;
 } moe_tensors;
 
 moe_status moe_layer_forward(const moe_desc* d, const moe_tensors* t, void* compute_stream,
@@ -448,6 +557,25 @@ moe_status moe_layer_backward(const moe_desc* d, const moe_tensors* t, void* com
                               void* aux_stream);
 moe_status moe_layer_forward_backward(const moe_desc* d, const moe_tensors* t,
                                       void* compute_stream, void* aux_stream);
+
+/* The update that follows a layer's backward: AdamW on W1, W2 (local experts) and W_r with dw1, dw2 and dwr, in this order,
+ * and, with MOE_FLAG_ROUTER_SCORES, a router_bias and a bias_rate other than 0, moe_router_bias_update from counts. t->w1,
+ * t->w2 and t->w_r are written. With `norm` set, moe_grad_norm over the three runs first (max_norm, norm_workspace) and
+ * scales the gradients; adamw.grad_scale must be NULL then. F32 and BF16 descriptors. Gradients (dwr at least), their
+ * norm and counts are this GPU's: sum them over GPUs before where weights are shared, with the stage calls. FP8 copies
+ * of the weights (w1t, w2t) are the caller's to renew. */
+typedef struct moe_adamw_state {
+  float* master; void* m; void* v; float* m_scale; float* v_scale;
+  float lr_scale, weight_decay;
+} moe_adamw_state;
+typedef struct moe_layer_optimizer {
+  moe_adamw_options adamw;
+  moe_adamw_state w1, w2, w_r;
+  double max_norm;
+  float* norm; void* norm_workspace;
+  float bias_rate;
+} moe_layer_optimizer;
+moe_status moe_layer_update(const moe_desc* d, const moe_tensors* t, const moe_layer_optimizer* o, void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * Host-only helpers: they never initialise HIP.

@@ -26,12 +26,14 @@ Modules:
   stash     paged activation stash: page-aligned store/load of saved rows with live-prefix and
             page-tail masks.
   int8      8-bit integer quantisation per row, grouped integer products, the integer forward.
+  router_scores  routing by softmax or sigmoid scores with a bias and groups, its gradient, the bias update.
+  adamw     AdamW with FP32 or 8-bit averages.
   router_loss  balance loss over segments, z-loss, per-expert counts and their gradient to the logits.
 
 Every function here is pinned by a ``-m "not gpu"`` test (brute force, closed forms, library
 special cases, finite differences, autograd, printed numbers); none is "parity unpinned".
 """
-from . import routing, ffn, brute, fp8, extent, stash, router_loss, int8  # noqa: F401
+from . import routing, ffn, brute, fp8, extent, stash, router_loss, int8, router_scores, adamw  # noqa: F401
 from .routing import (round4, chunk_bounds, required_extent, route, layout,  # noqa: F401
                       dispatch, unpermute, router_logits)
 from .ffn import expert_ffn, combine, forward, backward  # noqa: F401

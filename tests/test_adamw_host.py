@@ -1,0 +1,131 @@
+"""Refusals of the weight update (no GPU: every check runs before a launch)."""
+import os
+
+import pytest
+
+mh = pytest.importorskip("combine_moe_route_02_amd")
+
+
+@pytest.fixture(autouse=True)
+def _built():
+    if not os.path.exists(mh.LIB_PATH):
+        pytest.skip("libmoe.so not built (run __graft_entry__.build())")
+
+
+def _status(fn, *a):
+    try:
+        fn(*a)
+    except mh.MoeError as e:
+        return e.status
+    return 0
+
+
+class _Table:
+    """Rows as the C ABI takes them, with made-up addresses."""
+
+    def __init__(self, *rows):
+        self.table = (mh.MoeAdamwTensor * max(1, len(rows)))()
+        self.n = len(rows)
+        for i, r in enumerate(rows):
+            base = dict(w=4096 * (i + 1), grad=16, m=16, v=16, m_scale=16, v_scale=16, n=10, w_dtype=mh.MOE_BF16,
+                        grad_dtype=mh.MOE_BF16, lr_scale=1.0, weight_decay=0.0)
+            base.update(r)
+            for k, v in base.items():
+                setattr(self.table[i], k, v)
+
+    def __len__(self):
+        return self.n
+
+
+def _step(rows, **kw):
+    return _status(mh.moe_adamw_step, mh.make_adamw_options(**{"lr": 1e-3, **kw}), _Table(*rows), 0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(lr=-1.0), -1), (dict(lr=float("nan")), -1), (dict(lr=float("inf")), -1), (dict(eps=-1e-8), -1), (dict(eps=float("nan")), -1),
+    (dict(beta1=0.0), -1), (dict(beta1=1.0), -1), (dict(beta2=1.5), -1), (dict(beta2=float("nan")), -1),
+    (dict(step=0), -1), (dict(step=-3), -1), (dict(state_bits=16), -3), (dict(state_bits=0), -3),
+])
+def test_options_are_checked(kw, status):
+    assert _step([{}], **kw) == status
+    assert _step([], **kw) == status
+
+
+@pytest.mark.parametrize("row,status", [
+    (dict(n=-1), -1), (dict(n=2 ** 34 + 1), -3), (dict(w=None), -1), (dict(grad=None), -1), (dict(m=None), -1), (dict(v=None), -1),
+    (dict(w=4104), -1), (dict(grad=8), -1), (dict(m=4), -1), (dict(v=20), -1), (dict(master=8), -1),
+    (dict(w_dtype=mh.MOE_FP8_E4M3), -3), (dict(grad_dtype=mh.MOE_INT8), -3), (dict(w_dtype=mh.MOE_F32, master=16), -1),
+    (dict(lr_scale=float("nan")), -1), (dict(weight_decay=float("inf")), -1),
+])
+def test_tensors_are_checked(row, status):
+    assert _step([row]) == status
+    assert _step([{}, row]) == status
+
+
+def test_scales_of_8_bit_averages():
+    assert _step([dict(m_scale=None)], state_bits=8) == -1 and _step([dict(v_scale=None)], state_bits=8) == -1
+    assert _step([dict(m_scale=18)], state_bits=8) == -1
+
+
+def test_a_weight_listed_twice():
+    assert _step([{}, dict(w=8192), dict(w=4096)]) == -1
+    assert _step([dict(w=8192), dict(w=8192)]) == -1
+
+
+def test_nothing_to_do():
+    assert _step([]) == 0
+    assert _step([dict(n=0, w=None, grad=None, m=None, v=None)]) == 0
+    assert _step([dict(n=0), dict(n=0, w=4096)]) == 0
+    assert _status(mh.moe_adamw_pack, 0, None, None, None, None, None, None, 0) == 0
+    assert _status(mh.moe_adamw_unpack, 0, None, None, None, None, None, None, 0) == 0
+
+
+def test_norm_is_checked():
+    t = _Table({})
+    f = mh.moe_grad_norm
+    assert _status(f, t, 0.0, 16, 16, 0) == -1 and _status(f, t, float("nan"), 16, 16, 0) == -1
+    assert _status(f, t, 1.0, None, 16, 0) == -1 and _status(f, t, 1.0, 16, None, 0) == -1
+    assert _status(f, t, 1.0, 16, 20, 0) == -1
+    assert _status(f, _Table(dict(grad=None)), 1.0, 16, 16, 0) == -1
+    assert mh.moe_grad_norm_bytes() > 0
+
+
+def test_pack_is_checked():
+    for f in (mh.moe_adamw_pack, mh.moe_adamw_unpack):
+        assert _status(f, -1, 16, 16, 16, 16, 16, 16, 0) == -1
+        assert _status(f, 2 ** 34 + 1, 16, 16, 16, 16, 16, 16, 0) == -3
+        scales = (3, 5) if f is mh.moe_adamw_pack else (1, 3)
+        for i in range(6):
+            a = [16] * 6
+            a[i] = None
+            assert _status(f, 5, *a, 0) == -1
+            if i not in scales:
+                a[i] = 20
+                assert _status(f, 5, *a, 0) == -1
+
+
+def _layer(**kw):
+    d = mh.make_desc(T=64, H=64, I=64, E=8, E_local=4, k=2, n_chunks=1, dtype="bf16", flags=kw.pop("flags", 0))
+    bufs = {f: 4096 * (i + 1) for i, f in enumerate(mh.TENSOR_FIELDS)}
+    bufs.update(kw.pop("bufs", {}))
+    o = mh.MoeLayerOptimizer()
+    o.adamw = mh.make_adamw_options(1e-3, **kw.pop("adamw", {}))
+    for f in ("w1", "w2", "w_r"):
+        setattr(o, f, mh.MoeAdamwState(None, 16, 16, None, None, 1.0, 0.0))
+    for k, v in kw.items():
+        setattr(o, k, v)
+    return _status(mh.moe_layer_update, d, bufs, o, 0)
+
+
+def test_layer_update_is_checked():
+    assert _layer(bufs={"dw1": None}) == -1 and _layer(bufs={"dwr": None}) == -1 and _layer(bufs={"w2": None}) == -1
+    assert _layer(w1=mh.MoeAdamwState()) == -1
+    assert _layer(adamw=dict(step=0)) == -1
+    assert _layer(norm=16, max_norm=0.0, norm_workspace=16) == -1 and _layer(norm=16, max_norm=1.0) == -1
+    assert _layer(norm=16, max_norm=1.0, norm_workspace=16, adamw=dict(grad_scale=16)) == -1
+    assert _layer(flags=mh.FLAG_ROUTER_SCORES, bias_rate=float("nan"), bufs={"router_bias": 16}) == -1
+    assert _layer(flags=mh.FLAG_ROUTER_SCORES, bias_rate=0.1, bufs={"router_bias": 16, "counts": None}) == -1
+    d = mh.make_desc(T=64, H=64, I=64, E=8, E_local=4, k=2, n_chunks=1, dtype="fp8")
+    assert _status(mh.moe_layer_update, d, {f: 16 for f in mh.TENSOR_FIELDS}, mh.MoeLayerOptimizer(), 0) == -3
+    d = mh.make_desc(T=64, H=64, I=64, E=8, E_local=4, k=2, n_chunks=1, dtype="bf16")
+    assert _status(mh.moe_layer_update, d, {f: 16 for f in mh.TENSOR_FIELDS}, None, 0) == -1
