@@ -47,6 +47,7 @@ moe_status hip_check(hipError_t e, const char* what) {
 #define MOE_NEED(p) \
   do { if (!(p)) return fail(MOE_ERR_ARG, "%s: argument '%s' is NULL", __func__, #p); } while (0)
 
+bool misaligned(const void* p, uintptr_t to) { return (uintptr_t)p & (to - 1); }
 int64_t round4(int64_t x) { return (x + 3) / 4 * 4; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t tokens_per_chunk(const moe_desc* d) { return cdiv(d->T, d->n_chunks); }
@@ -579,6 +580,8 @@ moe_status moe_route_scores_bwd(const moe_desc* d, int chunk, const moe_router_s
   MOE_TRY(bwd_extent(d));
   MOE_NEED(dwr_acc); MOE_NEED(workspace);
   if (chunk < 0 || chunk == d->n_chunks - 1) MOE_NEED(dwr);
+  if (is_bf16_rows(d) && (misaligned(logits, 16) || misaligned(dlogits, 16)))
+    return fail(MOE_ERR_ARG, "%s: logits and dlogits must be 16-byte aligned", __func__);
   return route_bwd_chunks(d, chunk, x, dlogits, dwr_acc, dwr, workspace, stream, launch);
 }
 
@@ -818,8 +821,6 @@ moe_status moe_router_loss_bwd(const moe_desc* d, int32_t n_segments, float bala
 }
 
 // ----------------------------------------------------------------------------- weight update
-
-static bool misaligned(const void* p, uintptr_t to) { return (uintptr_t)p & (to - 1); }
 
 // Tensors of a call: sizes, types and gradients (norm), and what the update needs besides (update).
 static moe_status check_adamw_tensors(const char* fn, int32_t n, const moe_adamw_tensor* t, bool update, int32_t bits) {

@@ -6,7 +6,16 @@
 //   gate_j = scale s_j, divided by the sum of the chosen s where they are renormalised.
 //
 // A choice hangs on the last bit of c, so c is defined by FP64 scores, rounded once: two programs, or two kernels,
-// that follow the formula choose the same experts.
+// that follow the formula choose the same experts. FP64 exponentials for every logit would take several times the time of
+// reading it, though, and nearly every choice is clear without them: choose() first selects by FP32 scores whose error has a
+// bound, and only a wave with a token where two neighbours in the order (or the last chosen group and the first one left
+// out) are nearer than that bound goes through choose_exact(). (62 of 131072 tokens with 256 experts in 8 groups.)
+//
+// 16 lanes hold a token's row in registers (4 tokens per wave, float4 loads). Per lane the row's share becomes a sorted
+// list of four and the fifth largest; k + 1 rounds of a maximum over the 16 lanes (DPP) pop the chosen experts and the
+// first one left out (a token with five of them in one lane, one of 5000, goes through choose_exact() too). The lists are
+// made of doubles, a score's FP32 bits above the expert's index: they order as the scores do, and a compare-exchange is one
+// v_max_f64 and one v_min_f64 (64-bit integer keys take five instructions).
 #include "common.h"
 #include "launch.h"
 #include "route_keys.h"
@@ -15,231 +24,571 @@
 namespace moe {
 
 constexpr float kMaxFloat = 3.402823466e38f;
-// NaN counts as -inf, +inf as the largest finite value
-MOE_DEV float clean_logit(float x) { return x != x ? -__builtin_huge_valf() : fminf(x, kMaxFloat); }
+// NaN counts as -inf, +inf as the largest finite value: a median of three with a NaN is the smallest of the others. (The
+// compiler takes a median with the constant -inf for a minimum, which a NaN would leave at the other constant.)
+MOE_DEV float clean_logit(float x) {
+  float low = -__builtin_huge_valf();
+  asm("" : "+v"(low));
+  return __builtin_amdgcn_fmed3f(x, low, kMaxFloat);
+}
+// exp(x) for x <= 0 within 2^-22 of itself (0 below 2^-126): the hardware's exp2 of the rounded product, and the product's
+// rounding put back, which plain exp2(x log2 e) would carry |x| times
+MOE_DEV float exp_neg(float x) {
+  constexpr float kL = 1.44269504088896341f, kLow = 1.92596299112661746887e-8f, kLn2 = 0.693147180559945309f;
+  x = fmaxf(x, -200.f);
+  const float t = x * kL;
+  const float r = __builtin_fmaf(x, kLow, __builtin_fmaf(x, kL, -t));
+  return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(r, kLn2, 1.f);
+}
 
 struct ScoreArgs {
   int softmax, groups, keep, top, renorm;
   float scale;
 };
+// route_layout's outputs, for a chunk that fits one workgroup; counts null: left to route_layout
+struct LayoutArgs {
+  int32_t *counts, *offsets, *row_of, *src_token;
+  int64_t P_c;
+  int e0, El;
+};
 
-MOE_DEV double group16_sum(double x) {
-#pragma unroll
-  for (int o = kGroup / 2; o > 0; o >>= 1) x += __shfl_xor(x, o, kWave);
-  return x;
+// Reductions over the 16 lanes of a token: DPP within a row of 16 (neighbours, pairs, mirrored halves, mirrored row).
+template <int CTRL> MOE_DEV int dpp_i(int x) { return __builtin_amdgcn_mov_dpp(x, CTRL, 0xf, 0xf, true); }
+template <int CTRL> MOE_DEV float dpp_f(float x) { return __int_as_float(dpp_i<CTRL>(__float_as_int(x))); }
+template <int CTRL> MOE_DEV uint32_t dpp_u(uint32_t x) { return (uint32_t)dpp_i<CTRL>((int)x); }
+template <int CTRL> MOE_DEV double dpp_d(double x) {
+  return __hiloint2double(dpp_i<CTRL>(__double2hiint(x)), dpp_i<CTRL>(__double2loint(x)));
+}
+#define MOE_ROW16(x, op, get)                              \
+  x = op(x, get<0xB1>(x)); x = op(x, get<0x4E>(x));        \
+  x = op(x, get<0x141>(x)); x = op(x, get<0x140>(x))
+MOE_DEV float add_f(float a, float b) { return a + b; }
+MOE_DEV double add_d(double a, double b) { return a + b; }
+MOE_DEV uint32_t add_u(uint32_t a, uint32_t b) { return a + b; }
+MOE_DEV uint32_t or_u(uint32_t a, uint32_t b) { return a | b; }
+MOE_DEV uint32_t max_u(uint32_t a, uint32_t b) { return a > b ? a : b; }
+MOE_DEV float row_max(float x) { MOE_ROW16(x, fmaxf, dpp_f); return x; }
+MOE_DEV float row_min(float x) { MOE_ROW16(x, fminf, dpp_f); return x; }
+MOE_DEV float row_sum(float x) { MOE_ROW16(x, add_f, dpp_f); return x; }
+MOE_DEV double row_sum_d(double x) { MOE_ROW16(x, add_d, dpp_d); return x; }
+MOE_DEV uint32_t row_or(uint32_t x) { MOE_ROW16(x, or_u, dpp_u); return x; }
+MOE_DEV uint32_t row_sum_u(uint32_t x) { MOE_ROW16(x, add_u, dpp_u); return x; }
+MOE_DEV uint32_t row_max_u(uint32_t x) { MOE_ROW16(x, max_u, dpp_u); return x; }
+
+// LDS between lanes of one wave: program order, which the compiler has to keep.
+MOE_DEV void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); __builtin_amdgcn_wave_barrier(); }
+
+// Group of expert e, without a division: e < 1024, so floor(e / gs) = (e (2^20 / gs + 1)) >> 20.
+MOE_DEV int group_of(int e, uint32_t magic) { return (int)(((uint32_t)e * magic) >> 20); }
+MOE_DEV uint32_t group_magic(int gs) { return (1u << 20) / (uint32_t)gs + 1; }
+
+// (a median of three is a maximum or minimum that leaves its operands as they are: fmaxf first makes them canonical)
+MOE_DEV void two_largest(float& b0, float& b1, float x) {
+  b1 = __builtin_amdgcn_fmed3f(b0, b1, x);
+  b0 = __builtin_amdgcn_fmed3f(b0, x, __builtin_huge_valf());
 }
 
-// 16 lanes per token, 16 tokens per workgroup. c of a token's experts goes through LDS for the group sums.
-template <int K>
-__global__ __launch_bounds__(kTopkThreads) void route_scores_kernel(
-    const float* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ topk_idx,
-    float* __restrict__ gates, int32_t* __restrict__ block_hist, int64_t T, int E, int n, int chunk0, int nbpc,
-    ScoreArgs a) {
-  extern __shared__ int smem[];  // [E] histogram, [16][E] c
-  int* hist = smem;
-  const int tid = threadIdx.x, q = tid & (kGroup - 1), tl = tid / kGroup;
-  float* c = (float*)(smem + E) + tl * E;
-  const int ch = chunk0 + blockIdx.x / nbpc;
-  const int bl = blockIdx.x % nbpc;
-  const ChunkRange cr = chunk_range(T, n, ch);
-  for (int e = tid; e < E; e += kTopkThreads) hist[e] = 0;
-  __syncthreads();
-  const int64_t t = cr.t0 + (int64_t)bl * kHistTok + tl;
-  const bool valid = t < cr.t1;
-  const float* row = logits + (valid ? t : 0) * (int64_t)E;
-  float m = -__builtin_huge_valf();
+// The eligible groups of a token, one bit each, from the c of its experts in LDS. P lanes share a group (16 of them with
+// up to one group, 1 with nine or more), and lane q has the groups q / P, q / P + 16 / P, ... Lanes start at
+// different places of their groups, which lie a multiple of their size apart: the same bank. near: whether the last eligible
+// and the first other group are within `margin` (relative to 1 or the largest c that any group adds), where c is not
+// exact; two groups with one sum are near.
+template <bool EXACT>
+MOE_DEV uint64_t eligible_groups(const float* c, int gs, int q, const ScoreArgs& a, float margin, bool& near) {
+  const float ninf = -__builtin_huge_valf();
+  int lp = 0;  // log2 P: whole float4 per lane, and no more lanes than there are for the groups
+  while (lp < 4 && (a.groups << (lp + 1)) <= kGroup && gs % (8 << lp) == 0) ++lp;
+  const int P = 1 << lp, part = q & (P - 1), first = q >> lp, per_pass = kGroup >> lp;
+  float mine[4], size = 1.f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int g = first + per_pass * u;
+    mine[u] = ninf;
+    if (per_pass * u >= a.groups) continue;
+    float b0 = ninf, b1 = ninf;
+    if (g < a.groups) {
+      if ((gs & 3) == 0) {
+        const int nv = gs >> (2 + lp);
+        const float4* p = (const float4*)(c + g * gs) + part * nv;
+        int i = nv > 16 ? g & 15 : nv > 8 ? g & 7 : nv > 4 ? g & 3 : 0;
+        for (int n = 0; n < nv; ++n) {
+          const float4 x = p[i];
+          two_largest(b0, b1, x.x); two_largest(b0, b1, x.y); two_largest(b0, b1, x.z); two_largest(b0, b1, x.w);
+          i = i + 1 == nv ? 0 : i + 1;
+        }
+      } else {
+        for (int e = g * gs; e < (g + 1) * gs; ++e) two_largest(b0, b1, c[e]);
+      }
+    }
+#define MOE_STEP(CTRL) { const float o0 = dpp_f<CTRL>(b0), o1 = dpp_f<CTRL>(b1); two_largest(b0, b1, o0); two_largest(b0, b1, o1); }
+    if (lp > 0) MOE_STEP(0xB1)
+    if (lp > 1) MOE_STEP(0x4E)
+    if (lp > 2) MOE_STEP(0x141)
+    if (lp > 3) MOE_STEP(0x140)
+#undef MOE_STEP
+    if (g < a.groups) {
+      const bool two = a.top == 2 && gs > 1;
+      mine[u] = two ? b0 + b1 : b0;
+      size = fmaxf(size, two ? fmaxf(fabsf(b0), fabsf(b1)) : fabsf(b0));
+    }
+  }
+  uint32_t lo = 0, hi = 0;
+  float least = __builtin_huge_valf(), most = ninf;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int g = first + per_pass * u;
+    if (per_pass * u >= a.groups) continue;
+    int beaten = 0;
+    const uint32_t own = logit_key(mine[u]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (per_pass * w >= a.groups) continue;
+      const uint32_t key = logit_key(mine[w]);
+      const int count = min(per_pass, a.groups - per_pass * w);
+      for (int j = 0; j < count; ++j) {
+        const uint32_t other = (uint32_t)__shfl((int)key, j << lp, kGroup);
+        if constexpr (EXACT) beaten += other > own || (other == own && per_pass * w + j < g);
+        else beaten += other > own;
+      }
+    }
+    if (g < a.groups) {
+      if (beaten < a.keep) {
+        if (g < 32) lo |= 1u << g; else hi |= 1u << (g - 32);
+        least = fminf(least, mine[u]);
+      } else {
+        most = fmaxf(most, mine[u]);
+      }
+    }
+  }
+  lo = row_or(lo);
+  hi = a.groups > 32 ? row_or(hi) : 0;
+  if constexpr (!EXACT) {
+    least = row_min(least);
+    most = row_max(most);
+    near |= !(least - most > margin * row_max(size)) || __popc(lo) + __popc(hi) != a.keep;
+  }
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// The choice by exact c: lane j < k returns slot j's expert. c: the token's row in LDS [E]. Every lane of the wave calls.
+MOE_DEV int choose_exact(const float* row, const float* bias, float* c, int E, int K, int q, const ScoreArgs& a) {
+  const float ninf = -__builtin_huge_valf(), taken = __builtin_nanf("");
+  float m = ninf;
   double den = 1.0;
   if (a.softmax) {
-    if (valid) for (int e = q; e < E; e += kGroup) m = fmaxf(m, clean_logit(row[e]));
-#pragma unroll
-    for (int o = kGroup / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+    if (row)
+#pragma unroll 4
+      for (int e = q; e < E; e += kGroup) m = fmaxf(m, clean_logit(row[e]));
+    m = row_max(m);
     den = 0.0;
-    if (valid && m > -__builtin_huge_valf())
+    if (row && m > ninf)
+#pragma unroll 4
       for (int e = q; e < E; e += kGroup) den += exp((double)clean_logit(row[e]) - (double)m);
-    den = group16_sum(den);
+    den = row_sum_d(den);
   }
-  if (valid)
-    for (int e = q; e < E; e += kGroup) {
-      const double l = clean_logit(row[e]);
-      const double s = !a.softmax ? 1.0 / (1.0 + exp(-l)) : den > 0.0 ? exp(l - (double)m) / den : 0.0;
-      const float x = (float)(bias ? s + (double)bias[e] : s);
-      c[e] = x != x ? -__builtin_huge_valf() : x;
-    }
-  __syncthreads();
-  uint64_t kept = ~0ull;
+#pragma unroll 4
+  for (int e = q; e < E; e += kGroup) {
+    const double l = row ? clean_logit(row[e]) : 0.f;
+    const double s = !a.softmax ? 1.0 / (1.0 + exp(-l)) : den > 0.0 ? exp(l - (double)m) / den : 0.0;
+    const float x = (float)(bias ? s + (double)bias[e] : s);
+    c[e] = x != x ? ninf : x;
+  }
+  wave_lds_fence();
   const int gs = E / a.groups;
-  if (a.groups > 1) {
-    uint32_t mine[4];  // keys of groups q, q + 16, ...
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int g = q + kGroup * u;
-      mine[u] = 0;
-      if (valid && g < a.groups) {
-        float b0 = -__builtin_huge_valf(), b1 = b0;
-        for (int e = g * gs; e < (g + 1) * gs; ++e) {
-          const float x = c[e];
-          b1 = fmaxf(b1, fminf(b0, x));
-          b0 = fmaxf(b0, x);
-        }
-        mine[u] = logit_key(a.top == 2 && gs > 1 ? b0 + b1 : b0);
-      }
-    }
-    uint32_t lo = 0, hi = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int g = q + kGroup * u;
-      if (kGroup * u >= a.groups) break;
-      int beaten = 0;
-      for (int o = 0; o < a.groups; ++o) {
-        // group o's key is in lane o % 16 of the token's lanes, entry o / 16
-        const uint32_t k0 = (uint32_t)__shfl((int)mine[0], o & 15, kGroup), k1 = (uint32_t)__shfl((int)mine[1], o & 15, kGroup);
-        const uint32_t k2 = (uint32_t)__shfl((int)mine[2], o & 15, kGroup), k3 = (uint32_t)__shfl((int)mine[3], o & 15, kGroup);
-        const uint32_t other = o < 16 ? k0 : o < 32 ? k1 : o < 48 ? k2 : k3;
-        beaten += other > mine[u] || (other == mine[u] && o < g);
-      }
-      if (g < a.groups && beaten < a.keep) { if (g < 32) lo |= 1u << g; else hi |= 1u << (g - 32); }
-    }
-#pragma unroll
-    for (int o = kGroup / 2; o > 0; o >>= 1) {
-      lo |= (uint32_t)__shfl_xor((int)lo, o, kWave);
-      hi |= (uint32_t)__shfl_xor((int)hi, o, kWave);
-    }
-    kept = ((uint64_t)hi << 32) | lo;
-  }
-  uint64_t l[K], sel[K];
-#pragma unroll
-  for (int s = 0; s < K; ++s) l[s] = 0;
-  if (valid)
+  if (a.keep < a.groups) {
+    bool unused = false;
+    const uint64_t open = eligible_groups<true>(c, gs, q, a, 0.f, unused);
+    wave_lds_fence();
+    const uint32_t magic = group_magic(gs);
     for (int e = q; e < E; e += kGroup)
-      if ((kept >> (e / gs)) & 1) insert_key<K>(l, full_key(c[e], e));
-#pragma unroll
+      if (!((open >> group_of(e, magic)) & 1)) c[e] = taken;
+  }
+  int id = 0;
   for (int s = 0; s < K; ++s) {
-    uint64_t best = l[0];
-#pragma unroll
-    for (int o = kGroup / 2; o > 0; o >>= 1) {
-      const uint64_t other = shfl_xor_u64(best, o);
-      best = other > best ? other : best;
+    // the lane's largest, the first of equal ones; then the row's, and of equal ones the lowest expert
+    uint32_t top = 0, at = 0;
+#pragma unroll 8
+    for (int e = q; e < E; e += kGroup) {
+      const float x = c[e];
+      const uint32_t key = x == x ? logit_key(x) : 0;
+      at = key > top ? (uint32_t)e : at;
+      top = key > top ? key : top;
     }
-    sel[s] = best;
-    if (l[0] == best) {
-#pragma unroll
-      for (int r = 0; r + 1 < K; ++r) l[r] = l[r + 1];
-      l[K - 1] = 0;
-    }
+    const uint32_t best = row_max_u(top);
+    const uint32_t e = 1023u - row_max_u(top == best ? 1023u - at : 0u);
+    if (q == s) id = (int)e;
+    if (q == (int)(e & (kGroup - 1))) c[e] = taken;  // (its own lane reads it again)
   }
-  if (valid && q < K) {
-    // gates, computed relative to the largest so that the sum of very small scores keeps its digits
-    float top = -__builtin_huge_valf(), mine = 0.f, sum = 0.f;
-    int id = 0;
-    float z[K];
-#pragma unroll
-    for (int s = 0; s < K; ++s) {
-      const int e = (int)(0xffffffffu - (uint32_t)sel[s]);
-      if (s == q) id = e;
-      z[s] = clean_logit(row[e]);
-      top = fmaxf(top, a.softmax ? z[s] : fminf(z[s], 0.f));
-    }
-    float g;
-    if (a.renorm) {
-#pragma unroll
-      for (int s = 0; s < K; ++s) {
-        float u = 0.f;
-        if (top > -__builtin_huge_valf())
-          u = a.softmax ? expf(z[s] - top) : expf(fminf(z[s], 0.f) - top) / (1.f + expf(-fabsf(z[s])));
-        sum += u;
-        if (s == q) mine = u;
-      }
-      g = sum > 0.f ? mine / sum : 0.f;
-    } else {
-      float zq = 0.f;
-#pragma unroll
-      for (int s = 0; s < K; ++s) if (s == q) zq = z[s];
-      if (a.softmax) g = den > 0.0 ? expf(zq - m) / (float)den : 0.f;
-      else g = expf(fminf(zq, 0.f)) / (1.f + expf(-fabsf(zq)));
-    }
-    topk_idx[t * K + q] = id;
-    gates[t * K + q] = a.scale * g;
-    atomicAdd(&hist[id], 1);
-  }
-  __syncthreads();
-  int32_t* out = block_hist + (int64_t)ch * E * nbpc + bl;
-  for (int e = tid; e < E; e += kTopkThreads) out[(int64_t)e * nbpc] = hist[e];
+  return id;
 }
 
-// Gradient to the logits, one wave per token. With gh_j = s_j / sum s over the chosen experts:
+constexpr int kTopList = 4;
+constexpr int kSelInts = 2 * kGroup;  // LDS of a token's slots: score and expert, one lane each
+
+// Keys of the lists: hi the bits of a score (finite: never a NaN or infinity as a double), lo the expert.
+MOE_DEV double list_key(float score, int e) { return __hiloint2double(__float_as_int(score), e); }
+MOE_DEV double key_max(double a, double b) { double r; asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b)); return r; }
+MOE_DEV double key_min(double a, double b) { double r; asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b)); return r; }
+MOE_DEV void key_swap(double& a, double& b) { const double t = key_max(a, b); b = key_min(a, b); a = t; }
+MOE_DEV void sort4(double (&l)[4]) {
+  key_swap(l[0], l[1]); key_swap(l[2], l[3]); key_swap(l[0], l[2]); key_swap(l[1], l[3]); key_swap(l[1], l[2]);
+}
+// l and f sorted: l becomes the four largest of both, sorted, rest the larger of itself and the others.
+MOE_DEV void merge4(double (&l)[4], double (&f)[4], double& rest) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) key_swap(l[i], f[3 - i]);
+  rest = key_max(rest, key_max(key_max(f[0], f[1]), key_max(f[2], f[3])));
+  key_swap(l[0], l[2]); key_swap(l[1], l[3]); key_swap(l[0], l[1]); key_swap(l[2], l[3]);
+}
+
+// Experts of a lane's elements: VEC: 64 (i / 4) + 4 q + i % 4 (float4 loads, E a multiple of 4), else 16 i + q.
+template <bool VEC> MOE_DEV int expert_of(int i, int q) { return VEC ? 64 * (i / 4) + 4 * q + i % 4 : kGroup * i + q; }
+template <int NE, bool VEC>
+MOE_DEV void load_row(const float* row, int E, int q, float none, float (&x)[NE]) {
+#pragma unroll
+  for (int i = 0; i < NE; i += VEC ? 4 : 1) {
+    const int e = expert_of<VEC>(i, q);
+    if constexpr (VEC) {
+      float4 f = make_float4(none, none, none, none);
+      if (row && e < E) f = *(const float4*)(row + e);
+      x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
+    } else {
+      x[i] = row && e < E ? row[e] : none;
+    }
+  }
+}
+
+// The choice of a token's 16 lanes: lane j < k returns slot j's expert. row: its logits, null without a token; c: its row in
+// LDS [E]; slots: its kSelInts in LDS. Every lane of the wave calls.
+//
+// Error of the FP32 sums, in units of 2^-24: sigmoid: the exponential's argument and its own ulp move s by at most 0.72 (s
+// (1 - s) |l| <= 0.224), 1 + e rounds by 1 and the reciprocal by 2, the sum with the bias by |c|, and the exact c
+// itself by |c|: 3.72 + 2 |c| each, so that sums further apart than 2 (3.72 + 2 |c|) < 16 max(1, |c|) are in order.
+// Softmax: the differences and products below an exponential move it by 2.2 x e^-x <= 0.82, its ulp by 2, relative to a
+// largest score p = 1 / sum; the sum (in FP64) by its terms' 3, the reciprocal and the product by 3: 9 p + 2 |c| each.
+// Group sums: twice that and their own rounding. Ties and sums within the margin go to choose_exact.
+// m, inv: softmax: the row's largest logit and 1 / the sum of exponentials (0 where no logit is above -inf).
+template <int NE, bool VEC>
+MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slots, int E, int K, int q,
+                   const ScoreArgs& a, float& m, float& inv) {
+  const float ninf = -__builtin_huge_valf();
+  constexpr float kLog2e = 1.44269504088896341f, kUnit = 0x1p-24f;
+  float x[NE];
+  load_row<NE, VEC>(row, E, q, ninf, x);
+  const float margin = (a.softmax ? 20.f : 16.f) * kUnit;  // relative to the sums and, softmax, p, or 1
+  m = ninf;
+  inv = 0.f;
+  if (a.softmax) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) { x[i] = clean_logit(x[i]); m = fmaxf(m, x[i]); }
+    m = row_max(m);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      x[i] = m > ninf ? __builtin_amdgcn_exp2f((x[i] - m) * kLog2e) : 0.f;
+      sum += (double)x[i];
+    }
+    const float total = (float)row_sum_d(sum);
+    inv = total > 0.f ? __builtin_amdgcn_rcpf(total) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) x[i] *= inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) x[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-clean_logit(x[i]) * kLog2e));
+  }
+  if (bias) {
+    float b[NE];
+    load_row<NE, VEC>(bias, E, q, 0.f, b);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) x[i] += b[i];
+  }
+#pragma unroll
+  for (int i = 0; i < NE; ++i) x[i] = __builtin_amdgcn_fmed3f(x[i], -kMaxFloat, kMaxFloat);  // NaN: the lowest
+  bool bad = false;
+  const int gs = E / a.groups;
+  const float none = __int_as_float(0xffc00000);  // no expert: its bits order below every score's
+  if (a.keep < a.groups) {
+#pragma unroll
+    for (int i = 0; i < NE; i += VEC ? 4 : 1) {
+      const int e = expert_of<VEC>(i, q);
+      if (e >= E) continue;
+      if constexpr (VEC) *(float4*)(c + e) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+      else c[e] = x[i];
+    }
+    wave_lds_fence();
+    // twice the margin of one c and the sums' rounding, relative to 1 (softmax scores are at most that)
+    const uint64_t open = eligible_groups<false>(c, gs, q, a, 2.f * margin + 4.f * kUnit, bad);
+    const uint32_t magic = group_magic(gs);
+    if (VEC && (gs & 3) == 0) {  // the four of a vector share a group
+#pragma unroll
+      for (int i = 0; i < NE; i += 4) {
+        const bool ok = (open >> (group_of(expert_of<VEC>(i, q), magic) & 63)) & 1;
+#pragma unroll
+        for (int j = i; j < i + 4; ++j) x[j] = ok ? x[j] : none;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (!((open >> (group_of(expert_of<VEC>(i, q), magic) & 63)) & 1)) x[i] = none;
+    }
+  }
+  if (E < kGroup * NE) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) x[i] = expert_of<VEC>(i, q) < E ? x[i] : none;
+  }
+  double l[kTopList], rest = list_key(none, 0);
+#pragma unroll
+  for (int i = 0; i < NE; i += 4) {
+    double f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = list_key(x[i + j], expert_of<VEC>(i + j, q));
+    sort4(f);
+    if (i == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) l[j] = f[j];
+    } else {
+      merge4(l, f, rest);
+    }
+  }
+  // The rounds: 32-bit keys that order as the scores, kUnknown after a lane's fifth where it had more. As many rounds as
+  // there are slots, and one more for the first expert left out.
+  constexpr uint32_t kUnknown = 0xffffffffu;
+  uint32_t key[kTopList + 1];
+  int ex[kTopList + 1];
+#pragma unroll
+  for (int j = 0; j <= kTopList; ++j) {
+    const double v = j < kTopList ? l[j] : rest;
+    const int u = __double2hiint(v);
+    key[j] = (uint32_t)(u ^ ((u >> 31) | (int)0x80000000u));
+    ex[j] = __double2loint(v);
+  }
+  const int rounds = min(K + 1, a.keep * gs);
+  uint32_t pops = 0;
+  for (int s = 0; s < rounds; ++s) {
+    const uint32_t best = row_max_u(key[0]);
+    if (key[0] == best) {
+      *(uint2*)(slots + 2 * s) = make_uint2(best, (uint32_t)ex[0]);
+      ++pops;
+#pragma unroll
+      for (int j = 0; j < kTopList; ++j) { key[j] = key[j + 1]; ex[j] = ex[j + 1]; }
+      key[kTopList] = NE > kTopList + 1 ? kUnknown : 0u;
+    }
+  }
+  wave_lds_fence();
+  const uint2 mine = *(const uint2*)(slots + 2 * q);
+  if (q < rounds) {
+    bad |= mine.x == kUnknown;
+    if (q + 1 < rounds) {  // whether slot q and the next are clear of each other
+      const float u = key_logit(mine.x), v = key_logit(slots[2 * q + 2]);
+      const float size = fmaxf(fabsf(u), fabsf(v));
+      bad |= !(u - v > margin * (a.softmax ? inv + size : fmaxf(1.f, size)) + 0x1p-100f);
+    }
+  }
+  // two lanes with one key popped both: more pops than rounds
+  bad |= row_sum_u(pops) != (uint32_t)rounds;
+  if (__any(row && bad)) return choose_exact(row, bias, c, E, K, q, a);
+  return (int)mine.y;
+}
+
+// Gate of lane j < k (live) for its expert; m and inv as choose() leaves them.
+MOE_DEV float gate_of(const float* row, int id, bool live, float m, float inv, const ScoreArgs& a) {
+  const float ninf = -__builtin_huge_valf();
+  const float z = live ? clean_logit(row[id]) : ninf;
+  float g;
+  if (a.renorm) {
+    // relative to the largest chosen score: a sum of very small ones keeps its digits
+    const float low = a.softmax ? z : fminf(z, 0.f);
+    const float top = row_max(low);
+    float u = 0.f;
+    if (live && top > ninf) u = a.softmax ? exp_neg(z - top) : exp_neg(low - top) * __builtin_amdgcn_rcpf(1.f + exp_neg(-fabsf(z)));
+    const float sum = row_sum(u);
+    g = sum > 0.f ? u * __builtin_amdgcn_rcpf(sum) : 0.f;
+  } else if (a.softmax) {
+    g = live && m > ninf ? exp_neg(z - m) * inv : 0.f;
+  } else {
+    g = exp_neg(fminf(z, 0.f)) * __builtin_amdgcn_rcpf(1.f + exp_neg(-fabsf(z)));
+  }
+  return a.scale * g;
+}
+
+// Where a chunk fits one workgroup: its counts, offsets, rows and the rows' tokens, as route_layout leaves them, from the
+// histogram of its tokens and the lanes' own expert (lane q < k of a token's 16; live).
+template <int THREADS>
+MOE_DEV void layout_chunk(const int* hist, int* space, const LayoutArgs& o, int id, bool live, int64_t t0, int tl, int q,
+                          int E, int K, int ch) {
+  const int tid = threadIdx.x, El = o.El;
+  uint64_t* mask = (uint64_t*)space;  // [El] the tokens that chose a local expert
+  int* off = space + 2 * El;          // [El + 1]
+  for (int e = tid; e < E; e += THREADS) o.counts[(int64_t)ch * E + e] = hist[e];
+  for (int el = tid; el < El; el += THREADS) mask[el] = 0;
+  if (tid < 64) {
+    int run = 0;
+    for (int b = 0; b < El; b += 64) {
+      const int v = b + tid < El ? hist[o.e0 + b + tid] : 0;
+      int incl = v;
+#pragma unroll
+      for (int s = 1; s < 64; s <<= 1) {
+        const int u = __shfl_up(incl, s, 64);
+        if (tid >= s) incl += u;
+      }
+      if (b + tid < El) off[b + tid] = run + incl - v;
+      run += __shfl(incl, 63, 64);
+    }
+    if (tid == 0) off[El] = run;
+  }
+  __syncthreads();
+  for (int el = tid; el <= El; el += THREADS) o.offsets[(int64_t)ch * (El + 1) + el] = off[el];
+  const int el = id - o.e0;
+  const bool local = live && el >= 0 && el < El;
+  if (local) atomicOr((unsigned long long*)&mask[el], 1ull << tl);
+  __syncthreads();
+  if (live) {
+    int32_t row = -1;
+    if (local) {
+      const uint64_t below = tl == 0 ? 0ull : ~0ull >> (64 - tl);
+      const int64_t r = (int64_t)ch * o.P_c + off[el] + __popcll(mask[el] & below);
+      o.src_token[r] = (int32_t)(t0 + tl);
+      row = (int32_t)r;
+    }
+    o.row_of[(t0 + tl) * K + q] = row;
+  }
+  for (int64_t r = off[El] + tid; r < o.P_c; r += THREADS) o.src_token[(int64_t)ch * o.P_c + r] = -1;
+}
+
+// THREADS / 16 tokens per workgroup: 64 (one histogram per layout block: its four 16-token places take the sum and
+// zeros, one 16-byte store) or, where 64 rows of LDS are too many, 16. Waves without a token leave the choice out.
+template <int NE, bool VEC, int THREADS>
+__global__ __launch_bounds__(THREADS, THREADS == 1024 && VEC ? 8 : 1) void route_scores_kernel(
+    const float* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ topk_idx,
+    float* __restrict__ gates, int32_t* __restrict__ block_hist, int64_t T, int64_t tc, int E, int K, int chunk0, int nbpc,
+    ScoreArgs a, LayoutArgs o) {
+  extern __shared__ __attribute__((aligned(16))) int smem[];  // slots, [E rounded up to 4] histogram, [tokens][E] c
+  constexpr int kTok = THREADS / kGroup;
+  const int E4 = (E + 3) & ~3;
+  int* hist = smem + kTok * kSelInts;
+  const int tid = threadIdx.x, q = tid & (kGroup - 1), tl = tid / kGroup;
+  uint32_t* slots = (uint32_t*)smem + tl * kSelInts;
+  float* c = (float*)(hist + E4) + tl * E;
+  const int ch = chunk0 + blockIdx.x / nbpc;
+  const int bl = blockIdx.x % nbpc;
+  for (int e = tid; e < E; e += THREADS) hist[e] = 0;
+  __syncthreads();
+  const int64_t t0 = ch * tc + (int64_t)bl * kTok, t = t0 + tl;
+  const bool valid = t < min(T, (ch + 1) * tc);
+  const float* row = valid ? logits + t * (int64_t)E : nullptr;
+  const bool live = valid && q < K;
+  int id = 0;
+  if (__any(valid)) {
+    float m, inv;
+    id = choose<NE, VEC>(row, bias, c, slots, E, K, q, a, m, inv);
+    const float g = gate_of(row, id, live, m, inv, a);
+    if (live) {
+      topk_idx[t * K + q] = id;
+      gates[t * K + q] = g;
+      atomicAdd(&hist[id], 1);
+    }
+  }
+  __syncthreads();
+  if (o.counts) {
+    layout_chunk<THREADS>(hist, (int*)(hist + E4), o, id, live, t0, tl, q, E, K, ch);
+    return;
+  }
+  // expert-major: the counts of an expert over the chunk's histograms lie one behind the other
+  if constexpr (THREADS == 1024) {
+    int4* out = (int4*)block_hist + (int64_t)ch * E * nbpc + bl;
+    for (int e = tid; e < E; e += THREADS) out[(int64_t)e * nbpc] = make_int4(hist[e], 0, 0, 0);
+  } else {
+    int32_t* out = block_hist + (int64_t)ch * E * nbpc + bl;
+    for (int e = tid; e < E; e += THREADS) out[(int64_t)e * nbpc] = hist[e];
+  }
+}
+
+// Gradient to the logits. With gh_j = s_j / sum s over the chosen experts:
 //   sigmoid: dl_j = scale gh_j (1 - s_j)(dg_j - sum gh_i dg_i), or scale s_j (1 - s_j) dg_j where gates are not renormalised
 //   softmax: dl_j = scale gh_j (dg_j - sum gh_i dg_i), or, for every expert, scale p_e ([e = idx_j] dg_j - sum p_i dg_i)
-// 1 - s_j is taken as sigmoid(-l_j). ADD: dlogits holds another term. The planes are route_bwd_dlogits'.
-template <bool ADD>
+// 1 - s_j is taken as sigmoid(-l_j). Bound by HBM: the row of E gradients is written, read too where every logit has one.
+// 16 lanes per token, as in the forward; a row of LDS per token, cleared by its lanes, takes the k values to their
+// places, so that each row leaves in float4 stores. ADD: dlogits holds another term. The planes are route_bwd_dlogits'.
+template <int NE, bool VEC, bool DENSE, bool ADD>
 __global__ __launch_bounds__(256) void route_scores_bwd_kernel(
     const float* __restrict__ logits, const float* __restrict__ dgates, const int32_t* __restrict__ idx,
     float* __restrict__ dlogits, uint16_t* __restrict__ dl_hi, uint16_t* __restrict__ dl_lo, int ldl, int64_t pitch,
     int64_t t0, int64_t t1, int K, int E, ScoreArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = t0 + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= t1) return;
+  extern __shared__ __attribute__((aligned(16))) int smem[];  // [16 tokens][16 NE]
+  const int tid = threadIdx.x, q = tid & (kGroup - 1), tl = tid / kGroup;
+  float* d_row = (float*)smem + tl * (kGroup * NE);
+  const int64_t t = t0 + (int64_t)blockIdx.x * kHistTok + tl;
+  const bool valid = t < t1;
   const float ninf = -__builtin_huge_valf();
-  const float* lr = logits + t * (int64_t)E;
-  float* row = dlogits + t * (int64_t)E;
-  const bool dense = a.softmax && !a.renorm;
-  const int id = lane < K ? idx[t * K + lane] : -1;
-  const float d = lane < K ? dgates[t * K + lane] : 0.f;
-  const float z = lane < K ? clean_logit(lr[id]) : ninf;
-  float v = 0.f, m = ninf, inv = 0.f, mean = 0.f;
-  if (dense) {
-    for (int e = lane; e < E; e += 64) m = fmaxf(m, clean_logit(lr[e]));
-    m = wave_max(m);
-    float s = 0.f;
-    if (m > ninf) for (int e = lane; e < E; e += 64) s += expf(clean_logit(lr[e]) - m);
-    s = wave_sum(s);
-    inv = s > 0.f ? 1.f / s : 0.f;
-    const float p = lane < K && m > ninf ? expf(z - m) * inv : 0.f;
-    mean = wave_sum(p * d);
-    v = a.scale * p * d;  // added to -scale p mean below
+  const float* lr = valid ? logits + t * (int64_t)E : nullptr;
+  const bool live = valid && q < K;
+  const int id = live ? idx[t * K + q] : 0;
+  const float d = live ? dgates[t * K + q] : 0.f;
+  float p[DENSE ? NE : 1];
+  if constexpr (DENSE) load_row<NE, VEC>(lr, E, q, ninf, p);
+  const float z = live ? clean_logit(lr[id]) : ninf;
+#pragma unroll
+  for (int i = 0; i < NE; i += 4) *(float4*)(d_row + 16 * i + 4 * q) = make_float4(0.f, 0.f, 0.f, 0.f);
+  float v, mean = 0.f;
+  if constexpr (DENSE) {
+    float m = ninf, s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) { p[i] = clean_logit(p[i]); m = fmaxf(m, p[i]); }
+    m = row_max(m);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) { p[i] = m > ninf ? expf(p[i] - m) : 0.f; s += p[i]; }
+    s = row_sum(s);
+    const float inv = s > 0.f ? 1.f / s : 0.f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) p[i] *= inv;
+    const float pj = live && m > ninf ? expf(z - m) * inv : 0.f;
+    mean = -a.scale * row_sum(pj * d);
+    v = a.scale * pj * d;
   } else if (a.renorm) {
-    const float top = wave_max(a.softmax ? z : fminf(z, 0.f));
+    const float low = a.softmax ? z : fminf(z, 0.f);
+    const float top = row_max(low);
     float u = 0.f;
-    if (lane < K && top > ninf)
-      u = a.softmax ? expf(z - top) : expf(fminf(z, 0.f) - top) / (1.f + expf(-fabsf(z)));
-    const float s = wave_sum(u);
+    if (live && top > ninf) u = a.softmax ? expf(z - top) : expf(low - top) / (1.f + expf(-fabsf(z)));
+    const float s = row_sum(u);
     const float gh = s > 0.f ? u / s : 0.f;
     const float rest = a.softmax ? 1.f : expf(-fmaxf(z, 0.f)) / (1.f + expf(-fabsf(z)));
-    v = a.scale * gh * rest * (d - wave_sum(gh * d));
+    v = a.scale * gh * rest * (d - row_sum(gh * d));
   } else {
     const float e1 = expf(-fabsf(z));
     v = a.scale * d * e1 / ((1.f + e1) * (1.f + e1));  // s (1 - s)
   }
-  float vs[8];
-  int ids[8];
+  wave_lds_fence();
+  if (live) d_row[id] = v;
+  wave_lds_fence();
+  if (!valid) return;
+  float* row = dlogits + t * (int64_t)E;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    ids[j] = j < K ? __shfl(id, j, 64) : -1;
-    vs[j] = j < K ? __shfl(v, j, 64) : 0.f;
-  }
-  auto value = [&](int e) {
-    float x = dense && m > ninf ? -a.scale * mean * (expf(clean_logit(lr[e]) - m) * inv) : 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) if (ids[j] == e) x += vs[j];
-    if constexpr (ADD) x += row[e];
-    return x;
-  };
-  if (!dl_hi) {
-    for (int e = lane; e < E; e += 64) row[e] = value(e);
-    return;
-  }
-  // two columns per lane (E is a multiple of 4 where planes are written), zeros past E
-  uint32_t* hr = (uint32_t*)(dl_hi + (t - t0) * pitch);
-  uint32_t* lp = (uint32_t*)(dl_lo + (t - t0) * pitch);
-  for (int e = 2 * lane; e < ldl; e += 128) {
-    float x0 = 0.f, x1 = 0.f;
-    if (e < E) {
-      x0 = value(e);
-      x1 = value(e + 1);
-      *(float2*)(row + e) = make_float2(x0, x1);
+  for (int i = 0; i < NE; i += VEC ? 4 : 1) {
+    const int e = expert_of<VEC>(i, q);
+    if constexpr (VEC) {
+      float4 f = *(const float4*)(d_row + e);
+      if constexpr (DENSE) {
+        f.x += mean * p[i]; f.y += mean * p[i + 1]; f.z += mean * p[i + 2]; f.w += mean * p[i + 3];
+      }
+      if (e < E) {
+        if constexpr (ADD) {
+          const float4 o = *(const float4*)(row + e);
+          f.x += o.x; f.y += o.y; f.z += o.z; f.w += o.w;
+        }
+        *(float4*)(row + e) = f;
+      }
+      if (dl_hi && e < ldl) {  // zeros past E
+        const uint32_t h0 = pack_bf2(f.x, f.y), h1 = pack_bf2(f.z, f.w);
+        *(uint2*)(dl_hi + (t - t0) * pitch + e) = make_uint2(h0, h1);
+        *(uint2*)(dl_lo + (t - t0) * pitch + e) = make_uint2(pack_bf2(f.x - bf2f(h0 & 0xffff), f.y - bf2f(h0 >> 16)),
+                                                             pack_bf2(f.z - bf2f(h1 & 0xffff), f.w - bf2f(h1 >> 16)));
+      }
+    } else if (e < E) {
+      float f = d_row[e];
+      if constexpr (DENSE) f += mean * p[i];
+      if constexpr (ADD) f += row[e];
+      row[e] = f;
     }
-    const uint16_t h0 = f2bf(x0), h1 = f2bf(x1);
-    hr[e / 2] = (uint32_t)h0 | ((uint32_t)h1 << 16);
-    lp[e / 2] = (uint32_t)f2bf(x0 - bf2f(h0)) | ((uint32_t)f2bf(x1 - bf2f(h1)) << 16);
   }
 }
 
@@ -266,45 +615,95 @@ static ScoreArgs score_args(const moe_router_scores& r) {
   return {r.score == MOE_SCORE_SOFTMAX, r.n_groups, r.topk_groups, r.group_top, r.renormalize != 0, r.scale};
 }
 
+// Elements per lane: the row's experts over 16 lanes, 4, 8, ... 64.
+static int elements_per_lane(int E) {
+  int ne = 4;
+  while (ne * kGroup < E) ne *= 2;
+  return ne;
+}
+#define MOE_NE(E, VECTOR, CALL)                              \
+  do {                                                       \
+    if ((VECTOR)) {                                          \
+      constexpr bool VEC = true;                             \
+      switch (elements_per_lane(E)) {                        \
+        case 4: { constexpr int NE = 4; CALL; break; }       \
+        case 8: { constexpr int NE = 8; CALL; break; }       \
+        case 16: { constexpr int NE = 16; CALL; break; }     \
+        case 32: { constexpr int NE = 32; CALL; break; }     \
+        default: { constexpr int NE = 64; CALL; }            \
+      }                                                      \
+    } else {                                                 \
+      constexpr bool VEC = false;                            \
+      switch (elements_per_lane(E)) {                        \
+        case 4: { constexpr int NE = 4; CALL; break; }       \
+        case 8: { constexpr int NE = 8; CALL; break; }       \
+        case 16: { constexpr int NE = 16; CALL; break; }     \
+        case 32: { constexpr int NE = 32; CALL; break; }     \
+        default: { constexpr int NE = 64; CALL; }            \
+      }                                                      \
+    }                                                        \
+  } while (0)
+// float4 loads need rows that start at 16 bytes
+static bool vector_rows(int E, const void* a, const void* b) { return E % 4 == 0 && (((uintptr_t)a | (uintptr_t)b) & 15) == 0; }
+
+template <typename Kernel>
+static hipError_t allow_lds(Kernel k, size_t bytes) {
+  return bytes > 65536 ? hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
+                       : hipSuccess;
+}
+
 hipError_t launch_route_scores(const moe_router_scores& r, const float* logits, const float* bias, int32_t* topk_idx,
                                float* gates, int32_t* counts, int32_t* offsets, int32_t* row_of, int32_t* src_token,
                                int32_t* scratch, int64_t T, int E, int e0, int El, int K, int n, int chunk0, int nchunks,
                                int64_t P_c, hipStream_t s) {
-  const int nbpc = route_blocks_per_chunk(T, n) * kSub;
-  const size_t lds = (size_t)E * (1 + kHistTok) * 4;
+  const int blocks = route_blocks_per_chunk(T, n);
+  const int64_t tc = (T + n - 1) / n;
+  const ScoreArgs a = score_args(r);
+  const bool wide = E <= 256;  // 64 rows of c, and two workgroups in a CU
+  const int tok = wide ? 64 : kHistTok;
+  const int nbpc = wide ? blocks : blocks * kSub;
+  const bool whole = tc <= tok;  // a chunk is one workgroup
+  LayoutArgs o{};
+  if (whole) o = LayoutArgs{counts, offsets, row_of, src_token, P_c, e0, El};
+  const size_t lds = (size_t)(tok * kSelInts + (E + 3) / 4 * 4 + tok * E) * 4;
+  hipError_t err = hipSuccess;
   {
     MOE_TRACE("route_scores", s);
-    switch (K) {
-#define MOE_RS_K(KK)                                                                                              \
-  case KK: {                                                                                                      \
-    auto k = route_scores_kernel<KK>;                                                                             \
-    if (lds > 65536) {                                                                                            \
-      hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);   \
-      if (e != hipSuccess) return e;                                                                              \
-    }                                                                                                             \
-    MOE_LAUNCH(k, dim3(nbpc * nchunks), dim3(kTopkThreads), lds, s, logits, bias, topk_idx, gates, scratch, T, E, \
-               n, chunk0, nbpc, score_args(r));                                                                   \
-    break;                                                                                                        \
-  }
-      MOE_RS_K(1) MOE_RS_K(2) MOE_RS_K(3) MOE_RS_K(4) MOE_RS_K(5) MOE_RS_K(6) MOE_RS_K(7) MOE_RS_K(8)
-#undef MOE_RS_K
-      default: return hipErrorInvalidValue;
+#define MOE_RS(THREADS)                                                                                          \
+    {                                                                                                            \
+      auto k = route_scores_kernel<NE, VEC, THREADS>;                                                            \
+      err = allow_lds(k, lds);                                                                                   \
+      if (err == hipSuccess)                                                                                     \
+        MOE_LAUNCH(k, dim3((whole ? 1 : nbpc) * nchunks), dim3(THREADS), lds, s, logits, bias, topk_idx, gates,  \
+                   scratch, T, tc, E, K, chunk0, whole ? 1 : nbpc, a, o);                                        \
     }
+    const bool vec = vector_rows(E, logits, bias);
+    MOE_NE(E, vec, if constexpr (NE <= 16) { MOE_RS(1024) } else { MOE_RS(256) });
+#undef MOE_RS
   }
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
+  if (err == hipSuccess) err = hipGetLastError();
+  if (err != hipSuccess || whole) return err;
   return launch_layout(topk_idx, scratch, counts, offsets, row_of, src_token, T, E, e0, El, K, n, chunk0, nchunks, P_c, s);
 }
 
 hipError_t launch_route_scores_bwd(const moe_router_scores& r, const float* logits, const float* dgates,
                                    const int32_t* idx, float* dlogits, int64_t t0, int64_t t1, int K, int E,
                                    hipStream_t s, uint16_t* dl_hi, uint16_t* dl_lo, int ldl, int64_t pitch, bool add) {
-  if (dl_hi && (!dl_lo || E % 2 || ldl < E || ldl % 8 || pitch % 2 || pitch < ldl)) return hipErrorInvalidValue;
+  const bool vec = vector_rows(E, logits, dlogits);
+  const int width = dl_hi && ldl > E ? ldl : E;  // columns that a lane's elements have to reach
+  const int ne = elements_per_lane(width);
+  if (dl_hi && (!vec || !dl_lo || ldl < E || ldl > ne * kGroup || ldl % 4 || pitch % 4 || pitch < ldl)) return hipErrorInvalidValue;
   if (t1 <= t0) return hipSuccess;
+  const ScoreArgs a = score_args(r);
+  const bool dense = a.softmax && !a.renorm;
+  const size_t lds = (size_t)kHistTok * kGroup * ne * 4;
   MOE_TRACE("route_scores_bwd", s);
-  auto k = add ? route_scores_bwd_kernel<true> : route_scores_bwd_kernel<false>;
-  MOE_LAUNCH(k, dim3((unsigned)((t1 - t0 + 3) / 4)), dim3(256), 0, s, logits, dgates, idx, dlogits, dl_hi, dl_lo, ldl,
-             pitch, t0, t1, K, E, score_args(r));
+#define MOE_RSB(DENSE, ADD)                                                                                            \
+  MOE_LAUNCH((route_scores_bwd_kernel<NE, VEC, DENSE, ADD>), dim3((unsigned)((t1 - t0 + kHistTok - 1) / kHistTok)),    \
+             dim3(256), lds, s, logits, dgates, idx, dlogits, dl_hi, dl_lo, ldl, pitch, t0, t1, K, E, a)
+  MOE_NE(width, vec, if (dense && add) MOE_RSB(true, true); else if (dense) MOE_RSB(true, false);
+         else if (add) MOE_RSB(false, true); else MOE_RSB(false, false));
+#undef MOE_RSB
   return hipGetLastError();
 }
 

@@ -196,7 +196,8 @@ moe_status moe_route_scores(const moe_desc* d, int chunk, const moe_router_score
  * forward, then the router weight gradient, exactly as moe_route_bwd does with its dlogits. Softmax scores that are
  * not renormalised give every expert a gradient: set MOE_FLAG_ROUTER_LOSS for moe_dispatch_bwd then (the layer
  * primitives see to it themselves). With MOE_FLAG_ROUTER_LOSS the gradient is added to what dlogits holds. x NULL:
- * only dlogits is written, and dwr_acc, dwr and workspace are not used. dlogits may not be the logits buffer. */
+ * only dlogits is written, and dwr_acc, dwr and workspace are not used. dlogits may not be the logits buffer; with BF16
+ * rows and x both must be 16-byte aligned (MOE_ERR_ARG). */
 moe_status moe_route_scores_bwd(const moe_desc* d, int chunk, const moe_router_scores* r, const float* logits,
                                 const float* dgates, const int32_t* topk_idx, const void* x, float* dlogits,
                                 float* dwr_acc, void* dwr, void* workspace, void* stream);

@@ -31,7 +31,7 @@ def _fwd(d, r, chunk=-1, **null):
 
 
 def _bwd(d, r, chunk=-1, **null):
-    return _status(mh.moe_route_scores_bwd, d, chunk, r, *[null.get(n, 16 + i) for i, n in enumerate(BWD)], 0)
+    return _status(mh.moe_route_scores_bwd, d, chunk, r, *[null.get(n, 16 + 16 * i) for i, n in enumerate(BWD)], 0)
 
 
 @pytest.mark.parametrize("call", [_fwd, _bwd])
@@ -71,6 +71,7 @@ def test_backward_types_and_alias():
     r = mh.make_router_scores()
     assert _bwd(_desc(dtype="fp8"), r) == -3 and _bwd(_desc(dtype="int8"), r) == -3
     assert _bwd(_desc(), r, dlogits=16) == -1  # the logits buffer
+    assert _bwd(_desc(), r, dlogits=24) == -1 and _bwd(_desc(), r, logits=20) == -1  # not 16-byte aligned
     # without x nothing but dlogits is asked for; no tokens, no work
     assert _bwd(_desc(T=0), r, x=None, dwr_acc=None, dwr=None, workspace=None, logits=None, dgates=None, topk_idx=None, dlogits=None) == 0
     assert _bwd(_desc(), r, x=None, dwr_acc=None, dwr=None, workspace=None, dlogits=None) == -1
