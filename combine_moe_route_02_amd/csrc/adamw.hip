@@ -30,7 +30,7 @@ constexpr int kAdamThreads = 256;
 constexpr int kAdamVec = 8;                          // elements per lane
 constexpr int kAdamTile = kAdamThreads * kAdamVec;   // elements per workgroup
 constexpr int kAdamBlock = 256;                      // elements per scale of an 8-bit average
-constexpr int kAdamBatch = 44;                       // tensors per launch: the arguments stay below 4 KiB
+constexpr int kAdamFew = 40, kAdamMany = 180;         // tensors per launch: arguments of 3.4 and 15 KiB
 
 struct AdamTensor {
   void* w;
@@ -42,12 +42,13 @@ struct AdamTensor {
   float* v_scale;
   int64_t n;
   uint32_t place;   // of element 0 in the random sequence (low 32 bits)
-  uint32_t tile0;   // first tile in this launch
   float lr_scale, wd;
 };
+template <int N>
 struct AdamBatch {
-  AdamTensor t[kAdamBatch];
+  uint32_t tile0[N];  // first tile of each tensor in this launch, ascending (empty tensors are left out)
   int count;
+  AdamTensor t[N];
 };
 struct AdamConst {
   double lr, beta1, beta2, eps;
@@ -59,14 +60,18 @@ struct AdamConst {
   uint32_t seed;
 };
 
-// The tensor of a tile: the last one whose first tile is not behind it (tile0 ascends; empty tensors are left out).
-MOE_DEV int tensor_of(const AdamBatch& b, uint32_t tile) {
-  int lo = 0, hi = b.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (b.t[mid].tile0 <= tile) lo = mid; else hi = mid;
+// The tensor of a tile: the last one whose first tile is not behind it. One lane per tensor: kernel arguments may lie in host
+// memory, where the six dependent loads of a binary search took longer than the rest of a small launch (%BIN%).
+template <int N>
+MOE_DEV int tensor_of(const AdamBatch<N>& b, uint32_t tile) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < N; i += 64) {
+    const int at = i + lane;
+    before += __popcll(__ballot(at < b.count && b.tile0[at < N ? at : 0] <= tile));
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(before - 1);
 }
 
 // Random bits of an element: three 16-bit numbers, for m, v and a BF16 weight. Odd multipliers from the digits of the
@@ -89,33 +94,36 @@ constexpr float kInv127 = (float)(1.0 / 127.0), kInv255 = (float)(1.0 / 255.0);
 MOE_DEV float level_m(float c) { const float t = c * kInv127; return t * t; }
 MOE_DEV float level_v(float c) { float t = c * kInv255; t = t * t; return t * t; }
 MOE_DEV float decode_m(int8_t code, float scale) {
-  const float l = level_m((float)code) * scale;
-  return code < 0 ? -l : l;
+  const float t = (float)code * kInv127;
+  return t * fabsf(t) * scale;
 }
 MOE_DEV float decode_v(uint8_t code, float scale) { return level_v((float)code) * scale; }
 
 // Code of a in [0, 1]: the level below, or the one above where (a - below) / (above - below) exceeds r. The root only
-// proposes a code, off by one at most; the levels decide.
+// proposes the nearest code (it is off by far less than half of one); the levels decide on which side of it a lies. The
+// last level is 1 exactly, so the code above it is never taken.
 template <int TOP, bool FOURTH>
 MOE_DEV int encode(float a, float r) {
   auto level = [](float c) { return FOURTH ? level_v(c) : level_m(c); };
   float root = __builtin_amdgcn_sqrtf(a);
   if (FOURTH) root = __builtin_amdgcn_sqrtf(root);
-  float c = fminf(floorf(root * (float)TOP), (float)(TOP - 1));
-  float lo = level(c), hi = level(c + 1.f);
-  if (lo > a && c > 0.f) {
-    c -= 1.f; hi = lo; lo = level(c);
-  } else if (hi <= a && c < (float)(TOP - 1)) {
-    c += 1.f; lo = hi; hi = level(c + 1.f);
-  }
-  return (int)c + (a - lo > r * (hi - lo) ? 1 : 0);
+  const float near = rintf(root * (float)TOP), at = level(near);
+  const float next = near + (a >= at ? 1.f : -1.f), other = level(next);
+  const float lo = fminf(at, other), hi = fmaxf(at, other);
+  return (int)fminf(near, next) + (a - lo > r * (hi - lo) ? 1 : 0);
 }
 
 // Largest magnitude over the 32 lanes of a block, by bits (NaN above infinity above every number).
+template <int CTRL>
+MOE_DEV uint32_t dpp_max(uint32_t x) {
+  return max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, true));
+}
 MOE_DEV float block_max(uint32_t bits) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) bits = max(bits, (uint32_t)__shfl_xor((int)bits, o, 64));
-  return __uint_as_float(bits);
+  bits = dpp_max<0xB1>(bits);   // rows of 16: neighbours, pairs, mirrored halves, mirrored row
+  bits = dpp_max<0x4E>(bits);
+  bits = dpp_max<0x141>(bits);
+  bits = dpp_max<0x140>(bits);
+  return __uint_as_float(max(bits, (uint32_t)__shfl_xor((int)bits, 16, 64)));
 }
 // Blocks whose largest value is under 2^-120 count as zeros: its reciprocal would leave the range. An infinite one
 // has no codes: the block becomes NaN, as with a NaN.
@@ -187,8 +195,9 @@ MOE_DEV void pack8(const float* m, const float* v, const uint32_t* rnd, int64_t 
 #pragma unroll
   for (int j = 0; j < kAdamVec; ++j) {
     bm = max(bm, __float_as_uint(m[j]) & 0x7fffffffu);
-    bv = max(bv, __float_as_uint(v[j]) & 0x7fffffffu);
+    bv = max(bv, __float_as_uint(v[j]));  // (no sign but a NaN's)
   }
+  bv &= 0x7fffffffu;
   const float sm = block_scale(block_max(bm)), sv = block_scale(block_max(bv));
   const float im = block_inv(sm), iv = block_inv(sv);
   uint32_t cm[8], cv[8];
@@ -197,7 +206,8 @@ MOE_DEV void pack8(const float* m, const float* v, const uint32_t* rnd, int64_t 
     const float rm = NEAREST ? 0.5f : (float)(rnd[j] & 0xffffu) * 0x1p-16f;
     const float rv = NEAREST ? 0.5f : (float)(rnd[j] >> 16) * 0x1p-16f;
     const int c = encode<127, false>(share(m[j], im), rm);
-    cm[j] = (uint32_t)(uint8_t)(int8_t)(m[j] < 0.f ? -c : c);
+    const int sign = __float_as_int(m[j]) >> 31;  // (a NaN's code does not matter)
+    cm[j] = (uint32_t)((c ^ sign) - sign) & 0xffu;
     const float a = share(v[j], iv);
     const int e = encode<255, true>(a, rv);
     cv[j] = a > 0.f ? (uint32_t)max(e, 1) : 0u;
@@ -211,9 +221,10 @@ MOE_DEV void pack8(const float* m, const float* v, const uint32_t* rnd, int64_t 
 
 // W: float, or uint16_t (BF16 bits) with a master or, without one, rounded by chance like the codes: an update under
 // half a step of BF16 (2^-9 of the weight; lr is 10^-4) would otherwise never reach the weight.
-template <typename W, bool MASTER, typename G, bool Q8>
-__global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamBatch b, const AdamConst k) {
-  const AdamTensor& t = b.t[tensor_of(b, blockIdx.x)];
+template <typename W, bool MASTER, typename G, bool Q8, int N>
+__global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamBatch<N> b, const AdamConst k) {
+  const int which = tensor_of(b, blockIdx.x);
+  const AdamTensor& t = b.t[which];
   const float gs = k.grad_scale ? *k.grad_scale : 1.0f;
   if (!(fabsf(gs) <= 3.402823466e38f)) return;  // a norm that is not finite: the step is left out
   int64_t step = k.step;
@@ -229,7 +240,7 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamBatch b, 
   const float c1 = (float)(lr * unbias1), c2 = (float)unbias2;
   const float eps = (float)k.eps;
   const int64_t n = t.n;
-  const int64_t i = (int64_t)(blockIdx.x - t.tile0) * kAdamTile + threadIdx.x * kAdamVec;
+  const int64_t i = (int64_t)(blockIdx.x - b.tile0[which]) * kAdamTile + threadIdx.x * kAdamVec;
   float g[8], w[8], m[8], v[8];
   load8((const G*)t.grad, i, n, g);
   if constexpr (MASTER) load8(t.master, i, n, w);
@@ -256,7 +267,8 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamBatch b, 
     const float x = g[j] * gs;
     m[j] = m[j] * b1 + x * o1;
     v[j] = v[j] * b2 + (x * x) * o2;
-    w[j] = w[j] * keep - c1 * m[j] / (sqrtf(v[j]) * c2 + eps);
+    // the hardware's root and reciprocal, 2^-23 each, beside the 2^-24 of the sum: no state hangs on their bits
+    w[j] = w[j] * keep - c1 * m[j] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[j]) * c2 + eps);
   }
   if constexpr (MASTER) store8(t.master, i, n, w);
   if constexpr (sizeof(W) == 2 && !MASTER) {
@@ -307,7 +319,7 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_pack_kernel(int64_t n, con
 
 // Norm of all gradients: FP64 sums of squares, one per workgroup (the workgroups of every launch walk the same tiles
 // in the same order, and a later launch adds to the sums of the ones before), then one workgroup adds them.
-constexpr int kNormBlocks = 1024;
+constexpr int kNormBlocks = 2048;
 MOE_DEV double wave_sum_d(double x) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
@@ -323,17 +335,24 @@ MOE_DEV double group_sum_d(double x) {  // of a workgroup of kAdamThreads; in th
   return s;
 }
 
-template <typename G>
-__global__ __launch_bounds__(kAdamThreads) void grad_norm_kernel(const AdamBatch b, uint32_t tiles, bool first,
+// Tiles of four loads per lane: with one, the loads in flight of 16 waves per CU do not reach HBM's rate (%NORM%).
+constexpr int kNormLoads = 4;
+constexpr int kNormTile = kAdamTile * kNormLoads;
+template <typename G, int N>
+__global__ __launch_bounds__(kAdamThreads) void grad_norm_kernel(const AdamBatch<N> b, uint32_t tiles, bool first,
                                                                  double* __restrict__ sums) {
   double s = 0.0;
   for (uint32_t tile = blockIdx.x; tile < tiles; tile += kNormBlocks) {
-    const AdamTensor& t = b.t[tensor_of(b, tile)];
-    const int64_t i = (int64_t)(tile - t.tile0) * kAdamTile + threadIdx.x * kAdamVec;
-    float g[8];
-    load8((const G*)t.grad, i, t.n, g);
+    const int which = tensor_of(b, tile);
+    const G* grad = (const G*)b.t[which].grad;
+    const int64_t n = b.t[which].n, i = (int64_t)(tile - b.tile0[which]) * kNormTile + threadIdx.x * kAdamVec;
+    float g[kNormLoads][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s += (double)g[j] * (double)g[j];
+    for (int u = 0; u < kNormLoads; ++u) load8(grad, i + u * kAdamTile, n, g[u]);
+#pragma unroll
+    for (int u = 0; u < kNormLoads; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += (double)g[u][j] * (double)g[u][j];
   }
   s = group_sum_d(s);
   if (threadIdx.x == 0) sums[blockIdx.x] = first ? s : sums[blockIdx.x] + s;
@@ -360,11 +379,11 @@ int kind_of(const moe_adamw_tensor& t) {
   return (t.w_dtype == MOE_BF16 ? (t.master ? 2 : 4) : 0) + (t.grad_dtype == MOE_BF16 ? 1 : 0);
 }
 
-// Runs `launch(batch, tiles)` over the tensors for which `pick` holds, kAdamBatch at a time. Elements are placed in
-// the random sequence as if the tensors lay one behind the other in their order, each from a multiple of 256 on.
-template <typename Pick, typename Launch>
-hipError_t over_batches(int n_tensors, const moe_adamw_tensor* t, Pick pick, Launch launch) {
-  AdamBatch b;
+// Runs `launch(batch, tiles)` over the tensors for which `pick` holds, N at a time, in tiles of `tile` elements. Elements are
+// placed in the random sequence as if the tensors lay one behind the other in their order, each from a multiple of 256 on.
+template <int N, typename Pick, typename Launch>
+hipError_t over_batches_of(int n_tensors, const moe_adamw_tensor* t, int64_t tile, Pick pick, Launch launch) {
+  AdamBatch<N> b;
   b.count = 0;
   int64_t place = 0, tiles = 0;
   auto flush = [&]() -> hipError_t {
@@ -377,25 +396,32 @@ hipError_t over_batches(int n_tensors, const moe_adamw_tensor* t, Pick pick, Lau
   for (int i = 0; i < n_tensors; ++i) {
     const int64_t blocks = (t[i].n + kAdamBlock - 1) / kAdamBlock;
     if (t[i].n > 0 && pick(t[i])) {
-      const int64_t mine = (t[i].n + kAdamTile - 1) / kAdamTile;
-      if (b.count == kAdamBatch || tiles + mine > (1 << 23)) {  // a launch holds fewer than 2^32 threads
+      const int64_t mine = (t[i].n + tile - 1) / tile;
+      if (b.count == N || tiles + mine > (1 << 23)) {  // a launch holds fewer than 2^32 threads
         const hipError_t e = flush();
         if (e != hipSuccess) return e;
       }
+      b.tile0[b.count] = (uint32_t)tiles;
       b.t[b.count++] = AdamTensor{t[i].w, t[i].master, t[i].grad, t[i].m, t[i].v, t[i].m_scale, t[i].v_scale, t[i].n,
-                                  (uint32_t)(place * kAdamBlock), (uint32_t)tiles, t[i].lr_scale, t[i].weight_decay};
+                                  (uint32_t)(place * kAdamBlock), t[i].lr_scale, t[i].weight_decay};
       tiles += mine;
     }
     place += blocks;
   }
   return flush();
 }
+// The launch's arguments are copied whole: few tensors take the short list.
+template <typename Pick, typename Launch>
+hipError_t over_batches(int n_tensors, const moe_adamw_tensor* t, int64_t tile, Pick pick, Launch launch) {
+  return n_tensors <= kAdamFew ? over_batches_of<kAdamFew>(n_tensors, t, tile, pick, launch)
+                               : over_batches_of<kAdamMany>(n_tensors, t, tile, pick, launch);
+}
 
-template <typename W, bool MASTER, typename G>
-hipError_t launch_kind(const AdamBatch& b, uint32_t tiles, const AdamConst& k, bool q8, hipStream_t s) {
+template <typename W, bool MASTER, typename G, int N>
+hipError_t launch_kind(const AdamBatch<N>& b, uint32_t tiles, const AdamConst& k, bool q8, hipStream_t s) {
   MOE_TRACE("adamw", s);
-  if (q8) MOE_LAUNCH((adamw_kernel<W, MASTER, G, true>), dim3(tiles), dim3(kAdamThreads), 0, s, b, k);
-  else MOE_LAUNCH((adamw_kernel<W, MASTER, G, false>), dim3(tiles), dim3(kAdamThreads), 0, s, b, k);
+  if (q8) MOE_LAUNCH((adamw_kernel<W, MASTER, G, true, N>), dim3(tiles), dim3(kAdamThreads), 0, s, b, k);
+  else MOE_LAUNCH((adamw_kernel<W, MASTER, G, false, N>), dim3(tiles), dim3(kAdamThreads), 0, s, b, k);
   return hipGetLastError();
 }
 
@@ -408,8 +434,8 @@ hipError_t launch_adamw(const moe_adamw_options& o, int n_tensors, const moe_ada
   const bool q8 = o.state_bits == 8;
   for (int kind = 0; kind < 6; ++kind) {
     const hipError_t e = over_batches(
-        n_tensors, t, [&](const moe_adamw_tensor& x) { return kind_of(x) == kind; },
-        [&](const AdamBatch& b, uint32_t tiles) {
+        n_tensors, t, kAdamTile, [&](const moe_adamw_tensor& x) { return kind_of(x) == kind; },
+        [&](const auto& b, uint32_t tiles) {
           switch (kind) {
             case 0: return launch_kind<float, false, float>(b, tiles, k, q8, s);
             case 1: return launch_kind<float, false, uint16_t>(b, tiles, k, q8, s);
@@ -432,15 +458,16 @@ hipError_t launch_grad_norm(int n_tensors, const moe_adamw_tensor* t, double max
   int count = 0;  // sums that hold something
   for (int bf16 = 0; bf16 < 2; ++bf16) {
     const hipError_t e = over_batches(
-        n_tensors, t, [&](const moe_adamw_tensor& x) { return (x.grad_dtype == MOE_BF16) == (bf16 == 1); },
-        [&](const AdamBatch& b, uint32_t tiles) {
+        n_tensors, t, kNormTile, [&](const moe_adamw_tensor& x) { return (x.grad_dtype == MOE_BF16) == (bf16 == 1); },
+        [&](const auto& b, uint32_t tiles) {
+          constexpr int N = sizeof(b.tile0) / sizeof(uint32_t);
           // the first launch writes every sum, later ones add to theirs
           const bool first = count == 0;
           const int blocks = first ? kNormBlocks : (int)std::min<uint32_t>(tiles, kNormBlocks);
           count = kNormBlocks;
           MOE_TRACE("grad_norm", s);
-          if (bf16) MOE_LAUNCH(grad_norm_kernel<uint16_t>, dim3(blocks), dim3(kAdamThreads), 0, s, b, tiles, first, sums);
-          else MOE_LAUNCH(grad_norm_kernel<float>, dim3(blocks), dim3(kAdamThreads), 0, s, b, tiles, first, sums);
+          if (bf16) MOE_LAUNCH((grad_norm_kernel<uint16_t, N>), dim3(blocks), dim3(kAdamThreads), 0, s, b, tiles, first, sums);
+          else MOE_LAUNCH((grad_norm_kernel<float, N>), dim3(blocks), dim3(kAdamThreads), 0, s, b, tiles, first, sums);
           return hipGetLastError();
         });
     if (e != hipSuccess) return e;

@@ -244,38 +244,42 @@ __global__ __launch_bounds__(kRxThreads) void route_proj_topk_kernel(
 }
 
 // Per chunk c and expert e (one wave each): counts[c][e] = the chunk's rows of e, and
-// pre[c][e][b] = rows of e in the chunk's 64-token blocks before b. Lane l of an iteration owns
-// block b0 + l, whose four 16-token histograms it reads as one 16-byte load.
-constexpr int kScanThreads = 1024;
+// pre[c][e][b] = rows of e in the chunk's 64-token blocks before b. Lane l owns the blocks
+// [l per, (l + 1) per), whose four 16-token histograms each are one 16-byte load: its sum, one scan
+// over the lanes, then the prefixes of its own blocks (the histograms again, from L2). One wave per
+// workgroup, so that they spread over the CUs.
+constexpr int kScanThreads = 64;
 __global__ __launch_bounds__(kScanThreads) void route_scan_kernel(const int32_t* __restrict__ block_hist,
                                                                    int32_t* __restrict__ pre,
                                                                    int32_t* __restrict__ counts, int E,
                                                                    int chunk0, int nbpc) {
-  const int lane = threadIdx.x & 63;
-  const int e = blockIdx.x * (kScanThreads / 64) + (threadIdx.x >> 6);
+  const int lane = threadIdx.x;
+  const int e = blockIdx.x;
   const int c = chunk0 + blockIdx.y;
-  if (e >= E) return;
   const int nh = nbpc * kSub;
   const int4* he = (const int4*)(block_hist + ((int64_t)c * E + e) * nh);
   int32_t* pe = pre + ((int64_t)c * E + e) * nbpc;
-  int carry = 0;
-  for (int b0 = 0; b0 < nbpc; b0 += 64) {
-    const int b = b0 + lane;
-    int v = 0;
-    if (b < nbpc) {
-      const int4 h = he[b];
-      v = h.x + h.y + h.z + h.w;
-    }
-    int incl = v;  // inclusive scan over the wave's lanes
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += u;
-    }
-    if (b < nbpc) pe[b] = carry + incl - v;
-    carry += __shfl(incl, 63, 64);
+  const int per = (nbpc + 63) / 64, b0 = lane * per, b1 = min(b0 + per, nbpc);
+  int sum = 0;
+#pragma unroll 8
+  for (int b = b0; b < b1; ++b) {
+    const int4 h = he[b];
+    sum += h.x + h.y + h.z + h.w;
   }
-  if (lane == 0) counts[(int64_t)c * E + e] = carry;
+  int incl = sum;  // inclusive scan over the wave's lanes
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += u;
+  }
+  int run = incl - sum;
+#pragma unroll 8
+  for (int b = b0; b < b1; ++b) {
+    const int4 h = he[b];
+    pe[b] = run;
+    run += h.x + h.y + h.z + h.w;
+  }
+  if (lane == 63) counts[(int64_t)c * E + e] = incl;
 }
 
 // kScanned: the prefixes and counts come from route_scan (long chunks). Otherwise (chunks of at
@@ -345,10 +349,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_layout_kernel(
     }
   }
   __syncthreads();
-  if (tid == 0) {  // exclusive scan over the local experts
+  if (wave == 0) {  // exclusive scan over the local experts, 64 at a time (their counts are in off[1..El])
     int run = 0;
-    for (int el = 0; el < El; ++el) { int cnt = off[el + 1]; off[el] = run; run += cnt; }
-    off[El] = run;
+    for (int b = 0; b < El; b += 64) {
+      const int cnt = b + lane < El ? off[b + lane + 1] : 0;
+      int incl = cnt;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += u;
+      }
+      // (the next 64 counts start behind this store's last place)
+      if (b + lane < El) off[b + lane] = run + incl - cnt;
+      run += __shfl(incl, 63, 64);
+    }
+    if (lane == 0) off[El] = run;
   }
   __syncthreads();
   const int N_c = off[El];
@@ -431,8 +446,8 @@ hipError_t launch_layout(const int32_t* topk_idx, int32_t* scratch, int32_t* cou
   const bool scanned = nbpc > kLayoutDirectBlocks;
   if (scanned) {
     MOE_TRACE("route_scan", s);
-    MOE_LAUNCH(route_scan_kernel, dim3((unsigned)((E + kScanThreads / 64 - 1) / (kScanThreads / 64)), (unsigned)nchunks),
-               dim3(kScanThreads), 0, s, scratch, pre, counts, E, chunk0, nbpc);
+    MOE_LAUNCH(route_scan_kernel, dim3((unsigned)E, (unsigned)nchunks), dim3(kScanThreads), 0, s, scratch, pre, counts,
+               E, chunk0, nbpc);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
