@@ -4,10 +4,10 @@
 //   w' = w (1 - lr wd) - lr / (1 - b1^t) * m' / (sqrt(v' / (1 - b2^t)) + eps)
 //
 // Bound by HBM: 28 bytes per parameter with a BF16 gradient, an FP32 master and FP32 averages (gradient 2, master 8,
-// averages 16, BF16 weight 2), 16 with averages in 8 bits. One lane owns 8 consecutive elements (16-byte loads of
-// BF16, 8-byte ones of codes), so 32 lanes own one block of 256 elements that share a scale, and its largest value
-// is a reduction inside half a wave. A workgroup takes tiles of 2048 elements; the tensors of a launch and the tile
-// each starts at are kernel arguments, so no table travels to the device.
+// averages 16, BF16 weight 2), 16 with averages in 8 bits. A wave owns a block of 256 elements that share a scale, four
+// in a row per lane, so that each FP32 access is 1 KiB without gaps and the block's largest value and scale are scalars;
+// two blocks per wave keep enough loads in flight. A workgroup takes tiles of 2048 elements; the tensors of a launch
+// and the tile each starts at are kernel arguments, so no table travels to the device.
 //
 // 8-bit averages. m = s c|c| / 127^2 and v = s c^4 / 255^4 with s the block's largest magnitude: the steps grow with
 // the value, so that entries 10^-4 (m) or 10^-9 (v) of the block's largest keep digits, which equal steps would lose.
@@ -27,10 +27,9 @@
 namespace moe {
 
 constexpr int kAdamThreads = 256;
-constexpr int kAdamVec = 8;                          // elements per lane
-constexpr int kAdamTile = kAdamThreads * kAdamVec;   // elements per workgroup
-constexpr int kAdamBlock = 256;                      // elements per scale of an 8-bit average
-constexpr int kAdamFew = 40, kAdamMany = 180;         // tensors per launch: arguments of 3.4 and 15 KiB
+constexpr int kAdamBlock = 256;                      // elements per scale of an 8-bit average: four per lane of a wave
+constexpr int kAdamTile = kAdamThreads / 64 * 2 * kAdamBlock;  // elements per workgroup
+constexpr int kAdamFew = 40, kAdamMany = 256;         // tensors per launch: arguments of 3.4 and 21 KiB
 
 struct AdamTensor {
   void* w;
@@ -113,17 +112,19 @@ MOE_DEV int encode(float a, float r) {
   return (int)fminf(near, next) + (a - lo > r * (hi - lo) ? 1 : 0);
 }
 
-// Largest magnitude over the 32 lanes of a block, by bits (NaN above infinity above every number).
+// Largest magnitude over the wave, by bits (NaN above infinity above every number): DPP within rows of 16, then scalars.
 template <int CTRL>
 MOE_DEV uint32_t dpp_max(uint32_t x) {
   return max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, true));
 }
 MOE_DEV float block_max(uint32_t bits) {
-  bits = dpp_max<0xB1>(bits);   // rows of 16: neighbours, pairs, mirrored halves, mirrored row
+  bits = dpp_max<0xB1>(bits);   // neighbours, pairs, mirrored halves, mirrored row
   bits = dpp_max<0x4E>(bits);
   bits = dpp_max<0x141>(bits);
   bits = dpp_max<0x140>(bits);
-  return __uint_as_float(max(bits, (uint32_t)__shfl_xor((int)bits, 16, 64)));
+  const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)bits, 0), (uint32_t)__builtin_amdgcn_readlane((int)bits, 16));
+  const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)bits, 32), (uint32_t)__builtin_amdgcn_readlane((int)bits, 48));
+  return __uint_as_float(max(a, b));
 }
 // Blocks whose largest value is under 2^-120 count as zeros: its reciprocal would leave the range. An infinite one
 // has no codes: the block becomes NaN, as with a NaN.
@@ -135,74 +136,75 @@ MOE_DEV float share(float x, float inv) {
   return fminf(fabsf(x) * inv, 1.0f);  // never NaN (infinity times 0 gives 1: the scale is NaN then)
 }
 
+// Four elements from i on, of a tensor of n: vectors inside, single ones at its end. Stores pass the L2 (nontemporal): what a
+// step writes is read again a step later at the earliest (%NT%).
 template <typename T>
-MOE_DEV void load8(const T* p, int64_t i, int64_t n, float* f) {
-  if (i + kAdamVec <= n) {
+MOE_DEV void load4(const T* p, int64_t i, int64_t n, float* f) {
+  if (i + 4 <= n) {
     if constexpr (sizeof(T) == 2) {
-      const u32x4 v = *(const u32x4*)(p + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) { f[2 * j] = bf2f(w[j] & 0xffff); f[2 * j + 1] = bf2f(w[j] >> 16); }
+      const uint2 v = *(const uint2*)(p + i);
+      f[0] = bf2f(v.x & 0xffff); f[1] = bf2f(v.x >> 16); f[2] = bf2f(v.y & 0xffff); f[3] = bf2f(v.y >> 16);
     } else {
-      const float4 a = *(const float4*)(p + i), b = *(const float4*)(p + i + 4);
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+      const float4 v = *(const float4*)(p + i);
+      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < kAdamVec; ++j) f[j] = i + j < n ? ld_elem(p + i + j) : 0.f;
+    for (int j = 0; j < 4; ++j) f[j] = i + j < n ? ld_elem(p + i + j) : 0.f;
   }
 }
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
 template <typename T>
-MOE_DEV void store8(T* p, int64_t i, int64_t n, const float* f) {
-  if (i + kAdamVec <= n) {
-    if constexpr (sizeof(T) == 2) {
-      *(u32x4*)(p + i) = u32x4{pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7])};
-    } else {
-      *(float4*)(p + i) = make_float4(f[0], f[1], f[2], f[3]);
-      *(float4*)(p + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
-    }
+MOE_DEV void store4(T* p, int64_t i, int64_t n, const float* f) {
+  if (i + 4 <= n) {
+    if constexpr (sizeof(T) == 2)
+      __builtin_nontemporal_store(u32x2_t{pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3])}, (u32x2_t*)(p + i));
+    else
+      __builtin_nontemporal_store(f32x4_t{f[0], f[1], f[2], f[3]}, (f32x4_t*)(p + i));
   } else {
 #pragma unroll
-    for (int j = 0; j < kAdamVec; ++j) if (i + j < n) st_elem(p + i + j, f[j]);
+    for (int j = 0; j < 4; ++j) if (i + j < n) st_elem(p + i + j, f[j]);
   }
 }
-MOE_DEV void load_codes(const uint8_t* p, int64_t i, int64_t n, uint8_t* c) {
-  if (i + kAdamVec <= n) {
-    const uint2 v = *(const uint2*)(p + i);
+MOE_DEV uint32_t load_codes(const uint8_t* p, int64_t i, int64_t n) {
+  if (i + 4 <= n) return *(const uint32_t*)(p + i);
+  uint32_t c = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = (uint8_t)((j < 4 ? v.x : v.y) >> (8 * (j & 3)));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = i + j < n ? p[i + j] : 0;
-  }
+  for (int j = 0; j < 4; ++j) if (i + j < n) c |= (uint32_t)p[i + j] << (8 * j);
+  return c;
 }
 MOE_DEV void store_codes(uint8_t* p, int64_t i, int64_t n, const uint32_t* c) {
-  if (i + kAdamVec <= n) {
-    *(uint2*)(p + i) = make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
-                                  c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
+  if (i + 4 <= n) {
+    __builtin_nontemporal_store(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24), (uint32_t*)(p + i));
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) if (i + j < n) p[i + j] = (uint8_t)c[j];
+    for (int j = 0; j < 4; ++j) if (i + j < n) p[i + j] = (uint8_t)c[j];
+  }
+}
+MOE_DEV void decode4(uint32_t mc, uint32_t vc, float ms, float vs, float* m, float* v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m[j] = decode_m((int8_t)(mc >> (8 * j)), ms);
+    v[j] = decode_v((uint8_t)(vc >> (8 * j)), vs);
   }
 }
 
-// Eight values of one lane to codes; the block's scale is stored by its first lane. half: r is 1/2 (nearest level).
+// A lane's four values to codes; a block's scales are stored by its first lane. NEAREST: r is 1/2.
 template <bool NEAREST>
-MOE_DEV void pack8(const float* m, const float* v, const uint32_t* rnd, int64_t i, int64_t n, uint8_t* mc, float* ms,
+MOE_DEV void pack4(const float* m, const float* v, const uint32_t* rnd, int64_t i, int64_t n, uint8_t* mc, float* ms,
                    uint8_t* vc, float* vs) {
   uint32_t bm = 0, bv = 0;
 #pragma unroll
-  for (int j = 0; j < kAdamVec; ++j) {
+  for (int j = 0; j < 4; ++j) {
     bm = max(bm, __float_as_uint(m[j]) & 0x7fffffffu);
     bv = max(bv, __float_as_uint(v[j]));  // (no sign but a NaN's)
   }
   bv &= 0x7fffffffu;
   const float sm = block_scale(block_max(bm)), sv = block_scale(block_max(bv));
   const float im = block_inv(sm), iv = block_inv(sv);
-  uint32_t cm[8], cv[8];
+  uint32_t cm[4], cv[4];
 #pragma unroll
-  for (int j = 0; j < kAdamVec; ++j) {
+  for (int j = 0; j < 4; ++j) {
     const float rm = NEAREST ? 0.5f : (float)(rnd[j] & 0xffffu) * 0x1p-16f;
     const float rv = NEAREST ? 0.5f : (float)(rnd[j] >> 16) * 0x1p-16f;
     const int c = encode<127, false>(share(m[j], im), rm);
@@ -217,6 +219,15 @@ MOE_DEV void pack8(const float* m, const float* v, const uint32_t* rnd, int64_t 
     store_codes(vc, i, n, cv);
     if (i % kAdamBlock == 0) { ms[i / kAdamBlock] = sm; vs[i / kAdamBlock] = sv; }
   }
+}
+// First element of a lane's four in block u (0, 1) of its wave, in a tile.
+MOE_DEV int64_t lane_element(int64_t tile, int u) {
+  return tile * kAdamTile + (int)(threadIdx.x >> 6) * 2 * kAdamBlock + u * kAdamBlock + (threadIdx.x & 63) * 4;
+}
+// The scale of a lane's block, the same for the wave; 0 behind the tensor's end.
+MOE_DEV float scale_of(const float* scale, int64_t i, int64_t n) {
+  const int64_t block = i / kAdamBlock;
+  return block * kAdamBlock < n ? scale[block] : 0.f;
 }
 
 // W: float, or uint16_t (BF16 bits) with a master or, without one, rounded by chance like the codes: an update under
@@ -239,51 +250,55 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamBatch<N> 
   const float keep = (float)(1.0 - lr * (double)t.wd);
   const float c1 = (float)(lr * unbias1), c2 = (float)unbias2;
   const float eps = (float)k.eps;
-  const int64_t n = t.n;
-  const int64_t i = (int64_t)(blockIdx.x - b.tile0[which]) * kAdamTile + threadIdx.x * kAdamVec;
-  float g[8], w[8], m[8], v[8];
-  load8((const G*)t.grad, i, n, g);
-  if constexpr (MASTER) load8(t.master, i, n, w);
-  else load8((const W*)t.w, i, n, w);
-  if constexpr (Q8) {
-    uint8_t cm[8], cv[8];
-    load_codes((const uint8_t*)t.m, i, n, cm);
-    load_codes((const uint8_t*)t.v, i, n, cv);
-    const float sm = i < n ? t.m_scale[i / kAdamBlock] : 0.f, sv = i < n ? t.v_scale[i / kAdamBlock] : 0.f;
+  const int64_t n = t.n, tile = blockIdx.x - b.tile0[which];
+  float g[2][4], w[2][4], m[2][4], v[2][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) { m[j] = decode_m((int8_t)cm[j], sm); v[j] = decode_v(cv[j], sv); }
-  } else {
-    load8((const float*)t.m, i, n, m);
-    load8((const float*)t.v, i, n, v);
-  }
-  uint32_t rnd[8];
-  if constexpr (Q8 || (sizeof(W) == 2 && !MASTER)) {
-    const uint32_t key = step_key(k.seed, step);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) rnd[j] = random_bits(t.place + (uint32_t)i + j, key);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float x = g[j] * gs;
-    m[j] = m[j] * b1 + x * o1;
-    v[j] = v[j] * b2 + (x * x) * o2;
-    // the hardware's root and reciprocal, 2^-23 each, beside the 2^-24 of the sum: no state hangs on their bits
-    w[j] = w[j] * keep - c1 * m[j] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[j]) * c2 + eps);
-  }
-  if constexpr (MASTER) store8(t.master, i, n, w);
-  if constexpr (sizeof(W) == 2 && !MASTER) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t u = __float_as_uint(w[j]);
-      if ((u & 0x7f800000u) != 0x7f800000u) w[j] = __uint_as_float((u + more_bits(rnd[j])) & 0xffff0000u);
+  for (int u = 0; u < 2; ++u) {
+    const int64_t i = lane_element(tile, u);
+    load4((const G*)t.grad, i, n, g[u]);
+    if constexpr (MASTER) load4(t.master, i, n, w[u]);
+    else load4((const W*)t.w, i, n, w[u]);
+    if constexpr (Q8) {
+      decode4(load_codes((const uint8_t*)t.m, i, n), load_codes((const uint8_t*)t.v, i, n), scale_of(t.m_scale, i, n),
+              scale_of(t.v_scale, i, n), m[u], v[u]);
+    } else {
+      load4((const float*)t.m, i, n, m[u]);
+      load4((const float*)t.v, i, n, v[u]);
     }
   }
-  store8((W*)t.w, i, n, w);
-  if constexpr (Q8) {
-    pack8<false>(m, v, rnd, i, n, (uint8_t*)t.m, t.m_scale, (uint8_t*)t.v, t.v_scale);
-  } else {
-    store8((float*)t.m, i, n, m);
-    store8((float*)t.v, i, n, v);
+  constexpr bool kChance = Q8 || (sizeof(W) == 2 && !MASTER);
+  const uint32_t key = kChance ? step_key(k.seed, step) : 0;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int64_t i = lane_element(tile, u);
+    uint32_t rnd[4];
+    if constexpr (kChance) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) rnd[j] = random_bits(t.place + (uint32_t)i + j, key);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = g[u][j] * gs;
+      m[u][j] = m[u][j] * b1 + x * o1;
+      v[u][j] = v[u][j] * b2 + (x * x) * o2;
+      // the hardware's root and reciprocal, 2^-23 each, beside the 2^-24 of the sum: no state hangs on their bits
+      w[u][j] = w[u][j] * keep - c1 * m[u][j] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[u][j]) * c2 + eps);
+    }
+    if constexpr (MASTER) store4(t.master, i, n, w[u]);
+    if constexpr (sizeof(W) == 2 && !MASTER) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = __float_as_uint(w[u][j]);
+        if ((x & 0x7f800000u) != 0x7f800000u) w[u][j] = __uint_as_float((x + more_bits(rnd[j])) & 0xffff0000u);
+      }
+    }
+    store4((W*)t.w, i, n, w[u]);
+    if constexpr (Q8) {
+      pack4<false>(m[u], v[u], rnd, i, n, (uint8_t*)t.m, t.m_scale, (uint8_t*)t.v, t.v_scale);
+    } else {
+      store4((float*)t.m, i, n, m[u]);
+      store4((float*)t.v, i, n, v[u]);
+    }
   }
 }
 
@@ -293,28 +308,28 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_unpack_kernel(int64_t n, c
                                                                     const uint8_t* __restrict__ vc,
                                                                     const float* __restrict__ vs,
                                                                     float* __restrict__ m, float* __restrict__ v) {
-  const int64_t i = (int64_t)blockIdx.x * kAdamTile + threadIdx.x * kAdamVec;
-  if (i >= n) return;
-  uint8_t cm[8], cv[8];
-  load_codes(mc, i, n, cm);
-  load_codes(vc, i, n, cv);
-  const float sm = ms[i / kAdamBlock], sv = vs[i / kAdamBlock];
-  float fm[8], fv[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) { fm[j] = decode_m((int8_t)cm[j], sm); fv[j] = decode_v(cv[j], sv); }
-  store8(m, i, n, fm);
-  store8(v, i, n, fv);
+  for (int u = 0; u < 2; ++u) {
+    const int64_t i = lane_element(blockIdx.x, u);
+    float fm[4], fv[4];
+    decode4(load_codes(mc, i, n), load_codes(vc, i, n), scale_of(ms, i, n), scale_of(vs, i, n), fm, fv);
+    store4(m, i, n, fm);
+    store4(v, i, n, fv);
+  }
 }
 
 __global__ __launch_bounds__(kAdamThreads) void adamw_pack_kernel(int64_t n, const float* __restrict__ m,
                                                                   const float* __restrict__ v, uint8_t* __restrict__ mc,
                                                                   float* __restrict__ ms, uint8_t* __restrict__ vc,
                                                                   float* __restrict__ vs) {
-  const int64_t i = (int64_t)blockIdx.x * kAdamTile + threadIdx.x * kAdamVec;
-  float fm[8], fv[8];
-  load8(m, i, n, fm);
-  load8(v, i, n, fv);
-  pack8<true>(fm, fv, nullptr, i, n, mc, ms, vc, vs);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int64_t i = lane_element(blockIdx.x, u);
+    float fm[4], fv[4];
+    load4(m, i, n, fm);
+    load4(v, i, n, fv);
+    pack4<true>(fm, fv, nullptr, i, n, mc, ms, vc, vs);
+  }
 }
 
 // Norm of all gradients: FP64 sums of squares, one per workgroup (the workgroups of every launch walk the same tiles
@@ -335,24 +350,43 @@ MOE_DEV double group_sum_d(double x) {  // of a workgroup of kAdamThreads; in th
   return s;
 }
 
-// Tiles of four loads per lane: with one, the loads in flight of 16 waves per CU do not reach HBM's rate (%NORM%).
+// Four 16-byte loads per lane and tile.
 constexpr int kNormLoads = 4;
-constexpr int kNormTile = kAdamTile * kNormLoads;
+template <typename G> constexpr int kNormVec = 16 / sizeof(G);
+template <typename G> constexpr int kNormTile = kAdamThreads * kNormVec<G> * kNormLoads;
 template <typename G, int N>
 __global__ __launch_bounds__(kAdamThreads) void grad_norm_kernel(const AdamBatch<N> b, uint32_t tiles, bool first,
                                                                  double* __restrict__ sums) {
+  constexpr int V = kNormVec<G>;
   double s = 0.0;
   for (uint32_t tile = blockIdx.x; tile < tiles; tile += kNormBlocks) {
     const int which = tensor_of(b, tile);
     const G* grad = (const G*)b.t[which].grad;
-    const int64_t n = b.t[which].n, i = (int64_t)(tile - b.tile0[which]) * kNormTile + threadIdx.x * kAdamVec;
-    float g[kNormLoads][8];
+    const int64_t n = b.t[which].n, i = (int64_t)(tile - b.tile0[which]) * kNormTile<G> + threadIdx.x * V;
+    float g[kNormLoads][V];
 #pragma unroll
-    for (int u = 0; u < kNormLoads; ++u) load8(grad, i + u * kAdamTile, n, g[u]);
+    for (int u = 0; u < kNormLoads; ++u) {
+      const int64_t at = i + u * (kAdamThreads * V);
+      if (at + V <= n) {
+        const u32x4 x = *(const u32x4*)(grad + at);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (V == 8) { g[u][2 * j] = bf2f(w[j] & 0xffff); g[u][2 * j + 1] = bf2f(w[j] >> 16); }
+          else g[u][j] = __uint_as_float(w[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) g[u][j] = at + j < n ? ld_elem(grad + at + j) : 0.f;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kNormLoads; ++u)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += (double)g[u][j] * (double)g[u][j];
+      for (int j = 0; j < V; ++j) {
+        if constexpr (V == 8) s += (double)(g[u][j] * g[u][j]);  // (a product of two BF16 values is exact in FP32)
+        else s = __builtin_fma((double)g[u][j], (double)g[u][j], s);
+      }
   }
   s = group_sum_d(s);
   if (threadIdx.x == 0) sums[blockIdx.x] = first ? s : sums[blockIdx.x] + s;
@@ -458,7 +492,7 @@ hipError_t launch_grad_norm(int n_tensors, const moe_adamw_tensor* t, double max
   int count = 0;  // sums that hold something
   for (int bf16 = 0; bf16 < 2; ++bf16) {
     const hipError_t e = over_batches(
-        n_tensors, t, kNormTile, [&](const moe_adamw_tensor& x) { return (x.grad_dtype == MOE_BF16) == (bf16 == 1); },
+        n_tensors, t, bf16 ? kNormTile<uint16_t> : kNormTile<float>, [&](const moe_adamw_tensor& x) { return (x.grad_dtype == MOE_BF16) == (bf16 == 1); },
         [&](const auto& b, uint32_t tiles) {
           constexpr int N = sizeof(b.tile0) / sizeof(uint32_t);
           // the first launch writes every sum, later ones add to theirs
