@@ -287,8 +287,11 @@ __global__ __launch_bounds__(kScanThreads) void route_scan_kernel(const int32_t*
 // local expert, and the blocks share the counts of all E experts between them: quadratic in the
 // chunk length but one launch fewer, which is the cheaper form for short chunks.
 constexpr int kLayoutDirectBlocks = 128;
+// After route_scan a block has nothing for more than the slots' waves to do: half the threads, so that a CU holds four
+// blocks (2048 blocks of 256 experts %LAYOUT% us).
+template <bool kScanned> constexpr int kLayoutThreads = kScanned ? kRouteThreads / 2 : kRouteThreads;
 template <bool kScanned>
-__global__ __launch_bounds__(kRouteThreads) void route_layout_kernel(
+__global__ __launch_bounds__(kLayoutThreads<kScanned>) void route_layout_kernel(
     const int32_t* __restrict__ topk_idx, const int32_t* __restrict__ block_hist, const int32_t* __restrict__ pre,
     int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ row_of,
     int32_t* __restrict__ src_token, int64_t T, int E, int e0, int El, int K, int n, int chunk0, int nbpc,
@@ -299,14 +302,15 @@ __global__ __launch_bounds__(kRouteThreads) void route_layout_kernel(
   int* off = base + El;
   uint64_t* mask = (uint64_t*)(((uintptr_t)(off + El + 1) + 7) & ~(uintptr_t)7);
 
+  constexpr int kThreads = kLayoutThreads<kScanned>;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int kWaves = kRouteThreads / 64;
+  constexpr int kWaves = kThreads / 64;
   const int c = chunk0 + blockIdx.x / nbpc;
   const int bl = blockIdx.x % nbpc;
   const ChunkRange cr = chunk_range(T, n, c);
 
   if constexpr (kScanned) {
-    for (int el = tid; el < El; el += kRouteThreads) {
+    for (int el = tid; el < El; el += kThreads) {
       base[el] = pre[((int64_t)c * E + e0 + el) * nbpc + bl];
       off[el + 1] = counts[(int64_t)c * E + e0 + el];
       mask[el] = 0;
@@ -332,7 +336,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_layout_kernel(
       total = wave_sum_int(total);
       if (lane == 0) { base[el] = before; off[el + 1] = total; }
     }
-    for (int el = tid; el < El; el += kRouteThreads) mask[el] = 0;
+    for (int el = tid; el < El; el += kThreads) mask[el] = 0;
     // per-expert counts over all E experts, spread over the chunk's blocks, one wave per expert
     for (int e = bl + nbpc * wave; e < E; e += nbpc * kWaves) {
       const int32_t* he = bh + (int64_t)e * nh;
@@ -368,7 +372,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_layout_kernel(
   __syncthreads();
   const int N_c = off[El];
   if (bl == 0)
-    for (int el = tid; el <= El; el += kRouteThreads) offsets[(int64_t)c * (El + 1) + el] = off[el];
+    for (int el = tid; el <= El; el += kThreads) offsets[(int64_t)c * (El + 1) + el] = off[el];
 
   // wave j < K owns slot j of the block's 64 tokens (lane = token)
   const int64_t t = cr.t0 + (int64_t)bl * kRouteBlock + lane;
@@ -393,7 +397,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_layout_kernel(
     row_of[t * K + j] = row;
   }
   // rows N_c..P_c-1 of this chunk's region hold no token
-  for (int64_t r = N_c + (int64_t)bl * kRouteThreads + tid; r < P_c; r += (int64_t)nbpc * kRouteThreads)
+  for (int64_t r = N_c + (int64_t)bl * kThreads + tid; r < P_c; r += (int64_t)nbpc * kThreads)
     src_token[(int64_t)c * P_c + r] = -1;
 }
 
@@ -454,10 +458,10 @@ hipError_t launch_layout(const int32_t* topk_idx, int32_t* scratch, int32_t* cou
   size_t sm2 = (size_t)El * 4 + (size_t)(El + 1) * 4 + 8 + (size_t)El * 8;
   MOE_TRACE("route_layout", s);
   if (scanned)
-    MOE_LAUNCH(route_layout_kernel<true>, dim3(nbpc * nchunks), dim3(kRouteThreads), sm2, s, topk_idx, scratch,
+    MOE_LAUNCH(route_layout_kernel<true>, dim3(nbpc * nchunks), dim3(kLayoutThreads<true>), sm2, s, topk_idx, scratch,
                pre, counts, offsets, row_of, src_token, T, E, e0, El, K, n, chunk0, nbpc, P_c);
   else
-    MOE_LAUNCH(route_layout_kernel<false>, dim3(nbpc * nchunks), dim3(kRouteThreads), sm2, s, topk_idx, scratch,
+    MOE_LAUNCH(route_layout_kernel<false>, dim3(nbpc * nchunks), dim3(kLayoutThreads<false>), sm2, s, topk_idx, scratch,
                pre, counts, offsets, row_of, src_token, T, E, e0, El, K, n, chunk0, nbpc, P_c);
   return hipGetLastError();
 }

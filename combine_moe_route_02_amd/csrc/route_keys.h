@@ -20,6 +20,11 @@ MOE_DEV uint32_t logit_key(float x) {
   const uint32_t u = __float_as_uint(x);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+// The same without the two exceptions.
+MOE_DEV uint32_t ordered(float x) {
+  const int u = __float_as_int(x);
+  return (uint32_t)(u ^ ((u >> 31) | (int)0x80000000u));
+}
 MOE_DEV float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }

@@ -7,15 +7,17 @@
 //
 // A choice hangs on the last bit of c, so c is defined by FP64 scores, rounded once: two programs, or two kernels,
 // that follow the formula choose the same experts. FP64 exponentials for every logit would take several times the time of
-// reading it, though, and nearly every choice is clear without them: choose() first selects by FP32 scores whose error has a
-// bound, and only a wave with a token where two neighbours in the order (or the last chosen group and the first one left
-// out) are nearer than that bound goes through choose_exact(). (62 of 131072 tokens with 256 experts in 8 groups.)
+// reading it, though, and nearly every choice is clear without them: choose() selects by FP32 scores whose error has a
+// bound. Where two neighbours in the order are nearer than that (one token of a thousand), their exact c puts the chosen
+// experts and the first one left out in order; where two groups are (one of 25000), or several scores in a row, or two are
+// one, the token's wave goes through choose_exact(). (All of these together took 17 of 86 us at 131072 tokens of 256
+// experts while all went there: a wave alone on code that no one else runs waits for its instructions.)
 //
-// 16 lanes hold a token's row in registers (4 tokens per wave, float4 loads). Per lane the row's share becomes a sorted
-// list of four and the fifth largest; k + 1 rounds of a maximum over the 16 lanes (DPP) pop the chosen experts and the
-// first one left out (a token with five of them in one lane, one of 5000, goes through choose_exact() too). The lists are
-// made of doubles, a score's FP32 bits above the expert's index: they order as the scores do, and a compare-exchange is one
-// v_max_f64 and one v_min_f64 (64-bit integer keys take five instructions).
+// 16 lanes hold a token's row in registers (4 tokens per wave, float4 loads), and arithmetic bounds the kernel, not HBM. Per
+// lane the row's share becomes a sorted list of its five largest: a score's FP32 bits, the last few of which give way to the
+// number of the element, so that one insertion is five medians of three and no index travels beside the score. k + 2 rounds
+// of a maximum over the 16 lanes (DPP) pop the chosen experts and the first two left out. Where a lane's five are used up
+// (one token of 5000), the lists are made again from what is left.
 #include "common.h"
 #include "launch.h"
 #include "route_keys.h"
@@ -82,10 +84,37 @@ MOE_DEV void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefr
 MOE_DEV int group_of(int e, uint32_t magic) { return (int)(((uint32_t)e * magic) >> 20); }
 MOE_DEV uint32_t group_magic(int gs) { return (1u << 20) / (uint32_t)gs + 1; }
 
-// (a median of three is a maximum or minimum that leaves its operands as they are: fmaxf first makes them canonical)
+// A median of three is also a maximum, one that leaves its operands as they are (fmaxf first makes them canonical; the
+// compiler takes a median with the constant +inf for fmaxf).
+MOE_DEV float plain_max(float a, float b) {
+  float high = __builtin_huge_valf();
+  asm("" : "+v"(high));
+  return __builtin_amdgcn_fmed3f(a, b, high);
+}
 MOE_DEV void two_largest(float& b0, float& b1, float x) {
   b1 = __builtin_amdgcn_fmed3f(b0, b1, x);
-  b0 = __builtin_amdgcn_fmed3f(b0, x, __builtin_huge_valf());
+  b0 = plain_max(b0, x);
+}
+
+// Softmax: the row's largest logit and FP64 sum of exponentials (0 where no logit is above -inf).
+MOE_DEV double exact_sum(const float* row, int E, int q, float& m) {
+  const float ninf = -__builtin_huge_valf();
+  m = ninf;
+  if (row)
+#pragma unroll 4
+    for (int e = q; e < E; e += kGroup) m = fmaxf(m, clean_logit(row[e]));
+  m = row_max(m);
+  double den = 0.0;
+  if (row && m > ninf)
+#pragma unroll 2
+    for (int e = q; e < E; e += kGroup) den += exp((double)clean_logit(row[e]) - (double)m);
+  return row_sum_d(den);
+}
+MOE_DEV float exact_c(float logit, const float* bias, int e, bool softmax, float m, double den) {
+  const double l = clean_logit(logit);
+  const double s = !softmax ? 1.0 / (1.0 + exp(-l)) : den > 0.0 ? exp(l - (double)m) / den : 0.0;
+  const float x = (float)(bias ? s + (double)bias[e] : s);
+  return x != x ? -__builtin_huge_valf() : x;
 }
 
 // The eligible groups of a token, one bit each, from the c of its experts in LDS. P lanes share a group (16 of them with
@@ -139,11 +168,11 @@ MOE_DEV uint64_t eligible_groups(const float* c, int gs, int q, const ScoreArgs&
     const int g = first + per_pass * u;
     if (per_pass * u >= a.groups) continue;
     int beaten = 0;
-    const uint32_t own = logit_key(mine[u]);
+    const uint32_t own = EXACT ? logit_key(mine[u]) : ordered(mine[u]);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       if (per_pass * w >= a.groups) continue;
-      const uint32_t key = logit_key(mine[w]);
+      const uint32_t key = EXACT ? logit_key(mine[w]) : ordered(mine[w]);
       const int count = min(per_pass, a.groups - per_pass * w);
       for (int j = 0; j < count; ++j) {
         const uint32_t other = (uint32_t)__shfl((int)key, j << lp, kGroup);
@@ -165,38 +194,41 @@ MOE_DEV uint64_t eligible_groups(const float* c, int gs, int q, const ScoreArgs&
   if constexpr (!EXACT) {
     least = row_min(least);
     most = row_max(most);
-    near |= !(least - most > margin * row_max(size)) || __popc(lo) + __popc(hi) != a.keep;
+    near = !(least - most > margin * row_max(size)) || __popc(lo) + __popc(hi) != a.keep;
   }
   return ((uint64_t)hi << 32) | lo;
 }
 
+// Slots in the order of their experts' exact c, ties to the lower expert: lane j < n brings slot j's expert, and takes the
+// one whose place j is. Every lane of the wave calls.
+MOE_DEV int order_exact(const float* row, const float* bias, uint32_t* slots, int id, int E, int n, int q, const ScoreArgs& a) {
+  float m = 0.f;
+  const double den = a.softmax ? exact_sum(row, E, q, m) : 0.0;
+  const bool live = row && q < n;
+  const uint32_t key = live ? logit_key(exact_c(row[id], bias, id, a.softmax, m, den)) : 0u;
+  int place = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint32_t other = (uint32_t)__shfl((int)key, j, kGroup);
+    const int other_id = __shfl(id, j, kGroup);
+    place += other > key || (other == key && other_id < id);
+  }
+  wave_lds_fence();
+  if (live) slots[place] = (uint32_t)id;
+  wave_lds_fence();
+  return live ? (int)slots[q] : 0;
+}
+
 // The choice by exact c: lane j < k returns slot j's expert. c: the token's row in LDS [E]. Every lane of the wave calls.
 MOE_DEV int choose_exact(const float* row, const float* bias, float* c, int E, int K, int q, const ScoreArgs& a) {
-  const float ninf = -__builtin_huge_valf(), taken = __builtin_nanf("");
-  float m = ninf;
-  double den = 1.0;
-  if (a.softmax) {
-    if (row)
-#pragma unroll 4
-      for (int e = q; e < E; e += kGroup) m = fmaxf(m, clean_logit(row[e]));
-    m = row_max(m);
-    den = 0.0;
-    if (row && m > ninf)
-#pragma unroll 4
-      for (int e = q; e < E; e += kGroup) den += exp((double)clean_logit(row[e]) - (double)m);
-    den = row_sum_d(den);
-  }
-#pragma unroll 4
-  for (int e = q; e < E; e += kGroup) {
-    const double l = row ? clean_logit(row[e]) : 0.f;
-    const double s = !a.softmax ? 1.0 / (1.0 + exp(-l)) : den > 0.0 ? exp(l - (double)m) / den : 0.0;
-    const float x = (float)(bias ? s + (double)bias[e] : s);
-    c[e] = x != x ? ninf : x;
-  }
+  const float taken = __builtin_nanf("");
+  float m = 0.f;
+  const double den = a.softmax ? exact_sum(row, E, q, m) : 0.0;
+#pragma unroll 2
+  for (int e = q; e < E; e += kGroup) c[e] = exact_c(row ? row[e] : 0.f, bias, e, a.softmax, m, den);
   wave_lds_fence();
   const int gs = E / a.groups;
   if (a.keep < a.groups) {
-    bool unused = false;
+    bool unused;
     const uint64_t open = eligible_groups<true>(c, gs, q, a, 0.f, unused);
     wave_lds_fence();
     const uint32_t magic = group_magic(gs);
@@ -207,7 +239,7 @@ MOE_DEV int choose_exact(const float* row, const float* bias, float* c, int E, i
   for (int s = 0; s < K; ++s) {
     // the lane's largest, the first of equal ones; then the row's, and of equal ones the lowest expert
     uint32_t top = 0, at = 0;
-#pragma unroll 8
+#pragma unroll 4
     for (int e = q; e < E; e += kGroup) {
       const float x = c[e];
       const uint32_t key = x == x ? logit_key(x) : 0;
@@ -222,24 +254,8 @@ MOE_DEV int choose_exact(const float* row, const float* bias, float* c, int E, i
   return id;
 }
 
-constexpr int kTopList = 4;
-constexpr int kSelInts = 2 * kGroup;  // LDS of a token's slots: score and expert, one lane each
-
-// Keys of the lists: hi the bits of a score (finite: never a NaN or infinity as a double), lo the expert.
-MOE_DEV double list_key(float score, int e) { return __hiloint2double(__float_as_int(score), e); }
-MOE_DEV double key_max(double a, double b) { double r; asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b)); return r; }
-MOE_DEV double key_min(double a, double b) { double r; asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b)); return r; }
-MOE_DEV void key_swap(double& a, double& b) { const double t = key_max(a, b); b = key_min(a, b); a = t; }
-MOE_DEV void sort4(double (&l)[4]) {
-  key_swap(l[0], l[1]); key_swap(l[2], l[3]); key_swap(l[0], l[2]); key_swap(l[1], l[3]); key_swap(l[1], l[2]);
-}
-// l and f sorted: l becomes the four largest of both, sorted, rest the larger of itself and the others.
-MOE_DEV void merge4(double (&l)[4], double (&f)[4], double& rest) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) key_swap(l[i], f[3 - i]);
-  rest = key_max(rest, key_max(key_max(f[0], f[1]), key_max(f[2], f[3])));
-  key_swap(l[0], l[2]); key_swap(l[1], l[3]); key_swap(l[0], l[1]); key_swap(l[2], l[3]);
-}
+constexpr int kTopList = 5;           // a lane's list
+constexpr int kSelInts = 2 * kGroup;  // LDS of a token's slots: key and lane, one slot per lane
 
 // Experts of a lane's elements: VEC: 64 (i / 4) + 4 q + i % 4 (float4 loads, E a multiple of 4), else 16 i + q.
 template <bool VEC> MOE_DEV int expert_of(int i, int q) { return VEC ? 64 * (i / 4) + 4 * q + i % 4 : kGroup * i + q; }
@@ -266,13 +282,15 @@ MOE_DEV void load_row(const float* row, int E, int q, float none, float (&x)[NE]
 // itself by |c|: 3.72 + 2 |c| each, so that sums further apart than 2 (3.72 + 2 |c|) < 16 max(1, |c|) are in order.
 // Softmax: the differences and products below an exponential move it by 2.2 x e^-x <= 0.82, its ulp by 2, relative to a
 // largest score p = 1 / sum; the sum (in FP64) by its terms' 3, the reciprocal and the product by 3: 9 p + 2 |c| each.
-// Group sums: twice that and their own rounding. Ties and sums within the margin go to choose_exact.
+// The bits that hold an element's number add 2 NE units of a sum's
+// size. Ties and sums within the margin go to choose_exact.
 // m, inv: softmax: the row's largest logit and 1 / the sum of exponentials (0 where no logit is above -inf).
 template <int NE, bool VEC>
 MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slots, int E, int K, int q,
                    const ScoreArgs& a, float& m, float& inv) {
   const float ninf = -__builtin_huge_valf();
   constexpr float kLog2e = 1.44269504088896341f, kUnit = 0x1p-24f;
+  constexpr float kLeast = 3e38f, none = -kMaxFloat;  // the lowest score, and no expert
   float x[NE];
   load_row<NE, VEC>(row, E, q, ninf, x);
   const float margin = (a.softmax ? 20.f : 16.f) * kUnit;  // relative to the sums and, softmax, p, or 1
@@ -303,10 +321,9 @@ MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slot
     for (int i = 0; i < NE; ++i) x[i] += b[i];
   }
 #pragma unroll
-  for (int i = 0; i < NE; ++i) x[i] = __builtin_amdgcn_fmed3f(x[i], -kMaxFloat, kMaxFloat);  // NaN: the lowest
+  for (int i = 0; i < NE; ++i) x[i] = __builtin_amdgcn_fmed3f(x[i], -kLeast, kMaxFloat);  // NaN: the lowest
   bool bad = false;
   const int gs = E / a.groups;
-  const float none = __int_as_float(0xffc00000);  // no expert: its bits order below every score's
   if (a.keep < a.groups) {
 #pragma unroll
     for (int i = 0; i < NE; i += VEC ? 4 : 1) {
@@ -322,7 +339,8 @@ MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slot
     if (VEC && (gs & 3) == 0) {  // the four of a vector share a group
 #pragma unroll
       for (int i = 0; i < NE; i += 4) {
-        const bool ok = (open >> (group_of(expert_of<VEC>(i, q), magic) & 63)) & 1;
+        const int g = group_of(expert_of<VEC>(i, q), magic);
+        const bool ok = ((a.groups <= 32 || g < 32 ? (uint32_t)open : (uint32_t)(open >> 32)) >> (g & 31)) & 1;
 #pragma unroll
         for (int j = i; j < i + 4; ++j) x[j] = ok ? x[j] : none;
       }
@@ -336,58 +354,74 @@ MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slot
 #pragma unroll
     for (int i = 0; i < NE; ++i) x[i] = expert_of<VEC>(i, q) < E ? x[i] : none;
   }
-  double l[kTopList], rest = list_key(none, 0);
-#pragma unroll
-  for (int i = 0; i < NE; i += 4) {
-    double f[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = list_key(x[i + j], expert_of<VEC>(i + j, q));
-    sort4(f);
-    if (i == 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) l[j] = f[j];
-    } else {
-      merge4(l, f, rest);
-    }
-  }
-  // The rounds: 32-bit keys that order as the scores, kUnknown after a lane's fifth where it had more. As many rounds as
-  // there are slots, and one more for the first expert left out.
+  constexpr uint32_t kNumber = NE - 1;  // the bits that hold an element's number
   constexpr uint32_t kUnknown = 0xffffffffu;
-  uint32_t key[kTopList + 1];
-  int ex[kTopList + 1];
+  uint32_t key[kTopList];
+  // The list: the five largest, sorted, as keys that order as the scores. again: of those below `limit`.
+  auto make_list = [&](bool again, float limit) {
+    float l[kTopList];
 #pragma unroll
-  for (int j = 0; j <= kTopList; ++j) {
-    const double v = j < kTopList ? l[j] : rest;
-    const int u = __double2hiint(v);
-    key[j] = (uint32_t)(u ^ ((u >> 31) | (int)0x80000000u));
-    ex[j] = __double2loint(v);
-  }
-  const int rounds = min(K + 1, a.keep * gs);
-  uint32_t pops = 0;
-  for (int s = 0; s < rounds; ++s) {
-    const uint32_t best = row_max_u(key[0]);
-    if (key[0] == best) {
-      *(uint2*)(slots + 2 * s) = make_uint2(best, (uint32_t)ex[0]);
-      ++pops;
+    for (int j = 0; j < kTopList; ++j) l[j] = none;
 #pragma unroll
-      for (int j = 0; j < kTopList; ++j) { key[j] = key[j + 1]; ex[j] = ex[j + 1]; }
-      key[kTopList] = NE > kTopList + 1 ? kUnknown : 0u;
+    for (int i = 0; i < NE; ++i) {
+      float v = __uint_as_float((__float_as_uint(x[i]) & ~kNumber) | i);
+      if (again) v = v < limit ? v : none;
+#pragma unroll
+      for (int j = kTopList - 1; j > 0; --j) l[j] = __builtin_amdgcn_fmed3f(l[j - 1], l[j], v);
+      l[0] = plain_max(l[0], v);
+    }
+#pragma unroll
+    for (int j = 0; j < kTopList; ++j) key[j] = ordered(l[j]);
+  };
+  // Rounds s0 .. rounds - 1. After a lane's fifth its next is unknown where it had more.
+  const int rounds = min(K + 2, a.keep * gs);  // the slots, and the first two experts left out where there are
+  auto play = [&](int s0) {
+    uint32_t pops = 0;
+    for (int s = s0; s < rounds; ++s) {
+      const uint32_t best = row_max_u(key[0]);
+      if (key[0] == best) {
+        *(uint2*)(slots + 2 * s) = make_uint2(best, (uint32_t)q);
+        ++pops;
+#pragma unroll
+        for (int j = 0; j + 1 < kTopList; ++j) key[j] = key[j + 1];
+        key[kTopList - 1] = NE > kTopList ? kUnknown : 0u;
+      }
+    }
+    wave_lds_fence();
+    // two lanes with one key popped both: more pops than rounds
+    return row_sum_u(pops) != (uint32_t)(rounds - s0);
+  };
+  make_list(false, 0.f);
+  bool twins = play(0);
+  uint2 mine = *(const uint2*)(slots + 2 * q);
+  if constexpr (NE > kTopList) {
+    while (__any(row && q < rounds && mine.x == kUnknown)) {
+      // from the first unknown slot of the wave's tokens on, with what each lane has left below its last
+      const uint64_t unknown = __ballot(row && q < rounds && mine.x == kUnknown);
+      int s0 = rounds;
+      for (uint64_t u = unknown; u; u &= u - 1) s0 = min(s0, (int)(__ffsll((unsigned long long)u) - 1) & (kGroup - 1));
+      uint32_t last = kUnknown;
+      for (int s = 0; s < s0; ++s) last = slots[2 * s + 1] == (uint32_t)q ? slots[2 * s] : last;
+      make_list(true, last == kUnknown ? __builtin_huge_valf() : key_logit(last));
+      wave_lds_fence();
+      twins |= play(s0);
+      mine = *(const uint2*)(slots + 2 * q);
     }
   }
-  wave_lds_fence();
-  const uint2 mine = *(const uint2*)(slots + 2 * q);
-  if (q < rounds) {
-    bad |= mine.x == kUnknown;
-    if (q + 1 < rounds) {  // whether slot q and the next are clear of each other
-      const float u = key_logit(mine.x), v = key_logit(slots[2 * q + 2]);
-      const float size = fmaxf(fabsf(u), fabsf(v));
-      bad |= !(u - v > margin * (a.softmax ? inv + size : fmaxf(1.f, size)) + 0x1p-100f);
-    }
+  const uint32_t bits = mine.x >> 31 ? mine.x : ~mine.x;  // (of a negative score the key holds the complement)
+  const int i = (int)(bits & kNumber);
+  int id = VEC ? 64 * (i / 4) + 4 * (int)mine.y + i % 4 : kGroup * i + (int)mine.y;
+  bool near = false;
+  if (q + 1 < rounds) {  // whether slot q and the next are clear of each other
+    const float u = key_logit(mine.x), v = key_logit(slots[2 * q + 2]);
+    const float size = fmaxf(fabsf(u), fabsf(v));
+    near = !(u - v > margin * (a.softmax ? inv + size : fmaxf(1.f, size)) + 2 * NE * kUnit * size + 0x1p-100f);
   }
-  // two lanes with one key popped both: more pops than rounds
-  bad |= row_sum_u(pops) != (uint32_t)rounds;
-  if (__any(row && bad)) return choose_exact(row, bias, c, E, K, q, a);
-  return (int)mine.y;
+  // The last one chosen near the first left out is settled between them; near the second left out too, it is not.
+  const uint32_t nears = (uint32_t)(__ballot(near) >> (threadIdx.x & 48)) & 0xffffu;
+  if (__any(row && (bad || twins || ((nears >> (K - 1)) & 3) == 3))) return choose_exact(row, bias, c, E, K, q, a);
+  if (__any(row && (nears & ((1u << K) - 1)))) id = order_exact(row, bias, slots, id, E, min(K + 1, rounds), q, a);
+  return id;
 }
 
 // Gate of lane j < k (live) for its expert; m and inv as choose() leaves them.
@@ -659,7 +693,10 @@ hipError_t launch_route_scores(const moe_router_scores& r, const float* logits, 
   const int blocks = route_blocks_per_chunk(T, n);
   const int64_t tc = (T + n - 1) / n;
   const ScoreArgs a = score_args(r);
-  const bool wide = E <= 256;  // 64 rows of c, and two workgroups in a CU
+  // 64 tokens per workgroup keep the histograms few and let a chunk of up to 64 tokens be one workgroup; 16 where 64 rows
+  // of c would leave a CU one workgroup, and where there are too few tokens for every CU: their waves, one per SIMD,
+  // then finish earlier (%SMALL%)
+  const bool wide = E <= 256 && tc > kHistTok && (tc <= 64 || T > 8192);
   const int tok = wide ? 64 : kHistTok;
   const int nbpc = wide ? blocks : blocks * kSub;
   const bool whole = tc <= tok;  // a chunk is one workgroup
@@ -678,7 +715,7 @@ hipError_t launch_route_scores(const moe_router_scores& r, const float* logits, 
                    scratch, T, tc, E, K, chunk0, whole ? 1 : nbpc, a, o);                                        \
     }
     const bool vec = vector_rows(E, logits, bias);
-    MOE_NE(E, vec, if constexpr (NE <= 16) { MOE_RS(1024) } else { MOE_RS(256) });
+    MOE_NE(E, vec, if constexpr (NE <= 16) { if (wide) MOE_RS(1024) else MOE_RS(256) } else { MOE_RS(256) });
 #undef MOE_RS
   }
   if (err == hipSuccess) err = hipGetLastError();
