@@ -11,7 +11,7 @@
 // bound. Where two neighbours in the order are nearer than that (one token of a thousand), their exact c puts the chosen
 // experts and the first one left out in order; where two groups are (one of 25000), or several scores in a row, or two are
 // one, the token's wave goes through choose_exact(). (All of these together took 17 of 86 us at 131072 tokens of 256
-// experts while all went there: a wave alone on code that no one else runs waits for its instructions.)
+// experts while all went there and took every expert's exact c: one such wave late in the launch holds up its end.)
 //
 // 16 lanes hold a token's row in registers (4 tokens per wave, float4 loads), and arithmetic bounds the kernel, not HBM. Per
 // lane the row's share becomes a sorted list of its five largest: a score's FP32 bits, the last few of which give way to the
@@ -25,7 +25,7 @@
 
 namespace moe {
 
-constexpr float kMaxFloat = 3.402823466e38f;
+constexpr float kMaxFloat = 3.402823466e38f, kLeast = -3e38f;
 // NaN counts as -inf, +inf as the largest finite value: a median of three with a NaN is the smallest of the others. (The
 // compiler takes a median with the constant -inf for a minimum, which a NaN would leave at the other constant.)
 MOE_DEV float clean_logit(float x) {
@@ -122,13 +122,15 @@ MOE_DEV float exact_c(float logit, const float* bias, int e, bool softmax, float
 // different places of their groups, which lie a multiple of their size apart: the same bank. near: whether the last eligible
 // and the first other group are within `margin` (relative to 1 or the largest c that any group adds), where c is not
 // exact; two groups with one sum are near.
+// cut: what no c that a group adds is below.
 template <bool EXACT>
-MOE_DEV uint64_t eligible_groups(const float* c, int gs, int q, const ScoreArgs& a, float margin, bool& near) {
+MOE_DEV uint64_t eligible_groups(const float* c, int gs, int q, const ScoreArgs& a, float margin, bool& near, float& cut) {
   const float ninf = -__builtin_huge_valf();
   int lp = 0;  // log2 P: whole float4 per lane, and no more lanes than there are for the groups
   while (lp < 4 && (a.groups << (lp + 1)) <= kGroup && gs % (8 << lp) == 0) ++lp;
   const int P = 1 << lp, part = q & (P - 1), first = q >> lp, per_pass = kGroup >> lp;
   float mine[4], size = 1.f;
+  cut = __builtin_huge_valf();
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int g = first + per_pass * u;
@@ -159,6 +161,7 @@ MOE_DEV uint64_t eligible_groups(const float* c, int gs, int q, const ScoreArgs&
       const bool two = a.top == 2 && gs > 1;
       mine[u] = two ? b0 + b1 : b0;
       size = fmaxf(size, two ? fmaxf(fabsf(b0), fabsf(b1)) : fabsf(b0));
+      cut = fminf(cut, two ? b1 : b0);
     }
   }
   uint32_t lo = 0, hi = 0;
@@ -194,7 +197,9 @@ MOE_DEV uint64_t eligible_groups(const float* c, int gs, int q, const ScoreArgs&
   if constexpr (!EXACT) {
     least = row_min(least);
     most = row_max(most);
-    near = !(least - most > margin * row_max(size)) || __popc(lo) + __popc(hi) != a.keep;
+    size = row_max(size);
+    near = !(least - most > margin * size) || __popc(lo) + __popc(hi) != a.keep;
+    cut = row_min(cut) - margin * size;
   }
   return ((uint64_t)hi << 32) | lo;
 }
@@ -218,38 +223,54 @@ MOE_DEV int order_exact(const float* row, const float* bias, uint32_t* slots, in
   return live ? (int)slots[q] : 0;
 }
 
-// The choice by exact c: lane j < k returns slot j's expert. c: the token's row in LDS [E]. Every lane of the wave calls.
-MOE_DEV int choose_exact(const float* row, const float* bias, float* c, int E, int K, int q, const ScoreArgs& a) {
-  const float taken = __builtin_nanf("");
+// The choice where the FP32 sums do not tell: lane j < k returns slot j's expert. c: the token's row in LDS [E], FP32 sums;
+// those not below `cut` are made exact, and the choice is among them. regroup: the eligible groups are chosen again (the row
+// holds every group's sums; otherwise the eligible ones', and lower values). Every lane of the wave calls.
+MOE_DEV int choose_exact(const float* row, const float* bias, float* c, int E, int K, int q, const ScoreArgs& a, float cut,
+                         bool regroup) {
   float m = 0.f;
   const double den = a.softmax ? exact_sum(row, E, q, m) : 0.0;
-#pragma unroll 2
-  for (int e = q; e < E; e += kGroup) c[e] = exact_c(row ? row[e] : 0.f, bias, e, a.softmax, m, den);
+  uint64_t mine = 0;  // of this lane's experts q, q + 16, ...
+#pragma unroll 4
+  for (int i = 0; i < 64; ++i) {
+    const int e = kGroup * i + q;
+    if (kGroup * i >= E) break;
+    if (e < E && c[e] >= cut) mine |= 1ull << i;
+  }
+  for (uint64_t u = row ? mine : 0; __any(u != 0); u &= u - 1) {
+    if (u) {
+      const int e = kGroup * (__ffsll((unsigned long long)u) - 1) + q;
+      c[e] = exact_c(row[e], bias, e, a.softmax, m, den);
+    }
+  }
   wave_lds_fence();
-  const int gs = E / a.groups;
-  if (a.keep < a.groups) {
+  if (regroup) {
     bool unused;
-    const uint64_t open = eligible_groups<true>(c, gs, q, a, 0.f, unused);
-    wave_lds_fence();
+    float none;
+    const int gs = E / a.groups;
+    const uint64_t open = eligible_groups<true>(c, gs, q, a, 0.f, unused, none);
     const uint32_t magic = group_magic(gs);
-    for (int e = q; e < E; e += kGroup)
-      if (!((open >> group_of(e, magic)) & 1)) c[e] = taken;
+    uint64_t kept = 0;
+    for (uint64_t u = mine; u; u &= u - 1) {
+      const int i = __ffsll((unsigned long long)u) - 1;
+      if ((open >> (group_of(kGroup * i + q, magic) & 63)) & 1) kept |= 1ull << i;
+    }
+    mine = kept;
   }
   int id = 0;
   for (int s = 0; s < K; ++s) {
     // the lane's largest, the first of equal ones; then the row's, and of equal ones the lowest expert
     uint32_t top = 0, at = 0;
-#pragma unroll 4
-    for (int e = q; e < E; e += kGroup) {
-      const float x = c[e];
-      const uint32_t key = x == x ? logit_key(x) : 0;
-      at = key > top ? (uint32_t)e : at;
+    for (uint64_t u = mine; u; u &= u - 1) {
+      const uint32_t e = (uint32_t)(kGroup * (__ffsll((unsigned long long)u) - 1) + q);
+      const uint32_t key = logit_key(c[e]);
+      at = key > top ? e : at;
       top = key > top ? key : top;
     }
     const uint32_t best = row_max_u(top);
-    const uint32_t e = 1023u - row_max_u(top == best ? 1023u - at : 0u);
-    if (q == s) id = (int)e;
-    if (q == (int)(e & (kGroup - 1))) c[e] = taken;  // (its own lane reads it again)
+    const uint32_t e = 1023u - row_max_u(top == best && best ? 1023u - at : 0u);
+    if (q == s) id = min((int)e, E - 1);
+    if (q == (int)(e & (kGroup - 1))) mine &= ~(1ull << (e / kGroup));
   }
   return id;
 }
@@ -290,7 +311,7 @@ MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slot
                    const ScoreArgs& a, float& m, float& inv) {
   const float ninf = -__builtin_huge_valf();
   constexpr float kLog2e = 1.44269504088896341f, kUnit = 0x1p-24f;
-  constexpr float kLeast = 3e38f, none = -kMaxFloat;  // the lowest score, and no expert
+  constexpr float none = -kMaxFloat;  // no expert: below kLeast, the lowest score
   float x[NE];
   load_row<NE, VEC>(row, E, q, ninf, x);
   const float margin = (a.softmax ? 20.f : 16.f) * kUnit;  // relative to the sums and, softmax, p, or 1
@@ -321,10 +342,10 @@ MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slot
     for (int i = 0; i < NE; ++i) x[i] += b[i];
   }
 #pragma unroll
-  for (int i = 0; i < NE; ++i) x[i] = __builtin_amdgcn_fmed3f(x[i], -kLeast, kMaxFloat);  // NaN: the lowest
-  bool bad = false;
+  for (int i = 0; i < NE; ++i) x[i] = __builtin_amdgcn_fmed3f(x[i], kLeast, kMaxFloat);  // NaN: the lowest
   const int gs = E / a.groups;
-  if (a.keep < a.groups) {
+  // the sums in LDS: for the groups, and for choose_exact
+  auto store_sums = [&]() {
 #pragma unroll
     for (int i = 0; i < NE; i += VEC ? 4 : 1) {
       const int e = expert_of<VEC>(i, q);
@@ -333,8 +354,17 @@ MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slot
       else c[e] = x[i];
     }
     wave_lds_fence();
+  };
+  bool regroup = false, exact = false;
+  float cut = kLeast;  // of choose_exact: every eligible expert
+  if (a.keep < a.groups) {
+    store_sums();
+    bool near;
+    float low;
     // twice the margin of one c and the sums' rounding, relative to 1 (softmax scores are at most that)
-    const uint64_t open = eligible_groups<false>(c, gs, q, a, 2.f * margin + 4.f * kUnit, bad);
+    const uint64_t open = eligible_groups<false>(c, gs, q, a, 2.f * margin + 4.f * kUnit, near, low);
+    regroup = __any(row && near);
+    if (a.keep * (a.top == 2 && gs > 1 ? 2 : 1) >= K) cut = fmaxf(low, kLeast);  // the eligible groups add k that are not below it
     const uint32_t magic = group_magic(gs);
     if (VEC && (gs & 3) == 0) {  // the four of a vector share a group
 #pragma unroll
@@ -350,77 +380,90 @@ MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slot
         if (!((open >> (group_of(expert_of<VEC>(i, q), magic) & 63)) & 1)) x[i] = none;
     }
   }
-  if (E < kGroup * NE) {
+  int id = 0;
+  if (!regroup) {
+    store_sums();
+    if (E < kGroup * NE) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) x[i] = expert_of<VEC>(i, q) < E ? x[i] : none;
-  }
-  constexpr uint32_t kNumber = NE - 1;  // the bits that hold an element's number
-  constexpr uint32_t kUnknown = 0xffffffffu;
-  uint32_t key[kTopList];
-  // The list: the five largest, sorted, as keys that order as the scores. again: of those below `limit`.
-  auto make_list = [&](bool again, float limit) {
-    float l[kTopList];
-#pragma unroll
-    for (int j = 0; j < kTopList; ++j) l[j] = none;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      float v = __uint_as_float((__float_as_uint(x[i]) & ~kNumber) | i);
-      if (again) v = v < limit ? v : none;
-#pragma unroll
-      for (int j = kTopList - 1; j > 0; --j) l[j] = __builtin_amdgcn_fmed3f(l[j - 1], l[j], v);
-      l[0] = plain_max(l[0], v);
+      for (int i = 0; i < NE; ++i) x[i] = expert_of<VEC>(i, q) < E ? x[i] : none;
     }
+    constexpr uint32_t kNumber = NE - 1;  // the bits that hold an element's number
+    constexpr uint32_t kUnknown = 0xffffffffu;
+    uint32_t key[kTopList];
+    // The list: the five largest, sorted, as keys that order as the scores. again: of those below `limit`.
+    auto make_list = [&](bool again, float limit) {
+      float l[kTopList];
 #pragma unroll
-    for (int j = 0; j < kTopList; ++j) key[j] = ordered(l[j]);
-  };
-  // Rounds s0 .. rounds - 1. After a lane's fifth its next is unknown where it had more.
-  const int rounds = min(K + 2, a.keep * gs);  // the slots, and the first two experts left out where there are
-  auto play = [&](int s0) {
-    uint32_t pops = 0;
-    for (int s = s0; s < rounds; ++s) {
-      const uint32_t best = row_max_u(key[0]);
-      if (key[0] == best) {
-        *(uint2*)(slots + 2 * s) = make_uint2(best, (uint32_t)q);
-        ++pops;
+      for (int j = 0; j < kTopList; ++j) l[j] = none;
 #pragma unroll
-        for (int j = 0; j + 1 < kTopList; ++j) key[j] = key[j + 1];
-        key[kTopList - 1] = NE > kTopList ? kUnknown : 0u;
+      for (int i = 0; i < NE; ++i) {
+        float v = __uint_as_float((__float_as_uint(x[i]) & ~kNumber) | i);
+        if (again) v = v < limit ? v : none;
+#pragma unroll
+        for (int j = kTopList - 1; j > 0; --j) l[j] = __builtin_amdgcn_fmed3f(l[j - 1], l[j], v);
+        l[0] = plain_max(l[0], v);
+      }
+#pragma unroll
+      for (int j = 0; j < kTopList; ++j) key[j] = ordered(l[j]);
+    };
+    // Rounds s0 .. rounds - 1. After a lane's fifth its next is unknown where it had more.
+    const int rounds = min(K + 2, a.keep * gs);  // the slots, and the first two experts left out where there are
+    auto play = [&](int s0) {
+      uint32_t pops = 0;
+      for (int s = s0; s < rounds; ++s) {
+        const uint32_t best = row_max_u(key[0]);
+        if (key[0] == best) {
+          *(uint2*)(slots + 2 * s) = make_uint2(best, (uint32_t)q);
+          ++pops;
+#pragma unroll
+          for (int j = 0; j + 1 < kTopList; ++j) key[j] = key[j + 1];
+          key[kTopList - 1] = NE > kTopList ? kUnknown : 0u;
+        }
+      }
+      wave_lds_fence();
+      // two lanes with one key popped both: more pops than rounds
+      return row_sum_u(pops) != (uint32_t)(rounds - s0);
+    };
+    make_list(false, 0.f);
+    bool twins = play(0);
+    uint2 mine = *(const uint2*)(slots + 2 * q);
+    if constexpr (NE > kTopList) {
+      while (__any(row && q < rounds && mine.x == kUnknown)) {
+        // from the first unknown slot of the wave's tokens on, with what each lane has left below its last
+        const uint64_t unknown = __ballot(row && q < rounds && mine.x == kUnknown);
+        int s0 = rounds;
+        for (uint64_t u = unknown; u; u &= u - 1) s0 = min(s0, (int)(__ffsll((unsigned long long)u) - 1) & (kGroup - 1));
+        uint32_t last = kUnknown;
+        for (int s = 0; s < s0; ++s) last = slots[2 * s + 1] == (uint32_t)q ? slots[2 * s] : last;
+        load_row<NE, VEC>(c, E, q, none, x);
+        make_list(true, last == kUnknown ? __builtin_huge_valf() : key_logit(last));
+        wave_lds_fence();
+        twins |= play(s0);
+        mine = *(const uint2*)(slots + 2 * q);
       }
     }
-    wave_lds_fence();
-    // two lanes with one key popped both: more pops than rounds
-    return row_sum_u(pops) != (uint32_t)(rounds - s0);
-  };
-  make_list(false, 0.f);
-  bool twins = play(0);
-  uint2 mine = *(const uint2*)(slots + 2 * q);
-  if constexpr (NE > kTopList) {
-    while (__any(row && q < rounds && mine.x == kUnknown)) {
-      // from the first unknown slot of the wave's tokens on, with what each lane has left below its last
-      const uint64_t unknown = __ballot(row && q < rounds && mine.x == kUnknown);
-      int s0 = rounds;
-      for (uint64_t u = unknown; u; u &= u - 1) s0 = min(s0, (int)(__ffsll((unsigned long long)u) - 1) & (kGroup - 1));
-      uint32_t last = kUnknown;
-      for (int s = 0; s < s0; ++s) last = slots[2 * s + 1] == (uint32_t)q ? slots[2 * s] : last;
-      make_list(true, last == kUnknown ? __builtin_huge_valf() : key_logit(last));
-      wave_lds_fence();
-      twins |= play(s0);
-      mine = *(const uint2*)(slots + 2 * q);
+    const uint32_t bits = mine.x >> 31 ? mine.x : ~mine.x;  // (of a negative score the key holds the complement)
+    const int i = (int)(bits & kNumber);
+    id = VEC ? 64 * (i / 4) + 4 * (int)mine.y + i % 4 : kGroup * i + (int)mine.y;
+    bool near = false;
+    if (q + 1 < rounds) {  // whether slot q and the next are clear of each other
+      const float u = key_logit(mine.x), v = key_logit(slots[2 * q + 2]);
+      const float size = fmaxf(fabsf(u), fabsf(v));
+      near = !(u - v > margin * (a.softmax ? inv + size : fmaxf(1.f, size)) + 2 * NE * kUnit * size + 0x1p-100f);
+    }
+    // The last one chosen near the first left out is settled between them; near the second left out too, it is not.
+    const uint32_t nears = (uint32_t)(__ballot(near) >> (threadIdx.x & 48)) & 0xffffu;
+    exact = __any(row && (twins || ((nears >> (K - 1)) & 3) == 3));
+    if (exact) {
+      // What is not below the last one popped, with room for its error. (Twins pop more than one a round: the last slot may
+      // hold no expert, or a NaN where the lists ran out.)
+      const float v = key_logit(slots[2 * (rounds - 1)]);
+      cut = fmaxf(v - 64.f * (margin + 2 * NE * kUnit) * fmaxf(1.f, fabsf(v)), kLeast);
+    } else if (__any(row && (nears & ((1u << K) - 1)))) {
+      id = order_exact(row, bias, slots, id, E, min(K + 1, rounds), q, a);
     }
   }
-  const uint32_t bits = mine.x >> 31 ? mine.x : ~mine.x;  // (of a negative score the key holds the complement)
-  const int i = (int)(bits & kNumber);
-  int id = VEC ? 64 * (i / 4) + 4 * (int)mine.y + i % 4 : kGroup * i + (int)mine.y;
-  bool near = false;
-  if (q + 1 < rounds) {  // whether slot q and the next are clear of each other
-    const float u = key_logit(mine.x), v = key_logit(slots[2 * q + 2]);
-    const float size = fmaxf(fabsf(u), fabsf(v));
-    near = !(u - v > margin * (a.softmax ? inv + size : fmaxf(1.f, size)) + 2 * NE * kUnit * size + 0x1p-100f);
-  }
-  // The last one chosen near the first left out is settled between them; near the second left out too, it is not.
-  const uint32_t nears = (uint32_t)(__ballot(near) >> (threadIdx.x & 48)) & 0xffffu;
-  if (__any(row && (bad || twins || ((nears >> (K - 1)) & 3) == 3))) return choose_exact(row, bias, c, E, K, q, a);
-  if (__any(row && (nears & ((1u << K) - 1)))) id = order_exact(row, bias, slots, id, E, min(K + 1, rounds), q, a);
+  if (regroup || exact) id = choose_exact(row, bias, c, E, K, q, a, cut, regroup);
   return id;
 }
 
