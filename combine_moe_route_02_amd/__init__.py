@@ -622,7 +622,8 @@ def allocate(d: MoeDesc, device="cuda", backward: bool = True, fill=None, n_segm
     (FP8 codes) / torch.int8 (integer codes) as the descriptor's dtype says; index arrays are int32; scales, gates and
     accumulators float32. With FLAG_ROUTER_LOSS the loss's outputs and workspace for ``n_segments``
     segments are among them; ``seg_offsets``, ``token_mask``, ``dloss`` and the coefficients are the
-    caller's. ``out`` is a fresh [P_out, H] tensor; use ``out[:T]`` for the logical rows.
+    caller's. With FLAG_ROUTER_SCORES ``router_logits`` is (for layers that route from x); ``router_bias`` and
+    ``router_scores`` are the caller's. ``out`` is a fresh [P_out, H] tensor; use ``out[:T]`` for the logical rows.
     """
     import torch
     T, H, I, E, El, k, n = d.T, d.H, d.I, d.E, d.E_local, d.k, d.n_chunks
@@ -660,6 +661,8 @@ def allocate(d: MoeDesc, device="cuda", backward: bool = True, fill=None, n_segm
         for name in ("dyd_cs", "dgu_cs", "xd_cs", "h_cs"):
             spec[name] = ((max(1, ws[name] // 4),), f32)
     out = {}
+    if d.flags & FLAG_ROUTER_SCORES:
+        spec["router_logits"] = ((T, E), f32)
     if d.flags & FLAG_ROUTER_LOSS:
         spec.update({"router_logits": ((T, E), f32), "router_lse": ((T,), f32), "seg_counts": ((n_segments, E), i32),
                      "seg_tokens": ((n_segments + 2,), i32), "seg_probs": ((n_segments, E), f32),

@@ -389,23 +389,30 @@ moe_status moe_router_bias_update(int32_t E, int32_t rows, const int32_t* counts
   return MOE_OK;
 }
 
-moe_status moe_route_x(const moe_desc* d, int chunk, const void* x, const void* w_r, float* logits,
-                       int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets, int32_t* row_of,
-                       int32_t* src_token, void* workspace, void* stream) {
+static moe_status route_x_impl(const char* fn, const moe_desc* d, int chunk, const void* x, const void* w_r, float* logits,
+                               int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets, int32_t* row_of,
+                               int32_t* src_token, void* workspace, bool layout, void* stream) {
   MOE_TRY(validate(d));
   MOE_TRY(check_chunk(d, chunk));
-  if (d->dtype == MOE_F32) return fail(MOE_ERR_UNSUPPORTED, "moe_route_x: x and W_r must be BF16 (dtype BF16 or FP8)");
+  if (d->dtype == MOE_F32) return fail(MOE_ERR_UNSUPPORTED, "%s: x and W_r must be BF16 (dtype BF16 or FP8)", fn);
   if (d->E % 32 || d->E > 256)
-    return fail(MOE_ERR_UNSUPPORTED, "moe_route_x: E = %d must be a multiple of 32, at most 256", d->E);
+    return fail(MOE_ERR_UNSUPPORTED, "%s: E = %d must be a multiple of 32, at most 256", fn, d->E);
   if (d->T > 0) { MOE_NEED(x); MOE_NEED(w_r); MOE_NEED(topk_idx); MOE_NEED(gates); MOE_NEED(row_of); }
   if ((int64_t)d->n_chunks * d->P_c > 0) MOE_NEED(src_token);  // rows past N_c are marked -1
   MOE_NEED(counts); MOE_NEED(offsets); MOE_NEED(workspace);
   Range r = range_of(d, chunk);
   MOE_HIP(moe::launch_route_x(x, w_r, logits, topk_idx, gates, counts, offsets, row_of, src_token,
                               (int32_t*)workspace, d->T, d->E, d->H, d->e0, d->E_local, d->k, d->n_chunks,
-                              r.c0, r.nc, d->P_c, (hipStream_t)stream),
+                              r.c0, r.nc, d->P_c, (hipStream_t)stream, layout),
           "route_x");
   return MOE_OK;
+}
+
+moe_status moe_route_x(const moe_desc* d, int chunk, const void* x, const void* w_r, float* logits,
+                       int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets, int32_t* row_of,
+                       int32_t* src_token, void* workspace, void* stream) {
+  return route_x_impl("moe_route_x", d, chunk, x, w_r, logits, topk_idx, gates, counts, offsets, row_of, src_token,
+                      workspace, true, stream);
 }
 
 moe_status moe_dispatch(const moe_desc* d, int chunk, const void* x, const int32_t* row_of, void* xd,
@@ -1017,19 +1024,28 @@ static moe_status check_bwd_tensors(const moe_desc* d, const moe_tensors* t) {
 // Routing of one chunk in a layer primitive: by scores (MOE_FLAG_ROUTER_SCORES), from the given logits, or (logits
 // NULL) from x and the router weight with the projection fused into the top-k.
 static bool by_scores(const moe_desc* d) { return d->flags & MOE_FLAG_ROUTER_SCORES; }
+static const float* routed_logits(const moe_tensors* t) { return t->logits ? t->logits : t->router_logits; }
 static moe_status check_score_tensors(const moe_desc* d, const moe_tensors* t, bool backward) {
   if (!by_scores(d)) return MOE_OK;
-  MOE_TRY(check_scores(__func__, d, &t->router_scores));
-  if (d->T > 0 && !t->logits)
-    return fail(MOE_ERR_UNSUPPORTED, "layer: routing by scores takes given logits (the projection fused into routing has none)");
-  if (backward && d->T > 0 && t->dlogits == t->logits)
-    return fail(MOE_ERR_ARG, "layer: dlogits may not be the logits buffer");
+  MOE_TRY(check_scores("layer", d, &t->router_scores));
+  if (d->T == 0) return MOE_OK;
+  if (!routed_logits(t)) return fail(MOE_ERR_ARG, "layer: logits and router_logits are both NULL");
+  if (!t->logits && (d->dtype == MOE_F32 || d->E % 32 || d->E > 256))
+    return fail(MOE_ERR_UNSUPPORTED, "layer: routing from x needs BF16 x and E = %d a multiple of 32, at most 256", d->E);
+  if (backward && t->dlogits == routed_logits(t)) return fail(MOE_ERR_ARG, "layer: dlogits may not be the logits buffer");
+  if (backward && d->dtype == MOE_BF16 && (misaligned(routed_logits(t), 16) || misaligned(t->dlogits, 16)))
+    return fail(MOE_ERR_ARG, "layer: logits and dlogits must be 16-byte aligned");
   return MOE_OK;
 }
 static moe_status route_any(const moe_desc* d, int c, const moe_tensors* t, hipStream_t s) {
-  if (by_scores(d))
-    return moe_route_scores(d, c, &t->router_scores, t->logits, t->router_bias, t->topk_idx, t->gates, t->counts,
+  if (by_scores(d)) {
+    // without logits the projection's kernel writes them (its own choice is written over)
+    if (!t->logits && d->T > 0)
+      MOE_TRY(route_x_impl("layer", d, c, t->x, t->w_r, t->router_logits, t->topk_idx, t->gates, t->counts, t->offsets,
+                           t->row_of, t->src_token, t->workspace, false, s));
+    return moe_route_scores(d, c, &t->router_scores, routed_logits(t), t->router_bias, t->topk_idx, t->gates, t->counts,
                             t->offsets, t->row_of, t->src_token, t->workspace, s);
+  }
   if (t->logits || d->T == 0)
     return moe_route(d, c, t->logits, t->topk_idx, t->gates, t->counts, t->offsets, t->row_of, t->src_token,
                      t->workspace, s);
@@ -1040,7 +1056,7 @@ static moe_status route_any(const moe_desc* d, int c, const moe_tensors* t, hipS
 
 // MOE_FLAG_ROUTER_LOSS: the loss over every chunk's tokens once all of them are routed, and its
 // gradient into dlogits before the first chunk's route backward.
-static const float* loss_logits(const moe_tensors* t) { return t->logits ? t->logits : t->router_logits; }
+static const float* loss_logits(const moe_tensors* t) { return routed_logits(t); }
 static moe_status check_loss_tensors(const moe_desc* d, const moe_tensors* t, bool backward) {
   if (!(d->flags & MOE_FLAG_ROUTER_LOSS)) return MOE_OK;
   MOE_TRY(check_router_loss(__func__, d, t->n_segments, t->balance_coef, t->z_coef, t->seg_offsets));
@@ -1066,7 +1082,7 @@ static moe_status layer_loss_bwd(const moe_desc* d, const moe_tensors* t, hipStr
 
 static moe_status layer_route_bwd(const moe_desc* d, int c, const moe_tensors* t, hipStream_t s) {
   if (by_scores(d))
-    return moe_route_scores_bwd(d, c, &t->router_scores, t->logits, t->dgates, t->topk_idx, t->x, t->dlogits, t->dwr_acc,
+    return moe_route_scores_bwd(d, c, &t->router_scores, routed_logits(t), t->dgates, t->topk_idx, t->x, t->dlogits, t->dwr_acc,
                                 t->dwr, t->workspace, s);
   return moe_route_bwd(d, c, t->dgates, t->gates, t->topk_idx, t->x, t->dlogits, t->dwr_acc, t->dwr, t->workspace, s);
 }

@@ -471,7 +471,7 @@ size_t route_x_lds_bytes(int E) { return (size_t)kRxNst * (kProjTok + E) * kRxRo
 hipError_t launch_route_x(const void* x, const void* w_r, float* logits, int32_t* topk_idx, float* gates,
                           int32_t* counts, int32_t* offsets, int32_t* row_of, int32_t* src_token,
                           int32_t* scratch, int64_t T, int E, int H, int e0, int El, int K, int n, int chunk0,
-                          int nchunks, int64_t P_c, hipStream_t s) {
+                          int nchunks, int64_t P_c, hipStream_t s, bool layout) {
   const int nb32 = route_blocks_per_chunk(T, n) * (kRouteBlock / kProjTok);
   const int NB = (E + 127) / 128;  // 32-expert blocks per wave (E <= 256)
   const size_t lds = route_x_lds_bytes(E);
@@ -496,7 +496,7 @@ hipError_t launch_route_x(const void* x, const void* w_r, float* logits, int32_t
     }
   }
   hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
+  if (err != hipSuccess || !layout) return err;
   return launch_layout(topk_idx, scratch, counts, offsets, row_of, src_token, T, E, e0, El, K, n, chunk0, nchunks,
                        P_c, s);
 }

@@ -124,8 +124,8 @@ typedef struct moe_desc {
 #define MOE_FLAG_ROUTER_LOSS 16
 /* (32 is not a flag.) */
 /* The layer primitives route by scores (moe_route_scores with the fields router_scores and router_bias of
- * moe_tensors, from given logits) and run moe_route_scores_bwd; any dtype, with or without the other flags.
- * The stage calls do not look at it. */
+ * moe_tensors) and run moe_route_scores_bwd; any dtype, with or without the other flags. Without given logits
+ * moe_route_x's projection (its descriptors) writes them to router_logits first. The stage calls do not look at it. */
 #define MOE_FLAG_ROUTER_SCORES 64
 
 /* ---------------------------------------------------------------------------------------
@@ -541,13 +541,14 @@ typedef struct moe_tensors {
   /* MOE_FLAG_ROUTER_LOSS only, read under that flag alone (see moe_router_loss): segments and mask
    * (nullable with n_segments = 1), the loss's outputs, its upstream gradient (nullable: 1), its
    * workspace of moe_router_loss_bytes() bytes, and, where `logits` is NULL, the buffer [T,E] that
-   * receives the logits routed on. */
+   * receives the logits routed on (MOE_FLAG_ROUTER_SCORES uses that one too). */
   const int32_t* seg_offsets; const uint8_t* token_mask; float* router_logits; float* router_lse;
   int32_t* seg_counts; int32_t* seg_tokens; float* seg_probs; float* router_loss; const float* dloss;
   void* loss_workspace;
   int32_t n_segments; float balance_coef; float z_coef;
   /* MOE_FLAG_ROUTER_SCORES only, read under that flag alone (see moe_route_scores): the balance bias [E] (nullable;
-   * moe_layer_update writes it) and the options. `logits` must be given. */
+   * moe_layer_update writes it) and the options. Where `logits` is NULL, router_logits (above) receives them and is
+   * read again by the backward. */
   float* router_bias;
   moe_router_scores router_scores;
 } moe_tensors;

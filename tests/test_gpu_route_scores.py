@@ -415,6 +415,33 @@ def test_layer(cfg, how, loss):
         assert torch.equal(rows(n, keep[n]), rows(n, b[n])), n
 
 
+@pytest.mark.parametrize("loss", [False, True])
+@pytest.mark.parametrize("how", HOWS[:2], ids=["grouped", "softmax"])
+def test_layer_from_x(how, loss):
+    """Without logits: the layer on the logits that the projection left is the same, bit for bit."""
+    torch, mh = _gpu()
+    cfg = LAYERS[1]
+    d, b, _, _ = _layer_bufs(torch, mh, cfg, how, mh.FLAG_ROUTER_LOSS if loss else 0)
+    cs, aux = torch.cuda.current_stream(), torch.cuda.Stream()
+    b["logits"] = None
+    b["w_r"].mul_(8.0)
+    b["router_logits"].fill_(float("nan"))
+    mh.moe_layer_forward_backward(d, b, cs, aux)
+    torch.cuda.synchronize()
+    # FP32 sums of H exact products, in any order: H 2^-24 of the sum of magnitudes
+    want = b["x"].double() @ b["w_r"].double().t().contiguous()
+    mag = b["x"].double().abs() @ b["w_r"].double().abs().t().contiguous()
+    assert ((b["router_logits"].double() - want).abs() <= cfg.H * F * mag).all()
+    keep = {n: b[n].clone() for n in OUT}
+    b["logits"] = b["router_logits"].clone()
+    for n in OUT:
+        b[n].fill_(3)
+    mh.moe_layer_forward_backward(d, b, cs, aux)
+    torch.cuda.synchronize()
+    for n in OUT:
+        assert torch.equal(keep[n][:cfg.T], b[n][:cfg.T]), n
+
+
 @pytest.mark.parametrize("dtype", ["fp8", "int8"])
 def test_serving_layer(dtype):
     """Forward-only payloads: the layer is dispatch, experts and combine behind the same routing."""

@@ -103,5 +103,9 @@ def test_layer_checks_the_options():
     for fn in (mh.moe_layer_forward, mh.moe_layer_backward, mh.moe_layer_forward_backward):
         assert _status(fn, d, bufs, 0, 0) == -1
         assert _status(fn, d, {**bufs, "router_scores": None}, 0, 0) == -1  # zeroed options: no group at all
-        assert _status(fn, d, {**bufs, "router_scores": mh.make_router_scores(), "logits": None}, 0, 0) == -3
+        assert _status(fn, d, {**bufs, "router_scores": mh.make_router_scores(), "logits": None, "router_logits": None}, 0, 0) == -1
+        # from x: the projection's descriptors only
+        from_x = {**bufs, "router_scores": mh.make_router_scores(), "logits": None}
+        assert _status(fn, _desc(flags=mh.FLAG_ROUTER_SCORES, E=36), from_x, 0, 0) == -3
+        assert _status(fn, _desc(flags=mh.FLAG_ROUTER_SCORES, dtype="f32"), from_x, 0, 0) == -3
     assert _status(mh.moe_layer_backward, d, {**bufs, "router_scores": mh.make_router_scores(), "dlogits": bufs["logits"]}, 0, 0) == -1
