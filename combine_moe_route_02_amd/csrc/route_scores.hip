@@ -80,6 +80,8 @@ MOE_DEV uint32_t row_max_u(uint32_t x) { MOE_ROW16(x, max_u, dpp_u); return x; }
 // LDS between lanes of one wave: program order, which the compiler has to keep.
 MOE_DEV void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); __builtin_amdgcn_wave_barrier(); }
 
+constexpr int kSelInts = 2 * kGroup;  // LDS of a token: its groups' keys, then its slots (key and lane, one slot per lane)
+
 // Group of expert e, without a division: e < 1024, so floor(e / gs) = (e (2^20 / gs + 1)) >> 20.
 MOE_DEV int group_of(int e, uint32_t magic) { return (int)(((uint32_t)e * magic) >> 20); }
 MOE_DEV uint32_t group_magic(int gs) { return (1u << 20) / (uint32_t)gs + 1; }
@@ -122,9 +124,10 @@ MOE_DEV float exact_c(float logit, const float* bias, int e, bool softmax, float
 // different places of their groups, which lie a multiple of their size apart: the same bank. near: whether the last eligible
 // and the first other group are within `margin` (relative to 1 or the largest c that any group adds), where c is not
 // exact; two groups with one sum are near.
-// cut: what no c that a group adds is below.
+// cut (where a token of the wave has near groups): what no c that a group adds is below. keys: LDS of the token, kSelInts.
 template <bool EXACT>
-MOE_DEV uint64_t eligible_groups(const float* c, int gs, int q, const ScoreArgs& a, float margin, bool& near, float& cut) {
+MOE_DEV uint64_t eligible_groups(const float* c, uint32_t* keys, int gs, int q, const ScoreArgs& a, float margin, bool& near,
+                                 float& cut) {
   const float ninf = -__builtin_huge_valf();
   int lp = 0;  // log2 P: whole float4 per lane, and no more lanes than there are for the groups
   while (lp < 4 && (a.groups << (lp + 1)) <= kGroup && gs % (8 << lp) == 0) ++lp;
@@ -166,21 +169,39 @@ MOE_DEV uint64_t eligible_groups(const float* c, int gs, int q, const ScoreArgs&
   }
   uint32_t lo = 0, hi = 0;
   float least = __builtin_huge_valf(), most = ninf;
+  // up to 32 groups' keys go through LDS, four to a load (0 behind the last)
+  const bool few = a.groups <= kSelInts;
+  if (few) {
+    keys[q] = 0;
+    keys[q + kGroup] = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int g = first + per_pass * u;
+      if (per_pass * u < a.groups && g < a.groups) keys[g] = EXACT ? logit_key(mine[u]) : ordered(mine[u]);
+    }
+    wave_lds_fence();
+  }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int g = first + per_pass * u;
     if (per_pass * u >= a.groups) continue;
     int beaten = 0;
     const uint32_t own = EXACT ? logit_key(mine[u]) : ordered(mine[u]);
+    auto meet = [&](uint32_t other, int o) {
+      if constexpr (EXACT) beaten += other > own || (other == own && o < g);
+      else beaten += other > own;
+    };
+    if (few) {
+      for (int o = 0; o < a.groups; o += 4) {
+        const uint4 k = *(const uint4*)(keys + o);
+        meet(k.x, o); meet(k.y, o + 1); meet(k.z, o + 2); meet(k.w, o + 3);
+      }
+    } else {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (per_pass * w >= a.groups) continue;
-      const uint32_t key = EXACT ? logit_key(mine[w]) : ordered(mine[w]);
-      const int count = min(per_pass, a.groups - per_pass * w);
-      for (int j = 0; j < count; ++j) {
-        const uint32_t other = (uint32_t)__shfl((int)key, j << lp, kGroup);
-        if constexpr (EXACT) beaten += other > own || (other == own && per_pass * w + j < g);
-        else beaten += other > own;
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t key = EXACT ? logit_key(mine[w]) : ordered(mine[w]);
+        const int count = min(kGroup, a.groups - kGroup * w);  // (more than 32 groups: one lane each)
+        for (int j = 0; j < count; ++j) meet((uint32_t)__shfl((int)key, j, kGroup), kGroup * w + j);
       }
     }
     if (g < a.groups) {
@@ -199,7 +220,7 @@ MOE_DEV uint64_t eligible_groups(const float* c, int gs, int q, const ScoreArgs&
     most = row_max(most);
     size = row_max(size);
     near = !(least - most > margin * size) || __popc(lo) + __popc(hi) != a.keep;
-    cut = row_min(cut) - margin * size;
+    if (__any(near)) cut = row_min(cut) - margin * size;
   }
   return ((uint64_t)hi << 32) | lo;
 }
@@ -226,8 +247,8 @@ MOE_DEV int order_exact(const float* row, const float* bias, uint32_t* slots, in
 // The choice where the FP32 sums do not tell: lane j < k returns slot j's expert. c: the token's row in LDS [E], FP32 sums;
 // those not below `cut` are made exact, and the choice is among them. regroup: the eligible groups are chosen again (the row
 // holds every group's sums; otherwise the eligible ones', and lower values). Every lane of the wave calls.
-MOE_DEV int choose_exact(const float* row, const float* bias, float* c, int E, int K, int q, const ScoreArgs& a, float cut,
-                         bool regroup) {
+MOE_DEV int choose_exact(const float* row, const float* bias, float* c, uint32_t* slots, int E, int K, int q,
+                         const ScoreArgs& a, float cut, bool regroup) {
   float m = 0.f;
   const double den = a.softmax ? exact_sum(row, E, q, m) : 0.0;
   uint64_t mine = 0;  // of this lane's experts q, q + 16, ...
@@ -248,7 +269,7 @@ MOE_DEV int choose_exact(const float* row, const float* bias, float* c, int E, i
     bool unused;
     float none;
     const int gs = E / a.groups;
-    const uint64_t open = eligible_groups<true>(c, gs, q, a, 0.f, unused, none);
+    const uint64_t open = eligible_groups<true>(c, slots, gs, q, a, 0.f, unused, none);
     const uint32_t magic = group_magic(gs);
     uint64_t kept = 0;
     for (uint64_t u = mine; u; u &= u - 1) {
@@ -275,8 +296,7 @@ MOE_DEV int choose_exact(const float* row, const float* bias, float* c, int E, i
   return id;
 }
 
-constexpr int kTopList = 5;           // a lane's list
-constexpr int kSelInts = 2 * kGroup;  // LDS of a token's slots: key and lane, one slot per lane
+constexpr int kTopList = 5;  // a lane's list
 
 // Experts of a lane's elements: VEC: 64 (i / 4) + 4 q + i % 4 (float4 loads, E a multiple of 4), else 16 i + q.
 template <bool VEC> MOE_DEV int expert_of(int i, int q) { return VEC ? 64 * (i / 4) + 4 * q + i % 4 : kGroup * i + q; }
@@ -362,7 +382,7 @@ MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slot
     bool near;
     float low;
     // twice the margin of one c and the sums' rounding, relative to 1 (softmax scores are at most that)
-    const uint64_t open = eligible_groups<false>(c, gs, q, a, 2.f * margin + 4.f * kUnit, near, low);
+    const uint64_t open = eligible_groups<false>(c, slots, gs, q, a, 2.f * margin + 4.f * kUnit, near, low);
     regroup = __any(row && near);
     if (a.keep * (a.top == 2 && gs > 1 ? 2 : 1) >= K) cut = fmaxf(low, kLeast);  // the eligible groups add k that are not below it
     const uint32_t magic = group_magic(gs);
@@ -374,10 +394,11 @@ MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slot
 #pragma unroll
         for (int j = i; j < i + 4; ++j) x[j] = ok ? x[j] : none;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (!((open >> (group_of(expert_of<VEC>(i, q), magic) & 63)) & 1)) x[i] = none;
+    } else if (!regroup) {  // expert by expert, in LDS
+      for (int e = q; e < E; e += kGroup)
+        if (!((open >> group_of(e, magic)) & 1)) c[e] = none;
+      wave_lds_fence();
+      load_row<NE, VEC>(c, E, q, none, x);
     }
   }
   int id = 0;
@@ -463,7 +484,7 @@ MOE_DEV int choose(const float* row, const float* bias, float* c, uint32_t* slot
       id = order_exact(row, bias, slots, id, E, min(K + 1, rounds), q, a);
     }
   }
-  if (regroup || exact) id = choose_exact(row, bias, c, E, K, q, a, cut, regroup);
+  if (regroup || exact) id = choose_exact(row, bias, c, slots, E, K, q, a, cut, regroup);
   return id;
 }
 
