@@ -371,6 +371,7 @@ moe_status moe_route_scores(const moe_desc* d, int chunk, const moe_router_score
   if (d->T > 0) { MOE_NEED(logits); MOE_NEED(topk_idx); MOE_NEED(gates); MOE_NEED(row_of); }
   if ((int64_t)d->n_chunks * d->P_c > 0) MOE_NEED(src_token);  // rows past N_c are marked -1
   MOE_NEED(counts); MOE_NEED(offsets); MOE_NEED(workspace);
+  if (misaligned(workspace, 16)) return fail(MOE_ERR_ARG, "%s: the workspace must be 16-byte aligned", __func__);
   Range g = range_of(d, chunk);
   MOE_HIP(moe::launch_route_scores(*r, logits, bias, topk_idx, gates, counts, offsets, row_of, src_token,
                                    (int32_t*)workspace, d->T, d->E, d->e0, d->E_local, d->k, d->n_chunks, g.c0, g.nc,
@@ -1032,6 +1033,7 @@ static moe_status check_score_tensors(const moe_desc* d, const moe_tensors* t, b
   if (!routed_logits(t)) return fail(MOE_ERR_ARG, "layer: logits and router_logits are both NULL");
   if (!t->logits && (d->dtype == MOE_F32 || d->E % 32 || d->E > 256))
     return fail(MOE_ERR_UNSUPPORTED, "layer: routing from x needs BF16 x and E = %d a multiple of 32, at most 256", d->E);
+  if (misaligned(t->workspace, 16)) return fail(MOE_ERR_ARG, "layer: the workspace must be 16-byte aligned");
   if (backward && t->dlogits == routed_logits(t)) return fail(MOE_ERR_ARG, "layer: dlogits may not be the logits buffer");
   if (backward && d->dtype == MOE_BF16 && (misaligned(routed_logits(t), 16) || misaligned(t->dlogits, 16)))
     return fail(MOE_ERR_ARG, "layer: logits and dlogits must be 16-byte aligned");

@@ -187,7 +187,8 @@ typedef struct moe_router_scores {
  * and the k largest c among their experts are chosen, slot 0 the largest; ties go to the lower index. Logits: NaN
  * counts as -inf, +inf as the largest finite value; a row of only -inf has s = 0 everywhere. Gates are FP32,
  * computed from the logits of the chosen experts. Scores that round to the same FP32 value are ties (sigmoid: logits
- * above about 17). Every other argument and output is moe_route's; bias [E] FP32. No aliasing. */
+ * above about 17). Every other argument and output is moe_route's; bias [E] FP32; the workspace 16-byte aligned
+ * (MOE_ERR_ARG). No aliasing. */
 moe_status moe_route_scores(const moe_desc* d, int chunk, const moe_router_scores* r, const float* logits,
                             const float* bias, int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets,
                             int32_t* row_of, int32_t* src_token, void* workspace, void* stream);

@@ -100,6 +100,68 @@ def test_chunks_and_local_experts(T, E, El, e0, k, n, dtype):
         assert torch.equal(b[x], c[x]), x
 
 
+def test_many_chunks_without_local_experts():
+    torch, mh = _gpu()
+    lg, bias = _draw(131, 8, 1)
+    how = dict(score="softmax", n_groups=2)
+    d, b = _forward(torch, mh, lg, bias, 2, how, n=70000, El=0)  # more than the chunks of one launch
+    _check(d, b, lg, bias, how)
+
+
+@pytest.mark.parametrize("E", [64, 256, 512])
+def test_rows_off_their_alignment(E):
+    torch, mh = _gpu()
+    T, k = 70, 8
+    lg, bias = _draw(T, E, E)
+    how = dict(score="sigmoid", n_groups=8, topk_groups=4, group_top=2)
+    d, want = _forward(torch, mh, lg, bias, k, how)
+    off = lambda a: torch.from_numpy(np.append(np.float32(0), a.ravel())).cuda()[1:].view(a.shape)  # noqa: E731
+    dg = np.ones((T, k), np.float32) + lg[:, :k]
+    for shift_logits, shift_bias in ((True, False), (False, True), (True, True)):
+        b = _buffers(torch, mh, d)
+        x, bi = off(lg) if shift_logits else torch.from_numpy(lg).cuda(), off(bias) if shift_bias else torch.from_numpy(bias).cuda()
+        assert x.data_ptr() % 16 == 4 * shift_logits and bi.data_ptr() % 16 == 4 * shift_bias
+        mh.moe_route_scores(d, -1, mh.make_router_scores(**how), x, bi, *[b[n] for n in NAMES])
+        torch.cuda.synchronize()
+        _check(d, b, lg, bias, how)
+    dl, off_dl = torch.zeros(T, E, device="cuda"), off(np.zeros((T, E), np.float32))
+    r, g = mh.make_router_scores(**how), torch.from_numpy(dg).cuda()
+    mh.moe_route_scores_bwd(d, -1, r, torch.from_numpy(lg).cuda(), g, want["topk_idx"], None, dl)
+    mh.moe_route_scores_bwd(d, -1, r, off(lg), g, want["topk_idx"], None, off_dl)
+    assert torch.equal(dl, off_dl) and float(dl.abs().max()) > 0
+
+
+def test_offsets_past_32_bits():
+    torch, mh = _gpu()
+    T, E, k, n = 2 ** 21 + 77, 1024, 2, 64  # 2^31 + 78848 logits
+    rng = np.random.default_rng(5)
+    rows = [0, 1, 2 ** 20, 2 ** 21 - 1, 2 ** 21, 2 ** 21 + 1, T - 1]
+    lg = rng.standard_normal((len(rows), E)).astype(np.float32)
+    x = torch.zeros(T, E, device="cuda")
+    x[rows] = torch.from_numpy(lg).cuda()
+    d = mh.make_desc(T=T, H=64, I=64, E=E, E_local=1, e0=1, k=k, n_chunks=1, dtype="f32")
+    b = _buffers(torch, mh, d)
+    for score, renorm in (("sigmoid", True), ("softmax", False)):
+        r = mh.make_router_scores(score=score, n_groups=n, topk_groups=3, renormalize=renorm)
+        mh.moe_route_scores(d, -1, r, x, None, *[b[i] for i in NAMES])
+        want = ors.choose(ors.scores(lg, score), None, k, n, 3, 1)
+        np.testing.assert_array_equal(b["topk_idx"][rows].cpu().numpy(), want)
+        plain = torch.ones(T, dtype=torch.bool, device="cuda")
+        plain[rows] = False  # the others are ties: the first experts
+        assert bool((b["topk_idx"][plain] == torch.arange(k, device="cuda")).all())
+        assert int(b["counts"].sum()) == T * k
+        dg = torch.ones(T, k, device="cuda")
+        dg[:, 1] = 3.0
+        dl = torch.full((T, E), 9.0, device="cuda")
+        mh.moe_route_scores_bwd(d, -1, r, x, dg, b["topk_idx"], None, dl)
+        ones = np.ones((len(rows), k), np.float32)
+        ones[:, 1] = 3.0
+        lim = TERM * ors.backward_bound(lg, want, ones, score, renorm, 1.0) + 2.0 ** -126
+        assert np.all(np.abs(dl[rows].cpu().numpy() - ors.backward(lg, want, ones, score, renorm)) <= lim)
+        assert float(dl.abs().max()) < 2.0
+        del dl
+
+
 def test_plain_routing_is_the_same_as_moe_route():
     torch, mh = _gpu()
     lg, _ = _draw(500, 64, 3)

@@ -67,6 +67,14 @@ def test_backward_needs_its_buffers(name):
     assert _bwd(_desc(), mh.make_router_scores(), **{name: None}) == -1
 
 
+def test_workspace_is_aligned():
+    assert _fwd(_desc(), mh.make_router_scores(), workspace=24) == -1
+    bufs = {f: 16 * (i + 1) for i, f in enumerate(mh.TENSOR_FIELDS)}
+    bufs.update(router_scores=mh.make_router_scores(), workspace=24)
+    for fn in (mh.moe_layer_forward, mh.moe_layer_backward, mh.moe_layer_forward_backward):
+        assert _status(fn, _desc(flags=mh.FLAG_ROUTER_SCORES), bufs, 0, 0) == -1
+
+
 def test_backward_types_and_alias():
     r = mh.make_router_scores()
     assert _bwd(_desc(dtype="fp8"), r) == -3 and _bwd(_desc(dtype="int8"), r) == -3
