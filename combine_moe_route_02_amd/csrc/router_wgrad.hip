@@ -147,6 +147,19 @@ __global__ __launch_bounds__(kThreads) void router_wgrad_paired_kernel(RouterPla
 
 }  // namespace gg
 
+template <int BN>
+static hipError_t launch_paired(const gg::RouterPlaneArgs& a, int S, hipStream_t s) {
+  using namespace gg;
+  const size_t ring = (size_t)kNst * (256 + BN) * kRowB, ep = (size_t)128 * (BN + 4) * sizeof(float);
+  const size_t lds = ring > ep ? ring : ep;
+  auto k = router_wgrad_paired_kernel<BN>;
+  const hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  MOE_TRACE("gemm_router_wgrad", s);
+  MOE_LAUNCH(k, dim3((unsigned)(S * ((a.H + BN - 1) / BN))), dim3(kThreads), lds, s, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_router_wgrad_planes(const uint16_t* hi, const uint16_t* lo, int ldl, const void* x, float* partials,
                                       int64_t t0, int64_t len, int ks, int S, int E, int H, hipStream_t s) {
   using namespace gg;
@@ -156,17 +169,11 @@ hipError_t launch_router_wgrad_planes(const uint16_t* hi, const uint16_t* lo, in
   if (E <= 128) {
     // side by side: the low plane starts 128 columns after the high one, rows of 256
     if (ldl != 128 || lo != hi + 128) return hipErrorInvalidValue;
-    const size_t ring = (size_t)kNst * (256 + BN) * kRowB, ep = (size_t)128 * (BN + 4) * sizeof(float);
-    const size_t lds = ring > ep ? ring : ep;
-    auto k = router_wgrad_paired_kernel<BN>;
-    hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-    RouterPlaneArgs a{hi, lo, (const uint16_t*)x, partials, t0, len, ks, ldl, E, H};
-    {
-      MOE_TRACE("gemm_router_wgrad", s);
-      MOE_LAUNCH(k, dim3((unsigned)(S * ((H + BN - 1) / BN))), dim3(kThreads), lds, s, a);
-    }
-    return hipGetLastError();
+    const RouterPlaneArgs a{hi, lo, (const uint16_t*)x, partials, t0, len, ks, ldl, E, H};
+    // Tiles of half the columns where the others would leave CUs idle; an element's sums are the same in both. Whole
+    // route backward with 128 experts: 16384 tokens of 2048 46.5 -> 41.3 us, 100000 of 448 167 -> 122 us; with a
+    // workgroup per CU the wider tile reads less: 16384 tokens of 7168 97 us against 110, 131072 of 4096 304 against 345.
+    return S * ((H + BN - 1) / BN) < 256 ? launch_paired<BN / 2>(a, S, s) : launch_paired<BN>(a, S, s);
   }
   const size_t lds = (size_t)kNst * (BM + BN) * kRowB;
   auto k = router_wgrad_planes_kernel<BM, BN>;
