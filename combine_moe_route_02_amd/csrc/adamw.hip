@@ -17,6 +17,7 @@
 // Every FP32 operation that decides a code is rounded once (no contraction), so the codes are defined bit by bit.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.h"
 #include "launch.h"
@@ -137,50 +138,67 @@ MOE_DEV float share(float x, float inv) {
   return fminf(fabsf(x) * inv, 1.0f);  // never NaN (infinity times 0 gives 1: the scale is NaN then)
 }
 
-// Four elements from i on, of a tensor of n: vectors inside, single ones at its end. Stores pass the L2 (nontemporal): what a
-// step writes is read again a step later at the earliest (75.8 million parameters: 414 -> 372 us, and with
-// the norm before it 467 -> 428).
-template <typename T>
-MOE_DEV void load4(const T* p, int64_t i, int64_t n, float* f) {
-  if (i + 4 <= n) {
-    if constexpr (sizeof(T) == 2) {
-      const uint2 v = *(const uint2*)(p + i);
-      f[0] = bf2f(v.x & 0xffff); f[1] = bf2f(v.x >> 16); f[2] = bf2f(v.y & 0xffff); f[3] = bf2f(v.y >> 16);
-    } else {
-      const float4 v = *(const float4*)(p + i);
-      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = i + j < n ? ld_elem(p + i + j) : 0.f;
-  }
-}
+// A tile: its elements are addressed by a scalar pointer and 32 bits per lane, half the registers of 64-bit addresses.
+template <typename T> MOE_DEV T* at(T* p, int i) { return (T*)((char*)p + (uint32_t)i * (uint32_t)sizeof(T)); }
+template <typename T> MOE_DEV const T* at(const T* p, int i) { return (const T*)((const char*)p + (uint32_t)i * (uint32_t)sizeof(T)); }
+
+// Four elements from i on, of a tile of n: vectors inside, single ones at its end. Loads and stores are nontemporal: a step
+// reads each value once, and what it writes is read again a step later at the earliest. (75.8 million parameters with the
+// norm before it: 467 us -> 428 by the stores, 427 -> 359 by the loads, which leave the gradients of the norm in the cache.
+// The norm's own loads are plain, and the codes' too: nontemporal ones took 204 us instead of 215 with 8-bit averages, but
+// reading the codes next 124 instead of 106.)
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
+// Loads leave the bits as they are: a conversion beside its load would wait for it, and so for every load before the next.
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+  f32x4_t x;
+  MOE_DEV void values(float* f) const { f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w; }
+};
+template <> struct Raw<uint16_t> {
+  u32x2_t x;
+  MOE_DEV void values(float* f) const {
+    f[0] = bf2f(x.x & 0xffff); f[1] = bf2f(x.x >> 16); f[2] = bf2f(x.y & 0xffff); f[3] = bf2f(x.y >> 16);
+  }
+};
+MOE_DEV Raw<float> load4(const float* p, int i, int n) {
+  if (i + 4 <= n) return {__builtin_nontemporal_load((const f32x4_t*)at(p, i))};
+  float f[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = i + j < n ? *at(p, i + j) : 0.f;
+  return {f32x4_t{f[0], f[1], f[2], f[3]}};
+}
+MOE_DEV Raw<uint16_t> load4(const uint16_t* p, int i, int n) {
+  if (i + 4 <= n) return {__builtin_nontemporal_load((const u32x2_t*)at(p, i))};
+  uint32_t f[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = i + j < n ? *at(p, i + j) : 0u;
+  return {u32x2_t{f[0] | (f[1] << 16), f[2] | (f[3] << 16)}};
+}
 template <typename T>
-MOE_DEV void store4(T* p, int64_t i, int64_t n, const float* f) {
+MOE_DEV void store4(T* p, int i, int n, const float* f) {
   if (i + 4 <= n) {
     if constexpr (sizeof(T) == 2)
-      __builtin_nontemporal_store(u32x2_t{pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3])}, (u32x2_t*)(p + i));
+      __builtin_nontemporal_store(u32x2_t{pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3])}, (u32x2_t*)at(p, i));
     else
-      __builtin_nontemporal_store(f32x4_t{f[0], f[1], f[2], f[3]}, (f32x4_t*)(p + i));
+      __builtin_nontemporal_store(f32x4_t{f[0], f[1], f[2], f[3]}, (f32x4_t*)at(p, i));
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) if (i + j < n) st_elem(p + i + j, f[j]);
+    for (int j = 0; j < 4; ++j) if (i + j < n) st_elem(at(p, i + j), f[j]);
   }
 }
-MOE_DEV uint32_t load_codes(const uint8_t* p, int64_t i, int64_t n) {
-  if (i + 4 <= n) return *(const uint32_t*)(p + i);
+MOE_DEV uint32_t load_codes(const uint8_t* p, int i, int n) {
+  if (i + 4 <= n) return *(const uint32_t*)at(p, i);
   uint32_t c = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) if (i + j < n) c |= (uint32_t)p[i + j] << (8 * j);
+  for (int j = 0; j < 4; ++j) if (i + j < n) c |= (uint32_t)*at(p, i + j) << (8 * j);
   return c;
 }
-MOE_DEV void store_codes(uint8_t* p, int64_t i, int64_t n, const uint32_t* c) {
+MOE_DEV void store_codes(uint8_t* p, int i, int n, const uint32_t* c) {
   if (i + 4 <= n) {
-    __builtin_nontemporal_store(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24), (uint32_t*)(p + i));
+    __builtin_nontemporal_store(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24), (uint32_t*)at(p, i));
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) if (i + j < n) p[i + j] = (uint8_t)c[j];
+    for (int j = 0; j < 4; ++j) if (i + j < n) *at(p, i + j) = (uint8_t)c[j];
   }
 }
 MOE_DEV void decode4(uint32_t mc, uint32_t vc, float ms, float vs, float* m, float* v) {
@@ -193,7 +211,7 @@ MOE_DEV void decode4(uint32_t mc, uint32_t vc, float ms, float vs, float* m, flo
 
 // A lane's four values to codes; a block's scales are stored by its first lane. NEAREST: r is 1/2.
 template <bool NEAREST>
-MOE_DEV void pack4(const float* m, const float* v, const uint32_t* rnd, int64_t i, int64_t n, uint8_t* mc, float* ms,
+MOE_DEV void pack4(const float* m, const float* v, const uint32_t* rnd, int i, int n, uint8_t* mc, float* ms,
                    uint8_t* vc, float* vs) {
   uint32_t bm = 0, bv = 0;
 #pragma unroll
@@ -219,17 +237,17 @@ MOE_DEV void pack4(const float* m, const float* v, const uint32_t* rnd, int64_t 
   if (i < n) {
     store_codes(mc, i, n, cm);
     store_codes(vc, i, n, cv);
-    if (i % kAdamBlock == 0) { ms[i / kAdamBlock] = sm; vs[i / kAdamBlock] = sv; }
+    if (i % kAdamBlock == 0) { *at(ms, i / kAdamBlock) = sm; *at(vs, i / kAdamBlock) = sv; }
   }
 }
 // First element of a lane's four in block u (0, 1) of its wave, in a tile.
-MOE_DEV int64_t lane_element(int64_t tile, int u) {
-  return tile * kAdamTile + (int)(threadIdx.x >> 6) * 2 * kAdamBlock + u * kAdamBlock + (threadIdx.x & 63) * 4;
-}
+MOE_DEV int lane_element(int u) { return (int)(threadIdx.x >> 6) * 2 * kAdamBlock + u * kAdamBlock + (threadIdx.x & 63) * 4; }
+// Elements of a tile.
+MOE_DEV int tile_size(int64_t n, int64_t first) { return (int)min(n - first, (int64_t)kAdamTile); }
 // The scale of a lane's block, the same for the wave; 0 behind the tensor's end.
-MOE_DEV float scale_of(const float* scale, int64_t i, int64_t n) {
-  const int64_t block = i / kAdamBlock;
-  return block * kAdamBlock < n ? scale[block] : 0.f;
+MOE_DEV float scale_of(const float* scale, int i, int n) {
+  const int block = i / kAdamBlock;
+  return block * kAdamBlock < n ? *at(scale, block) : 0.f;
 }
 
 // W: float, or uint16_t (BF16 bits) with a master or, without one, rounded by chance like the codes: an update under
@@ -252,67 +270,95 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamBatch<N> 
   const float keep = (float)(1.0 - lr * (double)t.wd);
   const float c1 = (float)(lr * unbias1), c2 = (float)unbias2;
   const float eps = (float)k.eps;
-  const int64_t n = t.n, tile = blockIdx.x - b.tile0[which];
-  float g[2][4], w[2][4], m[2][4], v[2][4];
+  const int64_t first = (int64_t)(blockIdx.x - b.tile0[which]) * kAdamTile;
+  const int n = tile_size(t.n, first);
+  const G* grad = (const G*)t.grad + first;
+  W* weight = (W*)t.w + first;
+  float* master = t.master + first;  // (MASTER)
+  using State = std::conditional_t<Q8, uint8_t, float>;
+  State *m_state = (State*)t.m + first, *v_state = (State*)t.v + first;
+  float *m_scale = t.m_scale + first / kAdamBlock, *v_scale = t.v_scale + first / kAdamBlock;  // (Q8)
+  const uint32_t place = t.place + (uint32_t)first;
+  using Weight = std::conditional_t<MASTER, float, W>;
+  Raw<G> g_raw[2];
+  Raw<Weight> w_raw[2];
+  Raw<float> m_raw[2], v_raw[2];  // FP32 averages
+  uint32_t m_code[2], v_code[2];  // 8 bits
+  float m_unit[2], v_unit[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int64_t i = lane_element(tile, u);
-    load4((const G*)t.grad, i, n, g[u]);
-    if constexpr (MASTER) load4(t.master, i, n, w[u]);
-    else load4((const W*)t.w, i, n, w[u]);
+    const int i = lane_element(u);
+    g_raw[u] = load4(grad, i, n);
+    if constexpr (MASTER) w_raw[u] = load4((const float*)master, i, n);
+    else w_raw[u] = load4((const W*)weight, i, n);
     if constexpr (Q8) {
-      decode4(load_codes((const uint8_t*)t.m, i, n), load_codes((const uint8_t*)t.v, i, n), scale_of(t.m_scale, i, n),
-              scale_of(t.v_scale, i, n), m[u], v[u]);
+      m_code[u] = load_codes(m_state, i, n);
+      v_code[u] = load_codes(v_state, i, n);
+      m_unit[u] = scale_of(m_scale, i, n);
+      v_unit[u] = scale_of(v_scale, i, n);
     } else {
-      load4((const float*)t.m, i, n, m[u]);
-      load4((const float*)t.v, i, n, v[u]);
+      m_raw[u] = load4((const float*)m_state, i, n);
+      v_raw[u] = load4((const float*)v_state, i, n);
     }
   }
   constexpr bool kChance = Q8 || (sizeof(W) == 2 && !MASTER);
   const uint32_t key = kChance ? step_key(k.seed, step) : 0;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int64_t i = lane_element(tile, u);
+    const int i = lane_element(u);
+    float g[4], w[4], m[4], v[4];
+    g_raw[u].values(g);
+    w_raw[u].values(w);
+    if constexpr (Q8) {
+      decode4(m_code[u], v_code[u], m_unit[u], v_unit[u], m, v);
+    } else {
+      m_raw[u].values(m);
+      v_raw[u].values(v);
+    }
     uint32_t rnd[4];
     if constexpr (kChance) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) rnd[j] = random_bits(t.place + (uint32_t)i + j, key);
+      for (int j = 0; j < 4; ++j) rnd[j] = random_bits(place + (uint32_t)i + j, key);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float x = g[u][j] * gs;
-      m[u][j] = m[u][j] * b1 + x * o1;
-      v[u][j] = v[u][j] * b2 + (x * x) * o2;
+      const float x = g[j] * gs;
+      m[j] = m[j] * b1 + x * o1;
+      v[j] = v[j] * b2 + (x * x) * o2;
       // the hardware's root and reciprocal, 2^-23 each, beside the 2^-24 of the sum: no state hangs on their bits
-      w[u][j] = w[u][j] * keep - c1 * m[u][j] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[u][j]) * c2 + eps);
+      w[j] = w[j] * keep - c1 * m[j] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[j]) * c2 + eps);
     }
-    if constexpr (MASTER) store4(t.master, i, n, w[u]);
+    if constexpr (MASTER) store4(master, i, n, w);
     if constexpr (sizeof(W) == 2 && !MASTER) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t x = __float_as_uint(w[u][j]);
-        if ((x & 0x7f800000u) != 0x7f800000u) w[u][j] = __uint_as_float((x + more_bits(rnd[j])) & 0xffff0000u);
+        const uint32_t x = __float_as_uint(w[j]);
+        if ((x & 0x7f800000u) != 0x7f800000u) w[j] = __uint_as_float((x + more_bits(rnd[j])) & 0xffff0000u);
       }
     }
-    store4((W*)t.w, i, n, w[u]);
+    store4(weight, i, n, w);
     if constexpr (Q8) {
-      pack4<false>(m[u], v[u], rnd, i, n, (uint8_t*)t.m, t.m_scale, (uint8_t*)t.v, t.v_scale);
+      pack4<false>(m, v, rnd, i, n, m_state, m_scale, v_state, v_scale);
     } else {
-      store4((float*)t.m, i, n, m[u]);
-      store4((float*)t.v, i, n, v[u]);
+      store4(m_state, i, n, m);
+      store4(v_state, i, n, v);
     }
   }
 }
 
 // 8-bit averages to FP32 and back (nearest level).
-__global__ __launch_bounds__(kAdamThreads) void adamw_unpack_kernel(int64_t n, const uint8_t* __restrict__ mc,
+__global__ __launch_bounds__(kAdamThreads) void adamw_unpack_kernel(int64_t size, const uint8_t* __restrict__ mc,
                                                                     const float* __restrict__ ms,
                                                                     const uint8_t* __restrict__ vc,
                                                                     const float* __restrict__ vs,
                                                                     float* __restrict__ m, float* __restrict__ v) {
+  const int64_t first = (int64_t)blockIdx.x * kAdamTile;
+  const int n = tile_size(size, first);
+  mc += first; vc += first; m += first; v += first;
+  ms += first / kAdamBlock; vs += first / kAdamBlock;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int64_t i = lane_element(blockIdx.x, u);
+    const int i = lane_element(u);
     float fm[4], fv[4];
     decode4(load_codes(mc, i, n), load_codes(vc, i, n), scale_of(ms, i, n), scale_of(vs, i, n), fm, fv);
     store4(m, i, n, fm);
@@ -320,16 +366,21 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_unpack_kernel(int64_t n, c
   }
 }
 
-__global__ __launch_bounds__(kAdamThreads) void adamw_pack_kernel(int64_t n, const float* __restrict__ m,
+__global__ __launch_bounds__(kAdamThreads) void adamw_pack_kernel(int64_t size, const float* __restrict__ m,
                                                                   const float* __restrict__ v, uint8_t* __restrict__ mc,
                                                                   float* __restrict__ ms, uint8_t* __restrict__ vc,
                                                                   float* __restrict__ vs) {
+  const int64_t first = (int64_t)blockIdx.x * kAdamTile;
+  const int n = tile_size(size, first);
+  mc += first; vc += first; m += first; v += first;
+  ms += first / kAdamBlock; vs += first / kAdamBlock;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int64_t i = lane_element(blockIdx.x, u);
+    const int i = lane_element(u);
     float fm[4], fv[4];
-    load4(m, i, n, fm);
-    load4(v, i, n, fv);
+    const Raw<float> rm = load4(m, i, n), rv = load4(v, i, n);
+    rm.values(fm);
+    rv.values(fv);
     pack4<true>(fm, fv, nullptr, i, n, mc, ms, vc, vs);
   }
 }
