@@ -83,8 +83,8 @@ MOE_DEV uint32_t step_key(uint32_t seed, int64_t step) {
   k *= 0xB7E15163u;
   return k ^ (k >> 15);
 }
-MOE_DEV uint32_t random_bits(uint32_t place, uint32_t key) {
-  uint32_t x = place * 0x9E3779B9u + key;
+MOE_DEV uint32_t random_bits(uint32_t place, uint32_t key, int j) {  // of element place + j
+  uint32_t x = place * 0x9E3779B9u + key + (uint32_t)j * 0x9E3779B9u;
   x = (x ^ (x >> 16)) * 0xB7E15163u;
   return x ^ (x >> 15);
 }
@@ -100,18 +100,23 @@ MOE_DEV float decode_m(int8_t code, float scale) {
 }
 MOE_DEV float decode_v(uint8_t code, float scale) { return level_v((float)code) * scale; }
 
-// Code of a in [0, 1]: the level below, or the one above where (a - below) / (above - below) exceeds r. The root only
-// proposes the nearest code (it is off by far less than half of one); the levels decide on which side of it a lies. The
-// last level is 1 exactly, so the code above it is never taken.
-template <int TOP, bool FOURTH>
-MOE_DEV int encode(float a, float r) {
+// Code of a in [0, 1], as a float: the level below, or the one above where (a - below) / (above - below) exceeds r. The root
+// only proposes the level below (it is off by far less than one); a neighbour takes its place where a lies outside. The last
+// level is 1 exactly, so the code above it is never taken.
+template <bool FOURTH>
+MOE_DEV float encode(float a, float r) {
   auto level = [](float c) { return FOURTH ? level_v(c) : level_m(c); };
   float root = __builtin_amdgcn_sqrtf(a);
   if (FOURTH) root = __builtin_amdgcn_sqrtf(root);
-  const float near = rintf(root * (float)TOP), at = level(near);
-  const float next = near + (a >= at ? 1.f : -1.f), other = level(next);
-  const float lo = fminf(at, other), hi = fmaxf(at, other);
-  return (int)fminf(near, next) + (a - lo > r * (hi - lo) ? 1 : 0);
+  float c = floorf(root * (FOURTH ? 255.f : 127.f));
+  float lo = level(c), hi = level(c + 1.f), d = a - lo, w = hi - lo;
+  if (__float_as_uint(d) >= __float_as_uint(w)) {  // below 0 (the sign) or not below w: of 64 lanes seldom one
+    c += a < lo ? -1.f : a >= hi ? 1.f : 0.f;
+    lo = level(c);
+    d = a - lo;
+    w = level(c + 1.f) - lo;
+  }
+  return c + (d > r * w ? 1.f : 0.f);
 }
 
 // Largest magnitude over the wave, by bits (NaN above infinity above every number): DPP within rows of 16, then scalars.
@@ -193,12 +198,12 @@ MOE_DEV uint32_t load_codes(const uint8_t* p, int i, int n) {
   for (int j = 0; j < 4; ++j) if (i + j < n) c |= (uint32_t)*at(p, i + j) << (8 * j);
   return c;
 }
-MOE_DEV void store_codes(uint8_t* p, int i, int n, const uint32_t* c) {
+MOE_DEV void store_codes(uint8_t* p, int i, int n, uint32_t c) {
   if (i + 4 <= n) {
-    __builtin_nontemporal_store(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24), (uint32_t*)at(p, i));
+    __builtin_nontemporal_store(c, (uint32_t*)at(p, i));
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) if (i + j < n) *at(p, i + j) = (uint8_t)c[j];
+    for (int j = 0; j < 4; ++j) if (i + j < n) *at(p, i + j) = (uint8_t)(c >> (8 * j));
   }
 }
 MOE_DEV void decode4(uint32_t mc, uint32_t vc, float ms, float vs, float* m, float* v) {
@@ -222,20 +227,18 @@ MOE_DEV void pack4(const float* m, const float* v, const uint32_t* rnd, int i, i
   bv &= 0x7fffffffu;
   const float sm = block_scale(block_max(bm)), sv = block_scale(block_max(bv));
   const float im = block_inv(sm), iv = block_inv(sv);
-  uint32_t cm[4], cv[4];
+  uint32_t cm[4], cv = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float rm = NEAREST ? 0.5f : (float)(rnd[j] & 0xffffu) * 0x1p-16f;
     const float rv = NEAREST ? 0.5f : (float)(rnd[j] >> 16) * 0x1p-16f;
-    const int c = encode<127, false>(share(m[j], im), rm);
-    const int sign = __float_as_int(m[j]) >> 31;  // (a NaN's code does not matter)
-    cm[j] = (uint32_t)((c ^ sign) - sign) & 0xffu;
+    cm[j] = (uint32_t)(int)copysignf(encode<false>(share(m[j], im), rm), m[j]);  // (a NaN's code does not matter)
     const float a = share(v[j], iv);
-    const int e = encode<255, true>(a, rv);
-    cv[j] = a > 0.f ? (uint32_t)max(e, 1) : 0u;
+    cv = __builtin_amdgcn_cvt_pk_u8_f32(fmaxf(encode<true>(a, rv), ceilf(a)), j, cv);  // (a > 0: 1 at least)
   }
   if (i < n) {
-    store_codes(mc, i, n, cm);
+    const uint32_t low = __builtin_amdgcn_perm(cm[1], cm[0], 0x0c0c0400u), high = __builtin_amdgcn_perm(cm[3], cm[2], 0x0c0c0400u);
+    store_codes(mc, i, n, low | (high << 16));
     store_codes(vc, i, n, cv);
     if (i % kAdamBlock == 0) { *at(ms, i / kAdamBlock) = sm; *at(vs, i / kAdamBlock) = sv; }
   }
@@ -318,7 +321,7 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamBatch<N> 
     uint32_t rnd[4];
     if constexpr (kChance) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) rnd[j] = random_bits(place + (uint32_t)i + j, key);
+      for (int j = 0; j < 4; ++j) rnd[j] = random_bits(place + (uint32_t)i, key, j);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
