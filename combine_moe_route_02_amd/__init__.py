@@ -440,10 +440,12 @@ def make_adamw_options(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, state_bits=3
 
 
 class AdamwTensors:
-    """The tensors of moe_adamw_step and moe_grad_norm: their table, made once, and the references it needs."""
+    """The tensors of moe_adamw_step and moe_grad_norm: their table, made once, and the references it needs.
+    ``state_bits`` is what their averages have (None without any)."""
 
     def __init__(self, parts):
         self.parts = [dict(p) for p in parts]
+        self.state_bits = None
         self.table = (MoeAdamwTensor * len(self.parts))()
         for row, p in zip(self.table, self.parts):
             for f in ("w", "master", "grad", "m", "v", "m_scale", "v_scale"):
@@ -455,9 +457,28 @@ class AdamwTensors:
             for f in ("w", "master", "m", "v"):
                 if p.get(f) is not None and p[f].numel() != row.n:
                     raise ValueError(f"{f} has {p[f].numel()} elements and its gradient {row.n}")
+            self._check_state(p, row.n)
             row.grad_dtype = _pay(p["grad"])
             row.w_dtype = _pay(p["w"]) if p.get("w") is not None else MOE_F32
             row.lr_scale, row.weight_decay = p.get("lr_scale", 1.0), p.get("weight_decay", 0.0)
+
+    def _check_state(self, p, n):
+        kinds = {f: str(p[f].dtype) for f in ("master", "m", "v", "m_scale", "v_scale") if p.get(f) is not None}
+        for f in ("master", "m_scale", "v_scale"):
+            if kinds.get(f, "torch.float32") != "torch.float32":
+                raise TypeError(f"{f} is float32, not {kinds[f]}")
+        for f in ("m", "v"):
+            if f not in kinds:
+                continue
+            bits = 32 if kinds[f] == "torch.float32" else 8
+            if bits == 8 and kinds[f] not in ("torch.int8", "torch.uint8"):
+                raise TypeError(f"{f} is float32, int8 or uint8, not {kinds[f]}")
+            if self.state_bits not in (None, bits):
+                raise ValueError("averages of one call are all in 32 bits or all in 8")
+            self.state_bits = bits
+            scale = p.get(f + "_scale")
+            if bits == 8 and scale is not None and scale.numel() < (n + 255) // 256:
+                raise ValueError(f"{f}_scale has {scale.numel()} elements for {n}: one per 256")
 
     def __len__(self):
         return len(self.parts)
@@ -470,6 +491,9 @@ def make_adamw_tensors(parts) -> AdamwTensors:
 
 
 def moe_adamw_step(options, tensors, stream=None):
+    bits = getattr(tensors, "state_bits", None)
+    if options is not None and bits not in (None, options.state_bits):
+        raise ValueError(f"the averages have {bits} bits and the options {options.state_bits}")
     _check(lib().moe_adamw_step(_ref(options), len(tensors), tensors.table, _stream(stream)), "moe_adamw_step")
 
 

@@ -879,6 +879,8 @@ static moe_status check_adamw(const char* fn, const moe_adamw_options* o) {
   if (!(o->beta1 > 0 && o->beta1 < 1 && o->beta2 > 0 && o->beta2 < 1))
     return fail(MOE_ERR_ARG, "%s: beta1 and beta2 must lie between 0 and 1", fn);
   if (!o->step_dev && o->step < 1) return fail(MOE_ERR_ARG, "%s: step = %lld below 1", fn, (long long)o->step);
+  if (misaligned(o->lr_dev, 8) || misaligned(o->step_dev, 8) || misaligned(o->grad_scale, 4))
+    return fail(MOE_ERR_ARG, "%s: lr_dev, step_dev or grad_scale is not aligned to its size", fn);
   if (o->state_bits != 8 && o->state_bits != 32) return fail(MOE_ERR_UNSUPPORTED, "%s: state_bits = %d is not 8 or 32", fn, o->state_bits);
   return MOE_OK;
 }
@@ -899,7 +901,8 @@ moe_status moe_grad_norm_bytes(int64_t* workspace) {
 static moe_status check_norm(const char* fn, double max_norm, const float* norm, const void* workspace) {
   if (!(max_norm > 0)) return fail(MOE_ERR_ARG, "%s: max_norm must be above 0", fn);
   if (!norm || !workspace) return fail(MOE_ERR_ARG, "%s: norm or its workspace is NULL", fn);
-  if (misaligned(workspace, 8)) return fail(MOE_ERR_ARG, "%s: the workspace must be 8-byte aligned", fn);
+  if (misaligned(workspace, 8) || misaligned(norm, 4))
+    return fail(MOE_ERR_ARG, "%s: the workspace must be 8-byte and the norm 4-byte aligned", fn);
   return MOE_OK;
 }
 
@@ -916,8 +919,8 @@ static moe_status check_pack(const char* fn, int64_t n, const void* m, const voi
   if (n < 0) return fail(MOE_ERR_ARG, "%s: n = %lld is negative", fn, (long long)n);
   if (n > ((int64_t)1 << 34)) return fail(MOE_ERR_UNSUPPORTED, "%s: n = %lld above 2^34", fn, (long long)n);
   if (n > 0 && (!m || !v || !mc || !ms || !vc || !vs)) return fail(MOE_ERR_ARG, "%s: a pointer is NULL", fn);
-  if (misaligned(m, 16) || misaligned(v, 16) || misaligned(mc, 8) || misaligned(vc, 8))
-    return fail(MOE_ERR_ARG, "%s: values must be 16-byte aligned and codes 8-byte aligned", fn);
+  if (misaligned(m, 16) || misaligned(v, 16) || misaligned(mc, 8) || misaligned(vc, 8) || misaligned(ms, 4) || misaligned(vs, 4))
+    return fail(MOE_ERR_ARG, "%s: values must be 16-byte, codes 8-byte and scales 4-byte aligned", fn);
   return MOE_OK;
 }
 

@@ -434,7 +434,7 @@ typedef struct moe_adamw_tensor {
 } moe_adamw_tensor;
 
 /* lr >= 0, 0 < beta < 1, eps >= 0, all finite; step counts from 1. For graphs that are replayed: lr_dev and step_dev
- * (device FP64 and int64, nullable) take the place of lr and step, read when the kernels run (a step below 1
+ * (device FP64 and int64, nullable, aligned to their size) take the place of lr and step, read when the kernels run (a step below 1
  * counts as 1). grad_scale (device FP32, nullable: 1) multiplies every gradient; where it is not finite the call writes
  * nothing. */
 typedef struct moe_adamw_options {

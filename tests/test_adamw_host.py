@@ -44,6 +44,7 @@ def _step(rows, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(lr=-1.0), -1), (dict(lr=float("nan")), -1), (dict(lr=float("inf")), -1), (dict(eps=-1e-8), -1), (dict(eps=float("nan")), -1),
     (dict(beta1=0.0), -1), (dict(beta1=1.0), -1), (dict(beta2=1.5), -1), (dict(beta2=float("nan")), -1),
+    (dict(lr_dev=20), -1), (dict(step_dev=12), -1), (dict(grad_scale=18), -1),
     (dict(step=0), -1), (dict(step=-3), -1), (dict(state_bits=16), -3), (dict(state_bits=0), -3),
 ])
 def test_options_are_checked(kw, status):
@@ -85,7 +86,7 @@ def test_norm_is_checked():
     f = mh.moe_grad_norm
     assert _status(f, t, 0.0, 16, 16, 0) == -1 and _status(f, t, float("nan"), 16, 16, 0) == -1
     assert _status(f, t, 1.0, None, 16, 0) == -1 and _status(f, t, 1.0, 16, None, 0) == -1
-    assert _status(f, t, 1.0, 16, 20, 0) == -1
+    assert _status(f, t, 1.0, 16, 20, 0) == -1 and _status(f, t, 1.0, 18, 16, 0) == -1
     assert _status(f, _Table(dict(grad=None)), 1.0, 16, 16, 0) == -1
     assert mh.moe_grad_norm_bytes() > 0
 
@@ -99,9 +100,29 @@ def test_pack_is_checked():
             a = [16] * 6
             a[i] = None
             assert _status(f, 5, *a, 0) == -1
-            if i not in scales:
-                a[i] = 20
-                assert _status(f, 5, *a, 0) == -1
+            a[i] = 18 if i in scales else 20
+            assert _status(f, 5, *a, 0) == -1
+
+
+def test_tables_are_checked():
+    torch = pytest.importorskip("torch")
+    f32, i8, u8 = (lambda n, t=t: torch.zeros(n, dtype=t) for t in (torch.float32, torch.int8, torch.uint8))  # noqa: E731
+    wide, small = dict(w=f32(300), grad=f32(300), m=f32(300), v=f32(300)), dict(m_scale=f32(2), v_scale=f32(2))
+    narrow = {**wide, **small, "m": i8(300), "v": u8(300)}
+    assert mh.make_adamw_tensors([wide]).state_bits == 32 and mh.make_adamw_tensors([narrow]).state_bits == 8
+    assert mh.make_adamw_tensors([dict(grad=f32(5))]).state_bits is None
+    for bad in ([wide, narrow], [{**narrow, "v": f32(300)}], [{**narrow, "m_scale": f32(1)}], [{**wide, "m": f32(299)}],
+                [{**wide, "v": f32(600)[::2]}]):
+        with pytest.raises(ValueError):
+            mh.make_adamw_tensors(bad)
+    for bad in ({**wide, "m": f32(300).double()}, {**wide, "v": f32(300).half()}, {**narrow, "v_scale": f32(2).half()},
+                {**wide, "master": f32(300).bfloat16()}, {**wide, "grad": f32(300).half()}, {**wide, "w": f32(300).double()}):
+        with pytest.raises(TypeError):
+            mh.make_adamw_tensors([bad])
+    # averages of another width than the call's: their bytes would end before the kernel's accesses do
+    for part, bits in ((wide, 8), (narrow, 32)):
+        with pytest.raises(ValueError):
+            mh.moe_adamw_step(mh.make_adamw_options(1e-3, state_bits=bits), mh.make_adamw_tensors([part]), 0)
 
 
 def _layer(**kw):

@@ -495,3 +495,74 @@ def test_layer_update(dtype, bits, master, clip):
             assert torch.equal(b[f], twin[f]), f
             assert not torch.equal(before[f], twin[f]), f
             assert all(torch.equal(o.buffers[f][x], ref.buffers[f][x]) for x in o.buffers[f]), f
+
+
+def _training_layer(torch, mh, bits, step):
+    """A layer that routes from x by scores, with its optimizer; the step number on the device."""
+    d = mh.make_desc(T=500, H=128, I=64, E=32, E_local=8, k=4, n_chunks=2, dtype="bf16", flags=mh.FLAG_ROUTER_SCORES)
+    b = mh.allocate(d)
+    gen = torch.Generator("cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    b.update(x=rand(500, 128), dy=rand(500, 128), w1=rand(8, 128, 128) * 0.05, w2=rand(8, 128, 64) * 0.05, w_r=rand(32, 128) * 0.05,
+             logits=None, router_bias=torch.zeros(32, device="cuda"), router_scores=mh.make_router_scores("sigmoid", 8, 4, 2))
+    opt = mh.make_adamw_options(LR, B1, B2, EPS, state_bits=bits, seed=8, step_dev=step)
+    return d, b, mh.make_layer_optimizer(d, b, opt, weight_decay=0.1, max_norm=0.5, bias_rate=0.01)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_captured_training_step_replays(bits):
+    torch, mh = _gpu()
+    step, step2 = (torch.zeros(1, dtype=torch.int64, device="cuda") for _ in range(2))
+    d, b, o = _training_layer(torch, mh, bits, step)
+    _, b2, o2 = _training_layer(torch, mh, bits, step2)
+    main, aux, aux2 = (torch.cuda.Stream() for _ in range(3))
+
+    def run(bufs, optimizer, number, side):
+        number.add_(1)
+        mh.moe_layer_forward_backward(d, bufs, torch.cuda.current_stream(), side)
+        mh.moe_layer_update(d, bufs, optimizer)
+
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=main):
+        run(b, o, step, aux)
+    start = b["w1"].clone()
+    for i in range(4):
+        for bufs in (b, b2):
+            bufs["x"].copy_(torch.randn(500, 128, generator=torch.Generator("cuda").manual_seed(i), device="cuda"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        run(b2, o2, step2, aux2)
+        torch.cuda.synchronize()
+        for f in ("w1", "w2", "w_r", "router_bias", "counts", "topk_idx"):
+            assert torch.equal(b[f], b2[f]), (i, f)
+        for f in ("w1", "w2", "w_r"):
+            assert all(torch.equal(o.buffers[f][x], o2.buffers[f][x]) for x in o.buffers[f]), (i, f)
+        assert torch.equal(o.buffers["norm"], o2.buffers["norm"])
+    assert int(step) == 4 and not torch.equal(start, b["w1"])
+
+
+def test_two_updates_at_once():
+    torch, mh = _gpu()
+    pair = [[_Set(torch, mh, [40_000, 999, 3], "master", "bf16", bits, seed=bits) for bits in (32, 8)] for _ in range(2)]
+    norms = [torch.empty(2, device="cuda") for _ in range(4)]
+    wss = [torch.empty(mh.moe_grad_norm_bytes(), dtype=torch.uint8, device="cuda") for _ in range(4)]
+
+    def run(s, norm, ws):
+        mh.moe_grad_norm(s.table, 0.5, norm, ws)
+        mh.moe_adamw_step(mh.make_adamw_options(LR, B1, B2, EPS, step=2, state_bits=s.bits, seed=1, grad_scale=norm[1:]), s.table)
+
+    for s, norm, ws in zip(pair[0], norms, wss):  # one after the other
+        run(s, norm, ws)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for stream, s, norm, ws in zip(streams, pair[1], norms[2:], wss[2:]):  # side by side
+        with torch.cuda.stream(stream):
+            run(s, norm, ws)
+    torch.cuda.synchronize()
+    for a, b in zip(*pair):
+        for p, q in zip(a.parts, b.parts):
+            for f in p:
+                if torch.is_tensor(p[f]):
+                    assert torch.equal(p[f], q[f]), f

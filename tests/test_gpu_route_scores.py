@@ -342,6 +342,25 @@ def test_bias_update(E, rows):
     np.testing.assert_array_equal(c.cpu().numpy(), ors.bias_update(bias, big, 0.5))
 
 
+def test_two_routings_at_once():
+    torch, mh = _gpu()
+    cases = [(20000, 256, dict(score="sigmoid", n_groups=8, topk_groups=4, group_top=2)), (3000, 128, dict(score="softmax"))]
+    want = [_forward(torch, mh, *_draw(T, E, T), 8, how)[1] for T, E, how in cases]
+    dev = []
+    for T, E, how in cases:
+        lg, bias = _draw(T, E, T)
+        d = mh.make_desc(T=T, H=64, I=64, E=E, E_local=E, k=8, n_chunks=1, dtype="f32")
+        dev.append((d, mh.make_router_scores(**how), torch.from_numpy(lg).cuda(), torch.from_numpy(bias).cuda(), _buffers(torch, mh, d), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for d, r, lg, bias, b, stream in dev:
+            mh.moe_route_scores(d, -1, r, lg, bias, *[b[x] for x in NAMES], stream)
+    torch.cuda.synchronize()
+    for (*_, b, _), ref in zip(dev, want):
+        for x in NAMES[:-1]:
+            assert torch.equal(b[x], ref[x]), x
+
+
 def test_on_another_stream_and_in_a_graph():
     torch, mh = _gpu()
     lg, bias = _draw(700, 128, 5)
