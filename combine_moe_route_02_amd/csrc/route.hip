@@ -309,6 +309,13 @@ __global__ __launch_bounds__(kLayoutThreads<kScanned>) void route_layout_kernel(
   const int bl = blockIdx.x % nbpc;
   const ChunkRange cr = chunk_range(T, n, c);
 
+  // wave j < K owns slot j of the block's 64 tokens (lane = token); its experts are on their way during the sums
+  const int64_t t = cr.t0 + (int64_t)bl * kRouteBlock + lane;
+  const bool valid = t < cr.t1;
+  const int j = wave;
+  int el_mine = -1;
+  if (valid && j < K) el_mine = topk_idx[t * K + j] - e0;
+
   if constexpr (kScanned) {
     for (int el = tid; el < El; el += kThreads) {
       base[el] = pre[((int64_t)c * E + e0 + el) * nbpc + bl];
@@ -353,6 +360,8 @@ __global__ __launch_bounds__(kLayoutThreads<kScanned>) void route_layout_kernel(
     }
   }
   __syncthreads();
+  const int el = el_mine >= 0 && el_mine < El ? el_mine : -1;
+  if (el >= 0) atomicOr((unsigned long long*)&mask[el], 1ull << lane);
   if (wave == 0) {  // exclusive scan over the local experts, 64 at a time (their counts are in off[1..El])
     int run = 0;
     for (int b = 0; b < El; b += 64) {
@@ -374,17 +383,6 @@ __global__ __launch_bounds__(kLayoutThreads<kScanned>) void route_layout_kernel(
   if (bl == 0)
     for (int el = tid; el <= El; el += kThreads) offsets[(int64_t)c * (El + 1) + el] = off[el];
 
-  // wave j < K owns slot j of the block's 64 tokens (lane = token)
-  const int64_t t = cr.t0 + (int64_t)bl * kRouteBlock + lane;
-  const bool valid = t < cr.t1;
-  const int j = wave;
-  int el = -1;
-  if (valid && j < K) {
-    el = topk_idx[t * K + j] - e0;
-    if (el >= 0 && el < El) atomicOr((unsigned long long*)&mask[el], 1ull << lane);
-    else el = -1;
-  }
-  __syncthreads();
   if (valid && j < K) {
     int32_t row = -1;
     if (el >= 0) {
