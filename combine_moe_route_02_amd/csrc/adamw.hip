@@ -500,7 +500,8 @@ hipError_t over_batches_of(int n_tensors, const moe_adamw_tensor* t, int64_t til
   }
   return flush();
 }
-// The launch's arguments are copied whole: few tensors take the short list.
+// The launch's arguments are copied whole: few tensors take the short list (100000 weights: 40 tensors 6.0 us, 41 with the
+// long list 6.3).
 template <typename Pick, typename Launch>
 hipError_t over_batches(int n_tensors, const moe_adamw_tensor* t, int64_t tile, Pick pick, Launch launch) {
   return n_tensors <= kAdamFew ? over_batches_of<kAdamFew>(n_tensors, t, tile, pick, launch)

@@ -135,7 +135,7 @@ def test_first_step_of_a_new_run(bits):
 @pytest.mark.parametrize("bits", [32, 8])
 def test_more_tensors_than_a_launch_holds(bits):
     torch, mh = _gpu()
-    sizes = [int(x) for x in np.random.default_rng(3).integers(1, 900, 150)]
+    sizes = [int(x) for x in np.random.default_rng(3).integers(1, 900, 300)]
     s = _Set(torch, mh, sizes, "f32", "bf16", bits, seed=3)
     mh.moe_adamw_step(mh.make_adamw_options(LR, B1, B2, EPS, step=5, state_bits=bits, seed=4), s.table)
     s.check(5, 4)
