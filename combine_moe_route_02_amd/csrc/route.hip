@@ -285,8 +285,15 @@ __global__ __launch_bounds__(kScanThreads) void route_scan_kernel(const int32_t*
 // kScanned: the prefixes and counts come from route_scan (long chunks). Otherwise (chunks of at
 // most kLayoutDirectBlocks blocks) each block sums the histograms before it itself, one wave per
 // local expert, and the blocks share the counts of all E experts between them: quadratic in the
-// chunk length but one launch fewer, which is the cheaper form for short chunks.
-constexpr int kLayoutDirectBlocks = 128;
+// chunk length but one launch fewer, which is the cheaper form for short chunks of few local experts: while
+// a wave has at most four such sums in a row (direct_sums; 256 experts, direct against scanned: 512 tokens with 16 local
+// experts, 3 sums, 13.1 and 13.5 us, with 64, 6 sums, 15.2 and 13.4, with 256, 18 sums, 24.0 and 14.5; 128 tokens with 16,
+// 9 sums, 15.9 and 13.0; 8192 with 16, 4 sums, 15.7 and 16.1, with 32, 6 sums, 16.9 and 16.0).
+constexpr int kLayoutDirectBlocks = 128, kLayoutDirectSums = 4;
+static int direct_sums(int nbpc, int E, int El) {
+  constexpr int waves = kRouteThreads / 64;
+  return ((El + waves - 1) / waves + (E + waves * nbpc - 1) / (waves * nbpc)) * ((nbpc * kSub + 255) / 256);
+}
 // After route_scan a block has nothing for more than the slots' waves to do: half the threads, so that a CU holds four
 // blocks (2048 blocks of 256 experts 13.9 -> 9.7 us).
 template <bool kScanned> constexpr int kLayoutThreads = kScanned ? kRouteThreads / 2 : kRouteThreads;
@@ -445,7 +452,7 @@ hipError_t launch_layout(const int32_t* topk_idx, int32_t* scratch, int32_t* cou
                          hipStream_t s) {
   const int nbpc = route_blocks_per_chunk(T, n);
   int32_t* pre = scratch + route_hist_ints(T, n, E);
-  const bool scanned = nbpc > kLayoutDirectBlocks;
+  const bool scanned = nbpc > kLayoutDirectBlocks || direct_sums(nbpc, E, El) > kLayoutDirectSums;
   if (scanned) {
     MOE_TRACE("route_scan", s);
     MOE_LAUNCH(route_scan_kernel, dim3((unsigned)E, (unsigned)nchunks), dim3(kScanThreads), 0, s, scratch, pre, counts,
