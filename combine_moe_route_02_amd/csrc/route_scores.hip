@@ -186,7 +186,8 @@ MOE_DEV uint64_t eligible_groups(const float* c, uint32_t* keys, int q, const Sc
     }
   }
   uint32_t lo = 0, hi = 0, least = ~0u, most = 0;
-  // up to 32 groups' keys go through LDS, four to a load (0 behind the last)
+  // up to 32 groups' keys go through LDS, four to a load (0 behind the last), instead of a shuffle each (131072 tokens, 8
+  // groups: 75 -> 73.5 us)
   const bool few = a.groups <= kSelInts;
   if (few) {
     keys[q] = 0;
