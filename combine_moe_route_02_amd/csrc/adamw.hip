@@ -389,7 +389,8 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_pack_kernel(int64_t size, 
 }
 
 // Norm of all gradients: FP64 sums of squares, one per workgroup (the workgroups of every launch walk the same tiles
-// in the same order, and a later launch adds to the sums of the ones before), then one workgroup adds them.
+// in the same order, and a later launch adds to the sums of the ones before), then one workgroup adds them. No more
+// workgroups than tiles (1105 weights: 12.9 -> 12.0 us for norm and update).
 constexpr int kNormBlocks = 2048;
 MOE_DEV double wave_sum_d(double x) {
 #pragma unroll
@@ -411,7 +412,7 @@ constexpr int kNormLoads = 4;
 template <typename G> constexpr int kNormVec = 16 / sizeof(G);
 template <typename G> constexpr int kNormTile = kAdamThreads * kNormVec<G> * kNormLoads;
 template <typename G, int N>
-__global__ __launch_bounds__(kAdamThreads) void grad_norm_kernel(const AdamBatch<N> b, uint32_t tiles, bool first,
+__global__ __launch_bounds__(kAdamThreads) void grad_norm_kernel(const AdamBatch<N> b, uint32_t tiles, int written,
                                                                  double* __restrict__ sums) {
   constexpr int V = kNormVec<G>;
   double s = 0.0;
@@ -445,7 +446,7 @@ __global__ __launch_bounds__(kAdamThreads) void grad_norm_kernel(const AdamBatch
       }
   }
   s = group_sum_d(s);
-  if (threadIdx.x == 0) sums[blockIdx.x] = first ? s : sums[blockIdx.x] + s;
+  if (threadIdx.x == 0) sums[blockIdx.x] = (int)blockIdx.x < written ? sums[blockIdx.x] + s : s;
 }
 
 __global__ __launch_bounds__(kAdamThreads) void grad_norm_total_kernel(const double* __restrict__ sums, int count,
@@ -552,13 +553,11 @@ hipError_t launch_grad_norm(int n_tensors, const moe_adamw_tensor* t, double max
         n_tensors, t, bf16 ? kNormTile<uint16_t> : kNormTile<float>, [&](const moe_adamw_tensor& x) { return (x.grad_dtype == MOE_BF16) == (bf16 == 1); },
         [&](const auto& b, uint32_t tiles) {
           constexpr int N = sizeof(b.tile0) / sizeof(uint32_t);
-          // the first launch writes every sum, later ones add to theirs
-          const bool first = count == 0;
-          const int blocks = first ? kNormBlocks : (int)std::min<uint32_t>(tiles, kNormBlocks);
-          count = kNormBlocks;
+          const int blocks = (int)std::min<uint32_t>(tiles, kNormBlocks), written = count;
+          count = std::max(count, blocks);
           MOE_TRACE("grad_norm", s);
-          if (bf16) MOE_LAUNCH((grad_norm_kernel<uint16_t, N>), dim3(blocks), dim3(kAdamThreads), 0, s, b, tiles, first, sums);
-          else MOE_LAUNCH((grad_norm_kernel<float, N>), dim3(blocks), dim3(kAdamThreads), 0, s, b, tiles, first, sums);
+          if (bf16) MOE_LAUNCH((grad_norm_kernel<uint16_t, N>), dim3(blocks), dim3(kAdamThreads), 0, s, b, tiles, written, sums);
+          else MOE_LAUNCH((grad_norm_kernel<float, N>), dim3(blocks), dim3(kAdamThreads), 0, s, b, tiles, written, sums);
           return hipGetLastError();
         });
     if (e != hipSuccess) return e;
