@@ -8,10 +8,11 @@
 // A choice hangs on the last bit of c, so c is defined by FP64 scores, rounded once: two programs, or two kernels,
 // that follow the formula choose the same experts. FP64 exponentials for every logit would take several times the time of
 // reading it, though, and nearly every choice is clear without them: choose() selects by FP32 scores whose error has a
-// bound. Where two neighbours in the order are nearer than that (one token of a thousand), their exact c puts the chosen
-// experts and the first one left out in order; where two groups are (one of 25000), or several scores in a row, or two are
-// one, the token's wave goes through choose_exact(). (All of these together took 17 of 86 us at 131072 tokens of 256
-// experts while all went there and took every expert's exact c: one such wave late in the launch holds up its end.)
+// bound. Where two neighbours in the order are nearer than that (one token of 2000), their exact c puts the chosen
+// experts and the first one left out in order; where two groups are (one of 25000), or the last one chosen and what is behind
+// the first one left out, or two keys are one, the token's wave goes through choose_exact(). (All of these together took 17
+// of 86 us at 131072 tokens of 256 experts while all went there and took every expert's exact c: one such wave late in the
+// launch holds up its end.)
 //
 // 16 lanes hold a token's row in registers (4 tokens per wave, float4 loads), and arithmetic bounds the kernel, not HBM. Per
 // lane the row's share becomes a sorted list of its five largest: a score's FP32 bits, the last few of which give way to the
@@ -355,8 +356,9 @@ MOE_DEV void load_lds(const float* row, int q, float (&x)[NE]) {
 // itself by |c|: 3.72 + 2 |c| each, so that sums further apart than 2 (3.72 + 2 |c|) < 16 max(1, |c|) are in order.
 // Softmax: the differences and products below an exponential move it by 2.2 x e^-x <= 0.82, its ulp by 2, relative to a
 // largest score p = 1 / sum; the sum (in FP64) by its terms' 3, the reciprocal and the product by 3: 9 p + 2 |c| each.
-// The bits that hold an element's number add 2 NE units of a sum's
-// size. Ties and sums within the margin go to choose_exact.
+// That is a bound for sums: keys, whose last bits hold an element's number, lie up to NE - 1 steps (2 (NE - 1) units of
+// a sum's size) from theirs on either side, so that they only say which sums to look at. Sums within the margin, ties
+// among them, go to order_exact or, where they are not all among the slots, to choose_exact.
 // m, inv: softmax: the row's largest logit and 1 / the sum of exponentials (0 where no logit is above -inf).
 template <int NE, bool VEC>
 MOE_DEV int choose(const Row& row, float (&x)[NE], const float* bias, const float* b_row, float* c, uint32_t* slots, int E,
@@ -491,21 +493,29 @@ MOE_DEV int choose(const Row& row, float (&x)[NE], const float* bias, const floa
     const uint32_t bits = mine.x >> 31 ? mine.x : ~mine.x;  // (of a negative score the key holds the complement)
     const int i = (int)(bits & kNumber);
     id = VEC ? 64 * (i / 4) + 4 * (int)mine.y + i % 4 : kGroup * i + (int)mine.y;
-    bool near = false;
-    if (q + 1 < rounds) {  // whether slot q and the next are clear of each other
-      const float u = key_logit(mine.x), v = key_logit(slots[2 * q + 2]);
+    // The keys propose an order, and the sums in LDS tell whether it holds: slots 0 .. K are clear of each other where each
+    // sum is above the next by more than the margin (a sum below the next one, which its number put in front, is not).
+    const float mine_c = q < rounds ? c[id] : 0.f;
+    const float next_c = dpp_f<0x101>(mine_c);  // of lane q + 1
+    auto above = [&](float u, float v) {
       const float size = fmaxf(fabsf(u), fabsf(v));
-      near = !(u - v > margin * (a.softmax ? inv + size : fmaxf(1.f, size)) + 2 * NE * kUnit * size + 0x1p-100f);
+      return u - v > margin * (a.softmax ? inv + size : fmaxf(1.f, size)) + 0x1p-100f;
+    };
+    const bool near = q < K && q + 1 < rounds && !above(mine_c, next_c);
+    // No expert behind slot K has a key above slot K + 1's, so none has a sum above all that share that key but for the
+    // number. The K slots in front are clear of these, or the choice is not among slots 0 .. K.
+    bool more = false;
+    if (rounds > K + 1) {
+      const float least = row_min(q < K ? mine_c : __builtin_huge_valf());
+      more = !above(least, key_logit(slots[2 * (K + 1)] | kNumber));
     }
-    // The last one chosen near the first left out is settled between them; near the second left out too, it is not.
-    const uint32_t nears = (uint32_t)(ballot(near) >> (threadIdx.x & 48)) & 0xffffu;
-    exact = twins || any_lane(row && ((nears >> (K - 1)) & 3) == 3);
+    exact = twins || any_lane(row && more);
     if (exact) {
       // What is not below the last one popped, with room for its error. (Twins pop more than one a round: the last slot may
       // hold no expert, or a NaN where the lists ran out.)
       const float v = key_logit(slots[2 * (rounds - 1)]);
       cut = fmaxf(v - 64.f * (margin + 2 * NE * kUnit) * fmaxf(1.f, fabsf(v)), kLeast);
-    } else if (any_lane(row && (nears & ((1u << K) - 1)))) {
+    } else if (any_lane(row && near)) {
       id = order_exact(row, bias, slots, id, E, min(K + 1, rounds), q, a);
     }
   }

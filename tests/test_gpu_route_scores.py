@@ -222,6 +222,59 @@ def test_nearest_neighbours_are_ordered_by_their_exact_sums():
             _check(d, b, lg, bias, how)
 
 
+def _close_rows(rng, T, E, score, above):
+    """Rows whose FP32 sums lie around an edge where the low bits that a lane's list gives to an element's number run over:
+    in every fourth row two to four experts within two FP32 steps of the edge, those with the highest and the lowest number
+    among them, behind `above` clear ones (the other rows are clear: what one row of a wave's four needs settled, all
+    get). Returns logits [T, E] and the bias [E]."""
+    ne = 4
+    while ne * 16 < E:
+        ne *= 2
+    e = np.arange(E)
+    number = 4 * (e // 64) + e % 4 if E % 4 == 0 else e // 16
+    sink, clear = E // 2, E // 2 + 1 + np.arange(above)
+    rest = np.setdiff1d(e, np.append(clear, sink))
+    low, high = rest[number[rest] == 0], rest[number[rest] == number[rest].max()]
+    if score == "sigmoid":
+        bias, span = rng.uniform(0.3, 0.4, E), 0.25
+    else:
+        bias, span = rng.uniform(0.78, 0.83, E), 0.04
+        bias[sink] = -1.0
+    bias[clear] = 1.5 + 0.01 * np.arange(above)
+    bias = bias.astype(np.float32)
+    want = np.full((T, E), 1e-7 if score == "softmax" else 0.007)  # the scores
+    x = rng.uniform(1.0, 1.0 + span, T).astype(np.float32)
+    x = (x.view(np.uint32) | np.uint32(ne - 1)).view(np.float32).astype(np.float64)  # the last value below an edge
+    for t in range(T):
+        more = rng.choice(rest, rng.integers(0, 4), replace=False)
+        near = np.concatenate([[rng.choice(low)], [rng.choice(high)], np.setdiff1d(more, np.append(low, high))])
+        near = near[:1 if t % 4 else 4 if score == "sigmoid" else 3].astype(int)
+        want[t, near] = x[t] + rng.uniform(-0.7, 1.7, near.size) * 2.0 ** -23 - bias[near]
+    if score == "sigmoid":
+        return np.log(want / (1.0 - want)).astype(np.float32), bias
+    want[:, sink] = 0.0
+    want[:, sink] = 1.0 - want.sum(axis=1)
+    assert want.min() > 0
+    return np.log(want).astype(np.float32), bias
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,above,k,G,tg", [(9000, 256, 0, 1, 1, 1), (3000, 256, 6, 8, 1, 1), (60, 256, 0, 1, 1, 1), (3000, 512, 0, 1, 1, 1),
+                                              (2000, 512, 3, 5, 1, 1), (2000, 1024, 0, 1, 1, 1), (2000, 1024, 2, 3, 1, 1), (2000, 250, 1, 2, 1, 1),
+                                              (2000, 1000, 0, 2, 1, 1), (2000, 64, 0, 1, 1, 1), (2000, 128, 2, 4, 1, 1), (3000, 256, 0, 2, 8, 7),
+                                              (2000, 1024, 0, 1, 4, 3)])
+def test_sums_a_step_apart_whose_keys_lie_further(score, T, E, above, k, G, tg):
+    torch, mh = _gpu()
+    print(f"[route_scores] close {score, T, E, above, k, G, tg}", flush=True)
+    lg, bias = _close_rows(np.random.default_rng(E + k), T, E, score, above)
+    how = dict(score=score, n_groups=G, topk_groups=tg, group_top=1)
+    want = ors.choose(ors.scores(lg, score), bias, k, G, tg, 1)
+    d, b = _forward(torch, mh, lg, bias, k, how)
+    bad = (b["topk_idx"].cpu().numpy() != want).any(axis=1)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3].ravel(), b["topk_idx"].cpu().numpy()[bad][:3], want[bad][:3])
+    _check(d, b, lg, bias, how)
+
+
 def test_no_tokens():
     torch, mh = _gpu()
     d, b = _forward(torch, mh, np.zeros((0, 16), np.float32), None, 2, dict(score="sigmoid"), n=2, El=4)
