@@ -476,8 +476,9 @@ MOE_DEV int choose(const Row& row, float (&x)[NE], const float* bias, const floa
     bool twins = play(0);
     uint2 mine = *(const uint2*)(slots + 2 * q);
     if constexpr (NE > kTopList) {
-      while (any_lane(row && q < rounds && mine.x == kUnknown)) {
-        // from the first unknown slot of the wave's tokens on, with what each lane has left below its last
+      while (!twins && any_lane(row && q < rounds && mine.x == kUnknown)) {
+        // From the first unknown slot of the wave's tokens on, with what each lane has left below its last. (Of twins a
+        // slot holds one only: the other's lane could not tell what it has left.)
         const uint64_t unknown = ballot(row && q < rounds && mine.x == kUnknown);
         int s0 = rounds;
         for (uint64_t u = unknown; u; u &= u - 1) s0 = min(s0, (int)(__ffsll((unsigned long long)u) - 1) & (kGroup - 1));
@@ -511,8 +512,9 @@ MOE_DEV int choose(const Row& row, float (&x)[NE], const float* bias, const floa
     }
     exact = twins || any_lane(row && more);
     if (exact) {
-      // What is not below the last one popped, with room for its error. (Twins pop more than one a round: the last slot may
-      // hold no expert, or a NaN where the lists ran out.)
+      // What is not below the last one popped, with room for its error: at least as many were popped as there are rounds.
+      // (Twins pop more than one a round: the last slot may hold no expert, or a NaN where a list ran out, and then every
+      // eligible one is looked at.)
       const float v = key_logit(slots[2 * (rounds - 1)]);
       cut = fmaxf(v - 64.f * (margin + 2 * NE * kUnit) * fmaxf(1.f, fabsf(v)), kLeast);
     } else if (any_lane(row && near)) {

@@ -275,6 +275,30 @@ def test_sums_a_step_apart_whose_keys_lie_further(score, T, E, above, k, G, tg):
     _check(d, b, lg, bias, how)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,tg", [(128, 1, 1), (256, 1, 1), (256, 8, 7), (252, 1, 1), (250, 1, 1), (1024, 1, 1)])
+def test_equal_scores_in_rows_where_one_lane_has_most(score, E, G, tg):
+    """Ties between experts of different lanes with the same number, and more of the largest in one lane than its list
+    holds: the experts chosen are distinct and the definition's."""
+    torch, mh = _gpu()
+    print(f"[route_scores] ties {score, E, G, tg}", flush=True)
+    T, k = 1200, 8
+    rng = np.random.default_rng(E + G)
+    e = np.arange(E)
+    lane, number = ((e // 4) % 16, 4 * (e // 64) + e % 4) if E % 4 == 0 else (e % 16, e // 16)
+    lg = rng.uniform(-2, -1, (T, E)).astype(np.float32)
+    for t in range(0, T, 2):
+        own = rng.permutation(e[lane == rng.integers(0, 16)])[:rng.integers(4, 9)]
+        lg[t, own] = 1.0 + rng.permutation(own.size) / 16.0  # in any order with the ties
+        for _ in range(rng.integers(1, 4)):
+            same = rng.permutation(e[number == rng.integers(0, number.max())])
+            lg[t, same[:rng.integers(2, 5)]] = rng.choice([0.5, 1.03125, 2.0])
+    for bias in (None, np.full(E, np.float32(0.25))):
+        how = dict(score=score, n_groups=G, topk_groups=tg, group_top=2)
+        d, b = _forward(torch, mh, lg, bias, k, how)
+        _check(d, b, lg, bias, how)
+
+
 def test_no_tokens():
     torch, mh = _gpu()
     d, b = _forward(torch, mh, np.zeros((0, 16), np.float32), None, 2, dict(score="sigmoid"), n=2, El=4)
