@@ -439,11 +439,9 @@ __global__ __launch_bounds__(kAdamThreads) void grad_norm_kernel(const AdamBatch
     }
 #pragma unroll
     for (int u = 0; u < kNormLoads; ++u)
+      // squares in FP64: those of BF16 values would be exact in FP32's digits, but not within its range
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if constexpr (V == 8) s += (double)(g[u][j] * g[u][j]);  // (a product of two BF16 values is exact in FP32)
-        else s = __builtin_fma((double)g[u][j], (double)g[u][j], s);
-      }
+      for (int j = 0; j < V; ++j) s = __builtin_fma((double)g[u][j], (double)g[u][j], s);
   }
   s = group_sum_d(s);
   if (threadIdx.x == 0) sums[blockIdx.x] = (int)blockIdx.x < written ? sums[blockIdx.x] + s : s;

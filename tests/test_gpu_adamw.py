@@ -350,6 +350,20 @@ def test_clipped_step(bits):
 @pytest.mark.parametrize("n", [1, 255, 256, 257, 2048, 10_001])
 def test_pack_and_unpack(n):
     torch, mh = _gpu()
+@pytest.mark.parametrize("gdt", ["f32", "bf16"])
+@pytest.mark.parametrize("sizes,value", [([1], 3e38), ([1000], 1e25), ([5000, 3], 2e19), ([1000, 70], 1e-25), ([9], 2.0 ** -126), ([300] * 50, 3e-22)])
+def test_norm_of_gradients_whose_squares_leave_fp32(sizes, value, gdt):
+    """The sum is FP64 throughout: the norm is good to its own rounding, 2^-24, and the sums' far smaller ones."""
+    torch, mh = _gpu()
+    dt = torch.float32 if gdt == "f32" else torch.bfloat16
+    grads = [torch.full((n,), value, device="cuda").to(dt) for n in sizes]
+    want = float(grads[0][0]) * np.sqrt(sum(sizes))
+    out, ws = torch.empty(2, device="cuda"), torch.empty(mh.moe_grad_norm_bytes(), dtype=torch.uint8, device="cuda")
+    mh.moe_grad_norm(mh.make_adamw_tensors([dict(grad=g) for g in grads]), want * 0.25, out, ws)
+    norm, factor = out.cpu().tolist()
+    assert abs(norm - want) <= 2 * F * want and abs(factor - 0.25) <= 2 * F
+
+
     rng = np.random.default_rng(n)
     m = (rng.standard_normal(n) * np.exp(3 * rng.standard_normal(n))).astype(np.float32)
     v = (m * rng.standard_normal(n)).astype(np.float32) ** 2
