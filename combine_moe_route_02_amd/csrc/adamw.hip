@@ -222,7 +222,7 @@ MOE_DEV void pack4(const float* m, const float* v, const uint32_t* rnd, int i, i
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     bm = max(bm, __float_as_uint(m[j]) & 0x7fffffffu);
-    bv = max(bv, __float_as_uint(v[j]));  // (no sign but a NaN's)
+    bv = max(bv, __float_as_uint(v[j]) & (NEAREST ? 0x7fffffffu : ~0u));  // (a step's v': no sign but a NaN's)
   }
   bv &= 0x7fffffffu;
   const float sm = block_scale(block_max(bm)), sv = block_scale(block_max(bv));

@@ -402,6 +402,22 @@ def test_every_code_stands_for_itself():
         flat[:x.size] = x
         full[:, 1:] = flat.reshape(blocks, 255)
         full = full.reshape(-1)
+def test_pack_of_negative_zeros():
+    """A second average of -0 counts as 0, also beside its block's largest."""
+    torch, mh = _gpu()
+    n = 1000
+    v = np.square(np.random.default_rng(3).standard_normal(n)).astype(np.float32)
+    v[1::4] = -0.0
+    v[[2, 258, 514, 770]] = 50.0
+    mc, vc = torch.empty(n, dtype=torch.int8, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
+    ms, vs = torch.empty(4, device="cuda"), torch.empty(4, device="cuda")
+    mh.moe_adamw_pack(n, torch.from_numpy(-v).cuda(), torch.from_numpy(v).cuda(), mc, ms, vc, vs)
+    for c, s, x, which in ((mc, ms, -v, "m"), (vc, vs, v, "v")):
+        want, ws = oa.encode(x, which)
+        np.testing.assert_array_equal(s.cpu().numpy(), ws)
+        np.testing.assert_array_equal(c.cpu().numpy(), want)
+
+
         n = full.size
         mc, vc = torch.empty(n, dtype=torch.int8, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
         ms, vs = torch.empty(blocks, device="cuda"), torch.empty(blocks, device="cuda")
