@@ -273,6 +273,23 @@ def test_gradients_that_are_not_finite_stay_where_they_are(kind, bits):
         assert torch.isnan(v[768:]).all()  # (3e38)^2
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("kind", ["f32", "master", "bf16"])
+def test_a_square_past_fp32_moves_nothing_but_the_decay(kind, bits):
+    """v' is infinite, the update 0: w (1 - lr wd) is left, two roundings of FP32, and in BF16 one of the two neighbours."""
+    torch, mh = _gpu()
+    s = _Set(torch, mh, [1000], kind, "f32", bits, seed=6)
+    p = s.parts[0]
+    p["grad"][999] = 3e38
+    mh.moe_adamw_step(mh.make_adamw_options(LR, B1, B2, EPS, step=3, state_bits=bits), s.table)
+    torch.cuda.synchronize()
+    want = float(s.w0[0][999]) * (1 - LR * p["lr_scale"] * p["weight_decay"])
+    got = float(_np(p["master"] if kind == "master" else p["w"])[999])
+    assert abs(got - want) <= (2.0 ** -7 if kind == "bf16" else 2 * F) * abs(want)
+    if kind == "master":
+        assert torch.equal(p["w"], p["master"].to(torch.bfloat16))
+
+
 def test_a_scale_that_is_not_finite_leaves_everything():
     torch, mh = _gpu()
     for bits in (32, 8):
@@ -333,6 +350,20 @@ def test_norm_of_mixed_types_and_of_nothing():
     np.testing.assert_allclose(out.cpu().numpy(), [np.float32(3e38), 1 / np.float64(np.float32(3e38))], rtol=2 * F)
 
 
+@pytest.mark.parametrize("gdt", ["f32", "bf16"])
+@pytest.mark.parametrize("sizes,value", [([1], 3e38), ([1000], 1e25), ([5000, 3], 2e19), ([1000, 70], 1e-25), ([9], 2.0 ** -126), ([300] * 50, 3e-22)])
+def test_norm_of_gradients_whose_squares_leave_fp32(sizes, value, gdt):
+    """The sum is FP64 throughout: the norm is good to its own rounding, 2^-24, and the sums' far smaller ones."""
+    torch, mh = _gpu()
+    dt = torch.float32 if gdt == "f32" else torch.bfloat16
+    grads = [torch.full((n,), value, device="cuda").to(dt) for n in sizes]
+    want = float(grads[0][0]) * np.sqrt(sum(sizes))
+    out, ws = torch.empty(2, device="cuda"), torch.empty(mh.moe_grad_norm_bytes(), dtype=torch.uint8, device="cuda")
+    mh.moe_grad_norm(mh.make_adamw_tensors([dict(grad=g) for g in grads]), want * 0.25, out, ws)
+    norm, factor = out.cpu().tolist()
+    assert abs(norm - want) <= 2 * F * want and abs(factor - 0.25) <= 2 * F
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_clipped_step(bits):
     torch, mh = _gpu()
@@ -350,20 +381,6 @@ def test_clipped_step(bits):
 @pytest.mark.parametrize("n", [1, 255, 256, 257, 2048, 10_001])
 def test_pack_and_unpack(n):
     torch, mh = _gpu()
-@pytest.mark.parametrize("gdt", ["f32", "bf16"])
-@pytest.mark.parametrize("sizes,value", [([1], 3e38), ([1000], 1e25), ([5000, 3], 2e19), ([1000, 70], 1e-25), ([9], 2.0 ** -126), ([300] * 50, 3e-22)])
-def test_norm_of_gradients_whose_squares_leave_fp32(sizes, value, gdt):
-    """The sum is FP64 throughout: the norm is good to its own rounding, 2^-24, and the sums' far smaller ones."""
-    torch, mh = _gpu()
-    dt = torch.float32 if gdt == "f32" else torch.bfloat16
-    grads = [torch.full((n,), value, device="cuda").to(dt) for n in sizes]
-    want = float(grads[0][0]) * np.sqrt(sum(sizes))
-    out, ws = torch.empty(2, device="cuda"), torch.empty(mh.moe_grad_norm_bytes(), dtype=torch.uint8, device="cuda")
-    mh.moe_grad_norm(mh.make_adamw_tensors([dict(grad=g) for g in grads]), want * 0.25, out, ws)
-    norm, factor = out.cpu().tolist()
-    assert abs(norm - want) <= 2 * F * want and abs(factor - 0.25) <= 2 * F
-
-
     rng = np.random.default_rng(n)
     m = (rng.standard_normal(n) * np.exp(3 * rng.standard_normal(n))).astype(np.float32)
     v = (m * rng.standard_normal(n)).astype(np.float32) ** 2
@@ -385,6 +402,22 @@ def test_norm_of_gradients_whose_squares_leave_fp32(sizes, value, gdt):
     assert (fm[n:] == 5.0).all() and (fv[n:] == 5.0).all()
 
 
+def test_pack_of_negative_zeros():
+    """A second average of -0 counts as 0, also beside its block's largest."""
+    torch, mh = _gpu()
+    n = 1000
+    v = np.square(np.random.default_rng(3).standard_normal(n)).astype(np.float32)
+    v[1::4] = -0.0
+    v[[2, 258, 514, 770]] = 50.0
+    mc, vc = torch.empty(n, dtype=torch.int8, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
+    ms, vs = torch.empty(4, device="cuda"), torch.empty(4, device="cuda")
+    mh.moe_adamw_pack(n, torch.from_numpy(-v).cuda(), torch.from_numpy(v).cuda(), mc, ms, vc, vs)
+    for c, s, x, which in ((mc, ms, -v, "m"), (vc, vs, v, "v")):
+        want, ws = oa.encode(x, which)
+        np.testing.assert_array_equal(s.cpu().numpy(), ws)
+        np.testing.assert_array_equal(c.cpu().numpy(), want)
+
+
 def test_every_code_stands_for_itself():
     """All levels, and values between them on both sides of each middle, as one block's shares of 1."""
     torch, mh = _gpu()
@@ -402,22 +435,6 @@ def test_every_code_stands_for_itself():
         flat[:x.size] = x
         full[:, 1:] = flat.reshape(blocks, 255)
         full = full.reshape(-1)
-def test_pack_of_negative_zeros():
-    """A second average of -0 counts as 0, also beside its block's largest."""
-    torch, mh = _gpu()
-    n = 1000
-    v = np.square(np.random.default_rng(3).standard_normal(n)).astype(np.float32)
-    v[1::4] = -0.0
-    v[[2, 258, 514, 770]] = 50.0
-    mc, vc = torch.empty(n, dtype=torch.int8, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
-    ms, vs = torch.empty(4, device="cuda"), torch.empty(4, device="cuda")
-    mh.moe_adamw_pack(n, torch.from_numpy(-v).cuda(), torch.from_numpy(v).cuda(), mc, ms, vc, vs)
-    for c, s, x, which in ((mc, ms, -v, "m"), (vc, vs, v, "v")):
-        want, ws = oa.encode(x, which)
-        np.testing.assert_array_equal(s.cpu().numpy(), ws)
-        np.testing.assert_array_equal(c.cpu().numpy(), want)
-
-
         n = full.size
         mc, vc = torch.empty(n, dtype=torch.int8, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
         ms, vs = torch.empty(blocks, device="cuda"), torch.empty(blocks, device="cuda")
