@@ -15,15 +15,16 @@
 //                the lower index), then K rounds of a 16-lane max merge the lists. A histogram
 //                over all E experts per 16 tokens is summed in LDS with integer atomics (the sum
 //                does not depend on their order).
-//   route_scan   (chunks of more than 128 64-token blocks) one wave per expert and chunk: the
-//                chunk's total per expert (counts) and, per 64-token block, the rows that the
-//                chunk's earlier blocks give the expert (an exclusive scan of the block sums, one
-//                block per lane), so the work is linear in the chunk's tokens.
+//   route_scan   (chunks of more than 128 64-token blocks, and shorter ones where route_layout's waves would take
+//                more than four sums in a row) one wave per expert and chunk: the chunk's total per expert (counts)
+//                and, per 64-token block, the rows that the chunk's earlier blocks give the expert (each lane sums a
+//                range of blocks, one exclusive scan over the lanes), so the work is linear in the chunk's tokens.
 //   route_layout per 64-token block: local offsets from the counts, then each token's rank among
 //                the block's earlier tokens choosing the same expert from a 64-bit ballot mask
 //                (popcount below the lane) plus the rows of the earlier blocks; one wave per top-k
-//                slot. For shorter chunks the block sums the earlier blocks' histograms itself
+//                slot. Without route_scan the block sums the earlier blocks' histograms itself
 //                (one launch fewer).
+#include <algorithm>
 #include <mutex>
 #include <type_traits>
 
@@ -455,10 +456,12 @@ hipError_t launch_layout(const int32_t* topk_idx, int32_t* scratch, int32_t* cou
   const bool scanned = nbpc > kLayoutDirectBlocks || direct_sums(nbpc, E, El) > kLayoutDirectSums;
   if (scanned) {
     MOE_TRACE("route_scan", s);
-    MOE_LAUNCH(route_scan_kernel, dim3((unsigned)E, (unsigned)nchunks), dim3(kScanThreads), 0, s, scratch, pre, counts,
-               E, chunk0, nbpc);
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
+    for (int ch = 0; ch < nchunks; ch += 65535) {  // chunks of a launch: the grid's y
+      MOE_LAUNCH(route_scan_kernel, dim3((unsigned)E, (unsigned)std::min(nchunks - ch, 65535)), dim3(kScanThreads), 0, s,
+                 scratch, pre, counts, E, chunk0 + ch, nbpc);
+      const hipError_t err = hipGetLastError();
+      if (err != hipSuccess) return err;
+    }
   }
   size_t sm2 = (size_t)El * 4 + (size_t)(El + 1) * 4 + 8 + (size_t)El * 8;
   MOE_TRACE("route_layout", s);

@@ -108,6 +108,36 @@ def test_many_chunks_without_local_experts():
     _check(d, b, lg, bias, how)
 
 
+def test_more_chunks_than_one_scan_takes():
+    """Chunks past 65535 whose histograms are scanned first: moe_route with short ones, score routing with two workgroups each."""
+    torch, mh = _gpu()
+    T, E, k, n = 131, 128, 4, 70000
+    lg, _ = _draw(T, E, 2)
+    d = mh.make_desc(T=T, H=64, I=64, E=E, E_local=0, k=k, n_chunks=n, dtype="f32")
+    b = _buffers(torch, mh, d)
+    mh.moe_route(d, -1, torch.from_numpy(lg).cuda(), *[b[x] for x in NAMES])
+    idx = oracle.route(lg, k)[0]
+    np.testing.assert_array_equal(b["topk_idx"].cpu().numpy(), idx)
+    want = np.zeros((n, E), np.int32)
+    np.add.at(want, (np.arange(T)[:, None], idx), 1)
+    np.testing.assert_array_equal(b["counts"].cpu().numpy(), want)
+    assert not b["offsets"].any() and (b["row_of"] == -1).all()
+    E, tc = 260, 17
+    T = tc * n
+    d = mh.make_desc(T=T, H=64, I=64, E=E, E_local=0, k=2, n_chunks=n, dtype="f32")
+    b = _buffers(torch, mh, d)
+    x = torch.zeros(T, E, device="cuda")
+    first = torch.arange(n, device="cuda").repeat_interleave(tc) % E  # one expert per chunk in front, and the lowest other
+    x.scatter_(1, first[:, None], 1.0)
+    mh.moe_route_scores(d, -1, mh.make_router_scores(score="sigmoid"), x, None, *[b[i] for i in NAMES])
+    assert torch.equal(b["topk_idx"], torch.stack([first, (first == 0).long()], 1).int())
+    counts = torch.zeros(n, E, dtype=torch.int32, device="cuda")
+    c = torch.arange(n, device="cuda")
+    counts[c, c % E] = tc
+    counts[c, (c % E == 0).long()] = tc
+    assert torch.equal(b["counts"], counts) and not b["offsets"].any()
+
+
 @pytest.mark.parametrize("E", [64, 256, 512])
 def test_rows_off_their_alignment(E):
     torch, mh = _gpu()
