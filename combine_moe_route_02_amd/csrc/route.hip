@@ -258,13 +258,15 @@ __global__ __launch_bounds__(kScanThreads) void route_scan_kernel(const int32_t*
   const int e = blockIdx.x;
   const int c = chunk0 + blockIdx.y;
   const int nh = nbpc * kSub;
-  const int4* he = (const int4*)(block_hist + ((int64_t)c * E + e) * nh);
+  // (a workspace of moe_route may start at any multiple of 4 bytes; 16-byte loads need no more)
+  typedef int32_t hist4_t __attribute__((ext_vector_type(4), aligned(4)));
+  const hist4_t* he = (const hist4_t*)(block_hist + ((int64_t)c * E + e) * nh);
   int32_t* pe = pre + ((int64_t)c * E + e) * nbpc;
   const int per = (nbpc + 63) / 64, b0 = lane * per, b1 = min(b0 + per, nbpc);
   int sum = 0;
 #pragma unroll 8
   for (int b = b0; b < b1; ++b) {
-    const int4 h = he[b];
+    const hist4_t h = he[b];
     sum += h.x + h.y + h.z + h.w;
   }
   int incl = sum;  // inclusive scan over the wave's lanes
@@ -276,7 +278,7 @@ __global__ __launch_bounds__(kScanThreads) void route_scan_kernel(const int32_t*
   int run = incl - sum;
 #pragma unroll 8
   for (int b = b0; b < b1; ++b) {
-    const int4 h = he[b];
+    const hist4_t h = he[b];
     pe[b] = run;
     run += h.x + h.y + h.z + h.w;
   }
@@ -289,7 +291,9 @@ __global__ __launch_bounds__(kScanThreads) void route_scan_kernel(const int32_t*
 // chunk length but one launch fewer, which is the cheaper form for short chunks of few local experts: while
 // a wave has at most four such sums in a row (direct_sums; 256 experts, direct against scanned: 512 tokens with 16 local
 // experts, 3 sums, 13.1 and 13.5 us, with 64, 6 sums, 15.2 and 13.4, with 256, 18 sums, 24.0 and 14.5; 128 tokens with 16,
-// 9 sums, 15.9 and 13.0; 8192 with 16, 4 sums, 15.7 and 16.1, with 32, 6 sums, 16.9 and 16.0).
+// 9 sums, 15.9 and 13.0; 8192 with 16, 4 sums, 15.7 and 16.1, with 32, 6 sums, 16.9 and 16.0; moe_route of one token and
+// 128 experts with 16 local, 9 sums, 12.0 and 9.9, with 128, 16 sums, 16.0 and 10.3, 64 tokens and 64 experts with 8, 5
+// sums, 10.4 and 9.9).
 constexpr int kLayoutDirectBlocks = 128, kLayoutDirectSums = 4;
 static int direct_sums(int nbpc, int E, int El) {
   constexpr int waves = kRouteThreads / 64;

@@ -172,3 +172,26 @@ def test_route_long_chunks_scanned_layout(cfg):
         assert nbpc > 128, nbpc
         print(f"[long] {cfg.name} blocks per chunk {nbpc}", flush=True)
         _check_route(cfg, d, b, lg)
+
+
+def test_workspace_at_any_multiple_of_four():
+    """Short chunks whose histograms are scanned: the same integers from a workspace off its 16 bytes."""
+    _require_gpu()
+    import torch
+    import combine_moe_route_02_amd as mh
+    T, E, k, n = 333, 128, 8, 2
+    d = mh.make_desc(T=T, H=64, I=64, E=E, E_local=E, k=k, n_chunks=n, dtype="f32")
+    lg = torch.from_numpy(np.random.default_rng(4).standard_normal((T, E)).astype(np.float32)).cuda()
+    b = mh.allocate(d, backward=False)
+    names = ("topk_idx", "gates", "counts", "offsets", "row_of", "src_token")
+    room = torch.empty(mh.workspace_bytes(d)["route_scratch"] + 16, dtype=torch.uint8, device="cuda")
+    want = None
+    for off in (0, 4, 8, 12):
+        for x in names:
+            b[x].fill_(-5)
+        room.fill_(0xff)
+        mh.moe_route(d, -1, lg, *[b[x] for x in names], room[off:])
+        got = [b[x].clone() for x in names]
+        want = got if want is None else want
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), off
+    assert int(want[2].sum()) == T * k
