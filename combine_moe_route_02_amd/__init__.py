@@ -431,12 +431,29 @@ def _pay(t) -> int:
     return MOE_F32 if name == "torch.float32" else MOE_BF16
 
 
+def _device_scalar(name, x, dtype):
+    """Address of a device scalar; its type and place are checked, which the bare address does not carry."""
+    if x is None or isinstance(x, int):
+        return x
+    if str(x.dtype) != dtype:
+        raise TypeError(f"{name} is {dtype[6:]}, not {x.dtype}")
+    if x.numel() < 1:
+        raise ValueError(f"{name} is empty")
+    if not (x.is_cuda or x.is_pinned()):
+        raise ValueError(f"{name} must be on the GPU")
+    return x.data_ptr()
+
+
 def make_adamw_options(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, state_bits=32, seed=0, lr_dev=None, step_dev=None,
                        grad_scale=None) -> MoeAdamwOptions:
     """Options of moe_adamw_step. ``step`` counts from 1: set ``options.step`` before each call, or pass ``step_dev`` (and
-    ``lr_dev``), device scalars that the kernels read, where the call is captured into a graph."""
-    return MoeAdamwOptions(lr, beta1, beta2, eps, _ptr(lr_dev), _ptr(step_dev), _ptr(grad_scale), step, state_bits,
-                           seed & 0xffffffff)
+    ``lr_dev``), device scalars that the kernels read (int64 and float64; ``grad_scale`` is float32), where the call is
+    captured into a graph. The options keep references to them."""
+    o = MoeAdamwOptions(lr, beta1, beta2, eps, _device_scalar("lr_dev", lr_dev, "torch.float64"),
+                        _device_scalar("step_dev", step_dev, "torch.int64"),
+                        _device_scalar("grad_scale", grad_scale, "torch.float32"), step, state_bits, seed & 0xffffffff)
+    o.scalars = (lr_dev, step_dev, grad_scale)
+    return o
 
 
 class AdamwTensors:
@@ -537,6 +554,7 @@ def make_layer_optimizer(d: MoeDesc, bufs, options, master=True, weight_decay=0.
     import torch
     o = MoeLayerOptimizer()
     o.adamw = options
+    o.options = options  # (o.adamw is a copy without the references that the options keep)
     o.buffers = {}
     for f in ("w1", "w2", "w_r"):
         w = bufs[f]

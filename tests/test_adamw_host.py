@@ -125,6 +125,55 @@ def test_tables_are_checked():
             mh.moe_adamw_step(mh.make_adamw_options(1e-3, state_bits=bits), mh.make_adamw_tensors([part]), 0)
 
 
+class _Scalar:
+    """A tensor on a GPU, as far as the options look at one."""
+    is_cuda = True
+
+    def __init__(self, dtype, n=1, address=4096):
+        self.dtype, self.n, self.address = dtype, n, address
+
+    def numel(self):
+        return self.n
+
+    def data_ptr(self):
+        return self.address
+
+
+def test_options_keep_their_device_scalars():
+    torch = pytest.importorskip("torch")
+    import gc
+    import weakref
+    kinds = dict(lr_dev=torch.float64, step_dev=torch.int64, grad_scale=torch.float32)
+    made = {f: _Scalar(t, address=64 * (i + 1)) for i, (f, t) in enumerate(kinds.items())}
+    o = mh.make_adamw_options(1e-3, **made)
+    assert [getattr(o, f) for f in kinds] == [64, 128, 192]
+    alive = [weakref.ref(x) for x in made.values()]
+    made.clear()
+    gc.collect()
+    assert all(r() is not None for r in alive)
+    bufs = {f: torch.zeros(256) for f in ("w1", "w2", "w_r")}
+    layer = mh.make_layer_optimizer(_layer_desc(), bufs, o, device="cpu")
+    del o
+    gc.collect()
+    assert all(r() is not None for r in alive) and layer.adamw.lr_dev == 64
+    del layer
+    gc.collect()
+    assert all(r() is None for r in alive)
+    for f, t in kinds.items():
+        for other in {torch.float64, torch.int64, torch.float32, torch.int32, torch.bfloat16} - {t}:
+            with pytest.raises(TypeError):
+                mh.make_adamw_options(1e-3, **{f: _Scalar(other)})
+        with pytest.raises(ValueError):
+            mh.make_adamw_options(1e-3, **{f: _Scalar(t, n=0)})
+        with pytest.raises(ValueError):  # host memory
+            mh.make_adamw_options(1e-3, **{f: torch.zeros(1, dtype=t)})
+        assert getattr(mh.make_adamw_options(1e-3, **{f: 64}), f) == 64  # addresses as they are
+
+
+def _layer_desc():
+    return mh.make_desc(T=64, H=64, I=64, E=8, E_local=4, k=2, n_chunks=1, dtype="bf16")
+
+
 def _layer(**kw):
     d = mh.make_desc(T=64, H=64, I=64, E=8, E_local=4, k=2, n_chunks=1, dtype="bf16", flags=kw.pop("flags", 0))
     bufs = {f: 4096 * (i + 1) for i, f in enumerate(mh.TENSOR_FIELDS)}
