@@ -546,12 +546,14 @@ def adamw_state(n, state_bits=32, device="cuda"):
 
 
 def make_layer_optimizer(d: MoeDesc, bufs, options, master=True, weight_decay=0.0, max_norm=None, bias_rate=0.0,
-                         device="cuda") -> MoeLayerOptimizer:
+                         device=None) -> MoeLayerOptimizer:
     """Optimizer of moe_layer_update for the layer's ``w1``, ``w2`` and ``w_r`` in ``bufs`` (which must stay the layer's): new
     moving averages, FP32 masters of BF16 weights (unless ``master`` is false), the norm's buffers where ``max_norm`` is
-    given. The router has no weight decay. The tensors are in ``optimizer.buffers``; set ``optimizer.adamw.step``
-    before each call."""
+    given, all on the weights' device unless ``device`` says otherwise. The router has no weight decay. The tensors are in
+    ``optimizer.buffers``; set ``optimizer.adamw.step`` before each call."""
     import torch
+    if device is None:
+        device = bufs["w1"].device
     o = MoeLayerOptimizer()
     o.adamw = options
     o.options = options  # (o.adamw is a copy without the references that the options keep)

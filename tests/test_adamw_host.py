@@ -174,6 +174,16 @@ def _layer_desc():
     return mh.make_desc(T=64, H=64, I=64, E=8, E_local=4, k=2, n_chunks=1, dtype="bf16")
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_layer_optimizer_lies_where_its_weights_do(bits):
+    torch = pytest.importorskip("torch")
+    bufs = {f: torch.ones(300, dtype=torch.bfloat16, device="meta") for f in ("w1", "w2", "w_r")}
+    o = mh.make_layer_optimizer(_layer_desc(), bufs, mh.make_adamw_options(1e-3, state_bits=bits), max_norm=1.0)
+    for f in ("w1", "w2", "w_r"):
+        assert all(x.device.type == "meta" for x in o.buffers[f].values()) and "master" in o.buffers[f]
+    assert o.buffers["norm"].device.type == o.buffers["norm_workspace"].device.type == "meta"
+
+
 def _layer(**kw):
     d = mh.make_desc(T=64, H=64, I=64, E=8, E_local=4, k=2, n_chunks=1, dtype="bf16", flags=kw.pop("flags", 0))
     bufs = {f: 4096 * (i + 1) for i, f in enumerate(mh.TENSOR_FIELDS)}
