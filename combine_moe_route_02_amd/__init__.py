@@ -457,7 +457,8 @@ def make_adamw_options(lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, state_bits=3
 
 
 class AdamwTensors:
-    """The tensors of moe_adamw_step and moe_grad_norm: their table, made once, and the references it needs.
+    """The tensors of moe_adamw_step and moe_grad_norm: their table, made once, and the references it needs. It holds
+    addresses: write gradients into the same tensors every step, or make a new table for new ones.
     ``state_bits`` is what their averages have (None without any)."""
 
     def __init__(self, parts):

@@ -332,7 +332,7 @@ moe_status moe_route_noalloc(const moe_desc* d, int chunk, const float* logits, 
   if (need > moe::kNoAllocRouteScratchBytes)
     return fail(MOE_ERR_UNSUPPORTED,
                 "moe_route_noalloc: the routing histograms need %lld bytes, above its fixed %lld-byte device "
-                "scratch (n_chunks * ceil(ceil(T/n_chunks)/64) * 4 * E * 4 bytes); use moe_route with a workspace",
+                "scratch (n_chunks * ceil(ceil(T/n_chunks)/64) * 5 * E * 4 bytes); use moe_route with a workspace",
                 (long long)need, (long long)moe::kNoAllocRouteScratchBytes);
   void* ws = nullptr;
   MOE_HIP(moe::route_noalloc_scratch(&ws), "moe_route_noalloc: hipGetSymbolAddress");

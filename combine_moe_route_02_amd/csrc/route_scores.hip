@@ -17,7 +17,7 @@
 // 16 lanes hold a token's row in registers (4 tokens per wave, float4 loads), and arithmetic bounds the kernel, not HBM. Per
 // lane the row's share becomes a sorted list of its five largest: a score's FP32 bits, the last few of which give way to the
 // number of the element, so that one insertion is five medians of three and no index travels beside the score. (131072
-// tokens of 256 experts in 8 groups: 51 us, 134 MB of logits; 727 vector instructions a wave, about 40 us of issue.) k + 2
+// tokens of 256 experts in 8 groups: 52 us, 134 MB of logits; 735 vector instructions a wave, about 40 us of issue.) k + 2
 // rounds of a maximum over the 16 lanes (DPP) pop the chosen experts and the first two left out. Where a lane's five are used
 // up (one token of 600 in groups, of 1200 without), the lists are made again from what is left.
 #include <algorithm>

@@ -150,8 +150,8 @@ moe_status moe_route(const moe_desc* d, int chunk, const float* logits, int32_t*
  * arguments and bitwise the same outputs, but its histogram scratch is a fixed 4 MiB device array
  * inside the library (one per GPU, held until the process ends). It allocates nothing and
  * returns MOE_ERR_UNSUPPORTED when the call needs more than that scratch:
- * n_chunks * ceil(ceil(T/n_chunks)/64) * 4 * E * 4 bytes > 4 MiB (at E = 128, more than 131072
- * tokens). Every call on one GPU shares the array, so calls that overlap on one GPU (different
+ * n_chunks * ceil(ceil(T/n_chunks)/64) * 5 * E * 4 bytes > 4 MiB (at E = 128, more than 104832
+ * tokens in one chunk). Every call on one GPU shares the array, so calls that overlap on one GPU (different
  * streams, or other host threads) race: order them on one stream or synchronise between them. */
 moe_status moe_route_noalloc(const moe_desc* d, int chunk, const float* logits, int32_t* topk_idx,
                              float* gates, int32_t* counts, int32_t* offsets, int32_t* row_of,
@@ -197,8 +197,9 @@ moe_status moe_route_scores(const moe_desc* d, int chunk, const moe_router_score
  * forward, then the router weight gradient, exactly as moe_route_bwd does with its dlogits. Softmax scores that are
  * not renormalised give every expert a gradient: set MOE_FLAG_ROUTER_LOSS for moe_dispatch_bwd then (the layer
  * primitives see to it themselves). With MOE_FLAG_ROUTER_LOSS the gradient is added to what dlogits holds. x NULL:
- * only dlogits is written, and dwr_acc, dwr and workspace are not used. dlogits may not be the logits buffer; with BF16
- * rows and x both must be 16-byte aligned (MOE_ERR_ARG). */
+ * only dlogits is written, and dwr_acc, dwr and workspace are not used (with T = 0 x may be NULL in either form: dwr_acc
+ * given, dwr_acc and dwr are written). dlogits may not be the logits buffer; with BF16 rows and x both must be 16-byte
+ * aligned (MOE_ERR_ARG). */
 moe_status moe_route_scores_bwd(const moe_desc* d, int chunk, const moe_router_scores* r, const float* logits,
                                 const float* dgates, const int32_t* topk_idx, const void* x, float* dlogits,
                                 float* dwr_acc, void* dwr, void* workspace, void* stream);
@@ -447,12 +448,12 @@ typedef struct moe_adamw_options {
 
 /* g = grad * grad_scale; m' = beta1 m + (1 - beta1) g; v' = beta2 v + (1 - beta2) g^2;
  * w' = w (1 - lr lr_scale weight_decay) - lr lr_scale / (1 - beta1^step) * m' / (sqrt(v' / (1 - beta2^step)) + eps),
- * in FP32 (m' and v' with each operation rounded once). A gradient that is not finite makes its element
+ * in FP32 (m' and v' with each operation rounded once; an eps below FP32's normal range counts as 0). A gradient that is not finite makes its element
  * NaN or infinite, and 8-bit averages of its block NaN; a v' below FP32's normal range may count as 0 in the root. One launch
  * per 256 tensors of a kind (weight, master and gradient types). */
 moe_status moe_adamw_step(const moe_adamw_options* o, int32_t n_tensors, const moe_adamw_tensor* tensors, void* stream);
 
-/* norm[0] = sqrt of the sum of squares of every gradient (FP64 sums in a fixed order, rounded once), norm[1] = max_norm /
+/* norm[0] = sqrt of the sum of squares of every gradient (FP64 squares and sums in a fixed order, rounded once), norm[1] = max_norm /
  * norm where the norm is above max_norm, 1 otherwise, NaN where it is not finite: moe_adamw_step's grad_scale. max_norm >
  * 0, infinity allowed. Of a tensor only grad, grad_dtype and n are used. workspace: moe_grad_norm_bytes() bytes, 8-byte
  * aligned, contents undefined before and after; calls that share one must be ordered. norm FP32 [2]. */
@@ -565,7 +566,8 @@ moe_status moe_layer_forward_backward(const moe_desc* d, const moe_tensors* t,
 /* The update that follows a layer's backward: AdamW on W1, W2 (local experts) and W_r with dw1, dw2 and dwr, in this order,
  * and, with MOE_FLAG_ROUTER_SCORES, a router_bias and a bias_rate other than 0, moe_router_bias_update from counts. t->w1,
  * t->w2 and t->w_r are written. With `norm` set, moe_grad_norm over the three runs first (max_norm, norm_workspace) and
- * scales the gradients; adamw.grad_scale must be NULL then. F32 and BF16 descriptors. Gradients (dwr at least), their
+ * scales the gradients; adamw.grad_scale must be NULL then. (A norm that is not finite leaves the weights and averages as
+ * they are, not the bias, whose counts do not hang on gradients.) F32 and BF16 descriptors. Gradients (dwr at least), their
  * norm and counts are this GPU's: sum them over GPUs before where weights are shared, with the stage calls. FP8 copies
  * of the weights (w1t, w2t) are the caller's to renew. */
 typedef struct moe_adamw_state {
