@@ -12,8 +12,8 @@
 // 8-bit averages. m = s c|c| / 127^2 and v = s c^4 / 255^4 with s the block's largest magnitude: the steps grow with
 // the value, so that entries 10^-4 (m) or 10^-9 (v) of the block's largest keep digits, which equal steps would lose.
 // A step of training moves m and v by some per cent or less, under half a code, and rounding to the nearest code
-// would hold them where they are; so the code above is taken with the chance of how near it is (the expected value
-// is exact), by a hash of the element's place, the step and the seed. v > 0 never rounds to 0: m / sqrt(v) stays bounded.
+// would hold them where they are; so the code above is taken with the chance of how near it is (by 16 bits: the expected value
+// is off by 2^-16 of a step of the codes at most), by a hash of the element's place, the step and the seed. v > 0 never rounds to 0: m / sqrt(v) stays bounded.
 // Every FP32 operation that decides a code is rounded once (no contraction), so the codes are defined bit by bit.
 #include <algorithm>
 #include <cmath>

@@ -422,8 +422,8 @@ moe_status moe_router_loss_bwd(const moe_desc* d, int32_t n_segments, float bala
  * Moving averages, state_bits 32: m and v FP32 [n], scales unused (NULL). state_bits 8: one byte each, blocks of 256
  * elements in a row with a scale, m_scale and v_scale FP32 [ceil(n / 256)]: m = s c |c| / 127^2 with int8 c, v = s (c /
  * 255)^4 with uint8 c (each product rounded in FP32; s is the block's largest magnitude, and blocks under 2^-120 are
- * zeros). A new value lies between two codes and takes the upper one with the chance of how near it is; a v above 0
- * keeps a code above 0. All zeros (codes and scales) is the state of a new run in either width.
+ * zeros). A new value lies between two codes and takes the upper one with the chance of how near it is (in steps of
+ * 2^-16, rounded up); a v above 0 keeps a code above 0. All zeros (codes and scales) is the state of a new run in either width.
  *
  * The chances come from a hash of `seed`, the step and the element's place (tensors one behind the other in the order
  * of the call, each from a multiple of 256 on): the same call gives the same bits. */

@@ -449,6 +449,39 @@ def test_every_code_stands_for_itself():
 # ------------------------------------------------------------------ streams, graphs, the layer
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_long_lists_replay_from_a_graph(bits):
+    """More tensors than the short argument list and than a launch holds, captured; the table is gone before the replays."""
+    torch, mh = _gpu()
+    sizes = [int(x) for x in np.random.default_rng(21).integers(0, 900, 300)]
+    a, b = (_Set(torch, mh, sizes, "master", "bf16", bits, seed=22) for _ in range(2))
+    step = torch.ones(1, dtype=torch.int64, device="cuda")
+    norm, ws = torch.empty(2, device="cuda"), torch.empty(mh.moe_grad_norm_bytes(), dtype=torch.uint8, device="cuda")
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        table = mh.make_adamw_tensors(a.parts)
+        mh.moe_grad_norm(table, 0.05, norm, ws)
+        mh.moe_adamw_step(mh.make_adamw_options(LR, B1, B2, EPS, state_bits=bits, seed=2, step_dev=step, grad_scale=norm[1:]), table)
+        for row in table.table:
+            row.n = row.w = row.grad = 0
+    norm2, ws2 = torch.empty(2, device="cuda"), torch.empty_like(ws)
+    for i in range(1, 4):
+        for p, q in zip(a.parts, b.parts):
+            p["grad"].mul_(1.5)
+            q["grad"].mul_(1.5)
+        step.fill_(i)
+        torch.cuda.synchronize()
+        g.replay()
+        mh.moe_grad_norm(b.table, 0.05, norm2, ws2)
+        mh.moe_adamw_step(mh.make_adamw_options(LR, B1, B2, EPS, step=i, state_bits=bits, seed=2, grad_scale=norm2[1:]), b.table)
+        torch.cuda.synchronize()
+        assert torch.equal(norm, norm2)
+        for p, q in zip(a.parts, b.parts):
+            for name in ("w", "master", "m", "v") + (("m_scale", "v_scale") if bits == 8 else ()):
+                assert torch.equal(p[name], q[name]), (i, name)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_replayed_with_step_and_rate_on_the_device(bits):
     torch, mh = _gpu()
     a, b = (_Set(torch, mh, [5000, 77], "bf16", "bf16", bits, seed=13) for _ in range(2))

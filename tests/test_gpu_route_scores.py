@@ -661,6 +661,34 @@ def test_serving_layer(dtype):
     assert rel <= (0.095 if dtype == "fp8" else 0.06), rel
 
 
+@pytest.mark.parametrize("dtype", ["fp8", "int8"])
+def test_serving_layer_from_x(dtype):
+    """Without logits: the layer on the logits that the projection left is the same, bit for bit."""
+    torch, mh = _gpu()
+    cfg = MoeConfig("rsx_" + dtype, T=300, H=256, I=128, E=32, E_local=8, e0=2, k=2, n_chunks=2, dtype="bf16", seed_base=1130)
+    _, b, _, _ = _layer_bufs(torch, mh, cfg, HOWS[0], backward=False)
+    d = mh.make_desc(T=cfg.T, H=cfg.H, I=cfg.I, E=cfg.E, E_local=cfg.E_local, k=cfg.k, n_chunks=2, dtype=dtype, e0=cfg.e0, flags=mh.FLAG_ROUTER_SCORES)
+    c = mh.allocate(d, backward=False)
+    c.update({n: b[n] for n in ("x", "router_bias", "router_scores", "w_r")})
+    c["w_r"].mul_(8.0)
+    for n, rows, cols in (("w1", 8 * 2 * cfg.I, cfg.H), ("w2", 8 * cfg.H, cfg.I)):
+        c[n] = torch.empty(rows, cols, dtype=torch.uint8, device="cuda")
+        c[n + "_scale"] = torch.empty(rows, device="cuda")
+        (mh.moe_quantize_rows_fp8 if dtype == "fp8" else mh.moe_quantize_rows_i8)(rows, cols, b[n], c[n], c[n + "_scale"])
+    got = {}
+    for logits in (None, "router_logits"):
+        c["logits"] = None if logits is None else c[logits].clone()
+        c["out"].fill_(3)
+        mh.moe_layer_forward(d, c, torch.cuda.current_stream(), torch.cuda.Stream())
+        torch.cuda.synchronize()
+        now = {n: c[n][:cfg.T].clone() for n in ("out", "topk_idx", "gates")}
+        assert not got or all(torch.equal(got[n], now[n]) for n in now)
+        got = now
+    lg, bias = c["router_logits"].cpu().numpy(), c["router_bias"].cpu().numpy()
+    np.testing.assert_array_equal(got["topk_idx"].cpu().numpy(), ors.route(lg, bias, cfg.k, **HOWS[0])[0])
+    assert float(got["out"].float().abs().max()) > 0
+
+
 @pytest.mark.parametrize("how", HOWS[:2], ids=["grouped", "softmax"])
 def test_layer_replays_in_a_graph(how):
     torch, mh = _gpu()
